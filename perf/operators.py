@@ -1,0 +1,425 @@
+"""Cases for four serving operators: a paged key/value cache held in 8 bits (its
+write, its read-back and the decode attention over it), and the decode attention
+of a batch whose rows share a long prefix.
+
+``own = False`` computes each operator in its plain form from elementary torch
+operations in 32 bits; ``own = True`` makes the calls of this package. Shapes are
+the ones this repository serves (32 query heads over 8 KV heads of 128, the
+tensor-parallel shard of 8 over 1, pages of 16 tokens, rows up to 32768 keys)
+and smaller and odd ones around them.
+
+The 8-bit cache: keys and values [num_blocks, h_kv, 16, d] in e4m3 with one
+power-of-two scale for each token and head, held as its biased exponent in
+[num_blocks, h_kv, 16] bytes. A stored value is code * 2^(byte - 127). For a row
+x of d numbers whose largest finite magnitude is a, the exponent is the smallest
+e in [-117, 119] with a <= 448 * 2^e, and the codes are x * 2^-e rounded to e4m3
+(ties to even); both products are exact, so codes are defined without rounding
+in between.
+"""
+import math
+
+import torch
+
+own = False
+
+PAGE = 16
+E_MIN, E_MAX = -117, 119
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+def listed():
+    return [
+        # One token of one sequence enters the cache: a decode step at batch 1,
+        # where only latency counts.
+        {"name": "write_one_token", "op": "write", "B": 1, "new": 1, "old": 1000, "h_kv": 8, "d": 128,
+         "dtype": "bf16", "ragged": False},
+        # A whole prompt, its keys and values still inside the fused projection's output.
+        {"name": "write_prompt_8192", "op": "write", "B": 1, "new": 8192, "old": 0, "h_kv": 8, "d": 128,
+         "dtype": "bf16", "ragged": False},
+        # Chunks of many sequences in 32 bits, heads of 64, lengths that start and end inside pages.
+        {"name": "write_ragged_f32", "op": "write", "B": 24, "new": 2731, "old": 517, "h_kv": 8, "d": 64,
+         "dtype": "f32", "ragged": True},
+        # The context of one short request, read back for a chunk of its prompt.
+        {"name": "read_row_333", "op": "read", "B": 1, "new": 333, "old": 0, "h_kv": 8, "d": 128,
+         "dtype": "bf16", "ragged": False},
+        # One long context read back whole.
+        {"name": "read_row_32768", "op": "read", "B": 1, "new": 32768, "old": 0, "h_kv": 8, "d": 128,
+         "dtype": "bf16", "ragged": False},
+        # The tails of many rows in 32 bits, odd head count.
+        {"name": "read_ragged_f32", "op": "read", "B": 40, "new": 1999, "old": 301, "h_kv": 5, "d": 64,
+         "dtype": "f32", "ragged": True},
+        # One short row, odd group of 5 query heads: launch latency.
+        {"name": "decode_e4m3_row_1000", "op": "decode", "B": 1, "h_kv": 8, "g": 5, "d": 128, "max_len": 1000,
+         "empty": 0, "ragged": False},
+        # One row of 32768 keys: the key axis has to fill the machine.
+        {"name": "decode_e4m3_row_32768", "op": "decode", "B": 1, "h_kv": 8, "g": 4, "d": 128, "max_len": 32768,
+         "empty": 0, "ragged": False},
+        # A serving batch: 64 rows of 1 to 16384 keys, shuffled pages, two rows still empty.
+        {"name": "decode_e4m3_batch_66", "op": "decode", "B": 66, "h_kv": 8, "g": 4, "d": 128, "max_len": 16384,
+         "empty": 2, "ragged": True},
+        # A few rows over a short common instruction, own parts of 0 to 100 keys.
+        {"name": "shared_3x333", "op": "shared", "B": 3, "h_kv": 8, "g": 4, "d": 128, "prefix": 333,
+         "suffix": 100, "ragged": True},
+        # A batch that shares a long system prompt.
+        {"name": "shared_64x8192", "op": "shared", "B": 64, "h_kv": 8, "g": 4, "d": 128, "prefix": 8192,
+         "suffix": 1000, "ragged": True},
+        # Many samples from one long document.
+        {"name": "shared_256x32768", "op": "shared", "B": 256, "h_kv": 8, "g": 4, "d": 128, "prefix": 32768,
+         "suffix": 700, "ragged": True},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["write", "read", "decode", "shared"])
+    d = rng.choice([64, 128, 128])
+    ragged = rng.random() < 0.7
+    if op in ("write", "read"):
+        B = _log(rng, 1, 64)
+        h_kv = rng.choice([1, 2, 3, 5, 8])
+        new = _log(rng, 1, 65536 // B)
+        return {"op": op, "B": B, "new": new, "old": rng.randrange(0, 2000), "h_kv": h_kv, "d": d,
+                "dtype": rng.choice(["bf16", "bf16", "f32"]), "ragged": ragged}
+    if op == "decode":
+        B = _log(rng, 1, 80)
+        max_len = _log(rng, 1, min(32768, 1000000 // B))
+        return {"op": op, "B": B, "h_kv": rng.choice([1, 2, 5, 8]), "g": rng.randint(1, 8), "d": d,
+                "max_len": max_len, "empty": rng.choice([0, 0, 1]) if B > 1 else 0, "ragged": ragged}
+    B = _log(rng, 1, 200)
+    return {"op": op, "B": B, "h_kv": rng.choice([1, 2, 4, 8]), "g": rng.choice([1, 2, 4, 8] if B <= 100 else [1, 2, 4]),
+            "d": d, "prefix": _log(rng, 1, 32768), "suffix": _log(rng, 1, 700), "ragged": ragged}
+
+
+# ---------------------------------------------------------------------------
+# Inputs
+# ---------------------------------------------------------------------------
+def _generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(seed))
+    return g
+
+
+def _lengths(case, seed):
+    """Row lengths (old keys, new keys) or key counts: on the host, from the
+    case alone, so that every seed does the same work in another order."""
+    g = torch.Generator()
+    g.manual_seed(12345)
+    B = case["B"]
+    if case["op"] in ("write", "read"):
+        new, old = torch.full((B,), case["new"]), torch.full((B,), case["old"])
+        if case["ragged"]:
+            new = torch.randint(1, case["new"] + 1, (B,), generator=g)
+            old = torch.randint(0, case["old"] + 1, (B,), generator=g)
+        lens = (new, old)
+    elif case["op"] == "decode":
+        n = torch.full((B,), case["max_len"])
+        if case["ragged"]:
+            n = torch.randint(1, case["max_len"] + 1, (B,), generator=g)
+        if case["empty"]:
+            n[torch.randperm(B, generator=g)[:case["empty"]]] = 0
+        lens = (n,)
+    else:
+        n = torch.full((B,), case["suffix"])
+        if case["ragged"]:
+            n = torch.randint(0, case["suffix"] + 1, (B,), generator=g)
+        lens = (n,)
+    order = torch.randperm(B, generator=torch.Generator().manual_seed(int(seed)))
+    return [n[order] for n in lens]
+
+
+def _table(lens, seed, first=0, width=None):
+    """Block table over a shuffled pool: unused entries are -1."""
+    need = (lens + PAGE - 1) // PAGE
+    width = max(1, int(need.max())) if width is None else width
+    total = int(need.sum())
+    perm = torch.randperm(total, generator=torch.Generator().manual_seed(int(seed) + 1)).to(torch.int32) + first
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
+    live = torch.arange(width)[None, :] < need[:, None]
+    table[live] = perm
+    return table.cuda(), total
+
+
+def _rows(g, shape):
+    """Keys as they meet a cache: N(0,1) with a few strong channels and token
+    norms that vary."""
+    x = torch.randn(shape, generator=g, device="cuda")
+    x[..., 1] *= 8.0
+    x[..., shape[-1] // 2] *= 5.0
+    return x * torch.exp2(2 * torch.rand(shape[:-1] + (1,), generator=g, device="cuda") - 1)
+
+
+def prepare(case, seed):
+    g = _generator(seed)
+    op, B, h_kv, d = case["op"], case["B"], case["h_kv"], case["d"]
+    s = {"op": op, "scale": 1.0 / math.sqrt(d)}
+    if op in ("write", "read"):
+        new, old = _lengths(case, seed)
+        lens = new + old
+        s["table"], nb = _table(lens, seed)
+        s["cu"] = torch.cat([torch.zeros(1, dtype=torch.int64), new.cumsum(0)]).to(torch.int32).cuda()
+        s["lens"] = lens.to(torch.int32).cuda()
+        s["total"] = int(new.sum())
+        s["dtype"] = torch.float32 if case["dtype"] == "f32" else torch.bfloat16
+        shape = (nb, h_kv, PAGE, d)
+        if op == "write":
+            # The fused projection's output: 4 query heads for each KV head, then keys, then values.
+            qkv = _rows(g, (s["total"], 6 * h_kv, d)).to(s["dtype"])
+            s["k"], s["v"] = qkv[:, 4 * h_kv:5 * h_kv], qkv[:, 5 * h_kv:]
+            s["kc"] = torch.zeros(shape, dtype=torch.float8_e4m3fn, device="cuda")
+            s["vc"] = torch.zeros(shape, dtype=torch.float8_e4m3fn, device="cuda")
+            s["ks"] = torch.zeros(shape[:3], dtype=torch.uint8, device="cuda")
+            s["vs"] = torch.zeros(shape[:3], dtype=torch.uint8, device="cuda")
+        else:
+            s["kc"], s["ks"] = _quantise(_rows(g, shape).to(torch.bfloat16))
+            s["vc"], s["vs"] = _quantise(torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16))
+            s["k"] = torch.empty((s["total"], h_kv, d), dtype=s["dtype"], device="cuda")
+            s["v"] = torch.empty_like(s["k"])
+        return s
+    h = h_kv * case["g"]
+    (n,) = _lengths(case, seed)
+    s["lens"] = n.to(torch.int32).cuda()
+    s["q"] = torch.randn((B, h, d), generator=g, device="cuda").to(torch.bfloat16)
+    s["o"] = torch.empty_like(s["q"])
+    s["lse"] = torch.empty((B, h), device="cuda")
+    if op == "decode":
+        s["table"], nb = _table(n, seed)
+        shape = (max(nb, 1), h_kv, PAGE, d)
+        s["kc"], s["ks"] = _quantise(_rows(g, shape).to(torch.bfloat16))
+        s["vc"], s["vs"] = _quantise(torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16))
+        return s
+    # The shared prefix's pages and the rows' own ones in one pool, each part shuffled.
+    s["ptable"], pages = _table(torch.tensor([case["prefix"]]), seed + 7)
+    s["ptable"] = s["ptable"].reshape(-1).contiguous()
+    s["plen"] = torch.tensor([case["prefix"]], dtype=torch.int32, device="cuda")
+    s["table"], nb = _table(n, seed, first=pages)
+    shape = (pages + nb, PAGE, h_kv, d)
+    s["kc"] = _rows(g, shape).to(torch.bfloat16)
+    s["vc"] = torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+    return s
+
+
+# ---------------------------------------------------------------------------
+# Plain forms
+# ---------------------------------------------------------------------------
+def _quantise(x):
+    """Codes and biased exponents of the rows of x."""
+    x = x.float()
+    m, e = torch.frexp(x.abs().amax(-1))  # a = m * 2^e, m in [0.5, 1): 448 = 0.875 * 2^9
+    e = (e - 9 + (m > 0.875).to(e.dtype)).clamp(E_MIN, E_MAX)
+    e = torch.where(m == 0, torch.full_like(e, E_MIN), e)
+    codes = (x * _power(127 - e)).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    return codes, (e + 127).to(torch.uint8)
+
+
+def _power(biased):
+    """2^(biased - 127) as a column of 32-bit numbers, by its bits."""
+    return torch.bitwise_left_shift(biased.to(torch.int32), 23).view(torch.float32)[..., None]
+
+
+def _values(codes, exponents):
+    return codes.float() * _power(exponents)
+
+
+def _slots(s):
+    """Page and slot of every token between cu[0] and cu[B]."""
+    t = torch.arange(s["total"], device="cuda", dtype=torch.int32)
+    b = torch.bucketize(t, s["cu"], right=True) - 1
+    pos = s["lens"][b].long() - s["cu"][b + 1] + t
+    return s["table"][b, pos // PAGE].long(), pos % PAGE
+
+
+def _softmax_parts(scores, values):
+    """(max, sum, weighted sum) over the last axis of scores; a row without keys has sum 0."""
+    m = scores.amax(-1, keepdim=True)
+    p = torch.exp(scores - torch.where(torch.isinf(m), torch.zeros_like(m), m))
+    return m[..., 0], p.sum(-1), torch.matmul(p, values)
+
+
+def _gather(s, cache):
+    """Rows' keys or values [B, h_kv, keys, d] and which of them exist, from a
+    cache that holds [blocks, h_kv, 16, d]."""
+    table = s["table"].long().clamp(min=0)
+    x = cache[table].transpose(1, 2)
+    x = x.reshape(x.shape[0], x.shape[1], -1, x.shape[-1])
+    return x, torch.arange(x.shape[2], device="cuda")[None, :] < s["lens"][:, None]
+
+
+def _run_plain(s):
+    op = s["op"]
+    if op == "write":
+        page, slot = _slots(s)
+        for x, c, e in ((s["k"], s["kc"], s["ks"]), (s["v"], s["vc"], s["vs"])):
+            codes, exponents = _quantise(x)
+            c.view(torch.uint8)[page, :, slot] = codes.view(torch.uint8)
+            e[page, :, slot] = exponents
+        return {"k_cache": s["kc"], "v_cache": s["vc"], "k_scale": s["ks"], "v_scale": s["vs"]}
+    if op == "read":
+        page, slot = _slots(s)
+        u8 = torch.uint8
+        k = _values(s["kc"].view(u8)[page, :, slot].view(s["kc"].dtype), s["ks"][page, :, slot])
+        v = _values(s["vc"].view(u8)[page, :, slot].view(s["vc"].dtype), s["vs"][page, :, slot])
+        return {"k": k.to(s["dtype"]), "v": v.to(s["dtype"])}
+    q = s["q"].float()
+    B, h, d = q.shape
+    if op == "decode":
+        k = _values(_gather(s, s["kc"].view(torch.uint8))[0].view(s["kc"].dtype), _gather(s, s["ks"][..., None])[0][..., 0])
+        v, live = _gather(s, s["vc"].view(torch.uint8))
+        v = _values(v.view(s["vc"].dtype), _gather(s, s["vs"][..., None])[0][..., 0])
+    else:
+        k, live = _gather(s, s["kc"].transpose(1, 2))
+        v, _ = _gather(s, s["vc"].transpose(1, 2))
+        k, v = k.float(), v.float()
+    h_kv = k.shape[1]
+    q = q.reshape(B, h_kv, h // h_kv, d) * s["scale"]
+    scores = torch.matmul(q, k.transpose(2, 3)).masked_fill(~live[:, None, None, :], -math.inf)
+    m, l, acc = _softmax_parts(scores, v)
+    if op == "shared":
+        n = s["plen"].long()
+        pk = s["kc"][s["ptable"].long()].float().reshape(-1, h_kv, d).transpose(0, 1)
+        pv = s["vc"][s["ptable"].long()].float().reshape(-1, h_kv, d).transpose(0, 1)
+        qp = q.transpose(0, 1).reshape(h_kv, -1, d)
+        ps = torch.matmul(qp, pk.transpose(1, 2))
+        ps = ps.masked_fill(torch.arange(pk.shape[1], device="cuda")[None, None, :] >= n, -math.inf)
+        pm, pl, pacc = _softmax_parts(ps, pv)
+        pm, pl = (x.reshape(h_kv, B, -1).transpose(0, 1) for x in (pm, pl))
+        pacc = pacc.reshape(h_kv, B, -1, d).transpose(0, 1)
+        top = torch.maximum(m, pm)
+        wa, wb = torch.exp(m - top), torch.exp(pm - top)
+        m, l, acc = top, l * wa + pl * wb, acc * wa[..., None] + pacc * wb[..., None]
+    empty = l == 0
+    o = acc / torch.where(empty, torch.ones_like(l), l)[..., None]
+    lse = torch.where(empty, torch.full_like(l, -math.inf), m + torch.log(l))
+    return {"o": o.reshape(B, h, d).to(torch.bfloat16), "lse": lse.reshape(B, h)}
+
+
+def _run_own(s):
+    import online_softmax_attn_gb300 as attn
+
+    op = s["op"]
+    if op == "write":
+        attn.attn_cache_write_e4m3(s["k"], s["v"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["cu"], s["lens"])
+        return {"k_cache": s["kc"], "v_cache": s["vc"], "k_scale": s["ks"], "v_scale": s["vs"]}
+    if op == "read":
+        attn.attn_cache_read_e4m3(s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["cu"], s["lens"], s["k"], s["v"])
+        return {"k": s["k"], "v": s["v"]}
+    B, h, d = s["q"].shape
+    if op == "decode":
+        if "ws" not in s:  # a program keeps its scratch memory from step to step
+            n = attn.attn_decode_e4m3_workspace_bytes(B, h, s["kc"].shape[1], d)
+            s["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")
+        o, lse = attn.attn_decode_paged_e4m3(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"],
+                                             s["scale"], workspace=s["ws"], o=s["o"], lse=s["lse"])
+    else:
+        if "ws" not in s:
+            n = attn.attn_decode_shared_workspace_bytes(B, h, s["kc"].shape[2], d, s["table"].shape[1])
+            s["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")
+        o, lse = attn.attn_decode_paged_shared(s["q"], s["kc"], s["vc"], s["ptable"], s["plen"], s["table"], s["lens"],
+                                               s["scale"], workspace=s["ws"], o=s["o"], lse=s["lse"])
+    return {"o": o, "lse": lse}
+
+
+def run(state):
+    return _run_own(state) if own else _run_plain(state)
+
+
+# ---------------------------------------------------------------------------
+# Work and exact values
+# ---------------------------------------------------------------------------
+def work(case):
+    h_kv, d, B = case["h_kv"], case["d"], case["B"]
+    if case["op"] in ("write", "read"):
+        new, _ = _lengths(case, 0)
+        size = 4 if case["dtype"] == "f32" else 2
+        rows = 2 * int(new.sum()) * h_kv
+        return {"bytes": rows * (d * (size + 1) + 1), "flops": 2 * rows * d}
+    (n,) = _lengths(case, 0)
+    h, keys = h_kv * case["g"], int(n.sum())
+    ends = B * h * d * 4 + B * h * 4 + B * 4
+    if case["op"] == "decode":
+        return {"bytes": 2 * keys * h_kv * (d + 1) + ends, "flops": 4 * keys * h * d}
+    return {"bytes": 2 * (keys + case["prefix"]) * h_kv * d * 2 + ends,
+            "flops": 4 * (keys + B * case["prefix"]) * h * d}
+
+
+def _power64(e):
+    """2^e in 64 bits, by its bits (a library's power may be off in the last one)."""
+    return torch.bitwise_left_shift(e.to(torch.int64) + 1023, 52).view(torch.float64)
+
+
+def _grid64(x):
+    """Codes (as their values) and exponents of the rows of x in 64 bits, by the
+    definition: e is the smallest exponent in range with |x| <= 448 * 2^e."""
+    x = x.double()
+    a = x.abs().amax(-1)
+    e = torch.ceil(torch.log2(torch.clamp(a, min=2.0 ** -140) / 448.0)).clamp(E_MIN, E_MAX)
+    e = torch.where((e > E_MIN) & (a <= 448.0 * _power64(e - 1)), e - 1, e)  # log2 may land one off at a border
+    e = torch.where((e < E_MAX) & (a > 448.0 * _power64(e)), e + 1, e)
+    y = (x / _power64(e)[..., None]).clamp(-448.0, 448.0)
+    step = _power64(torch.clamp(torch.frexp(y)[1] - 1, min=-6) - 3)
+    return torch.round(y / step) * step, (e + 127).to(torch.uint8)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op, d, h_kv = s["op"], case["d"], case["h_kv"]
+    lens = s["lens"].tolist()
+    table = s["table"].long()
+    if op in ("write", "read"):
+        cu = s["cu"].tolist()
+        at = torch.cat([torch.arange(lens[b] - (cu[b + 1] - cu[b]), lens[b], device="cuda") + b * table.shape[1] * PAGE
+                        for b in range(len(lens))])
+        where = table.reshape(-1)[at // PAGE] * PAGE + at % PAGE  # flat slot of each token
+        if op == "write":
+            out = {}
+            for x, c, name in ((s["k"], s["kc"], "k"), (s["v"], s["vc"], "v")):
+                codes, exps = _grid64(x)
+                full = torch.zeros((c.shape[0] * PAGE, h_kv, d), dtype=torch.float64, device="cuda")
+                full[where] = codes
+                fe = torch.zeros((c.shape[0] * PAGE, h_kv), dtype=torch.uint8, device="cuda")
+                fe[where] = exps
+                out[name + "_cache"] = full.view(-1, PAGE, h_kv, d).transpose(1, 2).contiguous()
+                out[name + "_scale"] = fe.view(-1, PAGE, h_kv).transpose(1, 2).contiguous()
+            return out
+        out = {}
+        for c, e, name in ((s["kc"], s["ks"], "k"), (s["vc"], s["vs"], "v")):
+            flat = c.view(torch.uint8).transpose(1, 2).reshape(-1, h_kv, d)[where].view(c.dtype).double()
+            ex = e.transpose(1, 2).reshape(-1, h_kv)[where].long()
+            out[name] = flat * _power64(ex - 127)[..., None]
+        return out
+    B, h = s["q"].shape[:2]
+    g = h // h_kv
+    o = torch.zeros((B, h, d), dtype=torch.float64, device="cuda")
+    lse = torch.full((B, h), -math.inf, dtype=torch.float64, device="cuda")
+
+    def rows(pages, n, cache, exps):
+        """Values [h_kv, n, d] in 64 bits of a list of pages."""
+        if exps is None:
+            return cache[pages].reshape(-1, h_kv, d)[:n].double().transpose(0, 1)
+        x = cache.view(torch.uint8)[pages].view(cache.dtype).double() * _power64(exps[pages].long() - 127)[..., None]
+        return x.transpose(1, 2).reshape(-1, h_kv, d)[:n].transpose(0, 1)
+
+    def two(kc, vc, ks, vs, pages, n):
+        return rows(pages, n, kc, ks), rows(pages, n, vc, vs)
+
+    ks, vs = s.get("ks"), s.get("vs")
+    if op == "shared":
+        pk, pv = two(s["kc"], s["vc"], None, None, s["ptable"].long(), case["prefix"])
+    for b in range(B):
+        k, v = two(s["kc"], s["vc"], ks, vs, table[b, :(lens[b] + PAGE - 1) // PAGE], lens[b])
+        if op == "shared":
+            k, v = torch.cat([pk, k], 1), torch.cat([pv, v], 1)
+        if k.shape[1] == 0:
+            continue
+        qb = s["q"][b].double().view(h_kv, g, d)
+        scores = torch.einsum("hgd,hnd->hgn", qb, k) / math.sqrt(d)
+        top = scores.amax(-1, keepdim=True)
+        p = torch.exp(scores - top)
+        total = p.sum(-1)
+        o[b] = (torch.einsum("hgn,hnd->hgd", p, v) / total[..., None]).reshape(h, d)
+        lse[b] = (top[..., 0] + torch.log(total)).reshape(h)
+    return {"o": o, "lse": lse}
