@@ -521,6 +521,110 @@ attn_status_t attn_merge_lse_pair(const void* o_a, const float* lse_a, const voi
                                   void* o, float* lse, attn_dtype_t out_dtype, void* stream);
 
 /*
+ * The 8-bit cache. Keys and values of a token and KV head are held as d_h
+ * e4m3 codes and one exponent byte E: value = code * 2^(E - 127). Written rows
+ * have, with a the largest finite magnitude of the row, E - 127 = the smallest
+ * e in [-117, 119] with a <= 448 * 2^e, and codes e4m3(x * 2^-e), ties to even;
+ * magnitudes beyond 448 * 2^119 take the largest code. The scale is a power of
+ * two, so it adds no rounding and every stored value is a bf16 number. NaN and
+ * infinities are stored as NaN codes (e4m3 has no infinity) and do not take
+ * part in the row's scale. (The pages name no 8-bit cache; layout and scale
+ * are this library's.)
+ *   k_cache, v_cache  [num_blocks, h_kv, 16, d_h] e4m3 codes: head-major
+ *                     inside a page, unlike the bf16 caches, so that one
+ *                     head's page is one run of 16 * d_h bytes
+ *   k_scale, v_scale  [num_blocks, h_kv, 16] exponent bytes
+ * All four 16-byte aligned.
+ */
+
+/*
+ * attn_cache_write_e4m3 -- quantise new tokens into the 8-bit cache. Tokens are
+ * packed as the queries of attn_prefill_paged are: row b's new tokens are
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1 and sit at the last positions of its
+ * seq_lens[b] keys (the length after the write), position p in slot p % 16 of
+ * page block_table[b][p / 16].
+ *   k, v          [total, h_kv, d_h] dtype, d_h contiguous, token and head
+ *                 strides in elements (each a multiple of 16 bytes; slices of
+ *                 a fused projection's output need no copy)           (read)
+ *   block_table   [B, max_blocks_per_seq], cu_seqlens [B + 1] non-decreasing,
+ *                 seq_lens [B], int32                                  (read)
+ *   caches        as above; slots that no token maps to keep their
+ *                 contents                                             (written)
+ * Tokens before cu_seqlens[0] or from cu_seqlens[B] on (a padded batch) are
+ * ignored. Two tokens must not map to the same slot: what it then holds may
+ * mix the two. A token whose position is outside [0, max_blocks_per_seq * 16)
+ * is dropped and sets ATTN_DEVERR_BAD_SEQ_LEN; one whose page is outside the
+ * cache is dropped and sets ATTN_DEVERR_BAD_PAGE. One kernel, no workspace.
+ * Errors: INVALID_ARG for NULL or misaligned pointers or strides, negative or
+ * zero sizes (B == 0 and total == 0 are no-ops), h_kv > 65535, an unknown
+ * dtype; UNSUPPORTED for d_h other than 64 / 128 or page_size != 16.
+ */
+attn_status_t attn_cache_write_e4m3(const void* k, const void* v, long long k_stride_token,
+                                    long long k_stride_head, long long v_stride_token,
+                                    long long v_stride_head, attn_dtype_t dtype,
+                                    const int32_t* block_table, const int32_t* cu_seqlens,
+                                    const int32_t* seq_lens, int B, int total, int h_kv, int d_h,
+                                    int page_size, int num_blocks, int max_blocks_per_seq,
+                                    void* k_cache, void* v_cache, uint8_t* k_scale,
+                                    uint8_t* v_scale, void* stream);
+
+/*
+ * attn_cache_read_e4m3 -- read tokens back from the 8-bit cache, exactly (the
+ * stored values are bf16 and fp32 numbers): the reverse of
+ * attn_cache_write_e4m3 with the same arguments, row b's
+ * cu_seqlens[b+1] - cu_seqlens[b] last tokens going to
+ * k, v [total, h_kv, d_h] (strided as there; written). With head stride
+ * total * d_h and token stride d_h the result is the [h_kv, T, d_h] that
+ * attn_prefill reads; dense, a row that starts at a multiple of 16 is a run
+ * of pages of the bf16 caches. Tokens outside the sequences, or whose
+ * position is outside the table row (ATTN_DEVERR_BAD_SEQ_LEN), are not
+ * written; a page outside the cache reads as zeros (ATTN_DEVERR_BAD_PAGE).
+ * The outputs must not overlap each other or the cache. Errors as above.
+ */
+attn_status_t attn_cache_read_e4m3(const void* k_cache, const void* v_cache,
+                                   const uint8_t* k_scale, const uint8_t* v_scale,
+                                   const int32_t* block_table, const int32_t* cu_seqlens,
+                                   const int32_t* seq_lens, int B, int total, int h_kv, int d_h,
+                                   int page_size, int num_blocks, int max_blocks_per_seq, void* k,
+                                   void* v, long long k_stride_token, long long k_stride_head,
+                                   long long v_stride_token, long long v_stride_head,
+                                   attn_dtype_t dtype, void* stream);
+
+/*
+ * attn_decode_paged_e4m3 -- attn_decode_paged over the 8-bit cache: one query
+ * token per row, o = softmax(scale q K^T) V with K and V the stored values
+ * ([DEC] throughout; method and results as attn_decode_paged, fp32 statistics
+ * and accumulation). The keys of all rows, laid end to end, are cut into equal
+ * runs on the device, so there is no split count to choose, any mix of lengths
+ * is balanced, the launch does not depend on the lengths (capturable), and the
+ * result does not depend on timing (no atomics).
+ *   q           [B, h, d_h] bf16                                     (read)
+ *   caches      as above                                             (read)
+ *   block_table [B, max_blocks_per_seq], seq_lens [B], int32         (read)
+ *   workspace   256-byte aligned, attn_decode_e4m3_workspace_bytes(B, h, h_kv,
+ *               d_h) bytes, overwritten; calls (and captured graphs) that
+ *               share one must not overlap on the GPU
+ *   o           [B, h, d_h] bf16                                     (written)
+ *   lse         [B, h] fp32, natural log, may be NULL                (written)
+ * Any h / h_kv; more than 8 query heads per KV head read its keys once per 8.
+ * A row of length 0 gives o = 0, lse = -inf. Lengths outside the table row are
+ * clamped (ATTN_DEVERR_BAD_SEQ_LEN), pages outside the cache read as zeros
+ * (ATTN_DEVERR_BAD_PAGE). NaN codes reach the rows that attend them; slots
+ * past a row's length never do.
+ * Errors: INVALID_ARG for NULL or misaligned pointers, B outside [0, 65535],
+ * bad sizes, num_blocks * h_kv or B * h beyond int32, scale not finite and
+ * > 0, a small workspace; UNSUPPORTED for d_h other than 64 / 128 or page_size
+ * != 16. B == 0 is a no-op.
+ */
+size_t attn_decode_e4m3_workspace_bytes(int B, int h, int h_kv, int d_h);
+attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                     const uint8_t* k_scale, const uint8_t* v_scale,
+                                     const int32_t* block_table, const int32_t* seq_lens, int B,
+                                     int h, int h_kv, int d_h, int page_size, int num_blocks,
+                                     int max_blocks_per_seq, float scale, void* workspace,
+                                     size_t workspace_bytes, void* o, float* lse, void* stream);
+
+/*
  * attn_get_device_error -- synchronise `stream`, then read and clear the
  * device error word of every kernel module (ATTN_DEVERR_* bits, 0 = none)
  * into *bits. Returns ATTN_ERR_CUDA if the synchronisation fails.

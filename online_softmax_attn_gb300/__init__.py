@@ -8,6 +8,7 @@ library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -25,6 +26,10 @@ __all__ = [
     "attn_recommended_splits",
     "attn_recommended_splits_ragged",
     "attn_decode_workspace_bytes",
+    "attn_cache_write_e4m3",
+    "attn_cache_read_e4m3",
+    "attn_decode_paged_e4m3",
+    "attn_decode_e4m3_workspace_bytes",
     "attn_get_device_error",
     "attn_get_last_device_error",
     "attn_selftest_prefill_stall",
@@ -107,6 +112,14 @@ def library() -> ctypes.CDLL:
     lib.attn_merge_states.restype = I
     lib.attn_merge_lse_pair.argtypes = [P, P, P, P, I, I, I, P, P, I, P]
     lib.attn_merge_lse_pair.restype = I
+    lib.attn_cache_write_e4m3.argtypes = [P, P, Z, Z, Z, Z, I, P, P, P, I, I, I, I, I, I, I, P, P, P, P, P]
+    lib.attn_cache_write_e4m3.restype = I
+    lib.attn_cache_read_e4m3.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, Z, Z, Z, Z, I, P]
+    lib.attn_cache_read_e4m3.restype = I
+    lib.attn_decode_e4m3_workspace_bytes.argtypes = [I, I, I, I]
+    lib.attn_decode_e4m3_workspace_bytes.restype = S
+    lib.attn_decode_paged_e4m3.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, S, P, P, P]
+    lib.attn_decode_paged_e4m3.restype = I
     lib.attn_selftest_delayed_copy.argtypes = [P, P, I, ctypes.c_uint, P]
     lib.attn_selftest_delayed_copy.restype = I
     lib.attn_selftest_prefill_stall.argtypes = [I]
@@ -514,6 +527,134 @@ def attn_merge_lse_pair(o_a, lse_a, o_b, lse_b, out_dtype=torch.bfloat16, o=None
     st = library().attn_merge_lse_pair(_ptr(o_a), _ptr(lse_a), _ptr(o_b), _ptr(lse_b), rows, d,
                                        dt_in, _ptr(o), _ptr(lse), dt_out, _stream(stream))
     _check("attn_merge_lse_pair", st)
+    return o, lse
+
+
+def _same_device(*ts):
+    """Every tensor on the current CUDA device (kernels launch there)."""
+    dev = ts[0].device
+    _need(dev.type == "cuda" and dev.index == torch.cuda.current_device(),
+          "tensors must be on the current CUDA device")
+    for t in ts:
+        _need(t.device == dev, "tensors must be on one CUDA device")
+
+
+def _cache_e4m3(k_cache, v_cache, k_scale, v_scale):
+    """Shape (num_blocks, h_kv, page, d) of a checked 8-bit cache."""
+    _need(k_cache.dtype == v_cache.dtype == torch.float8_e4m3fn, "caches must be float8_e4m3fn")
+    _need(k_scale.dtype == v_scale.dtype == torch.uint8, "scales must be uint8 exponents")
+    _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and
+          k_scale.shape == v_scale.shape == k_cache.shape[:3],
+          "caches [num_blocks,h_kv,16,d] and scales [num_blocks,h_kv,16] expected")
+    for t in (k_cache, v_cache, k_scale, v_scale):
+        _need(t.is_contiguous(), "caches and scales must be contiguous")
+    return k_cache.shape
+
+
+def _cache_tokens(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens):
+    _same_device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens)
+    nb, h_kv, page, d = _cache_e4m3(k_cache, v_cache, k_scale, v_scale)
+    _need(k.dtype == v.dtype and k.dtype in (torch.bfloat16, torch.float32), "k, v must share dtype bf16 or fp32")
+    _need(k.dim() == 3 and k.shape == v.shape and k.shape[1] == h_kv and k.shape[2] == d,
+          "k, v [total,h_kv,d] expected")
+    ks, vs = k.stride(), v.stride()
+    _need(ks[2] == 1 and vs[2] == 1, "k, v must be contiguous in d")
+    _need(block_table.dtype == cu_seqlens.dtype == seq_lens.dtype == torch.int32,
+          "block_table, cu_seqlens and seq_lens must be int32")
+    _need(block_table.is_contiguous() and cu_seqlens.is_contiguous() and seq_lens.is_contiguous(),
+          "block_table, cu_seqlens and seq_lens must be contiguous")
+    B = seq_lens.numel()
+    _need(seq_lens.dim() == 1 and cu_seqlens.shape == (B + 1,) and block_table.dim() == 2 and
+          block_table.shape[0] == B, "block_table [B,max_blocks], cu_seqlens [B+1] and seq_lens [B] expected")
+    dt = ATTN_DTYPE_BF16 if k.dtype == torch.bfloat16 else ATTN_DTYPE_F32
+    return ks, vs, dt, (B, k.shape[0], h_kv, d, page, nb, block_table.shape[1])
+
+
+def attn_cache_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens,
+                          stream=None) -> None:
+    """Quantise new tokens into the 8-bit paged cache. k, v [total, h_kv, d]
+    (bf16 or fp32, d contiguous, 16-byte aligned rows; slices of a fused
+    projection need no copy): row b's tokens cu_seqlens[b] .. cu_seqlens[b+1]-1
+    are the last of its seq_lens[b] positions. Caches [num_blocks, h_kv, 16, d]
+    float8_e4m3fn and scales [num_blocks, h_kv, 16] uint8 are updated in place:
+    value = code * 2^(byte - 127)."""
+    ks, vs, dt, shape = _cache_tokens(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens)
+    st = library().attn_cache_write_e4m3(
+        k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], dt, block_table.data_ptr(),
+        cu_seqlens.data_ptr(), seq_lens.data_ptr(), *shape, k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), _stream(stream))
+    _check("attn_cache_write_e4m3", st)
+
+
+def attn_cache_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens, k, v,
+                         stream=None):
+    """Read tokens back from the 8-bit paged cache into k, v [total, h_kv, d]
+    (bf16 or fp32, strided as in attn_cache_write_e4m3): row b's last
+    cu_seqlens[b+1] - cu_seqlens[b] positions go to its tokens, exactly.
+    Returns (k, v)."""
+    ks, vs, dt, shape = _cache_tokens(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens)
+    st = library().attn_cache_read_e4m3(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), *shape, k.data_ptr(),
+        v.data_ptr(), ks[0], ks[1], vs[0], vs[1], dt, _stream(stream))
+    _check("attn_cache_read_e4m3", st)
+    return k, v
+
+
+def _outputs(q, B, h, need, workspace, o, lse, return_lse, stream):
+    """Workspace and outputs of a decode call: the caller's, checked, or new
+    ones, allocated for the stream that the call runs on."""
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        else:
+            _same_device(q, workspace)
+            _need(workspace.is_contiguous(), "workspace must be contiguous")
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _need(o.shape == q.shape and o.dtype == q.dtype and o.is_contiguous() and o.device == q.device,
+                  "o must be like q")
+        if lse is not None:
+            _need(lse.shape == (B, h) and lse.dtype == torch.float32 and lse.is_contiguous() and
+                  lse.device == q.device, "lse must be contiguous fp32 [B,h]")
+        elif return_lse:
+            lse = torch.empty((B, h), dtype=torch.float32, device=q.device)
+    return workspace, o, lse
+
+
+def attn_decode_e4m3_workspace_bytes(B: int, h: int, h_kv: int, d_h: int) -> int:
+    """Workspace bytes of attn_decode_paged_e4m3."""
+    return int(library().attn_decode_e4m3_workspace_bytes(int(B), int(h), int(h_kv), int(d_h)))
+
+
+def attn_decode_paged_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                           scale: float | None = None, workspace=None, o=None, lse=None,
+                           return_lse: bool = True, stream=None):
+    """Paged decode over the 8-bit cache of attn_cache_write_e4m3. q [B,h,d]
+    bf16, block_table [B,max_blocks] int32, seq_lens [B] int32 (all CUDA,
+    contiguous); any h / h_kv. The keys are divided over the GPU on the device,
+    so the call can be captured and replayed with new lengths.
+    Returns (o [B,h,d] bf16, lse [B,h] fp32 or None)."""
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    nb, h_kv, page, d = _cache_e4m3(k_cache, v_cache, k_scale, v_scale)
+    _need(q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_contiguous() and q.shape[2] == d,
+          "q must be contiguous bf16 [B,h,d]")
+    _need(block_table.dtype == seq_lens.dtype == torch.int32, "block_table and seq_lens must be int32")
+    B, h, _ = q.shape
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and seq_lens.shape == (B,) and
+          block_table.is_contiguous() and seq_lens.is_contiguous(),
+          "contiguous block_table [B,max_blocks] and seq_lens [B] expected")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    lib = library()
+    need = lib.attn_decode_e4m3_workspace_bytes(B, h, h_kv, d)
+    workspace, o, lse = _outputs(q, B, h, need, workspace, o, lse, return_lse, stream)
+    st = lib.attn_decode_paged_e4m3(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), B, h, h_kv, d, page, nb, block_table.shape[1],
+        scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(), o.data_ptr(),
+        None if lse is None else lse.data_ptr(), _stream(stream))
+    _check("attn_decode_paged_e4m3", st)
     return o, lse
 
 

@@ -434,6 +434,147 @@ attn_status_t attn_merge_lse_pair(const void* o_a, const float* lse_a, const voi
                                      out_dtype, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+// Shared checks of attn_cache_write_e4m3 and attn_cache_read_e4m3.
+attn_status_t cache_tokens(const void* k, const void* v, long long k_tok, long long k_head,
+                           long long v_tok, long long v_head, attn_dtype_t dtype,
+                           const int32_t* block_table, const int32_t* cu_seqlens,
+                           const int32_t* seq_lens, int B, int total, int h_kv, int d_h,
+                           int page_size, int num_blocks, int max_blocks_per_seq,
+                           const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                           const uint8_t* v_scale, CacheTokens* a) {
+  if (B < 0 || total < 0 || h_kv < 1 || h_kv > 65535 || num_blocks < 1 || max_blocks_per_seq < 1)
+    return ATTN_ERR_INVALID_ARG;
+  if (dtype != ATTN_DTYPE_F32 && dtype != ATTN_DTYPE_BF16) return ATTN_ERR_INVALID_ARG;
+  if ((d_h != 64 && d_h != 128) || page_size != 16) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_blocks_per_seq) * page_size > (1ll << 30))
+    return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || total == 0) return ATTN_OK;
+  if (!k || !v || !block_table || !cu_seqlens || !seq_lens || !k_cache || !v_cache || !k_scale ||
+      !v_scale)
+    return ATTN_ERR_INVALID_ARG;
+  const long long unit = dtype == ATTN_DTYPE_BF16 ? 8 : 4;  // elements in 16 bytes
+  if (k_tok % unit || k_head % unit || v_tok % unit || v_head % unit) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(block_table, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  a->k = const_cast<void*>(k);
+  a->v = const_cast<void*>(v);
+  a->k_tok = k_tok;
+  a->k_head = k_head;
+  a->v_tok = v_tok;
+  a->v_head = v_head;
+  a->dtype = dtype;
+  a->block_table = block_table;
+  a->cu = cu_seqlens;
+  a->seq_lens = seq_lens;
+  a->B = B;
+  a->total = total;
+  a->h_kv = h_kv;
+  a->d_h = d_h;
+  a->num_blocks = num_blocks;
+  a->max_blocks = max_blocks_per_seq;
+  a->k_codes = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+  a->v_codes = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+  a->k_exp = const_cast<uint8_t*>(k_scale);
+  a->v_exp = const_cast<uint8_t*>(v_scale);
+  return ATTN_OK;
+}
+attn_status_t from_launch(cudaError_t e) {
+  return e == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : from_cuda(e);
+}
+}  // namespace
+
+attn_status_t attn_cache_write_e4m3(const void* k, const void* v, long long k_stride_token,
+                                    long long k_stride_head, long long v_stride_token,
+                                    long long v_stride_head, attn_dtype_t dtype,
+                                    const int32_t* block_table, const int32_t* cu_seqlens,
+                                    const int32_t* seq_lens, int B, int total, int h_kv, int d_h,
+                                    int page_size, int num_blocks, int max_blocks_per_seq,
+                                    void* k_cache, void* v_cache, uint8_t* k_scale,
+                                    uint8_t* v_scale, void* stream) {
+  CacheTokens a{};
+  const attn_status_t st = cache_tokens(
+      k, v, k_stride_token, k_stride_head, v_stride_token, v_stride_head, dtype, block_table,
+      cu_seqlens, seq_lens, B, total, h_kv, d_h, page_size, num_blocks, max_blocks_per_seq, k_cache,
+      v_cache, k_scale, v_scale, &a);
+  if (st != ATTN_OK || a.total == 0) return st;
+  return from_launch(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_cache_read_e4m3(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                                   const uint8_t* v_scale, const int32_t* block_table,
+                                   const int32_t* cu_seqlens, const int32_t* seq_lens, int B,
+                                   int total, int h_kv, int d_h, int page_size, int num_blocks,
+                                   int max_blocks_per_seq, void* k, void* v,
+                                   long long k_stride_token, long long k_stride_head,
+                                   long long v_stride_token, long long v_stride_head,
+                                   attn_dtype_t dtype, void* stream) {
+  CacheTokens a{};
+  const attn_status_t st = cache_tokens(
+      k, v, k_stride_token, k_stride_head, v_stride_token, v_stride_head, dtype, block_table,
+      cu_seqlens, seq_lens, B, total, h_kv, d_h, page_size, num_blocks, max_blocks_per_seq, k_cache,
+      v_cache, k_scale, v_scale, &a);
+  if (st != ATTN_OK || a.total == 0) return st;
+  return from_launch(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_decode_e4m3_workspace_bytes(int B, int h, int h_kv, int d_h) {
+  if (B < 0 || h < 1 || h_kv < 1 || h % h_kv != 0 || (d_h != 64 && d_h != 128)) return 0;
+  return decode8_layout(B, d_h).total;
+}
+
+attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                     const uint8_t* k_scale, const uint8_t* v_scale,
+                                     const int32_t* block_table, const int32_t* seq_lens, int B,
+                                     int h, int h_kv, int d_h, int page_size, int num_blocks,
+                                     int max_blocks_per_seq, float scale, void* workspace,
+                                     size_t workspace_bytes, void* o, float* lse, void* stream) {
+  if (B < 0 || B > 65535 || h < 1 || h_kv < 1 || h_kv > 65535 || h % h_kv != 0 || num_blocks < 1 ||
+      max_blocks_per_seq < 1 || !std::isfinite(scale) || !(scale > 0.f))
+    return ATTN_ERR_INVALID_ARG;
+  if ((d_h != 64 && d_h != 128) || page_size != 16) return ATTN_ERR_UNSUPPORTED;
+  // Row lengths, cache pages of one head, and (row, head) pairs index ints.
+  if (static_cast<long long>(max_blocks_per_seq) * page_size > (1ll << 30) ||
+      static_cast<long long>(num_blocks) * h_kv > 0x7fffffffll ||
+      static_cast<long long>(B) * h > 0x7fffffffll)
+    return ATTN_ERR_INVALID_ARG;
+  if (B == 0) return ATTN_OK;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens ||
+      !workspace || !o)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
+      !aligned(v_scale, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  const Decode8Layout L = decode8_layout(B, d_h);
+  if (workspace_bytes < L.total) return ATTN_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Decode8Args a;
+  a.q = q;
+  a.k_codes = k_cache;
+  a.v_codes = v_cache;
+  a.k_exp = k_scale;
+  a.v_exp = v_scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.B = B;
+  a.h = h;
+  a.h_kv = h_kv;
+  a.d_h = d_h;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.scale = scale;
+  a.plan = reinterpret_cast<long long*>(ws);
+  a.o_part = reinterpret_cast<float*>(ws + L.o_off);
+  a.m_part = reinterpret_cast<float*>(ws + L.m_off);
+  a.l_part = reinterpret_cast<float*>(ws + L.l_off);
+  a.o = o;
+  a.lse = lse;
+  return from_cuda(launch_decode8(a, static_cast<cudaStream_t>(stream)));
+}
+
 attn_status_t attn_selftest_wait_timeout(unsigned int limit_us, void* stream) {
   if (limit_us < 1 || limit_us > 1000000) return ATTN_ERR_INVALID_ARG;
   return from_cuda(launch_wait_timeout_selftest(uint64_t(limit_us) * 1000ull,
@@ -460,12 +601,16 @@ attn_status_t attn_get_device_error(void* stream, unsigned int* bits) {
   if (bits == nullptr) return ATTN_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess, e4 = cudaSuccess;
+  cudaError_t e5 = cudaSuccess, e6 = cudaSuccess;
   unsigned int v = decode_read_and_clear_error(s, &e1);
   v |= merge_read_and_clear_error(s, &e2);
   v |= prefill_read_and_clear_error(s, &e3);
   v |= simt_read_and_clear_error(s, &e4);
+  v |= cache8_read_and_clear_error(s, &e5);
+  v |= decode8_read_and_clear_error(s, &e6);
   *bits = v;
-  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess || e4 != cudaSuccess)
+  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess || e4 != cudaSuccess ||
+      e5 != cudaSuccess || e6 != cudaSuccess)
     return ATTN_ERR_CUDA;
   return ATTN_OK;
 }

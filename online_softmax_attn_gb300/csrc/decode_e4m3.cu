@@ -1,0 +1,730 @@
+// decode_e4m3.cu -- paged decode attention over the 8-bit cache.
+//
+// One query token per row over keys and values held as e4m3 codes with a
+// power-of-two scale per (token, KV head) (e4m3.cuh). With c_j, e_j the codes
+// and exponent of key j, w_j, f_j those of its value:
+//   s_j = scale * 2^e_j (q . c_j),  o = sum_j exp(s_j) 2^f_j w_j / sum_j exp(s_j).
+// The online recurrence of "Naive attention and the online softmax" runs in
+// base 2 with two references of its own per head: m for the normaliser (the
+// running max of s) and r for the accumulator (the running max of s + f, the
+// log2 weight with which a code of V enters). Any common shift is legal, and a
+// weight 2^(s + f - r) fits fp16 whatever the values' magnitudes are, so P V is
+// one fp16 product against the codes themselves.
+//
+// The codes go to fp16 (exact) in registers, and both contractions are
+// mma.m16n8k16 with the keys (S^T = K q^T) or the value dimensions
+// (O^T = V^T P^T) as the 16 rows and up to 8 query heads of the KV head as the
+// 8 columns: one MMA covers 16 keys x 8 heads x 16 dims. q is scaled per head
+// by a power of two to a largest magnitude in [2^14, 2^15), where an fp16 holds
+// bf16's 8 significant bits down to 2^-31 of that maximum.
+//   * K: the contraction index may be permuted freely, so a lane reads 16
+//     consecutive codes of a key with one shared load and takes them four at a
+//     time as its A fragment; no ldmatrix, no byte shuffles.
+//   * V: ldmatrix.trans moves byte pairs (two dims of a key); one prmt puts
+//     the same dim of two keys side by side.
+//   * P^T: the S^T accumulator holds key rows; movmatrix transposes the 8x8
+//     fp16 block into the B fragment.
+//
+// Bound by memory: 2 (d_h + 1) bytes per key and KV head. A warp owns a ring
+// of NST stages, each one page of K and V (TMA, swizzled) with their exponents
+// (16-byte bulk copies).
+//
+// Work split: the (row, KV head, head block) units' pages, laid end to end,
+// are cut into equal runs, one per CTA (two CTAs per SM), so any mix of lengths
+// fills the machine and the launch does not depend on the lengths. A CTA works
+// through its run unit by unit; its warps take the pages of a unit in turn and
+// join their states at the unit's end. A unit inside one run is finished there;
+// one cut by a run border leaves at most one partial state per CTA, which
+// decode8_merge_kernel joins in run order.
+#include "common.cuh"
+#include "e4m3.cuh"
+#include "internal.h"
+#include "pdl.cuh"
+
+namespace attn {
+
+static __device__ unsigned int g_decode8_err;
+// Exponents of a page outside the cache (its codes read as zeros).
+static __device__ __align__(16) const uint8_t g_unit_exp[16] = {127, 127, 127, 127, 127, 127, 127, 127,
+                                                                127, 127, 127, 127, 127, 127, 127, 127};
+
+namespace {
+
+using e4m3::kPage;
+
+constexpr int kNW = 8;       // warps per CTA
+constexpr int kMinPages = 8; // least pages per CTA: one per warp
+// Weights are at most 2^15 (fp16's largest finite number is 65504): the
+// reference r is set to 13 below a new running max's weight and moves once a
+// weight would pass 2^15. Weights down to 2^-27 of the largest are then normal
+// fp16 numbers, and what fp16 drops below 2^-38 of it is under 2^-20 of the sum
+// even for 2^18 keys.
+constexpr float kTop = 13.0f, kSlack = 2.0f;
+constexpr float kNone = -1e30f;  // reference before the first key
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void bulk_load16(uint32_t dst, const void* src, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
+      "l"(src), "r"(bar)
+      : "memory");
+}
+
+template <int D, int NST>
+struct Cfg {
+  static constexpr int PAGE_BYTES = kPage * D;          // codes of one page of one KV head
+  static constexpr int STAGE_BYTES = 2 * PAGE_BYTES;    // K then V
+  static constexpr int RING_BYTES = kNW * NST * STAGE_BYTES;
+  static constexpr int EXP_OFF = RING_BYTES;            // [warp][stage][K 16 | V 16]
+  static constexpr int NREG = D / 4;                    // accumulators per lane
+  static constexpr int JOIN_OFF = EXP_OFF + kNW * NST * 32;
+  static constexpr int JOIN_BYTES = (kNW / 2) * 32 * NREG * 4;
+  static constexpr int ML_OFF = JOIN_OFF + JOIN_BYTES;  // [2][warp][8 heads] floats
+  static constexpr int BAR_OFF = ML_OFF + 2 * kNW * 8 * 4;
+  static constexpr int SMEM = BAR_OFF + kNW * NST * 8 + 1024;
+};
+
+// 16-byte chunk `c` of key row `r` of a page: the TMA's 128-byte (d_h = 128)
+// or 64-byte (d_h = 64) swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t page, int r, int c) {
+  return page + r * D + ((c ^ (D == 128 ? (r & 7) : ((r >> 1) & 3))) << 4);
+}
+
+// A CTA's run, unit by unit. Warp-uniform.
+struct Walk {
+  int b, u, len, np;   // row, unit within the row, its keys and pages
+  int lo, hi;          // pages of the unit that lie in the run
+  long long rem;       // pages of the run from lo on
+};
+
+struct Rows {
+  const int32_t* seq_lens;
+  int B, max_len, upr;  // upr: units per row
+};
+
+__device__ __forceinline__ int row_len(const Rows& rw, int b) {
+  const int n = __ldcg(rw.seq_lens + b);
+  return min(max(n, 0), rw.max_len);
+}
+
+__device__ __forceinline__ void walk_open(Walk& w) {
+  w.hi = static_cast<int>(min(static_cast<long long>(w.np), w.lo + w.rem));
+}
+// Next unit of the run; false at its end.
+__device__ __forceinline__ bool walk_next(Walk& w, const Rows& rw) {
+  w.rem -= w.hi - w.lo;
+  if (w.rem <= 0) return false;
+  w.lo = 0;
+  if (++w.u == rw.upr) {
+    w.u = 0;
+    do {
+      ++w.b;
+      if (w.b >= rw.B) return false;
+      w.len = row_len(rw, w.b);
+      w.np = (w.len + kPage - 1) / kPage;
+    } while (w.np == 0);
+  }
+  walk_open(w);
+  return true;
+}
+
+template <int D, int NST>
+__global__ void __launch_bounds__(kNW * 32, 2)
+    decode8_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, const uint8_t* __restrict__ ks,
+                   const uint8_t* __restrict__ vs, const __nv_bfloat16* __restrict__ q,
+                   const int32_t* __restrict__ block_table, Rows rw, int h, int h_kv, int g,
+                   int max_blocks, int num_blocks, float qscale, long long* __restrict__ plan,
+                   float* __restrict__ o_part, float* __restrict__ m_part,
+                   float* __restrict__ l_part, __nv_bfloat16* __restrict__ o,
+                   float* __restrict__ lse) {
+  using C = Cfg<D, NST>;
+  constexpr int KS = D / 16;  // MMA steps over d_h
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gid = lane >> 2, tq = lane & 3;
+  const int n_gb = rw.upr / h_kv;
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  float* join = reinterpret_cast<float*>(smem + C::JOIN_OFF);
+  float* ms = reinterpret_cast<float*>(smem + C::ML_OFF);  // [warp][8]
+  float* ls = ms + kNW * 8;
+  __shared__ long long s_warp[kNW];
+  __shared__ long long s_start;
+  __shared__ int s_b;
+
+  if (warp == 0) {
+    if (lane < kNW * NST) mbar_init(sbase + C::BAR_OFF + lane * 8, 1);
+    fence_barrier_init();
+    if (lane == 0) {
+      prefetch_tmap(&tmap_k);
+      prefetch_tmap(&tmap_v);
+    }
+  }
+  static_assert(kNW * NST <= 32, "one lane initialises each barrier");
+  pdl_wait();     // lengths, table, q and the cache are earlier kernels' output
+  pdl_trigger();
+
+  // ---- the run: prefix sums of the rows' pages ----
+  const int per_t = (rw.B + kNW * 32 - 1) / (kNW * 32);
+  const int b0 = min(tid * per_t, rw.B), b1 = min(b0 + per_t, rw.B);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (blockIdx.x == 0) (void)clamp_seq_len(__ldcg(rw.seq_lens + b), rw.max_len, &g_decode8_err);
+    sum += (row_len(rw, b) + kPage - 1) / kPage;
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  long long before = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kNW; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  const long long all = total * rw.upr;
+  const long long per = max(static_cast<long long>(kMinPages), (all + gridDim.x - 1) / gridDim.x);
+  const long long p0 = per * blockIdx.x;
+  if (blockIdx.x == 0) {  // for the merge
+    if (tid == 0) plan[0] = per;
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      plan[1 + b] = at;
+      at += (row_len(rw, b) + kPage - 1) / kPage;
+      if (b == rw.B - 1) plan[1 + rw.B] = at;
+    }
+  }
+  if (p0 >= all) return;
+  if (p0 >= before * rw.upr && p0 < (before + sum) * rw.upr) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int np = (row_len(rw, b) + kPage - 1) / kPage;
+      if (p0 < (at + np) * rw.upr) {
+        s_b = b;
+        s_start = at;
+        break;
+      }
+      at += np;
+    }
+  }
+  __syncthreads();
+  Walk cw;
+  cw.b = s_b;
+  cw.len = row_len(rw, cw.b);
+  cw.np = (cw.len + kPage - 1) / kPage;
+  {
+    const long long off = p0 - s_start * rw.upr;
+    cw.u = static_cast<int>(off / cw.np);
+    cw.lo = static_cast<int>(off % cw.np);
+  }
+  cw.rem = min(per, all - p0);
+  walk_open(cw);
+
+  // ---- producer state: the same walk, NST pages ahead ----
+  Walk pw = cw;
+  bool more = true;
+  int pi = warp;  // page within the unit's part of the run
+  int bt = -1;    // table entries of this warp's pages, 32 at a time
+  int issued = 0;
+  auto load_bt = [&](int i) {
+    const int j = i + kNW * lane;
+    bt = pw.lo + j < pw.hi
+             ? __ldcg(block_table + static_cast<size_t>(pw.b) * max_blocks + pw.lo + j)
+             : -1;
+  };
+  const uint32_t ring = sbase + warp * NST * C::STAGE_BYTES;
+  const uint32_t exps = sbase + C::EXP_OFF + warp * NST * 32;
+  const uint32_t bars = sbase + C::BAR_OFF + warp * NST * 8;
+  const uint64_t policy = policy_evict_first();
+  int bt_i = 0;  // pages taken from bt
+  load_bt(pi);
+  // Issues this warp's next page, if there is one, into stage issued % NST.
+  auto issue_next = [&]() {
+    while (more && pw.lo + pi >= pw.hi) {
+      more = walk_next(pw, rw);
+      pi = warp;
+      bt_i = 0;
+      if (more) load_bt(pi);
+    }
+    if (!more) return;
+    if (bt_i == 32) {
+      bt_i = 0;
+      load_bt(pi);
+    }
+    const int phys = __shfl_sync(0xffffffffu, bt, bt_i);
+    if (lane == 0) {
+      const int st = issued % NST;
+      const uint32_t dst = ring + st * C::STAGE_BYTES, bar = bars + st * 8;
+      const int kvh = pw.u / n_gb;
+      const bool bad = phys < 0 || phys >= num_blocks;
+      if (bad) atomicOr(&g_decode8_err, ATTN_DEVERR_BAD_PAGE);
+      // An out-of-range coordinate is filled with zeros by the copy engine.
+      const int slab = bad ? -1 : phys * h_kv + kvh;
+      const size_t eo = static_cast<size_t>(bad ? 0 : slab) * kPage;
+      mbar_arrive_expect_tx(bar, C::STAGE_BYTES + 32);
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+          " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+          "l"(reinterpret_cast<uint64_t>(&tmap_k)), "r"(bar), "r"(0), "r"(0), "r"(slab), "l"(policy)
+          : "memory");
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+          " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst + C::PAGE_BYTES),
+          "l"(reinterpret_cast<uint64_t>(&tmap_v)), "r"(bar), "r"(0), "r"(0), "r"(slab), "l"(policy)
+          : "memory");
+      bulk_load16(exps + st * 32, bad ? g_unit_exp : ks + eo, bar);
+      bulk_load16(exps + st * 32 + 16, bad ? g_unit_exp : vs + eo, bar);
+    }
+    ++issued;
+    ++bt_i;
+    pi += kNW;
+  };
+  for (int i = 0; i < NST; ++i) issue_next();
+
+  int used = 0;      // stages consumed
+  bool dead = false; // a wait gave up: results are void, the error word says so
+  const int v_row = 8 * ((lane >> 3) & 1) + (lane & 7), v_dc = lane >> 4;
+
+  do {  // ---- one unit of the run ----
+    const int kvh = cw.u / n_gb, gb = cw.u % n_gb;
+    const int hq0 = kvh * g + gb * 8;     // first query head of the block
+    const int nh = min(8, g - gb * 8);    // heads in the block
+
+    // q as the B operand: lane (gid, tq) holds head gid's dims of the chunks
+    // that lanes tq read of K: 32 consecutive dims (d_h = 128) or 16.
+    uint32_t qb[KS][2];
+    float hc;
+    {
+      constexpr int NC = D / 64;  // 16-dim chunks per lane
+      float x[NC * 16];
+#pragma unroll
+      for (int c = 0; c < NC * 2; ++c) {
+        uint4 t = make_uint4(0u, 0u, 0u, 0u);
+        if (gid < nh)
+          t = __ldcg(reinterpret_cast<const uint4*>(
+              q + (static_cast<size_t>(cw.b) * h + hq0 + gid) * D + tq * (NC * 16) + c * 8));
+        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[c * 8 + 2 * i] = bf16lo(w[i]);
+          x[c * 8 + 2 * i + 1] = bf16hi(w[i]);
+        }
+      }
+      uint32_t a = 0;
+#pragma unroll
+      for (int i = 0; i < NC * 16; ++i) {
+        const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
+        a = max(a, b >= 0x7f800000u ? 0u : b);
+      }
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      // Largest finite magnitude to [2^14, 2^15); exponents below 2^-112 (and
+      // zero rows) are treated as 2^-112.
+      const int be = max(static_cast<int>(a >> 23), 15);     // biased exponent
+      const float up = __uint_as_float(static_cast<uint32_t>(min(254, 127 + 14 + 127 - be)) << 23);
+      const int down = min(be - 14, 240);
+      hc = qscale * __uint_as_float(static_cast<uint32_t>(max(down, 1)) << 23);
+#pragma unroll
+      for (int ksi = 0; ksi < KS; ++ksi) {
+        qb[ksi][0] = pack_f16x2(x[ksi * 4] * up, x[ksi * 4 + 1] * up);
+        qb[ksi][1] = pack_f16x2(x[ksi * 4 + 2] * up, x[ksi * 4 + 3] * up);
+      }
+    }
+    const float hc0 = __shfl_sync(0xffffffffu, hc, (2 * tq) * 4);
+    const float hc1 = __shfl_sync(0xffffffffu, hc, (2 * tq + 1) * 4);
+
+    // State of heads 2tq, 2tq + 1: normaliser share l of this lane's keys
+    // relative to 2^m, accumulators relative to 2^r.
+    float m0 = kNone, m1 = kNone, r0 = kNone, r1 = kNone, l0 = 0.f, l1 = 0.f;
+    float acc[KS][4];
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+
+    const int span = cw.hi - cw.lo;
+    for (int i = warp; i < span; i += kNW) {
+      const int st = used % NST;
+      if (!dead && !mbar_wait(bars + st * 8, (used / NST) & 1, &g_decode8_err)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) break;
+      const uint32_t kp = ring + st * C::STAGE_BYTES, vp = kp + C::PAGE_BYTES;
+      const int valid = min(kPage, cw.len - (cw.lo + i) * kPage);
+      if (valid < kPage) {
+        // Slots past the row's end hold whatever the cache holds there (NaN
+        // codes among it); their weights are 0, but 0 * NaN is not.
+        constexpr int CPR = D / 16;
+        for (int c = lane; c < (kPage - valid) * CPR; c += 32)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                           chunk_at<D>(vp, valid + c / CPR, c % CPR)),
+                       "r"(0u)
+                       : "memory");
+        fence_proxy_async_smem();  // before the stage is refilled by the copy engine
+        __syncwarp();
+      }
+
+      // ---- S^T = K q^T: keys gid and gid + 8, heads 2tq and 2tq + 1 ----
+      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const int ch = tq * (D / 64) + c;
+        const uint4 x = lds128(chunk_at<D>(kp, gid, ch));
+        const uint4 y = lds128(chunk_at<D>(kp, gid + 8, ch));
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = e4m3::decode2(static_cast<uint16_t>(xw[j]));
+          const uint32_t a1 = e4m3::decode2(static_cast<uint16_t>(yw[j]));
+          const uint32_t a2 = e4m3::decode2(static_cast<uint16_t>(xw[j] >> 16));
+          const uint32_t a3 = e4m3::decode2(static_cast<uint16_t>(yw[j] >> 16));
+          if (j & 1)
+            mma_f16(sb, a0, a1, a2, a3, qb[c * 4 + j][0], qb[c * 4 + j][1]);
+          else
+            mma_f16(sa, a0, a1, a2, a3, qb[c * 4 + j][0], qb[c * 4 + j][1]);
+        }
+      }
+      const uint32_t ep = exps + st * 32;
+      const float ka = e4m3::scale_of(lds_u8(ep + gid)), kb = e4m3::scale_of(lds_u8(ep + gid + 8));
+      const float va = static_cast<float>(static_cast<int>(lds_u8(ep + 16 + gid)) - 127);
+      const float vb = static_cast<float>(static_cast<int>(lds_u8(ep + 24 + gid)) - 127);
+      float s0 = (sa[0] + sb[0]) * hc0 * ka, s1 = (sa[1] + sb[1]) * hc1 * ka;
+      float s2 = (sa[2] + sb[2]) * hc0 * kb, s3 = (sa[3] + sb[3]) * hc1 * kb;
+      if (valid < kPage) {
+        if (gid >= valid) s0 = s1 = -INFINITY;
+        if (gid + 8 >= valid) s2 = s3 = -INFINITY;
+      }
+      const float t0 = s0 + va, t1 = s1 + va, t2 = s2 + vb, t3 = s3 + vb;
+
+      // ---- references: they move only when a score passes them by kSlack ----
+      // (a NaN never compares, and reaches l and O through its weight)
+      const bool up = s0 > m0 + kSlack || s2 > m0 + kSlack || s1 > m1 + kSlack ||
+                      s3 > m1 + kSlack || t0 > r0 + (kTop + kSlack) ||
+                      t2 > r0 + (kTop + kSlack) || t1 > r1 + (kTop + kSlack) ||
+                      t3 > r1 + (kTop + kSlack);
+      if (__any_sync(0xffffffffu, up)) {
+        float n0 = fmaxf(s0, s2), n1 = fmaxf(s1, s3), w0 = fmaxf(t0, t2), w1 = fmaxf(t1, t3);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+          n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+          w0 = fmaxf(w0, __shfl_xor_sync(0xffffffffu, w0, off));
+          w1 = fmaxf(w1, __shfl_xor_sync(0xffffffffu, w1, off));
+        }
+        n0 = fmaxf(n0, m0);
+        n1 = fmaxf(n1, m1);
+        w0 = fmaxf(w0 - kTop, r0);
+        w1 = fmaxf(w1 - kTop, r1);
+        l0 *= ex2_approx(m0 - n0);
+        l1 *= ex2_approx(m1 - n1);
+        const float a0 = ex2_approx(r0 - w0), a1 = ex2_approx(r1 - w1);
+        m0 = n0;
+        m1 = n1;
+        r0 = w0;
+        r1 = w1;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          acc[k][0] *= a0;
+          acc[k][1] *= a1;
+          acc[k][2] *= a0;
+          acc[k][3] *= a1;
+        }
+      }
+      l0 += ex2_approx(s0 - m0) + ex2_approx(s2 - m0);
+      l1 += ex2_approx(s1 - m1) + ex2_approx(s3 - m1);
+      const uint32_t pb0 = movmatrix_t(pack_f16x2(ex2_approx(t0 - r0), ex2_approx(t1 - r1)));
+      const uint32_t pb1 = movmatrix_t(pack_f16x2(ex2_approx(t2 - r0), ex2_approx(t3 - r1)));
+
+      // ---- O^T += V^T P^T: rows gid, gid + 8 of step k are dims
+      // 16k + 2 gid and 16k + 2 gid + 1 ----
+#pragma unroll
+      for (int k = 0; k < KS; k += 2) {
+        uint32_t r[4];
+        ldsm_x4_t(chunk_at<D>(vp, v_row, k + v_dc), r);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t x, y;
+          asm("prmt.b32 %0, %1, %1, 0x3120;" : "=r"(x) : "r"(r[2 * e]));
+          asm("prmt.b32 %0, %1, %1, 0x3120;" : "=r"(y) : "r"(r[2 * e + 1]));
+          mma_f16(acc[k + e], e4m3::decode2(static_cast<uint16_t>(x)),
+                  e4m3::decode2(static_cast<uint16_t>(x >> 16)),
+                  e4m3::decode2(static_cast<uint16_t>(y)),
+                  e4m3::decode2(static_cast<uint16_t>(y >> 16)), pb0, pb1);
+        }
+      }
+      __syncwarp();
+      ++used;
+      if (lane == 0) fence_proxy_async_smem();  // generic reads (and zeroing) before the refill
+      issue_next();
+    }
+
+    // ---- join the warps' states ----
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+    if (gid == 0) {
+      ms[warp * 8 + 2 * tq] = m0;
+      ms[warp * 8 + 2 * tq + 1] = m1;
+      ls[warp * 8 + 2 * tq] = l0;
+      ls[warp * 8 + 2 * tq + 1] = l1;
+    }
+    __syncthreads();
+    float M0 = kNone, M1 = kNone;
+#pragma unroll
+    for (int w = 0; w < kNW; ++w) {
+      M0 = fmaxf(M0, ms[w * 8 + 2 * tq]);
+      M1 = fmaxf(M1, ms[w * 8 + 2 * tq + 1]);
+    }
+    {
+      const float f0 = ex2_approx(r0 - M0), f1 = ex2_approx(r1 - M1);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        acc[k][0] *= f0;
+        acc[k][1] *= f1;
+        acc[k][2] *= f0;
+        acc[k][3] *= f1;
+      }
+    }
+#pragma unroll
+    for (int half = kNW / 2; half >= 1; half >>= 1) {
+      if (warp >= half && warp < 2 * half) {
+#pragma unroll
+        for (int i = 0; i < C::NREG; ++i)
+          join[((warp - half) * C::NREG + i) * 32 + lane] = acc[i >> 2][i & 3];
+      }
+      __syncthreads();
+      if (warp < half) {
+#pragma unroll
+        for (int i = 0; i < C::NREG; ++i) acc[i >> 2][i & 3] += join[(warp * C::NREG + i) * 32 + lane];
+      }
+      if (half > 1) __syncthreads();
+    }
+    if (warp == 0) {
+      float L0 = 0.f, L1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kNW; ++w) {
+        L0 = fmaf(ls[w * 8 + 2 * tq], ex2_approx(ms[w * 8 + 2 * tq] - M0), L0);
+        L1 = fmaf(ls[w * 8 + 2 * tq + 1], ex2_approx(ms[w * 8 + 2 * tq + 1] - M1), L1);
+      }
+      const bool whole = cw.lo == 0 && cw.hi == cw.np;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int head = 2 * tq + e;
+        if (head >= nh) continue;
+        const float L = e ? L1 : L0, M = e ? M1 : M0;
+        if (whole) {
+          const bool empty = L == 0.f;  // every logit -inf
+          const float inv = empty ? 0.f : 1.f / L;
+          const size_t row = static_cast<size_t>(cw.b) * h + hq0 + head;
+          if (!ATTN_GUARD(row < static_cast<size_t>(rw.B) * h, &g_decode8_err)) continue;
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            *reinterpret_cast<uint32_t*>(o + row * D + 16 * k + 2 * gid) =
+                empty ? 0u : pack_bf16x2(acc[k][e] * inv, acc[k][2 + e] * inv);
+          if (lse != nullptr && gid == 0) lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
+        } else {
+          const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (cw.lo == 0 ? 1 : 0)) * 8 + head;
+          if (!ATTN_GUARD(slot < static_cast<size_t>(gridDim.x) * 16, &g_decode8_err)) continue;
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            *reinterpret_cast<float2*>(o_part + slot * D + 16 * k + 2 * gid) =
+                make_float2(acc[k][e], acc[k][2 + e]);
+          if (gid == 0) {
+            m_part[slot] = M;
+            l_part[slot] = L;
+          }
+        }
+      }
+    }
+    __syncthreads();  // join, ms and ls are free for the next unit
+  } while (walk_next(cw, rw));
+  if (dead) {
+    // Bounded chance for the copies in flight to land before the CTA exits.
+    for (int j = used; j < issued; ++j)
+      (void)mbar_wait(bars + (j % NST) * 8, (j / NST) & 1, &g_decode8_err);
+  }
+}
+
+// Joins the partial states of each (row, head) that a run border cut, and
+// writes empty rows. One CTA per (row, head), warps take its partials in turn.
+template <int D>
+__global__ void __launch_bounds__(128)
+    decode8_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m_part,
+                         const float* __restrict__ l_part, const long long* __restrict__ plan,
+                         int h, int g, int n_gb, int upr, __nv_bfloat16* __restrict__ o,
+                         float* __restrict__ lse) {
+  constexpr int VEC = D / 32, U = 4, NW = 4;
+  __shared__ float sm[NW], sl[NW], so[NW][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x / h, hq = blockIdx.x % h;
+  pdl_wait();
+  pdl_trigger();
+  const long long per = __ldcg(plan), at = __ldcg(plan + 1 + b);
+  const long long np = __ldcg(plan + 2 + b) - at;
+  const size_t row = static_cast<size_t>(b) * h + hq;
+  if (np == 0) {
+    for (int i = threadIdx.x; i < D / 2; i += 128) reinterpret_cast<uint32_t*>(o + row * D)[i] = 0u;
+    if (lse != nullptr && threadIdx.x == 0) lse[row] = -INFINITY;
+    return;
+  }
+  const int u = (hq / g) * n_gb + (hq % g) / 8;
+  const long long s = at * upr + u * np;
+  const long long c0 = s / per;
+  const int n = static_cast<int>((s + np - 1) / per - c0) + 1;
+  if (n == 1) return;  // finished by its CTA
+  float M = kNone, L = 0.f, acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  for (int base = warp; base < n; base += NW * U) {
+    float m[U], l[U], x[U][VEC];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = base + i * NW;
+      m[i] = kNone;
+      l[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[i][e] = 0.f;
+      if (j < n) {
+        const size_t slot = (2 * (c0 + j) + (j == 0 ? 1 : 0)) * 8 + (hq % g) % 8;
+        m[i] = __ldcg(m_part + slot);
+        l[i] = __ldcg(l_part + slot);
+        const float* src = o_part + slot * D + lane * VEC;
+        if constexpr (VEC == 4) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+          x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+        } else {
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+          x[i][0] = t.x; x[i][1] = t.y;
+        }
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int i = 0; i < U; ++i) Mn = fmaxf(Mn, m[i]);
+    const float sc = ex2_approx(M - Mn);
+    M = Mn;
+    L *= sc;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] *= sc;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const float w = ex2_approx(m[i] - Mn);
+      L = fmaf(w, l[i], L);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
+    }
+  }
+  if (lane == 0) {
+    sm[warp] = M;
+    sl[warp] = L;
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) so[warp][lane * VEC + e] = acc[e];
+  __syncthreads();
+  float Mt = kNone, Lt = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) Mt = fmaxf(Mt, sm[w]);
+#pragma unroll
+  for (int w = 0; w < NW; ++w) Lt = fmaf(sl[w], ex2_approx(sm[w] - Mt), Lt);
+  const bool empty = Lt == 0.f;
+  const float inv = empty ? 0.f : 1.f / Lt;
+  for (int e = threadIdx.x; e < D; e += 128) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v = fmaf(so[w][e], ex2_approx(sm[w] - Mt), v);
+    o[row * D + e] = __float2bfloat16(empty ? 0.f : v * inv);
+  }
+  if (lse != nullptr && threadIdx.x == 0) lse[row] = empty ? -INFINITY : Mt * kLn2 + logf(Lt);
+}
+
+template <int D, int NST>
+cudaError_t launch_cfg(const Decode8Args& a, int sms, cudaStream_t stream) {
+  using C = Cfg<D, NST>;
+  CUtensorMap tk, tv;
+  const uint64_t dims[3] = {uint64_t(D), uint64_t(kPage), uint64_t(a.num_blocks) * a.h_kv};
+  const uint64_t strides[2] = {uint64_t(D), uint64_t(kPage) * D};
+  const uint32_t box[3] = {uint32_t(D), uint32_t(kPage), 1u};
+  const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (encode_tensor_map(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a.k_codes), dims,
+                        strides, box, sw) != CUDA_SUCCESS ||
+      encode_tensor_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a.v_codes), dims,
+                        strides, box, sw) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  auto kern = decode8_kernel<D, NST>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * sms < kDecode8MaxCtas ? 2 * sms : kDecode8MaxCtas;
+  const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
+  const Rows rw{a.seq_lens, a.B, a.max_blocks * kPage, a.h_kv * n_gb};
+  e = launch_pdl(kern, dim3(grid), dim3(kNW * 32), size_t(C::SMEM), stream, tk, tv, a.k_exp, a.v_exp,
+                 static_cast<const __nv_bfloat16*>(a.q), a.block_table, rw, a.h, a.h_kv, g,
+                 a.max_blocks, a.num_blocks, a.scale * kLog2e, a.plan, a.o_part, a.m_part, a.l_part,
+                 static_cast<__nv_bfloat16*>(a.o), a.lse);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode8_merge_kernel<D>, dim3(unsigned(a.B) * a.h), dim3(128), 0, stream,
+                    static_cast<const float*>(a.o_part), static_cast<const float*>(a.m_part),
+                    static_cast<const float*>(a.l_part), static_cast<const long long*>(a.plan), a.h,
+                    g, n_gb, rw.upr, static_cast<__nv_bfloat16*>(a.o), a.lse);
+}
+
+}  // namespace
+
+cudaError_t launch_decode8(const Decode8Args& a, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  return a.d_h == 128 ? launch_cfg<128, 2>(a, sms, stream) : launch_cfg<64, 3>(a, sms, stream);
+}
+
+unsigned int decode8_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_decode8_err, sizeof(v), 0,
+                                            cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyToSymbolAsync(g_decode8_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
+                                stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (st) *st = e;
+  return v;
+}
+
+}  // namespace attn

@@ -75,6 +75,62 @@ cudaError_t launch_wait_timeout_selftest(uint64_t limit_ns, cudaStream_t stream)
 cudaError_t launch_delayed_copy(int32_t* dst, const int32_t* src, int n, uint64_t delay_ns,
                                 cudaStream_t stream);
 
+// cache_e4m3.cu --------------------------------------------------------------
+// Tokens packed row after row (cu [B + 1]); row b's are the last of its
+// seq_lens[b] positions. Strides in elements.
+struct CacheTokens {
+  void* k;  // [total, h_kv, d_h], read by the write and written by the read
+  void* v;
+  long long k_tok, k_head, v_tok, v_head;
+  attn_dtype_t dtype;
+  const int32_t* block_table;
+  const int32_t* cu;
+  const int32_t* seq_lens;
+  int B, total, h_kv, d_h, num_blocks, max_blocks;
+  uint8_t* k_codes;  // [num_blocks, h_kv, 16, d_h]
+  uint8_t* v_codes;
+  uint8_t* k_exp;    // [num_blocks, h_kv, 16]
+  uint8_t* v_exp;
+};
+cudaError_t launch_cache_write(const CacheTokens& a, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheTokens& a, cudaStream_t stream);
+unsigned int cache8_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
+
+// decode_e4m3.cu -------------------------------------------------------------
+constexpr int kDecode8MaxCtas = 320;  // bounds the workspace; two CTAs on each of 160 SMs
+// Plan (int64: pages per CTA, then the rows' first pages [B + 1]), then two
+// partial states per CTA: O~ [2 * 320, 8, d_h], m and l [2 * 320, 8].
+struct Decode8Layout {
+  size_t o_off, m_off, l_off, total;
+};
+inline Decode8Layout decode8_layout(int B, int d_h) {
+  Decode8Layout L;
+  L.o_off = align256((size_t(B) + 2) * sizeof(long long));
+  L.m_off = L.o_off + size_t(2 * kDecode8MaxCtas) * 8 * d_h * sizeof(float);
+  L.l_off = L.m_off + size_t(2 * kDecode8MaxCtas) * 8 * sizeof(float);
+  L.total = L.l_off + size_t(2 * kDecode8MaxCtas) * 8 * sizeof(float);
+  return L;
+}
+struct Decode8Args {
+  const void* q;
+  const void* k_codes;
+  const void* v_codes;
+  const uint8_t* k_exp;
+  const uint8_t* v_exp;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int B, h, h_kv, d_h, num_blocks, max_blocks;
+  float scale;
+  long long* plan;
+  float* o_part;
+  float* m_part;
+  float* l_part;
+  void* o;
+  float* lse;
+};
+cudaError_t launch_decode8(const Decode8Args& a, cudaStream_t stream);
+unsigned int decode8_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
+
 // prefill_simt.cu ----------------------------------------------------------
 cudaError_t launch_prefill_f32(const float* q, const float* k, const float* v, float* o,
                                float* lse, int T, int h, int h_kv, int d_h, int causal,
