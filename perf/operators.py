@@ -316,7 +316,7 @@ def _run_own(s):
                                              s["scale"], workspace=s["ws"], o=s["o"], lse=s["lse"])
     else:
         if "ws" not in s:
-            n = attn.attn_decode_shared_workspace_bytes(B, h, s["kc"].shape[2], d, s["table"].shape[1])
+            n = attn.attn_decode_shared_workspace_bytes(B, h, s["kc"].shape[2], d)
             s["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")
         o, lse = attn.attn_decode_paged_shared(s["q"], s["kc"], s["vc"], s["ptable"], s["plen"], s["table"], s["lens"],
                                                s["scale"], workspace=s["ws"], o=s["o"], lse=s["lse"])
