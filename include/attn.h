@@ -625,6 +625,49 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
                                      size_t workspace_bytes, void* o, float* lse, void* stream);
 
 /*
+ * attn_decode_paged_shared -- attn_decode_paged for a batch whose rows share a
+ * prefix of keys ([NA] cascade: attend to the shared prefix once, to each
+ * row's own keys, and merge the states). Row b attends to the prefix's
+ * prefix_len[0] keys and to its own seq_lens[b] ones; both live in the same
+ * bf16 caches. The prefix is read once for all rows: its scores are dense
+ * products on the tensor cores with the B * h / h_kv query rows of a KV head
+ * as their rows. The three kernels' launches depend on B, h and h_kv only
+ * (capturable, replayable with new lengths and tables); the result does not
+ * depend on timing.
+ *   q            [B, h, d_h] bf16                                     (read)
+ *   k_cache,
+ *   v_cache      [num_blocks, page_size, h_kv, d_h] bf16              (read)
+ *   prefix_table [max_prefix_blocks] int32: pages of the prefix; the first
+ *                ceil(prefix_len / 16) are read                       (read)
+ *   prefix_len   [1] int32 in device memory, any length >= 0          (read)
+ *   block_table  [B, max_blocks_per_seq] int32: the rows' own pages. A row's
+ *                own keys start in a page of their own, whatever the prefix's
+ *                length                                               (read)
+ *   seq_lens     [B] int32: the rows' own keys, without the prefix; 0 is
+ *                allowed                                              (read)
+ *   workspace    256-byte aligned, attn_decode_shared_workspace_bytes(B, h,
+ *                h_kv, d_h) bytes, overwritten; calls (and captured graphs)
+ *                that share one must not overlap on the GPU
+ *   o            [B, h, d_h] bf16                                     (written)
+ *   lse          [B, h] fp32, natural log, over all keys; may be NULL (written)
+ * Without any key (prefix_len 0 and seq_lens 0) o = 0 and lse = -inf. Lengths
+ * outside their table are clamped (ATTN_DEVERR_BAD_SEQ_LEN), pages outside the
+ * cache read as zeros (ATTN_DEVERR_BAD_PAGE). Slots past a length never reach
+ * a row; non-finite keys and values that are attended do, as in
+ * attn_decode_paged.
+ * Errors: as attn_decode_paged_e4m3, plus INVALID_ARG for max_prefix_blocks < 1
+ * or beyond 2^30 / 16; UNSUPPORTED also for h / h_kv not in {1, 2, 4, 8}.
+ */
+size_t attn_decode_shared_workspace_bytes(int B, int h, int h_kv, int d_h);
+attn_status_t attn_decode_paged_shared(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* prefix_table, const int32_t* prefix_len,
+                                       const int32_t* block_table, const int32_t* seq_lens, int B,
+                                       int h, int h_kv, int d_h, int page_size, int num_blocks,
+                                       int max_prefix_blocks, int max_blocks_per_seq, float scale,
+                                       void* workspace, size_t workspace_bytes, void* o, float* lse,
+                                       void* stream);
+
+/*
  * attn_get_device_error -- synchronise `stream`, then read and clear the
  * device error word of every kernel module (ATTN_DEVERR_* bits, 0 = none)
  * into *bits. Returns ATTN_ERR_CUDA if the synchronisation fails.

@@ -30,6 +30,8 @@ __all__ = [
     "attn_cache_read_e4m3",
     "attn_decode_paged_e4m3",
     "attn_decode_e4m3_workspace_bytes",
+    "attn_decode_paged_shared",
+    "attn_decode_shared_workspace_bytes",
     "attn_get_device_error",
     "attn_get_last_device_error",
     "attn_selftest_prefill_stall",
@@ -120,6 +122,10 @@ def library() -> ctypes.CDLL:
     lib.attn_decode_e4m3_workspace_bytes.restype = S
     lib.attn_decode_paged_e4m3.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, S, P, P, P]
     lib.attn_decode_paged_e4m3.restype = I
+    lib.attn_decode_shared_workspace_bytes.argtypes = [I, I, I, I]
+    lib.attn_decode_shared_workspace_bytes.restype = S
+    lib.attn_decode_paged_shared.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, P, S, P, P, P]
+    lib.attn_decode_paged_shared.restype = I
     lib.attn_selftest_delayed_copy.argtypes = [P, P, I, ctypes.c_uint, P]
     lib.attn_selftest_delayed_copy.restype = I
     lib.attn_selftest_prefill_stall.argtypes = [I]
@@ -655,6 +661,48 @@ def attn_decode_paged_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, s
         scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(), o.data_ptr(),
         None if lse is None else lse.data_ptr(), _stream(stream))
     _check("attn_decode_paged_e4m3", st)
+    return o, lse
+
+
+def attn_decode_shared_workspace_bytes(B: int, h: int, h_kv: int, d_h: int) -> int:
+    """Workspace bytes of attn_decode_paged_shared."""
+    return int(library().attn_decode_shared_workspace_bytes(int(B), int(h), int(h_kv), int(d_h)))
+
+
+def attn_decode_paged_shared(q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens,
+                             scale: float | None = None, workspace=None, o=None, lse=None,
+                             return_lse: bool = True, stream=None):
+    """Paged decode of a batch that shares a prefix: row b attends to the
+    prefix_len[0] keys of the pages in prefix_table [max_prefix_blocks] and to
+    its own seq_lens[b] keys in block_table [B,max_blocks] (all int32). q
+    [B,h,d] bf16, caches [num_blocks,16,h_kv,d] bf16 (all CUDA, contiguous).
+    The prefix is read once for all rows. Returns (o [B,h,d] bf16, lse [B,h]
+    fp32 over all keys, or None)."""
+    _same_device(q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens)
+    _need(q.dtype == k_cache.dtype == v_cache.dtype == torch.bfloat16, "q and caches must be bf16")
+    _need(q.dim() == 3 and k_cache.dim() == 4 and v_cache.shape == k_cache.shape,
+          "q [B,h,d] and caches [num_blocks,16,h_kv,d] expected")
+    _need(prefix_table.dtype == prefix_len.dtype == block_table.dtype == seq_lens.dtype == torch.int32,
+          "tables and lengths must be int32")
+    for t in (q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens):
+        _need(t.is_contiguous(), "tensors must be contiguous")
+    B, h, d = q.shape
+    nb, page, h_kv, d2 = k_cache.shape
+    _need(d2 == d, "cache shape mismatch")
+    _need(prefix_table.dim() == 1 and prefix_len.shape == (1,) and block_table.dim() == 2 and
+          block_table.shape[0] == B and seq_lens.shape == (B,),
+          "prefix_table [max_prefix_blocks], prefix_len [1], block_table [B,max_blocks], seq_lens [B] expected")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    lib = library()
+    need = lib.attn_decode_shared_workspace_bytes(B, h, h_kv, d)
+    workspace, o, lse = _outputs(q, B, h, need, workspace, o, lse, return_lse, stream)
+    st = lib.attn_decode_paged_shared(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_table.data_ptr(),
+        prefix_len.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), B, h, h_kv, d, page, nb,
+        prefix_table.shape[0], block_table.shape[1], scale, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), o.data_ptr(),
+        None if lse is None else lse.data_ptr(), _stream(stream))
+    _check("attn_decode_paged_shared", st)
     return o, lse
 
 

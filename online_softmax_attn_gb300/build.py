@@ -32,7 +32,8 @@ DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG, "libattn_gb300_debug.so")
 
 SOURCES = ["api.cu", "merge.cu", "decode.cu", "prefill_simt.cu", "prefill_tc.cu",
-           "decode_static.cu", "host_prefill.cu", "cache_e4m3.cu", "decode_e4m3.cu"]
+           "decode_static.cu", "host_prefill.cu", "cache_e4m3.cu", "decode_runs.cu",
+           "decode_shared.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

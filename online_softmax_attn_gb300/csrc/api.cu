@@ -522,7 +522,7 @@ attn_status_t attn_cache_read_e4m3(const void* k_cache, const void* v_cache, con
 
 size_t attn_decode_e4m3_workspace_bytes(int B, int h, int h_kv, int d_h) {
   if (B < 0 || h < 1 || h_kv < 1 || h % h_kv != 0 || (d_h != 64 && d_h != 128)) return 0;
-  return decode8_layout(B, d_h).total;
+  return runs_layout(B, d_h).total;
 }
 
 attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const void* v_cache,
@@ -548,13 +548,13 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
       !aligned(v_scale, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
       !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
     return ATTN_ERR_INVALID_ARG;
-  const Decode8Layout L = decode8_layout(B, d_h);
+  const RunsLayout L = runs_layout(B, d_h);
   if (workspace_bytes < L.total) return ATTN_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  Decode8Args a;
+  DecodeRunsArgs a;
   a.q = q;
-  a.k_codes = k_cache;
-  a.v_codes = v_cache;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
   a.k_exp = k_scale;
   a.v_exp = v_scale;
   a.block_table = block_table;
@@ -573,6 +573,75 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
   a.o = o;
   a.lse = lse;
   return from_cuda(launch_decode8(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_decode_shared_workspace_bytes(int B, int h, int h_kv, int d_h) {
+  if (B < 0 || B > 65535 || h < 1 || h_kv < 1 || h_kv > 65535 || h % h_kv != 0 || h / h_kv > 8 ||
+      (d_h != 64 && d_h != 128))
+    return 0;
+  return shared_layout(B < 1 ? 1 : B, h, h_kv, d_h).total;
+}
+
+attn_status_t attn_decode_paged_shared(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* prefix_table, const int32_t* prefix_len,
+                                       const int32_t* block_table, const int32_t* seq_lens, int B,
+                                       int h, int h_kv, int d_h, int page_size, int num_blocks,
+                                       int max_prefix_blocks, int max_blocks_per_seq, float scale,
+                                       void* workspace, size_t workspace_bytes, void* o, float* lse,
+                                       void* stream) {
+  if (B < 0 || B > 65535 || h < 1 || h_kv < 1 || h_kv > 65535 || h % h_kv != 0 || num_blocks < 1 ||
+      max_prefix_blocks < 1 || max_blocks_per_seq < 1 || !std::isfinite(scale) || !(scale > 0.f))
+    return ATTN_ERR_INVALID_ARG;
+  const int g = h / h_kv;
+  if ((d_h != 64 && d_h != 128) || page_size != 16 || (g != 1 && g != 2 && g != 4 && g != 8))
+    return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_blocks_per_seq) * page_size > (1ll << 30) ||
+      static_cast<long long>(max_prefix_blocks) * page_size > (1ll << 30) ||
+      static_cast<long long>(B) * h > 0x7fffffffll)
+    return ATTN_ERR_INVALID_ARG;
+  if (B == 0) return ATTN_OK;
+  if (!q || !k_cache || !v_cache || !prefix_table || !prefix_len || !block_table || !seq_lens ||
+      !workspace || !o)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
+      !aligned(prefix_table, 4) || !aligned(prefix_len, 4) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  const RunsLayout R = runs_layout(B, d_h);
+  const SharedLayout L = shared_layout(B, h, h_kv, d_h);
+  if (workspace_bytes < L.total) return ATTN_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto at = [ws](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  SharedArgs s;
+  DecodeRunsArgs& a = s.own;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.B = B;
+  a.h = h;
+  a.h_kv = h_kv;
+  a.d_h = d_h;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.scale = scale;
+  a.plan = reinterpret_cast<long long*>(ws);
+  a.o_part = at(R.o_off);
+  a.m_part = at(R.m_off);
+  a.l_part = at(R.l_off);
+  a.o_row = at(L.row_o);
+  a.m_row = at(L.row_m);
+  a.l_row = at(L.row_l);
+  a.o = o;
+  a.lse = lse;
+  s.prefix_table = prefix_table;
+  s.prefix_len = prefix_len;
+  s.max_prefix_blocks = max_prefix_blocks;
+  s.pre_o = at(L.pre_o);
+  s.pre_m = at(L.pre_m);
+  s.pre_l = at(L.pre_l);
+  return from_cuda(launch_shared(s, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_selftest_wait_timeout(unsigned int limit_us, void* stream) {
@@ -601,16 +670,17 @@ attn_status_t attn_get_device_error(void* stream, unsigned int* bits) {
   if (bits == nullptr) return ATTN_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess, e4 = cudaSuccess;
-  cudaError_t e5 = cudaSuccess, e6 = cudaSuccess;
+  cudaError_t e5 = cudaSuccess, e6 = cudaSuccess, e7 = cudaSuccess;
   unsigned int v = decode_read_and_clear_error(s, &e1);
   v |= merge_read_and_clear_error(s, &e2);
   v |= prefill_read_and_clear_error(s, &e3);
   v |= simt_read_and_clear_error(s, &e4);
   v |= cache8_read_and_clear_error(s, &e5);
-  v |= decode8_read_and_clear_error(s, &e6);
+  v |= decode_runs_read_and_clear_error(s, &e6);
+  v |= shared_read_and_clear_error(s, &e7);
   *bits = v;
   if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess || e4 != cudaSuccess ||
-      e5 != cudaSuccess || e6 != cudaSuccess)
+      e5 != cudaSuccess || e6 != cudaSuccess || e7 != cudaSuccess)
     return ATTN_ERR_CUDA;
   return ATTN_OK;
 }

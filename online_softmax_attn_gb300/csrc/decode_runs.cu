@@ -1,41 +1,45 @@
-// decode_e4m3.cu -- paged decode attention over the 8-bit cache.
+// decode_runs.cu -- paged decode attention with the keys of the whole batch cut
+// into equal runs: over the 8-bit cache (attn_decode_paged_e4m3), and over the
+// rows' own bf16 pages in attn_decode_paged_shared.
 //
-// One query token per row over keys and values held as e4m3 codes with a
-// power-of-two scale per (token, KV head) (e4m3.cuh). With c_j, e_j the codes
-// and exponent of key j, w_j, f_j those of its value:
+// One query token per row; the online recurrence of "Naive attention and the
+// online softmax" in base 2. Both contractions are mma.m16n8k16 with the keys
+// (S^T = K q^T) or the value dimensions (O^T = V^T P^T) as the 16 rows and up to
+// 8 query heads of the KV head as the 8 columns: one MMA covers 16 keys x 8
+// heads x 16 dims.
+//   * K: the contraction index may be permuted freely, so a lane reads 16-byte
+//     chunks of a key with one shared load each and takes them as its A
+//     fragment; no ldmatrix, no shuffles.
+//   * V: ldmatrix.trans. P^T: the S^T accumulator holds key rows; movmatrix
+//     transposes the 8x8 block of weights into the B fragment.
+//
+// 8-bit cache (e4m3.cuh). With c_j, e_j the codes and exponent of key j, w_j,
+// f_j those of its value,
 //   s_j = scale * 2^e_j (q . c_j),  o = sum_j exp(s_j) 2^f_j w_j / sum_j exp(s_j).
-// The online recurrence of "Naive attention and the online softmax" runs in
-// base 2 with two references of its own per head: m for the normaliser (the
-// running max of s) and r for the accumulator (the running max of s + f, the
-// log2 weight with which a code of V enters). Any common shift is legal, and a
-// weight 2^(s + f - r) fits fp16 whatever the values' magnitudes are, so P V is
-// one fp16 product against the codes themselves.
+// Codes go to fp16 (exact) in registers. Each head has two references: m for
+// the normaliser (a running max of s) and r for the accumulator (a running max
+// of s + f, the log2 weight with which a code of V enters). Any common shift
+// is legal, and a weight 2^(s + f - r) fits fp16 whatever the values'
+// magnitudes are, so P V is one fp16 product against the codes themselves. q
+// is scaled per head by a power of two to a largest magnitude in
+// [2^14, 2^15), where fp16 holds bf16's 8 significant bits down to 2^-28 of
+// that maximum. ldmatrix moves byte pairs (two dims of a key); one prmt puts
+// the same dim of two keys side by side.
 //
-// The codes go to fp16 (exact) in registers, and both contractions are
-// mma.m16n8k16 with the keys (S^T = K q^T) or the value dimensions
-// (O^T = V^T P^T) as the 16 rows and up to 8 query heads of the KV head as the
-// 8 columns: one MMA covers 16 keys x 8 heads x 16 dims. q is scaled per head
-// by a power of two to a largest magnitude in [2^14, 2^15), where an fp16 holds
-// bf16's 8 significant bits down to 2^-31 of that maximum.
-//   * K: the contraction index may be permuted freely, so a lane reads 16
-//     consecutive codes of a key with one shared load and takes them four at a
-//     time as its A fragment; no ldmatrix, no byte shuffles.
-//   * V: ldmatrix.trans moves byte pairs (two dims of a key); one prmt puts
-//     the same dim of two keys side by side.
-//   * P^T: the S^T accumulator holds key rows; movmatrix transposes the 8x8
-//     fp16 block into the B fragment.
+// bf16 cache: q, K and V enter as they are; P is the two-term bf16 split
+// P_hi + P_lo (a single bf16 weight would cost up to 2^-8 of itself).
 //
-// Bound by memory: 2 (d_h + 1) bytes per key and KV head. A warp owns a ring
-// of NST stages, each one page of K and V (TMA, swizzled) with their exponents
-// (16-byte bulk copies).
+// Bound by memory: 2 (d_h + 1) or 4 d_h bytes per key and KV head. A warp owns
+// a ring of NST stages, each one page of K and V (TMA, swizzled), for the 8-bit
+// cache with their exponents (16-byte bulk copies).
 //
 // Work split: the (row, KV head, head block) units' pages, laid end to end,
 // are cut into equal runs, one per CTA (two CTAs per SM), so any mix of lengths
 // fills the machine and the launch does not depend on the lengths. A CTA works
 // through its run unit by unit; its warps take the pages of a unit in turn and
 // join their states at the unit's end. A unit inside one run is finished there;
-// one cut by a run border leaves at most one partial state per CTA, which
-// decode8_merge_kernel joins in run order.
+// one cut by a run border leaves at most one partial state per CTA, which the
+// merge kernel joins in run order.
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "internal.h"
@@ -43,7 +47,7 @@
 
 namespace attn {
 
-static __device__ unsigned int g_decode8_err;
+static __device__ unsigned int g_decode_runs_err;
 // Exponents of a page outside the cache (its codes read as zeros).
 static __device__ __align__(16) const uint8_t g_unit_exp[16] = {127, 127, 127, 127, 127, 127, 127, 127,
                                                                 127, 127, 127, 127, 127, 127, 127, 127};
@@ -52,8 +56,6 @@ namespace {
 
 using e4m3::kPage;
 
-constexpr int kNW = 8;       // warps per CTA
-constexpr int kMinPages = 8; // least pages per CTA: one per warp
 // Weights are at most 2^15 (fp16's largest finite number is 65504): the
 // reference r is set to 13 below a new running max's weight and moves once a
 // weight would pass 2^15. Weights down to 2^-27 of the largest are then normal
@@ -66,6 +68,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -92,6 +102,14 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap, uint32_t bar,
+                                                 int c0, int c1, int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ void bulk_load16(uint32_t dst, const void* src, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
@@ -99,26 +117,56 @@ __device__ __forceinline__ void bulk_load16(uint32_t dst, const void* src, uint3
       : "memory");
 }
 
-template <int D, int NST>
+// Two fp32 numbers' upper halves (bf16, truncated) and what they leave out.
+__device__ __forceinline__ uint32_t split_hi(float a, float b) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(r) : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
+  return r;
+}
+__device__ __forceinline__ uint32_t split_lo(float a, float b) {
+  return pack_bf16x2(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u),
+                     b - __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+}
+
+// E8: the 8-bit cache. NW warps per CTA, NST stages per warp.
+template <bool E8, int D, int NW, int NST>
 struct Cfg {
-  static constexpr int PAGE_BYTES = kPage * D;          // codes of one page of one KV head
-  static constexpr int STAGE_BYTES = 2 * PAGE_BYTES;    // K then V
-  static constexpr int RING_BYTES = kNW * NST * STAGE_BYTES;
-  static constexpr int EXP_OFF = RING_BYTES;            // [warp][stage][K 16 | V 16]
-  static constexpr int NREG = D / 4;                    // accumulators per lane
-  static constexpr int JOIN_OFF = EXP_OFF + kNW * NST * 32;
-  static constexpr int JOIN_BYTES = (kNW / 2) * 32 * NREG * 4;
-  static constexpr int ML_OFF = JOIN_OFF + JOIN_BYTES;  // [2][warp][8 heads] floats
-  static constexpr int BAR_OFF = ML_OFF + 2 * kNW * 8 * 4;
-  static constexpr int SMEM = BAR_OFF + kNW * NST * 8 + 1024;
+  static constexpr int PAGE_BYTES = kPage * D * (E8 ? 1 : 2);  // one page of one KV head
+  static constexpr int STAGE_BYTES = 2 * PAGE_BYTES;           // K then V
+  static constexpr int RING_BYTES = NW * NST * STAGE_BYTES;
+  static constexpr int EXP_OFF = RING_BYTES;                   // [warp][stage][K 16 | V 16]
+  static constexpr int EXP_BYTES = E8 ? 32 : 0;
+  static constexpr int NREG = D / 4;                           // accumulators per lane
+  static constexpr int JOIN_OFF = EXP_OFF + NW * NST * EXP_BYTES;
+  static constexpr int JOIN_BYTES = (NW / 2) * 32 * NREG * 4;
+  static constexpr int ML_OFF = JOIN_OFF + JOIN_BYTES;         // [2][warp][8 heads] floats
+  static constexpr int BAR_OFF = ML_OFF + 2 * NW * 8 * 4;
+  static constexpr int SMEM = BAR_OFF + NW * NST * 8 + 1024;
+  static_assert(NW * NST <= 32, "one lane initialises each barrier");
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-// 16-byte chunk `c` of key row `r` of a page: the TMA's 128-byte (d_h = 128)
-// or 64-byte (d_h = 64) swizzle.
-template <int D>
+// 16-byte chunk `c` of key row `r` of a page: the TMA's swizzle. 8-bit codes:
+// rows of 128 (128-byte swizzle) or 64 bytes (64-byte swizzle); bf16: halves
+// of 64 elements, rows of 128 bytes.
+template <bool E8, int D>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t page, int r, int c) {
-  return page + r * D + ((c ^ (D == 128 ? (r & 7) : ((r >> 1) & 3))) << 4);
+  if constexpr (E8)
+    return page + r * D + ((c ^ (D == 128 ? (r & 7) : ((r >> 1) & 3))) << 4);
+  else
+    return page + (c >> 3) * (kPage * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
+
+// Where states and results go. Units cut by a run border: part (two slots of 8
+// heads per CTA). Other units: o and lse themselves (8-bit decode), or a state
+// per (row, head) in row_* (shared-prefix decode, whose merge adds the prefix).
+struct RunOut {
+  long long* plan;
+  float *o_part, *m_part, *l_part;
+  float *o_row, *m_row, *l_row;
+  __nv_bfloat16* o;
+  float* lse;
+};
 
 // A CTA's run, unit by unit. Warp-uniform.
 struct Walk {
@@ -158,17 +206,14 @@ __device__ __forceinline__ bool walk_next(Walk& w, const Rows& rw) {
   return true;
 }
 
-template <int D, int NST>
-__global__ void __launch_bounds__(kNW * 32, 2)
-    decode8_kernel(const __grid_constant__ CUtensorMap tmap_k,
+template <bool E8, int D, int NW, int NST>
+__global__ void __launch_bounds__(NW * 32, 2)
+    decode_runs_kernel(const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const uint8_t* __restrict__ ks,
                    const uint8_t* __restrict__ vs, const __nv_bfloat16* __restrict__ q,
                    const int32_t* __restrict__ block_table, Rows rw, int h, int h_kv, int g,
-                   int max_blocks, int num_blocks, float qscale, long long* __restrict__ plan,
-                   float* __restrict__ o_part, float* __restrict__ m_part,
-                   float* __restrict__ l_part, __nv_bfloat16* __restrict__ o,
-                   float* __restrict__ lse) {
-  using C = Cfg<D, NST>;
+                   int max_blocks, int num_blocks, float qscale, const RunOut out) {
+  using C = Cfg<E8, D, NW, NST>;
   constexpr int KS = D / 16;  // MMA steps over d_h
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tq = lane & 3;
@@ -180,29 +225,28 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   const uint32_t sbase = smem_u32(smem);
   float* join = reinterpret_cast<float*>(smem + C::JOIN_OFF);
   float* ms = reinterpret_cast<float*>(smem + C::ML_OFF);  // [warp][8]
-  float* ls = ms + kNW * 8;
-  __shared__ long long s_warp[kNW];
+  float* ls = ms + NW * 8;
+  __shared__ long long s_warp[NW];
   __shared__ long long s_start;
   __shared__ int s_b;
 
   if (warp == 0) {
-    if (lane < kNW * NST) mbar_init(sbase + C::BAR_OFF + lane * 8, 1);
+    if (lane < NW * NST) mbar_init(sbase + C::BAR_OFF + lane * 8, 1);
     fence_barrier_init();
     if (lane == 0) {
       prefetch_tmap(&tmap_k);
       prefetch_tmap(&tmap_v);
     }
   }
-  static_assert(kNW * NST <= 32, "one lane initialises each barrier");
   pdl_wait();     // lengths, table, q and the cache are earlier kernels' output
   pdl_trigger();
 
   // ---- the run: prefix sums of the rows' pages ----
-  const int per_t = (rw.B + kNW * 32 - 1) / (kNW * 32);
+  const int per_t = (rw.B + NW * 32 - 1) / (NW * 32);
   const int b0 = min(tid * per_t, rw.B), b1 = min(b0 + per_t, rw.B);
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
-    if (blockIdx.x == 0) (void)clamp_seq_len(__ldcg(rw.seq_lens + b), rw.max_len, &g_decode8_err);
+    if (blockIdx.x == 0) (void)clamp_seq_len(__ldcg(rw.seq_lens + b), rw.max_len, &g_decode_runs_err);
     sum += (row_len(rw, b) + kPage - 1) / kPage;
   }
   long long incl = sum;
@@ -215,20 +259,20 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   __syncthreads();
   long long before = incl - sum, total = 0;
 #pragma unroll
-  for (int w = 0; w < kNW; ++w) {
+  for (int w = 0; w < NW; ++w) {
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
   const long long all = total * rw.upr;
-  const long long per = max(static_cast<long long>(kMinPages), (all + gridDim.x - 1) / gridDim.x);
+  const long long per = max(static_cast<long long>(NW), (all + gridDim.x - 1) / gridDim.x);
   const long long p0 = per * blockIdx.x;
   if (blockIdx.x == 0) {  // for the merge
-    if (tid == 0) plan[0] = per;
+    if (tid == 0) out.plan[0] = per;
     long long at = before;
     for (int b = b0; b < b1; ++b) {
-      plan[1 + b] = at;
+      out.plan[1 + b] = at;
       at += (row_len(rw, b) + kPage - 1) / kPage;
-      if (b == rw.B - 1) plan[1 + rw.B] = at;
+      if (b == rw.B - 1) out.plan[1 + rw.B] = at;
     }
   }
   if (p0 >= all) return;
@@ -264,13 +308,13 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   int bt = -1;    // table entries of this warp's pages, 32 at a time
   int issued = 0;
   auto load_bt = [&](int i) {
-    const int j = i + kNW * lane;
+    const int j = i + NW * lane;
     bt = pw.lo + j < pw.hi
              ? __ldcg(block_table + static_cast<size_t>(pw.b) * max_blocks + pw.lo + j)
              : -1;
   };
   const uint32_t ring = sbase + warp * NST * C::STAGE_BYTES;
-  const uint32_t exps = sbase + C::EXP_OFF + warp * NST * 32;
+  const uint32_t exps = sbase + C::EXP_OFF + warp * NST * C::EXP_BYTES;
   const uint32_t bars = sbase + C::BAR_OFF + warp * NST * 8;
   const uint64_t policy = policy_evict_first();
   int bt_i = 0;  // pages taken from bt
@@ -294,27 +338,29 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       const uint32_t dst = ring + st * C::STAGE_BYTES, bar = bars + st * 8;
       const int kvh = pw.u / n_gb;
       const bool bad = phys < 0 || phys >= num_blocks;
-      if (bad) atomicOr(&g_decode8_err, ATTN_DEVERR_BAD_PAGE);
+      if (bad) atomicOr(&g_decode_runs_err, ATTN_DEVERR_BAD_PAGE);
       // An out-of-range coordinate is filled with zeros by the copy engine.
-      const int slab = bad ? -1 : phys * h_kv + kvh;
-      const size_t eo = static_cast<size_t>(bad ? 0 : slab) * kPage;
-      mbar_arrive_expect_tx(bar, C::STAGE_BYTES + 32);
-      asm volatile(
-          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-          " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
-          "l"(reinterpret_cast<uint64_t>(&tmap_k)), "r"(bar), "r"(0), "r"(0), "r"(slab), "l"(policy)
-          : "memory");
-      asm volatile(
-          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-          " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst + C::PAGE_BYTES),
-          "l"(reinterpret_cast<uint64_t>(&tmap_v)), "r"(bar), "r"(0), "r"(0), "r"(slab), "l"(policy)
-          : "memory");
-      bulk_load16(exps + st * 32, bad ? g_unit_exp : ks + eo, bar);
-      bulk_load16(exps + st * 32 + 16, bad ? g_unit_exp : vs + eo, bar);
+      mbar_arrive_expect_tx(bar, C::STAGE_BYTES + C::EXP_BYTES);
+      if constexpr (E8) {
+        const int slab = bad ? -1 : phys * h_kv + kvh;
+        const size_t eo = static_cast<size_t>(bad ? 0 : slab) * kPage;
+        tma_load_3d_hint(dst, &tmap_k, bar, 0, 0, slab, policy);
+        tma_load_3d_hint(dst + C::PAGE_BYTES, &tmap_v, bar, 0, 0, slab, policy);
+        bulk_load16(exps + st * 32, bad ? g_unit_exp : ks + eo, bar);
+        bulk_load16(exps + st * 32 + 16, bad ? g_unit_exp : vs + eo, bar);
+      } else {
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf) {
+          tma_load_4d_hint(dst + hf * (kPage * 128), &tmap_k, bar, hf * 64, kvh, 0, bad ? -1 : phys,
+                           policy);
+          tma_load_4d_hint(dst + C::PAGE_BYTES + hf * (kPage * 128), &tmap_v, bar, hf * 64, kvh, 0,
+                           bad ? -1 : phys, policy);
+        }
+      }
     }
     ++issued;
     ++bt_i;
-    pi += kNW;
+    pi += NW;
   };
   for (int i = 0; i < NST; ++i) issue_next();
 
@@ -328,10 +374,10 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     const int nh = min(8, g - gb * 8);    // heads in the block
 
     // q as the B operand: lane (gid, tq) holds head gid's dims of the chunks
-    // that lanes tq read of K: 32 consecutive dims (d_h = 128) or 16.
+    // that lanes tq read of K (8-bit: 32 or 16 consecutive dims).
     uint32_t qb[KS][2];
-    float hc;
-    {
+    float hc = qscale;
+    if constexpr (E8) {
       constexpr int NC = D / 64;  // 16-dim chunks per lane
       float x[NC * 16];
 #pragma unroll
@@ -366,6 +412,20 @@ __global__ void __launch_bounds__(kNW * 32, 2)
         qb[ksi][0] = pack_f16x2(x[ksi * 4] * up, x[ksi * 4 + 1] * up);
         qb[ksi][1] = pack_f16x2(x[ksi * 4 + 2] * up, x[ksi * 4 + 3] * up);
       }
+    } else {
+      // bf16: chunks 2tq, 2tq + 1 (8 dims each) of every 64-element half.
+#pragma unroll
+      for (int c = 0; c < KS / 2; ++c) {
+        uint4 t = make_uint4(0u, 0u, 0u, 0u);
+        if (gid < nh)
+          t = __ldcg(reinterpret_cast<const uint4*>(
+              q + (static_cast<size_t>(cw.b) * h + hq0 + gid) * D + (c >> 1) * 64 +
+              (2 * tq + (c & 1)) * 8));
+        qb[2 * c][0] = t.x;
+        qb[2 * c][1] = t.y;
+        qb[2 * c + 1][0] = t.z;
+        qb[2 * c + 1][1] = t.w;
+      }
     }
     const float hc0 = __shfl_sync(0xffffffffu, hc, (2 * tq) * 4);
     const float hc1 = __shfl_sync(0xffffffffu, hc, (2 * tq + 1) * 4);
@@ -380,9 +440,9 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
     const int span = cw.hi - cw.lo;
-    for (int i = warp; i < span; i += kNW) {
+    for (int i = warp; i < span; i += NW) {
       const int st = used % NST;
-      if (!dead && !mbar_wait(bars + st * 8, (used / NST) & 1, &g_decode8_err)) dead = true;
+      if (!dead && !mbar_wait(bars + st * 8, (used / NST) & 1, &g_decode_runs_err)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       if (dead) break;
       const uint32_t kp = ring + st * C::STAGE_BYTES, vp = kp + C::PAGE_BYTES;
@@ -390,10 +450,10 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       if (valid < kPage) {
         // Slots past the row's end hold whatever the cache holds there (NaN
         // codes among it); their weights are 0, but 0 * NaN is not.
-        constexpr int CPR = D / 16;
+        constexpr int CPR = C::PAGE_BYTES / (kPage * 16);
         for (int c = lane; c < (kPage - valid) * CPR; c += 32)
           asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                           chunk_at<D>(vp, valid + c / CPR, c % CPR)),
+                           chunk_at<E8, D>(vp, valid + c / CPR, c % CPR)),
                        "r"(0u)
                        : "memory");
         fence_proxy_async_smem();  // before the stage is refilled by the copy engine
@@ -402,28 +462,38 @@ __global__ void __launch_bounds__(kNW * 32, 2)
 
       // ---- S^T = K q^T: keys gid and gid + 8, heads 2tq and 2tq + 1 ----
       float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+      float va = 0.f, vb = 0.f, ka = 1.f, kb = 1.f;
+      if constexpr (E8) {
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const int ch = tq * (D / 64) + c;
-        const uint4 x = lds128(chunk_at<D>(kp, gid, ch));
-        const uint4 y = lds128(chunk_at<D>(kp, gid + 8, ch));
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        for (int c = 0; c < D / 64; ++c) {
+          const int ch = tq * (D / 64) + c;
+          const uint4 x = lds128(chunk_at<E8, D>(kp, gid, ch));
+          const uint4 y = lds128(chunk_at<E8, D>(kp, gid + 8, ch));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = e4m3::decode2(static_cast<uint16_t>(xw[j]));
-          const uint32_t a1 = e4m3::decode2(static_cast<uint16_t>(yw[j]));
-          const uint32_t a2 = e4m3::decode2(static_cast<uint16_t>(xw[j] >> 16));
-          const uint32_t a3 = e4m3::decode2(static_cast<uint16_t>(yw[j] >> 16));
-          if (j & 1)
-            mma_f16(sb, a0, a1, a2, a3, qb[c * 4 + j][0], qb[c * 4 + j][1]);
-          else
-            mma_f16(sa, a0, a1, a2, a3, qb[c * 4 + j][0], qb[c * 4 + j][1]);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = e4m3::decode2(static_cast<uint16_t>(xw[j]));
+            const uint32_t a1 = e4m3::decode2(static_cast<uint16_t>(yw[j]));
+            const uint32_t a2 = e4m3::decode2(static_cast<uint16_t>(xw[j] >> 16));
+            const uint32_t a3 = e4m3::decode2(static_cast<uint16_t>(yw[j] >> 16));
+            mma_f16((j & 1) ? sb : sa, a0, a1, a2, a3, qb[c * 4 + j][0], qb[c * 4 + j][1]);
+          }
+        }
+        const uint32_t ep = exps + st * 32;
+        ka = e4m3::scale_of(lds_u8(ep + gid));
+        kb = e4m3::scale_of(lds_u8(ep + gid + 8));
+        va = static_cast<float>(static_cast<int>(lds_u8(ep + 16 + gid)) - 127);
+        vb = static_cast<float>(static_cast<int>(lds_u8(ep + 24 + gid)) - 127);
+      } else {
+#pragma unroll
+        for (int c = 0; c < KS / 2; ++c) {
+          const int ch = (c >> 1) * 8 + 2 * tq + (c & 1);
+          const uint4 x = lds128(chunk_at<E8, D>(kp, gid, ch));
+          const uint4 y = lds128(chunk_at<E8, D>(kp, gid + 8, ch));
+          mma_bf16(sa, x.x, y.x, x.y, y.y, qb[2 * c][0], qb[2 * c][1]);
+          mma_bf16(sb, x.z, y.z, x.w, y.w, qb[2 * c + 1][0], qb[2 * c + 1][1]);
         }
       }
-      const uint32_t ep = exps + st * 32;
-      const float ka = e4m3::scale_of(lds_u8(ep + gid)), kb = e4m3::scale_of(lds_u8(ep + gid + 8));
-      const float va = static_cast<float>(static_cast<int>(lds_u8(ep + 16 + gid)) - 127);
-      const float vb = static_cast<float>(static_cast<int>(lds_u8(ep + 24 + gid)) - 127);
       float s0 = (sa[0] + sb[0]) * hc0 * ka, s1 = (sa[1] + sb[1]) * hc1 * ka;
       float s2 = (sa[2] + sb[2]) * hc0 * kb, s3 = (sa[3] + sb[3]) * hc1 * kb;
       if (valid < kPage) {
@@ -434,30 +504,37 @@ __global__ void __launch_bounds__(kNW * 32, 2)
 
       // ---- references: they move only when a score passes them by kSlack ----
       // (a NaN never compares, and reaches l and O through its weight)
-      const bool up = s0 > m0 + kSlack || s2 > m0 + kSlack || s1 > m1 + kSlack ||
-                      s3 > m1 + kSlack || t0 > r0 + (kTop + kSlack) ||
-                      t2 > r0 + (kTop + kSlack) || t1 > r1 + (kTop + kSlack) ||
-                      t3 > r1 + (kTop + kSlack);
+      bool up = s0 > m0 + kSlack || s2 > m0 + kSlack || s1 > m1 + kSlack || s3 > m1 + kSlack;
+      if constexpr (E8)
+        up = up || t0 > r0 + (kTop + kSlack) || t2 > r0 + (kTop + kSlack) ||
+             t1 > r1 + (kTop + kSlack) || t3 > r1 + (kTop + kSlack);
       if (__any_sync(0xffffffffu, up)) {
         float n0 = fmaxf(s0, s2), n1 = fmaxf(s1, s3), w0 = fmaxf(t0, t2), w1 = fmaxf(t1, t3);
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
           n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
           n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-          w0 = fmaxf(w0, __shfl_xor_sync(0xffffffffu, w0, off));
-          w1 = fmaxf(w1, __shfl_xor_sync(0xffffffffu, w1, off));
+          if constexpr (E8) {
+            w0 = fmaxf(w0, __shfl_xor_sync(0xffffffffu, w0, off));
+            w1 = fmaxf(w1, __shfl_xor_sync(0xffffffffu, w1, off));
+          }
         }
         n0 = fmaxf(n0, m0);
         n1 = fmaxf(n1, m1);
-        w0 = fmaxf(w0 - kTop, r0);
-        w1 = fmaxf(w1 - kTop, r1);
-        l0 *= ex2_approx(m0 - n0);
-        l1 *= ex2_approx(m1 - n1);
-        const float a0 = ex2_approx(r0 - w0), a1 = ex2_approx(r1 - w1);
+        const float am0 = ex2_approx(m0 - n0), am1 = ex2_approx(m1 - n1);
+        l0 *= am0;
+        l1 *= am1;
         m0 = n0;
         m1 = n1;
-        r0 = w0;
-        r1 = w1;
+        float a0 = am0, a1 = am1;
+        if constexpr (E8) {
+          w0 = fmaxf(w0 - kTop, r0);
+          w1 = fmaxf(w1 - kTop, r1);
+          a0 = ex2_approx(r0 - w0);
+          a1 = ex2_approx(r1 - w1);
+          r0 = w0;
+          r1 = w1;
+        }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           acc[k][0] *= a0;
@@ -466,26 +543,40 @@ __global__ void __launch_bounds__(kNW * 32, 2)
           acc[k][3] *= a1;
         }
       }
-      l0 += ex2_approx(s0 - m0) + ex2_approx(s2 - m0);
-      l1 += ex2_approx(s1 - m1) + ex2_approx(s3 - m1);
-      const uint32_t pb0 = movmatrix_t(pack_f16x2(ex2_approx(t0 - r0), ex2_approx(t1 - r1)));
-      const uint32_t pb1 = movmatrix_t(pack_f16x2(ex2_approx(t2 - r0), ex2_approx(t3 - r1)));
-
-      // ---- O^T += V^T P^T: rows gid, gid + 8 of step k are dims
-      // 16k + 2 gid and 16k + 2 gid + 1 ----
+      const float p0 = ex2_approx(s0 - m0), p1 = ex2_approx(s1 - m1);
+      const float p2 = ex2_approx(s2 - m0), p3 = ex2_approx(s3 - m1);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      if constexpr (E8) {
+        const uint32_t pb0 = movmatrix_t(pack_f16x2(ex2_approx(t0 - r0), ex2_approx(t1 - r1)));
+        const uint32_t pb1 = movmatrix_t(pack_f16x2(ex2_approx(t2 - r0), ex2_approx(t3 - r1)));
+        // O^T += V^T P^T: rows gid, gid + 8 of step k are dims 16k + 2 gid and
+        // 16k + 2 gid + 1.
 #pragma unroll
-      for (int k = 0; k < KS; k += 2) {
-        uint32_t r[4];
-        ldsm_x4_t(chunk_at<D>(vp, v_row, k + v_dc), r);
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t r[4];
+          ldsm_x4_t(chunk_at<E8, D>(vp, v_row, k + v_dc), r);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t x, y;
-          asm("prmt.b32 %0, %1, %1, 0x3120;" : "=r"(x) : "r"(r[2 * e]));
-          asm("prmt.b32 %0, %1, %1, 0x3120;" : "=r"(y) : "r"(r[2 * e + 1]));
-          mma_f16(acc[k + e], e4m3::decode2(static_cast<uint16_t>(x)),
-                  e4m3::decode2(static_cast<uint16_t>(x >> 16)),
-                  e4m3::decode2(static_cast<uint16_t>(y)),
-                  e4m3::decode2(static_cast<uint16_t>(y >> 16)), pb0, pb1);
+          for (int e = 0; e < 2; ++e) {
+            uint32_t x, y;
+            asm("prmt.b32 %0, %1, %1, 0x3120;" : "=r"(x) : "r"(r[2 * e]));
+            asm("prmt.b32 %0, %1, %1, 0x3120;" : "=r"(y) : "r"(r[2 * e + 1]));
+            mma_f16(acc[k + e], e4m3::decode2(static_cast<uint16_t>(x)),
+                    e4m3::decode2(static_cast<uint16_t>(x >> 16)),
+                    e4m3::decode2(static_cast<uint16_t>(y)),
+                    e4m3::decode2(static_cast<uint16_t>(y >> 16)), pb0, pb1);
+          }
+        }
+      } else {
+        const uint32_t h0 = movmatrix_t(split_hi(p0, p1)), h1 = movmatrix_t(split_hi(p2, p3));
+        const uint32_t e0 = movmatrix_t(split_lo(p0, p1)), e1 = movmatrix_t(split_lo(p2, p3));
+        // Rows gid, gid + 8 of step k are dims 16k + gid and 16k + 8 + gid.
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t r[4];
+          ldsm_x4_t(chunk_at<E8, D>(vp, v_row, 2 * k + v_dc), r);
+          mma_bf16(acc[k], r[0], r[2], r[1], r[3], h0, h1);
+          mma_bf16(acc[k], r[0], r[2], r[1], r[3], e0, e1);
         }
       }
       __syncwarp();
@@ -509,12 +600,12 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     __syncthreads();
     float M0 = kNone, M1 = kNone;
 #pragma unroll
-    for (int w = 0; w < kNW; ++w) {
+    for (int w = 0; w < NW; ++w) {
       M0 = fmaxf(M0, ms[w * 8 + 2 * tq]);
       M1 = fmaxf(M1, ms[w * 8 + 2 * tq + 1]);
     }
     {
-      const float f0 = ex2_approx(r0 - M0), f1 = ex2_approx(r1 - M1);
+      const float f0 = ex2_approx((E8 ? r0 : m0) - M0), f1 = ex2_approx((E8 ? r1 : m1) - M1);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         acc[k][0] *= f0;
@@ -524,7 +615,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       }
     }
 #pragma unroll
-    for (int half = kNW / 2; half >= 1; half >>= 1) {
+    for (int half = NW / 2; half >= 1; half >>= 1) {
       if (warp >= half && warp < 2 * half) {
 #pragma unroll
         for (int i = 0; i < C::NREG; ++i)
@@ -540,7 +631,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     if (warp == 0) {
       float L0 = 0.f, L1 = 0.f;
 #pragma unroll
-      for (int w = 0; w < kNW; ++w) {
+      for (int w = 0; w < NW; ++w) {
         L0 = fmaf(ls[w * 8 + 2 * tq], ex2_approx(ms[w * 8 + 2 * tq] - M0), L0);
         L1 = fmaf(ls[w * 8 + 2 * tq + 1], ex2_approx(ms[w * 8 + 2 * tq + 1] - M1), L1);
       }
@@ -550,27 +641,34 @@ __global__ void __launch_bounds__(kNW * 32, 2)
         const int head = 2 * tq + e;
         if (head >= nh) continue;
         const float L = e ? L1 : L0, M = e ? M1 : M0;
-        if (whole) {
+        const size_t row = static_cast<size_t>(cw.b) * h + hq0 + head;
+        if (!ATTN_GUARD(row < static_cast<size_t>(rw.B) * h, &g_decode_runs_err)) continue;
+        if (E8 && whole) {
           const bool empty = L == 0.f;  // every logit -inf
           const float inv = empty ? 0.f : 1.f / L;
-          const size_t row = static_cast<size_t>(cw.b) * h + hq0 + head;
-          if (!ATTN_GUARD(row < static_cast<size_t>(rw.B) * h, &g_decode8_err)) continue;
 #pragma unroll
           for (int k = 0; k < KS; ++k)
-            *reinterpret_cast<uint32_t*>(o + row * D + 16 * k + 2 * gid) =
+            *reinterpret_cast<uint32_t*>(out.o + row * D + 16 * k + 2 * gid) =
                 empty ? 0u : pack_bf16x2(acc[k][e] * inv, acc[k][2 + e] * inv);
-          if (lse != nullptr && gid == 0) lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
-        } else {
-          const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (cw.lo == 0 ? 1 : 0)) * 8 + head;
-          if (!ATTN_GUARD(slot < static_cast<size_t>(gridDim.x) * 16, &g_decode8_err)) continue;
+          if (out.lse != nullptr && gid == 0) out.lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
+          continue;
+        }
+        const size_t slot =
+            whole ? row : (2 * static_cast<size_t>(blockIdx.x) + (cw.lo == 0 ? 1 : 0)) * 8 + head;
+        if (!ATTN_GUARD(whole || slot < static_cast<size_t>(gridDim.x) * 16, &g_decode_runs_err)) continue;
+        float* so = (whole ? out.o_row : out.o_part) + slot * D;
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            *reinterpret_cast<float2*>(o_part + slot * D + 16 * k + 2 * gid) =
-                make_float2(acc[k][e], acc[k][2 + e]);
-          if (gid == 0) {
-            m_part[slot] = M;
-            l_part[slot] = L;
+        for (int k = 0; k < KS; ++k) {
+          if constexpr (E8) {
+            *reinterpret_cast<float2*>(so + 16 * k + 2 * gid) = make_float2(acc[k][e], acc[k][2 + e]);
+          } else {
+            so[16 * k + gid] = acc[k][e];
+            so[16 * k + 8 + gid] = acc[k][2 + e];
           }
+        }
+        if (gid == 0) {
+          (whole ? out.m_row : out.m_part)[slot] = M;
+          (whole ? out.l_row : out.l_part)[slot] = L;
         }
       }
     }
@@ -579,7 +677,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   if (dead) {
     // Bounded chance for the copies in flight to land before the CTA exits.
     for (int j = used; j < issued; ++j)
-      (void)mbar_wait(bars + (j % NST) * 8, (j / NST) & 1, &g_decode8_err);
+      (void)mbar_wait(bars + (j % NST) * 8, (j / NST) & 1, &g_decode_runs_err);
   }
 }
 
@@ -587,7 +685,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
 // writes empty rows. One CTA per (row, head), warps take its partials in turn.
 template <int D>
 __global__ void __launch_bounds__(128)
-    decode8_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m_part,
+    decode_runs_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m_part,
                          const float* __restrict__ l_part, const long long* __restrict__ plan,
                          int h, int g, int n_gb, int upr, __nv_bfloat16* __restrict__ o,
                          float* __restrict__ lse) {
@@ -675,52 +773,84 @@ __global__ void __launch_bounds__(128)
   if (lse != nullptr && threadIdx.x == 0) lse[row] = empty ? -INFINITY : Mt * kLn2 + logf(Lt);
 }
 
-template <int D, int NST>
-cudaError_t launch_cfg(const Decode8Args& a, int sms, cudaStream_t stream) {
-  using C = Cfg<D, NST>;
+template <bool E8, int D, int NW, int NST>
+cudaError_t launch_cfg(const DecodeRunsArgs& a, int sms, cudaStream_t stream) {
+  using C = Cfg<E8, D, NW, NST>;
   CUtensorMap tk, tv;
-  const uint64_t dims[3] = {uint64_t(D), uint64_t(kPage), uint64_t(a.num_blocks) * a.h_kv};
-  const uint64_t strides[2] = {uint64_t(D), uint64_t(kPage) * D};
-  const uint32_t box[3] = {uint32_t(D), uint32_t(kPage), 1u};
-  const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (encode_tensor_map(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a.k_codes), dims,
-                        strides, box, sw) != CUDA_SUCCESS ||
-      encode_tensor_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a.v_codes), dims,
-                        strides, box, sw) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  auto kern = decode8_kernel<D, NST>;
+  CUresult r;
+  if constexpr (E8) {
+    const uint64_t dims[3] = {uint64_t(D), uint64_t(kPage), uint64_t(a.num_blocks) * a.h_kv};
+    const uint64_t strides[2] = {uint64_t(D), uint64_t(kPage) * D};
+    const uint32_t box[3] = {uint32_t(D), uint32_t(kPage), 1u};
+    const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    r = encode_tensor_map(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a.k_cache), dims,
+                          strides, box, sw);
+    if (r == CUDA_SUCCESS)
+      r = encode_tensor_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(a.v_cache), dims,
+                            strides, box, sw);
+  } else {
+    const uint64_t dims[4] = {uint64_t(D), uint64_t(a.h_kv), uint64_t(kPage), uint64_t(a.num_blocks)};
+    const uint64_t strides[3] = {uint64_t(D) * 2, uint64_t(a.h_kv) * D * 2,
+                                 uint64_t(kPage) * a.h_kv * D * 2};
+    const uint32_t box[4] = {64u, 1u, uint32_t(kPage), 1u};
+    r = encode_tensor_map(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.k_cache), dims,
+                          strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (r == CUDA_SUCCESS)
+      r = encode_tensor_map(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.v_cache),
+                            dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  auto kern = decode_runs_kernel<E8, D, NW, NST>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * sms < kDecode8MaxCtas ? 2 * sms : kDecode8MaxCtas;
+  const int grid = 2 * sms < kRunsMaxCtas ? 2 * sms : kRunsMaxCtas;
   const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
   const Rows rw{a.seq_lens, a.B, a.max_blocks * kPage, a.h_kv * n_gb};
-  e = launch_pdl(kern, dim3(grid), dim3(kNW * 32), size_t(C::SMEM), stream, tk, tv, a.k_exp, a.v_exp,
-                 static_cast<const __nv_bfloat16*>(a.q), a.block_table, rw, a.h, a.h_kv, g,
-                 a.max_blocks, a.num_blocks, a.scale * kLog2e, a.plan, a.o_part, a.m_part, a.l_part,
-                 static_cast<__nv_bfloat16*>(a.o), a.lse);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(decode8_merge_kernel<D>, dim3(unsigned(a.B) * a.h), dim3(128), 0, stream,
-                    static_cast<const float*>(a.o_part), static_cast<const float*>(a.m_part),
-                    static_cast<const float*>(a.l_part), static_cast<const long long*>(a.plan), a.h,
-                    g, n_gb, rw.upr, static_cast<__nv_bfloat16*>(a.o), a.lse);
+  const RunOut out{a.plan,  a.o_part, a.m_part, a.l_part, a.o_row,
+                   a.m_row, a.l_row,  static_cast<__nv_bfloat16*>(a.o), a.lse};
+  return launch_pdl(kern, dim3(grid), dim3(NW * 32), size_t(C::SMEM), stream, tk, tv, a.k_exp, a.v_exp,
+                    static_cast<const __nv_bfloat16*>(a.q), a.block_table, rw, a.h, a.h_kv, g,
+                    a.max_blocks, a.num_blocks, a.scale * kLog2e, out);
+}
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e;
 }
 
 }  // namespace
 
-cudaError_t launch_decode8(const Decode8Args& a, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream) {
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  return a.d_h == 128 ? launch_cfg<128, 2>(a, sms, stream) : launch_cfg<64, 3>(a, sms, stream);
+  e = a.d_h == 128 ? launch_cfg<true, 128, 8, 2>(a, sms, stream)
+                   : launch_cfg<true, 64, 8, 3>(a, sms, stream);
+  if (e != cudaSuccess) return e;
+  const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
+  auto merge = a.d_h == 128 ? decode_runs_merge_kernel<128> : decode_runs_merge_kernel<64>;
+  return launch_pdl(merge, dim3(unsigned(a.B) * a.h), dim3(128), 0, stream,
+                    static_cast<const float*>(a.o_part), static_cast<const float*>(a.m_part),
+                    static_cast<const float*>(a.l_part), static_cast<const long long*>(a.plan), a.h,
+                    g, n_gb, a.h_kv * n_gb, static_cast<__nv_bfloat16*>(a.o), a.lse);
 }
 
-unsigned int decode8_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {
+cudaError_t launch_decode_runs_bf16(const DecodeRunsArgs& a, cudaStream_t stream) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  return a.d_h == 128 ? launch_cfg<false, 128, 4, 3>(a, sms, stream)
+                      : launch_cfg<false, 64, 4, 6>(a, sms, stream);
+}
+
+unsigned int decode_runs_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {
   unsigned int v = 0, zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_decode8_err, sizeof(v), 0,
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_decode_runs_err, sizeof(v), 0,
                                             cudaMemcpyDeviceToHost, stream);
   if (e == cudaSuccess)
-    e = cudaMemcpyToSymbolAsync(g_decode8_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
+    e = cudaMemcpyToSymbolAsync(g_decode_runs_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
                                 stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
   if (st) *st = e;

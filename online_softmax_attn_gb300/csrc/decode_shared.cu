@@ -1,0 +1,686 @@
+// decode_shared.cu -- decode of a batch whose rows share a prefix of keys.
+//
+// Row b attends to the prefix's keys and to its own. The two key sets are
+// disjoint, so their states merge ("Merge normalized attention without
+// averaging tile outputs"); the prefix's state is computed for all rows at
+// once: the B * g query rows of a KV head are the M rows of dense products
+// against each key tile, and the prefix is read once for all of them.
+//
+//   1. shared_prefix_kernel (here): tcgen05, states of every row over the
+//      prefix, cut along the keys.
+//   2. decode_runs_kernel (decode_runs.cu, bf16 form): states over the rows'
+//      own pages.
+//   3. shared_merge_kernel (here): the states of a row, joined in a fixed
+//      order and divided once.
+//
+// Prefix kernel. Query rows of a KV head are ordered (token, head of the
+// group), so a 128-row tile is one TMA box of 128 / g tokens x g heads. A CTA
+// has two softmax warpgroups ("streams"; thread = row), a TMA warp and an MMA
+// warp. NT = 2 (more than 128 rows): the streams are two row tiles that share
+// each key tile. NT = 1: the streams take the key tiles of one row tile in
+// turn, each with an accumulator of its own, so that one stream's exponentials
+// overlap the other's MMAs in this case too. Steps alternate between the
+// streams; per step S = Q K^T (SS), weights over S in tensor memory, O += P V
+// (TS), with S of step e + 2 issued behind P V of step e.
+//
+// Work split: `groups` runs of equal length over the (KV head, key tile) pairs,
+// times the row blocks (NT * 128 rows) as neighbouring CTAs, which read the
+// same tiles at the same time, so the L2 serves all but one of them. A run that
+// crosses a head border gives two states.
+//
+// P = P_hi + P_lo in bf16 (two MMAs), as for the prefill's V tiles that stay
+// bf16. The reference of the weights moves only when a row's maximum passes it
+// by kSlack.
+#include "common.cuh"
+#include "internal.h"
+#include "pdl.cuh"
+#include "tc.cuh"
+
+namespace attn {
+
+static __device__ unsigned int g_shared_err;
+
+namespace {
+
+constexpr int kPage = 16;
+constexpr int kBM = 128, kBN = 128;
+constexpr float kNone = -1e30f;  // reference before the first key
+constexpr float kSlack = 8.0f;
+
+template <int D, int NT>
+struct SpCfg {
+  static constexpr int SUBS = D / 64;
+  static constexpr int SUB_BYTES = 128 * 128;
+  static constexpr int TILE = kBN * D * 2;
+  static constexpr int NSK = NT == 2 ? 2 : 3;
+  static constexpr int NSV = 3;
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + NT * TILE;
+  static constexpr int V_OFF = K_OFF + NSK * TILE;
+  static constexpr int BAR_OFF = V_OFF + NSV * TILE;
+  // q_full, q_empty, k_full[], k_empty[], v_full[], v_empty[], s_full[2],
+  // p_full[2], o_final[2], mma_done
+  static constexpr int B_KF = 2, B_KE = B_KF + NSK, B_VF = B_KE + NSK, B_VE = B_VF + NSV,
+                       B_SF = B_VE + NSV, B_PF = B_SF + 2, B_OF = B_PF + 2, B_DONE = B_OF + 2,
+                       NBAR = B_DONE + 1;
+  static_assert(NBAR <= 32, "one warp initialises the barriers, one per lane");
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int SMEM = MISC_OFF + 16 + 1024;
+  static constexpr int THREADS = 384;  // two softmax warpgroups, one of control
+  static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;
+  static constexpr int REG_LAUNCH = 168, REG_CONTROL = 120, REG_SOFTMAX = 192;
+  static_assert(2 * 128 * REG_SOFTMAX + 128 * REG_CONTROL <= THREADS * REG_LAUNCH,
+                "register split exceeds the launch allocation");
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Bounded wait that also gives up at once when another role has aborted.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity,
+                                              volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > ATTN_WAIT_LIMIT_NS) {
+      atomicOr(&g_shared_err, ATTN_DEVERR_WAIT_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+struct PrefixArgs {
+  const int32_t* table;
+  const int32_t* len;
+  int max_blocks, num_blocks, h_kv, groups, n_rb, s_cap, rows;  // rows = B * g per KV head
+  float *o, *m, *l;
+};
+
+// The run of key tiles of one CTA group.
+struct PrefixRun {
+  int len, tiles;       // prefix length, key tiles per head
+  long long per, lo, hi;
+};
+__device__ __forceinline__ PrefixRun prefix_run(const PrefixArgs& a, int group) {
+  PrefixRun r;
+  r.len = min(max(__ldcg(a.len), 0), a.max_blocks * kPage);
+  r.tiles = (r.len + kBN - 1) / kBN;
+  const long long all = static_cast<long long>(r.tiles) * a.h_kv;
+  r.per = max(1ll, (all + a.groups - 1) / a.groups);
+  r.lo = min(all, r.per * group);
+  r.hi = min(all, r.lo + r.per);
+  return r;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(384, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                         const __grid_constant__ CUtensorMap tmap_k,
+                         const __grid_constant__ CUtensorMap tmap_v, const PrefixArgs a,
+                         int tok_per_tile, float scale_log2) {
+  using C = SpCfg<D, NT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::BAR_OFF + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rb = blockIdx.x % a.n_rb, group = blockIdx.x / a.n_rb;
+
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+    *abort_flag = 0;
+  }
+  if (warp == 0 && lane < C::NBAR) {
+    mbar_init(bar(lane), lane == C::B_PF || lane == C::B_PF + 1 ? 128u : 1u);
+    fence_barrier_init();
+  }
+  if (warp == C::MMA_WARP) tc::alloc(smem_u32(tmem_slot), 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();     // q, the prefix's length, table and pages are earlier kernels' output
+  pdl_trigger();
+  const PrefixRun run = prefix_run(a, group);
+  if (blockIdx.x == 0 && threadIdx.x == 0)
+    (void)clamp_seq_len(__ldcg(a.len), a.max_blocks * kPage, &g_shared_err);
+
+  // A segment: key tiles [t0, t0 + nt) of KV head kvh. Every role walks the
+  // same segments.
+  struct Seg {
+    int kvh, t0, nt;
+  };
+  auto seg_at = [&](long long p) -> Seg {
+    Seg s;
+    s.kvh = static_cast<int>(p / run.tiles);
+    s.t0 = static_cast<int>(p % run.tiles);
+    s.nt = static_cast<int>(min(static_cast<long long>(run.tiles - s.t0), run.hi - p));
+    return s;
+  };
+  // Steps e = 0, 1, ... of a segment alternate between the streams: stream
+  // e & 1; key tile e (NT = 1) or e / 2 (NT = 2).
+  auto n_steps = [](const Seg& s) { return NT == 2 ? 2 * s.nt : s.nt; };
+  auto tile_of = [](int e) { return NT == 2 ? e >> 1 : e; };
+  auto n_of = [&](const Seg& s, int t) { return (n_steps(s) + 1 - t) >> 1; };
+
+  if (warp >= C::PRODUCER_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_CONTROL));
+    if (warp == C::PRODUCER_WARP) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        int it = 0, g0 = 0, q_issued = 0, k_issued = 0, v_issued = 0;
+        bool ok = true;
+        const int n_pages = (run.len + kPage - 1) / kPage;
+        for (long long p = run.lo; ok && p < run.hi; ++it) {
+          const Seg s = seg_at(p);
+          p += s.nt;
+          if (it > 0 && !wait_or_abort(bar(1), (it - 1) & 1, abort_flag)) break;
+          mbar_arrive_expect_tx(bar(0), NT * C::TILE);
+          for (int t = 0; t < NT; ++t)
+            for (int u = 0; u < C::SUBS; ++u)
+              tma_load_4d(sbase + C::Q_OFF + t * C::TILE + u * C::SUB_BYTES, &tmap_q, bar(0), u * 64,
+                          0, s.kvh, (rb * NT + t) * tok_per_tile);
+          q_issued = it + 1;
+          int pg[8];
+          auto pages = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int page = (s.t0 + j) * 8 + i;
+              int phys = -1;  // reads as zeros
+              if (page < n_pages) {
+                phys = __ldcg(a.table + page);
+                if (phys < 0 || phys >= a.num_blocks) {
+                  atomicOr(&g_shared_err, ATTN_DEVERR_BAD_PAGE);
+                  phys = -1;
+                }
+              }
+              pg[i] = phys;
+            }
+          };
+          auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t b) {
+#pragma unroll
+            for (int u = 0; u < C::SUBS; ++u)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                tma_load_4d(dst + u * C::SUB_BYTES + i * kPage * 128, map, b, u * 64, s.kvh, 0, pg[i]);
+          };
+          for (int j = 0; j < s.nt; ++j) {
+            const int g = g0 + j, sk = g % C::NSK, sv = g % C::NSV;
+            pages(j);
+            if (g >= C::NSK &&
+                !wait_or_abort(bar(C::B_KE + sk), (g / C::NSK - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar(C::B_KF + sk), C::TILE);
+            load(sbase + C::K_OFF + sk * C::TILE, &tmap_k, bar(C::B_KF + sk));
+            k_issued = g + 1;
+            if (g >= C::NSV &&
+                !wait_or_abort(bar(C::B_VE + sv), (g / C::NSV - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar(C::B_VF + sv), C::TILE);
+            load(sbase + C::V_OFF + sv * C::TILE, &tmap_v, bar(C::B_VF + sv));
+            v_issued = g + 1;
+          }
+          g0 += s.nt;
+        }
+        if (*abort_flag) {
+          // Drain: the newest load of each stage is the only one that can
+          // still be in flight. Bounded waits, error already recorded.
+          if (q_issued > 0) (void)mbar_wait(bar(0), (q_issued - 1) & 1, &g_shared_err);
+          for (int g = max(0, k_issued - C::NSK); g < k_issued; ++g)
+            (void)mbar_wait(bar(C::B_KF + g % C::NSK), (g / C::NSK) & 1, &g_shared_err);
+          for (int g = max(0, v_issued - C::NSV); g < v_issued; ++g)
+            (void)mbar_wait(bar(C::B_VF + g % C::NSV), (g / C::NSV) & 1, &g_shared_err);
+        }
+      }
+    } else if (warp == C::MMA_WARP) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t idS = tc::idesc_bf16_f32(kBM, kBN, false, false);
+      constexpr uint32_t idO = tc::idesc_bf16_f32(kBM, D, false, true);
+      const uint64_t dq0 = tc::sw128_desc(sbase + C::Q_OFF, 16, 1024);
+      const uint64_t dk0 = tc::sw128_desc(sbase + C::K_OFF, 16, 1024);
+      const uint64_t dv0 = tc::sw128_desc(sbase + C::V_OFF, C::SUB_BYTES, 1024);
+      auto issue_s = [&](int t, int st) {
+        const uint64_t da = dq0 + uint64_t(((NT == 2 ? t : 0) * C::TILE) >> 4);
+        const uint64_t db = dk0 + uint64_t((st * C::TILE) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off16 = ((kk >> 2) * C::SUB_BYTES + (kk & 3) * 32) >> 4;
+          tc::mma_ss_elect(tmem + t * 256, da + off16, db + off16, idS, kk > 0 ? 1u : 0u);
+        }
+        tc::commit_elect(bar(C::B_SF + t));
+      };
+      auto issue_pv = [&](int t, int st, bool acc) {
+        const uint64_t db = dv0 + uint64_t((st * C::TILE) >> 4);
+        const uint32_t dO = tmem + t * 256 + 128, aP = tmem + t * 256;
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk) {
+          const uint64_t b = db + uint64_t((kk * 16 * 128) >> 4);
+          tc::mma_ts_elect(dO, aP + kk * 8, b, idO, (acc || kk > 0) ? 1u : 0u);
+          tc::mma_ts_elect(dO, aP + 64 + kk * 8, b, idO, 1u);
+        }
+      };
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_or_abort(b, parity, abort_flag));
+      };
+      bool ok = true;
+      int it = 0, g0 = 0, base[2] = {0, 0};
+      for (long long p = run.lo; ok && p < run.hi; ++it) {
+        const Seg s = seg_at(p);
+        p += s.nt;
+        const int n = n_steps(s);
+        ok = wait(bar(0), it & 1);
+        // S of step e once its K tile is there (first use) and, behind it,
+        // what it frees.
+        auto s_step = [&](int e) {
+          const int g = g0 + tile_of(e), st = g % C::NSK;
+          if (!wait(bar(C::B_KF + st), (g / C::NSK) & 1)) return false;
+          tc::fence_after();
+          issue_s(e & 1, st);
+          if (NT == 1 || (e & 1)) tc::commit_elect(bar(C::B_KE + st));
+          if (e == n - 1) tc::commit_elect(bar(1));  // Q's last reader
+          return true;
+        };
+        if (ok) ok = s_step(0);
+        if (ok && n > 1) ok = s_step(1);
+        for (int e = 0; ok && e < n; ++e) {
+          const int t = e & 1, g = g0 + tile_of(e), sv = g % C::NSV;
+          ok = wait(bar(C::B_PF + t), (base[t] + (e >> 1)) & 1) &&
+               wait(bar(C::B_VF + sv), (g / C::NSV) & 1);
+          if (!ok) break;
+          tc::fence_after();
+          issue_pv(t, sv, e >= 2);
+          if (NT == 1 || t == 1) tc::commit_elect(bar(C::B_VE + sv));
+          if (e + 2 >= n) tc::commit_elect(bar(C::B_OF + t));  // the stream's last step
+          if (e + 2 < n) ok = s_step(e + 2);
+        }
+        g0 += s.nt;
+        base[0] += n_of(s, 0);
+        base[1] += n_of(s, 1);
+      }
+      tc::commit_elect(bar(C::B_DONE));
+      (void)__all_sync(0xffffffffu, mbar_wait(bar(C::B_DONE), 0, &g_shared_err));
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_SOFTMAX));
+    const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
+    const uint32_t tS = tmem + (uint32_t(wq * 32) << 16) + t * 256, tO = tS + 128;
+    const long long row = (static_cast<long long>(rb) * NT + (NT == 2 ? t : 0)) * kBM + r;
+    int g0 = 0, cnt = 0, ofin = 0;
+    bool ok = true;
+    for (long long p = run.lo; ok && p < run.hi;) {
+      const Seg s = seg_at(p);
+      const int touch = group - static_cast<int>((static_cast<long long>(s.kvh) * run.tiles) / run.per);
+      p += s.nt;
+      const int n = n_of(s, t);
+      float ref = kNone, l = 0.f;
+      for (int i = 0; i < n; ++i, ++cnt) {
+        const int j = NT == 2 ? i : 2 * i + t;  // key tile within the segment
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_SF + t), cnt & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const int lim = min(kBN, run.len - (s.t0 + j) * kBN);  // keys that exist
+        if (lim < kBN && (NT == 1 || t == 0) && (lim & 15)) {
+          // Slots of the last page past the last key hold whatever the cache
+          // holds (possibly NaN or inf). Their weights are 0, but 0 * NaN is
+          // not, so they are zeroed before the arrival that lets the MMA warp
+          // issue the tile's first P V.
+          const int g = g0 + j, sv = g % C::NSV;
+          if (wait_or_abort(bar(C::B_VF + sv), (g / C::NSV) & 1, abort_flag)) {
+            if ((r >> 3) < 16 - (lim & 15)) {
+              const uint32_t at = sbase + C::V_OFF + sv * C::TILE + (lim + (r >> 3)) * 128 + (r & 7) * 16;
+#pragma unroll
+              for (int u = 0; u < C::SUBS; ++u)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + u * C::SUB_BYTES),
+                             "r"(0u)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+        }
+        tc::fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
+        tc::wait_ld();
+        if (lim < kBN) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i2 = 0; i2 < 32; ++i2)
+              if (c * 32 + i2 >= lim) sr[c][i2] = __float_as_uint(-INFINITY);
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float cm = -INFINITY;
+#pragma unroll
+          for (int i2 = 0; i2 < 32; i2 += 2)
+            cm = max3(cm, __uint_as_float(sr[c][i2]), __uint_as_float(sr[c][i2 + 1]));
+          mx = fmaxf(mx, cm);
+        }
+        const float cand = mx * scale_log2;
+        float alpha = 1.f;
+        if (cand > ref + kSlack) {
+          alpha = ex2_approx(ref - cand);
+          l *= alpha;
+          ref = cand;
+        }
+        const bool rescale = i > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+        // P_hi (upper 16 bits of the weight) in columns 0-63, P_lo = bf16(p -
+        // P_hi) in columns 64-127.
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t hi[32], lo[32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i2 = 0; i2 < 16; ++i2) {
+              const float p0 = ex2_approx(fmaf(__uint_as_float(sr[2 * half + c][2 * i2]), scale_log2, -ref));
+              const float p1 =
+                  ex2_approx(fmaf(__uint_as_float(sr[2 * half + c][2 * i2 + 1]), scale_log2, -ref));
+              sum0 += p0;
+              sum1 += p1;
+              const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+              asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(hi[16 * c + i2]) : "r"(u0), "r"(u1));
+              lo[16 * c + i2] = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u),
+                                            p1 - __uint_as_float(u1 & 0xffff0000u));
+            }
+          tc::st32(tS + 32 * half, hi);
+          tc::st32(tS + 64 + 32 * half, lo);
+        }
+        l += sum0 + sum1;
+        if (rescale) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) tc::ld32(tO + c * 32, sr[c]);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+            for (int i2 = 0; i2 < 32; ++i2)
+              sr[c][i2] = __float_as_uint(__uint_as_float(sr[c][i2]) * alpha);
+            tc::st32(tO + c * 32, sr[c]);
+          }
+        }
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(bar(C::B_PF + t));
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_OF + t), ofin & 1, abort_flag))) break;
+        ++ofin;
+        tc::fence_after();
+      }
+      // The state of this row over the segment (m in log2 units).
+      const size_t slot =
+          ((static_cast<size_t>(s.kvh) * a.s_cap + touch) * a.n_rb + rb) * 2 + t;
+      const size_t pi = slot * kBM + r;
+      const bool store = row < a.rows && touch >= 0 && touch < a.s_cap;
+      ATTN_DCHECK(touch >= 0 && touch < a.s_cap, &g_shared_err);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        if (n > 0) {
+          tc::ld32(tO + c * 32, ov);
+          tc::wait_ld();
+        }
+        if (store && n > 0) {
+#pragma unroll
+          for (int i2 = 0; i2 < 8; ++i2)
+            *reinterpret_cast<uint4*>(a.o + pi * D + c * 32 + i2 * 4) =
+                make_uint4(ov[4 * i2], ov[4 * i2 + 1], ov[4 * i2 + 2], ov[4 * i2 + 3]);
+        }
+      }
+      if (store) {
+        a.m[pi] = ref;
+        a.l[pi] = l;
+      }
+      // O is read out before the next segment's first P V, which waits for
+      // this thread's next P.
+      tc::fence_before();
+      g0 += s.nt;
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == C::MMA_WARP) tc::dealloc(tmem, 512);
+}
+
+// One CTA per (row, query head): the prefix's states (per CTA that had a part
+// of the head's tiles, two with NT = 1), then the row's own, joined in that
+// order.
+struct MergeArgs {
+  PrefixArgs p;
+  int NT, h, g, upr;
+  const long long* plan;
+  const float *o_part, *m_part, *l_part, *o_row, *m_row, *l_row;
+  __nv_bfloat16* out;
+  float* lse;
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a) {
+  constexpr int VEC = D / 32, U = 4, NW = 4;
+  __shared__ float sm[NW], sl[NW], so[NW][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x / a.h, hq = blockIdx.x % a.h;
+  pdl_wait();
+  pdl_trigger();
+  const size_t row = static_cast<size_t>(b) * a.h + hq;
+  const int kvh = hq / a.g, hh = hq % a.g;
+  // Prefix states.
+  const PrefixRun run = prefix_run(a.p, 0);
+  int n_pre = 0;
+  size_t pre0 = 0, pre_step = 0;
+  int per_touch = 1;
+  if (run.tiles > 0) {
+    const long long s = static_cast<long long>(kvh) * run.tiles;
+    n_pre = static_cast<int>((s + run.tiles - 1) / run.per - s / run.per) + 1;
+    const long long pr = static_cast<long long>(b) * a.g + hh;  // row of the KV head
+    const int rb = static_cast<int>(pr / (a.NT * kBM)), rt = static_cast<int>(pr % (a.NT * kBM));
+    pre0 = ((static_cast<size_t>(kvh) * a.p.s_cap * a.p.n_rb + rb) * 2 + rt / kBM) * kBM + rt % kBM;
+    pre_step = static_cast<size_t>(a.p.n_rb) * 2 * kBM;
+    per_touch = a.NT == 1 ? 2 : 1;
+    n_pre *= per_touch;
+  }
+  // Own states.
+  const long long per = __ldcg(a.plan), at = __ldcg(a.plan + 1 + b);
+  const long long np = __ldcg(a.plan + 2 + b) - at;
+  int n_own = 0;
+  long long c0 = 0;
+  if (np > 0) {
+    const long long s = at * a.upr + kvh * np;
+    c0 = s / per;
+    n_own = static_cast<int>((s + np - 1) / per - c0) + 1;
+  }
+  const int n = n_pre + n_own;
+  float M = kNone, L = 0.f, acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  for (int base = warp; base < n; base += NW * U) {
+    float m[U], l[U], x[U][VEC];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = base + i * NW;
+      m[i] = kNone;
+      l[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[i][e] = 0.f;
+      if (j < n) {
+        const float *po, *pm, *pl;
+        size_t idx;
+        if (j < n_pre) {
+          po = a.p.o; pm = a.p.m; pl = a.p.l;
+          idx = pre0 + (j / per_touch) * pre_step + (j % per_touch) * kBM;
+        } else if (n_own == 1) {
+          po = a.o_row; pm = a.m_row; pl = a.l_row;
+          idx = row;
+        } else {
+          po = a.o_part; pm = a.m_part; pl = a.l_part;
+          idx = (2 * (c0 + j - n_pre) + (j == n_pre ? 1 : 0)) * 8 + hh;
+        }
+        l[i] = __ldcg(pl + idx);
+        const float mi = __ldcg(pm + idx);
+        if (mi != kNone) {  // (a stream without key tiles stores no O~)
+          m[i] = mi;
+          const float* src = po + idx * D + lane * VEC;
+          if constexpr (VEC == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+            x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+            x[i][0] = t.x; x[i][1] = t.y;
+          }
+        }
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int i = 0; i < U; ++i) Mn = fmaxf(Mn, m[i]);
+    const float sc = ex2_approx(M - Mn);
+    M = Mn;
+    L *= sc;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] *= sc;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const float w = ex2_approx(m[i] - Mn);
+      L = fmaf(w, l[i], L);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
+    }
+  }
+  if (lane == 0) {
+    sm[warp] = M;
+    sl[warp] = L;
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) so[warp][lane * VEC + e] = acc[e];
+  __syncthreads();
+  float Mt = kNone, Lt = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) Mt = fmaxf(Mt, sm[w]);
+#pragma unroll
+  for (int w = 0; w < NW; ++w) Lt = fmaf(sl[w], ex2_approx(sm[w] - Mt), Lt);
+  const bool empty = Lt == 0.f;
+  const float inv = empty ? 0.f : 1.f / Lt;
+  for (int e = threadIdx.x; e < D; e += 128) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v = fmaf(so[w][e], ex2_approx(sm[w] - Mt), v);
+    a.out[row * D + e] = __float2bfloat16(empty ? 0.f : v * inv);
+  }
+  if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = empty ? -INFINITY : Mt * kLn2 + logf(Lt);
+}
+
+template <int D, int NT>
+cudaError_t launch_prefix(const SharedArgs& s, const SharedPlan& pl, const PrefixArgs& a,
+                          cudaStream_t stream) {
+  using C = SpCfg<D, NT>;
+  const DecodeRunsArgs& r = s.own;
+  const int g = r.h / r.h_kv;
+  CUtensorMap tq, tk, tv;
+  const uint64_t qd[4] = {uint64_t(D), uint64_t(g), uint64_t(r.h_kv), uint64_t(r.B)};
+  const uint64_t qs[3] = {uint64_t(D) * 2, uint64_t(g) * D * 2, uint64_t(r.h) * D * 2};
+  // Rows (token, head): box of g heads x 128 / g tokens; map order (d, g, KV
+  // head, token).
+  const uint32_t qb[4] = {64u, uint32_t(g), 1u, uint32_t(kBM / g)};
+  const uint64_t dims[4] = {uint64_t(D), uint64_t(r.h_kv), uint64_t(kPage), uint64_t(r.num_blocks)};
+  const uint64_t strides[3] = {uint64_t(D) * 2, uint64_t(r.h_kv) * D * 2,
+                               uint64_t(kPage) * r.h_kv * D * 2};
+  const uint32_t box[4] = {64u, 1u, uint32_t(kPage), 1u};
+  if (encode_tensor_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(r.q), qd, qs, qb,
+                        CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tensor_map(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(r.k_cache), dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tensor_map(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(r.v_cache), dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  auto kern = shared_prefix_kernel<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(unsigned(pl.groups) * pl.n_rb), dim3(C::THREADS), size_t(C::SMEM), stream,
+                    tq, tk, tv, a, kBM / g, r.scale * kLog2e);
+}
+
+}  // namespace
+
+cudaError_t launch_shared(const SharedArgs& s, cudaStream_t stream) {
+  const DecodeRunsArgs& r = s.own;
+  const int g = r.h / r.h_kv;
+  const SharedPlan pl = shared_plan(r.B, g, r.h_kv);
+  PrefixArgs a;
+  a.table = s.prefix_table;
+  a.len = s.prefix_len;
+  a.max_blocks = s.max_prefix_blocks;
+  a.num_blocks = r.num_blocks;
+  a.h_kv = r.h_kv;
+  a.groups = pl.groups;
+  a.n_rb = pl.n_rb;
+  a.s_cap = pl.s_cap;
+  a.rows = r.B * g;
+  a.o = s.pre_o;
+  a.m = s.pre_m;
+  a.l = s.pre_l;
+  cudaError_t e;
+  if (r.d_h == 128)
+    e = pl.nt == 2 ? launch_prefix<128, 2>(s, pl, a, stream) : launch_prefix<128, 1>(s, pl, a, stream);
+  else
+    e = pl.nt == 2 ? launch_prefix<64, 2>(s, pl, a, stream) : launch_prefix<64, 1>(s, pl, a, stream);
+  if (e != cudaSuccess) return e;
+  e = launch_decode_runs_bf16(r, stream);
+  if (e != cudaSuccess) return e;
+  MergeArgs m;
+  m.p = a;
+  m.NT = pl.nt;
+  m.h = r.h;
+  m.g = g;
+  m.upr = r.h_kv;
+  m.plan = r.plan;
+  m.o_part = r.o_part;
+  m.m_part = r.m_part;
+  m.l_part = r.l_part;
+  m.o_row = r.o_row;
+  m.m_row = r.m_row;
+  m.l_row = r.l_row;
+  m.out = static_cast<__nv_bfloat16*>(r.o);
+  m.lse = r.lse;
+  auto merge = r.d_h == 128 ? shared_merge_kernel<128> : shared_merge_kernel<64>;
+  return launch_pdl(merge, dim3(unsigned(r.B) * r.h), dim3(128), 0, stream, m);
+}
+
+unsigned int shared_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_shared_err, sizeof(v), 0, cudaMemcpyDeviceToHost,
+                                            stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyToSymbolAsync(g_shared_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (st) *st = e;
+  return v;
+}
+
+}  // namespace attn

@@ -96,27 +96,27 @@ cudaError_t launch_cache_write(const CacheTokens& a, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheTokens& a, cudaStream_t stream);
 unsigned int cache8_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
 
-// decode_e4m3.cu -------------------------------------------------------------
-constexpr int kDecode8MaxCtas = 320;  // bounds the workspace; two CTAs on each of 160 SMs
+// decode_runs.cu -------------------------------------------------------------
+constexpr int kRunsMaxCtas = 320;  // bounds the workspace; two CTAs on each of 160 SMs
 // Plan (int64: pages per CTA, then the rows' first pages [B + 1]), then two
 // partial states per CTA: O~ [2 * 320, 8, d_h], m and l [2 * 320, 8].
-struct Decode8Layout {
+struct RunsLayout {
   size_t o_off, m_off, l_off, total;
 };
-inline Decode8Layout decode8_layout(int B, int d_h) {
-  Decode8Layout L;
+inline RunsLayout runs_layout(int B, int d_h) {
+  RunsLayout L;
   L.o_off = align256((size_t(B) + 2) * sizeof(long long));
-  L.m_off = L.o_off + size_t(2 * kDecode8MaxCtas) * 8 * d_h * sizeof(float);
-  L.l_off = L.m_off + size_t(2 * kDecode8MaxCtas) * 8 * sizeof(float);
-  L.total = L.l_off + size_t(2 * kDecode8MaxCtas) * 8 * sizeof(float);
+  L.m_off = L.o_off + size_t(2 * kRunsMaxCtas) * 8 * d_h * sizeof(float);
+  L.l_off = L.m_off + size_t(2 * kRunsMaxCtas) * 8 * sizeof(float);
+  L.total = L.l_off + size_t(2 * kRunsMaxCtas) * 8 * sizeof(float);
   return L;
 }
-struct Decode8Args {
+struct DecodeRunsArgs {
   const void* q;
-  const void* k_codes;
-  const void* v_codes;
-  const uint8_t* k_exp;
-  const uint8_t* v_exp;
+  const void* k_cache;
+  const void* v_cache;
+  const uint8_t* k_exp = nullptr;  // 8-bit cache only
+  const uint8_t* v_exp = nullptr;
   const int32_t* block_table;
   const int32_t* seq_lens;
   int B, h, h_kv, d_h, num_blocks, max_blocks;
@@ -125,11 +125,68 @@ struct Decode8Args {
   float* o_part;
   float* m_part;
   float* l_part;
-  void* o;
-  float* lse;
+  float* o_row = nullptr;  // bf16 only: states of units that no run border cuts
+  float* m_row = nullptr;
+  float* l_row = nullptr;
+  void* o = nullptr;       // 8-bit cache only
+  float* lse = nullptr;
 };
-cudaError_t launch_decode8(const Decode8Args& a, cudaStream_t stream);
-unsigned int decode8_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
+cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream);  // and its merge
+cudaError_t launch_decode_runs_bf16(const DecodeRunsArgs& a, cudaStream_t stream);  // states only
+unsigned int decode_runs_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
+
+// decode_shared.cu -----------------------------------------------------------
+// How the prefix's dense products are cut, from the shape alone: nt row tiles
+// of 128 (token, head) rows share a CTA's key tiles, n_rb such row blocks per
+// KV head, `groups` equal runs of the (KV head, key tile) pairs, each with one
+// CTA per row block; at most s_cap groups touch one head's tiles. `groups` is
+// the least number whose waves over the GPU's 152 SMs take within 5% of the
+// least time per key tile.
+struct SharedPlan {
+  int nt, n_rb, groups, s_cap;
+};
+inline SharedPlan shared_plan(int B, int g, int h_kv) {
+  constexpr int kSms = 152;
+  SharedPlan p;
+  const long long rows = static_cast<long long>(B) * g;
+  p.nt = rows > 128 ? 2 : 1;
+  p.n_rb = static_cast<int>((rows + p.nt * 128 - 1) / (p.nt * 128));
+  auto cost = [&](long long k) { return double((k * p.n_rb + kSms - 1) / kSms) / double(k); };
+  const int most = p.n_rb < 4 * kSms ? 4 * kSms / p.n_rb : 1;
+  double least = cost(1);
+  for (int k = 2; k <= most; ++k) least = cost(k) < least ? cost(k) : least;
+  p.groups = 1;
+  while (cost(p.groups) > 1.05 * least) ++p.groups;
+  p.s_cap = p.groups / h_kv + 2;
+  return p;
+}
+struct SharedLayout {
+  size_t row_o, row_m, row_l, pre_o, pre_m, pre_l, total;  // behind runs_layout
+};
+inline SharedLayout shared_layout(int B, int h, int h_kv, int d_h) {
+  const SharedPlan p = shared_plan(B, h / h_kv, h_kv);
+  const size_t rows = size_t(B) * h, pre = size_t(h_kv) * p.s_cap * p.n_rb * 256;
+  SharedLayout L;
+  L.row_o = align256(runs_layout(B, d_h).total);
+  L.row_m = L.row_o + align256(rows * d_h * sizeof(float));
+  L.row_l = L.row_m + align256(rows * sizeof(float));
+  L.pre_o = L.row_l + align256(rows * sizeof(float));
+  L.pre_m = L.pre_o + pre * d_h * sizeof(float);
+  L.pre_l = L.pre_m + pre * sizeof(float);
+  L.total = L.pre_l + pre * sizeof(float);
+  return L;
+}
+struct SharedArgs {
+  DecodeRunsArgs own;  // the rows' own pages, and the workspace of their states
+  const int32_t* prefix_table;
+  const int32_t* prefix_len;
+  int max_prefix_blocks;
+  float* pre_o;
+  float* pre_m;
+  float* pre_l;
+};
+cudaError_t launch_shared(const SharedArgs& a, cudaStream_t stream);
+unsigned int shared_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
 
 // prefill_simt.cu ----------------------------------------------------------
 cudaError_t launch_prefill_f32(const float* q, const float* k, const float* v, float* o,
