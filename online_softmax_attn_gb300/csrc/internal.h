@@ -139,9 +139,9 @@ unsigned int decode_runs_read_and_clear_error(cudaStream_t stream, cudaError_t* 
 // How the prefix's dense products are cut, from the shape alone: nt row tiles
 // of 128 (token, head) rows share a CTA's key tiles, n_rb such row blocks per
 // KV head, `groups` equal runs of the (KV head, key tile) pairs, each with one
-// CTA per row block; at most s_cap groups touch one head's tiles. `groups` is
-// the least number whose waves over the GPU's 152 SMs take within 5% of the
-// least time per key tile.
+// CTA per row block; at most s_cap groups touch one head's tiles. The CTAs fill
+// the least number of waves over the GPU's 152 SMs whose time per key tile is
+// within 5% of the best.
 struct SharedPlan {
   int nt, n_rb, groups, s_cap;
 };
@@ -151,12 +151,14 @@ inline SharedPlan shared_plan(int B, int g, int h_kv) {
   const long long rows = static_cast<long long>(B) * g;
   p.nt = rows > 128 ? 2 : 1;
   p.n_rb = static_cast<int>((rows + p.nt * 128 - 1) / (p.nt * 128));
-  auto cost = [&](long long k) { return double((k * p.n_rb + kSms - 1) / kSms) / double(k); };
-  const int most = p.n_rb < 4 * kSms ? 4 * kSms / p.n_rb : 1;
+  auto groups_of = [&](int waves) { return waves * kSms / p.n_rb; };
+  auto cost = [&](int waves) { return groups_of(waves) ? double(waves) / groups_of(waves) : 1e30; };
+  const int most = p.n_rb / kSms + 4;
   double least = cost(1);
-  for (int k = 2; k <= most; ++k) least = cost(k) < least ? cost(k) : least;
-  p.groups = 1;
-  while (cost(p.groups) > 1.05 * least) ++p.groups;
+  for (int w = 2; w <= most; ++w) least = cost(w) < least ? cost(w) : least;
+  int waves = 1;
+  while (cost(waves) > 1.05 * least) ++waves;
+  p.groups = groups_of(waves);
   p.s_cap = p.groups / h_kv + 2;
   return p;
 }
