@@ -33,13 +33,18 @@
 // a ring of NST stages, each one page of K and V (TMA, swizzled), for the 8-bit
 // cache with their exponents (16-byte bulk copies).
 //
-// Work split: the (row, KV head, head block) units' pages, laid end to end,
-// are cut into equal runs, one per CTA (two CTAs per SM), so any mix of lengths
-// fills the machine and the launch does not depend on the lengths. A CTA works
-// through its run unit by unit; its warps take the pages of a unit in turn and
-// join their states at the unit's end. A unit inside one run is finished there;
-// one cut by a run border leaves at most one partial state per CTA, which the
-// merge kernel joins in run order.
+// Work split: the (row, KV head, head block) units, laid end to end with a
+// weight of np + kUnit for np pages, are cut into equal runs, one per warp, so
+// any mix of lengths fills the machine and the launch does not depend on the
+// lengths. A warp works through its run unit by unit on its own (no barrier, no
+// join between units) and finishes each unit that lies inside its run. Units
+// cut by a run border are joined at the CTA's end: the warp that has a unit's
+// first part adds the following warps' parts from shared memory. What reaches
+// past the CTA leaves at most two partial states per CTA (a unit that began
+// before it, one that goes on behind it), which the merge kernel joins in run
+// order. (Splitting a unit over all warps of a CTA and joining at every unit's
+// end instead took 57 us for 64 rows of up to 1000 keys, 131 MB: rows of a few
+// pages cost a CTA as much as rows of hundreds.)
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "internal.h"
@@ -138,12 +143,15 @@ struct Cfg {
   static constexpr int EXP_BYTES = E8 ? 32 : 0;
   static constexpr int NREG = D / 4;                           // accumulators per lane
   static constexpr int JOIN_OFF = EXP_OFF + NW * NST * EXP_BYTES;
-  static constexpr int JOIN_BYTES = (NW / 2) * 32 * NREG * 4;
+  static constexpr int JOIN_BYTES = NW * 32 * NREG * 4;        // a warp's part of a cut unit
   static constexpr int ML_OFF = JOIN_OFF + JOIN_BYTES;         // [2][warp][8 heads] floats
   static constexpr int BAR_OFF = ML_OFF + 2 * NW * 8 * 4;
   static constexpr int SMEM = BAR_OFF + NW * NST * 8 + 1024;
   static_assert(NW * NST <= 32, "one lane initialises each barrier");
-  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+  // Static shared memory (kLenCache lengths and some words, 1248) and the driver's
+  // 1 KB come on top.
+  static constexpr int CTAS = E8 ? 2 : 1;  // per SM
+  static_assert(CTAS * (SMEM + 1248 + 1024) <= 228 * 1024, "shared memory of the CTAs on an SM");
 };
 
 // 16-byte chunk `c` of key row `r` of a page: the TMA's swizzle. 8-bit codes:
@@ -168,46 +176,57 @@ struct RunOut {
   float* lse;
 };
 
-// A CTA's run, unit by unit. Warp-uniform.
-struct Walk {
-  int b, u, len, np;   // row, unit within the row, its keys and pages
-  int lo, hi;          // pages of the unit that lie in the run
-  long long rem;       // pages of the run from lo on
-};
+constexpr int kUnit = kRunsUnit;  // a unit's query, state and epilogue, in pages
+constexpr int kMinRun = 1;      // least weight of a warp's run
+constexpr int kLenCache = 256;  // row lengths kept in shared memory
 
 struct Rows {
   const int32_t* seq_lens;
   int B, max_len, upr;  // upr: units per row
 };
 
+// A warp's run, unit by unit. Warp-uniform.
+struct Walk {
+  int b, u, len, np;   // row, unit within the row, its keys and pages
+  int lo, hi;          // pages of the unit that lie in the run
+  long long rem;       // weight of the run behind this unit
+};
+
 __device__ __forceinline__ int row_len(const Rows& rw, int b) {
   const int n = __ldcg(rw.seq_lens + b);
   return min(max(n, 0), rw.max_len);
 }
-
-__device__ __forceinline__ void walk_open(Walk& w) {
-  w.hi = static_cast<int>(min(static_cast<long long>(w.np), w.lo + w.rem));
+__device__ __forceinline__ int row_len(const Rows& rw, const int* cached, int b) {
+  return rw.B <= kLenCache ? cached[b] : row_len(rw, b);
+}
+__device__ __forceinline__ int row_weight(int len) {  // of one unit of the row
+  return len > 0 ? (len + kPage - 1) / kPage + kUnit : 0;
+}
+// Opens unit w.u of row w.b at weight `off` within it.
+__device__ __forceinline__ void walk_open(Walk& w, long long off) {
+  const long long take = min(w.np + kUnit - off, w.rem);
+  w.lo = static_cast<int>(max(off - kUnit, 0ll));
+  w.hi = static_cast<int>(max(off + take - kUnit, 0ll));
+  w.rem -= take;
 }
 // Next unit of the run; false at its end.
-__device__ __forceinline__ bool walk_next(Walk& w, const Rows& rw) {
-  w.rem -= w.hi - w.lo;
+__device__ __forceinline__ bool walk_next(Walk& w, const Rows& rw, const int* cached) {
   if (w.rem <= 0) return false;
-  w.lo = 0;
   if (++w.u == rw.upr) {
     w.u = 0;
     do {
       ++w.b;
       if (w.b >= rw.B) return false;
-      w.len = row_len(rw, w.b);
-      w.np = (w.len + kPage - 1) / kPage;
-    } while (w.np == 0);
+      w.len = row_len(rw, cached, w.b);
+    } while (w.len == 0);
+    w.np = (w.len + kPage - 1) / kPage;
   }
-  walk_open(w);
+  walk_open(w, 0);
   return true;
 }
 
 template <bool E8, int D, int NW, int NST>
-__global__ void __launch_bounds__(NW * 32, 2)
+__global__ void __launch_bounds__(NW * 32, Cfg<E8, D, NW, NST>::CTAS)
     decode_runs_kernel(const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const uint8_t* __restrict__ ks,
                    const uint8_t* __restrict__ vs, const __nv_bfloat16* __restrict__ q,
@@ -219,7 +238,7 @@ __global__ void __launch_bounds__(NW * 32, 2)
   const int gid = lane >> 2, tq = lane & 3;
   const int n_gb = rw.upr / h_kv;
 
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  extern __shared__ __align__(16) uint8_t smem_raw[];  // (1024 would pad the static part)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -227,8 +246,10 @@ __global__ void __launch_bounds__(NW * 32, 2)
   float* ms = reinterpret_cast<float*>(smem + C::ML_OFF);  // [warp][8]
   float* ls = ms + NW * 8;
   __shared__ long long s_warp[NW];
-  __shared__ long long s_start;
-  __shared__ int s_b;
+  __shared__ long long s_off[NW];  // weight between a warp's first row and its run
+  __shared__ int s_b[NW];          // its first row
+  __shared__ int s_kind[NW];       // its stored part: 0 none, 1 the unit goes on, 2 it ends
+  __shared__ int s_len[kLenCache];
 
   if (warp == 0) {
     if (lane < NW * NST) mbar_init(sbase + C::BAR_OFF + lane * 8, 1);
@@ -241,13 +262,16 @@ __global__ void __launch_bounds__(NW * 32, 2)
   pdl_wait();     // lengths, table, q and the cache are earlier kernels' output
   pdl_trigger();
 
-  // ---- the run: prefix sums of the rows' pages ----
+  // ---- the runs: prefix sums of the rows' weights (per unit) ----
   const int per_t = (rw.B + NW * 32 - 1) / (NW * 32);
   const int b0 = min(tid * per_t, rw.B), b1 = min(b0 + per_t, rw.B);
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
-    if (blockIdx.x == 0) (void)clamp_seq_len(__ldcg(rw.seq_lens + b), rw.max_len, &g_decode_runs_err);
-    sum += (row_len(rw, b) + kPage - 1) / kPage;
+    const int raw = __ldcg(rw.seq_lens + b);
+    const int len = min(max(raw, 0), rw.max_len);
+    if (blockIdx.x == 0 && raw != len) atomicOr(&g_decode_runs_err, ATTN_DEVERR_BAD_SEQ_LEN);
+    if (b < kLenCache) s_len[b] = len;
+    sum += row_weight(len);
   }
   long long incl = sum;
 #pragma unroll
@@ -256,6 +280,7 @@ __global__ void __launch_bounds__(NW * 32, 2)
     if (lane >= off) incl += y;
   }
   if (lane == 31) s_warp[warp] = incl;
+  if (tid < NW) s_kind[tid] = 0;
   __syncthreads();
   long long before = incl - sum, total = 0;
 #pragma unroll
@@ -264,53 +289,62 @@ __global__ void __launch_bounds__(NW * 32, 2)
     total += s_warp[w];
   }
   const long long all = total * rw.upr;
-  const long long per = max(static_cast<long long>(NW), (all + gridDim.x - 1) / gridDim.x);
-  const long long p0 = per * blockIdx.x;
+  const long long n_runs = static_cast<long long>(gridDim.x) * NW;
+  const long long per = max(static_cast<long long>(kMinRun), (all + n_runs - 1) / n_runs);
+  const long long cta0 = per * NW * blockIdx.x;
   if (blockIdx.x == 0) {  // for the merge
-    if (tid == 0) out.plan[0] = per;
+    if (tid == 0) out.plan[0] = per * NW;
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       out.plan[1 + b] = at;
-      at += (row_len(rw, b) + kPage - 1) / kPage;
+      at += row_weight(row_len(rw, s_len, b));
       if (b == rw.B - 1) out.plan[1 + rw.B] = at;
     }
   }
-  if (p0 >= all) return;
-  if (p0 >= before * rw.upr && p0 < (before + sum) * rw.upr) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int np = (row_len(rw, b) + kPage - 1) / kPage;
-      if (p0 < (at + np) * rw.upr) {
-        s_b = b;
-        s_start = at;
-        break;
+  if (cta0 >= all) return;
+  {
+    long long at = before * rw.upr;
+    const long long end = (before + sum) * rw.upr;
+    if (cta0 + per * NW > at && cta0 < end) {
+      for (int b = b0; b < b1; ++b) {
+        const long long next = at + static_cast<long long>(row_weight(row_len(rw, s_len, b))) * rw.upr;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const long long p = cta0 + per * w;
+          if (p >= at && p < next) {
+            s_b[w] = b;
+            s_off[w] = p - at;
+          }
+        }
+        at = next;
       }
-      at += np;
     }
   }
   __syncthreads();
+  const long long p0 = cta0 + per * warp;
+  bool have = p0 < all;
   Walk cw;
-  cw.b = s_b;
-  cw.len = row_len(rw, cw.b);
+  cw.b = have ? s_b[warp] : 0;
+  cw.len = row_len(rw, s_len, cw.b);
   cw.np = (cw.len + kPage - 1) / kPage;
+  cw.rem = have ? min(per, all - p0) : 0;
+  cw.u = 0;
   {
-    const long long off = p0 - s_start * rw.upr;
-    cw.u = static_cast<int>(off / cw.np);
-    cw.lo = static_cast<int>(off % cw.np);
+    const long long off = have ? s_off[warp] : 0;
+    const int wu = cw.np + kUnit;
+    cw.u = static_cast<int>(off / wu);
+    walk_open(cw, off % wu);
   }
-  cw.rem = min(per, all - p0);
-  walk_open(cw);
 
   // ---- producer state: the same walk, NST pages ahead ----
   Walk pw = cw;
-  bool more = true;
-  int pi = warp;  // page within the unit's part of the run
-  int bt = -1;    // table entries of this warp's pages, 32 at a time
+  bool more = have;
+  int pi = pw.lo;  // next page to issue
+  int bt = -1;     // table entries of the next pages, 32 at a time
   int issued = 0;
   auto load_bt = [&](int i) {
-    const int j = i + NW * lane;
-    bt = pw.lo + j < pw.hi
-             ? __ldcg(block_table + static_cast<size_t>(pw.b) * max_blocks + pw.lo + j)
+    bt = i + lane < pw.hi
+             ? __ldcg(block_table + static_cast<size_t>(pw.b) * max_blocks + i + lane)
              : -1;
   };
   const uint32_t ring = sbase + warp * NST * C::STAGE_BYTES;
@@ -318,12 +352,12 @@ __global__ void __launch_bounds__(NW * 32, 2)
   const uint32_t bars = sbase + C::BAR_OFF + warp * NST * 8;
   const uint64_t policy = policy_evict_first();
   int bt_i = 0;  // pages taken from bt
-  load_bt(pi);
+  if (more) load_bt(pi);
   // Issues this warp's next page, if there is one, into stage issued % NST.
   auto issue_next = [&]() {
-    while (more && pw.lo + pi >= pw.hi) {
-      more = walk_next(pw, rw);
-      pi = warp;
+    while (more && pi >= pw.hi) {
+      more = walk_next(pw, rw, s_len);
+      pi = pw.lo;
       bt_i = 0;
       if (more) load_bt(pi);
     }
@@ -360,15 +394,67 @@ __global__ void __launch_bounds__(NW * 32, 2)
     }
     ++issued;
     ++bt_i;
-    pi += NW;
+    ++pi;
   };
   for (int i = 0; i < NST; ++i) issue_next();
+
+  // A unit cut at the end of this warp's run stays in registers and is joined
+  // with the next warps' parts at the end of the CTA: 1 if it began in this
+  // run, 2 if it began before the CTA.
+  int own = 0, own_nh = 0;
+  size_t own_row = 0;
+  float m0 = kNone, m1 = kNone, l0 = 0.f, l1 = 0.f;
+  float acc[KS][4];
+
+  // Emits a state (accumulators relative to 2^m, in log2 units): into `slot`
+  // of the partial states, or (slot < 0) as the row's final output (8-bit) or
+  // its own-keys state (bf16).
+  auto emit = [&](long long slot, size_t row0, int nh) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int head = 2 * tq + e;
+      if (head >= nh) continue;
+      const float L = e ? l1 : l0, M = e ? m1 : m0;
+      const size_t row = row0 + head;
+      if (!ATTN_GUARD(row < static_cast<size_t>(rw.B) * h, &g_decode_runs_err)) continue;
+      if (E8 && slot < 0) {
+        const bool empty = L == 0.f;  // every logit -inf
+        const float inv = empty ? 0.f : 1.f / L;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          *reinterpret_cast<uint32_t*>(out.o + row * D + 16 * k + 2 * gid) =
+              empty ? 0u : pack_bf16x2(acc[k][e] * inv, acc[k][2 + e] * inv);
+        if (out.lse != nullptr && gid == 0) out.lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
+        continue;
+      }
+      const size_t at = slot < 0 ? row : static_cast<size_t>(slot) * 8 + head;
+      if (!ATTN_GUARD(slot < 0 || at < static_cast<size_t>(gridDim.x) * 16, &g_decode_runs_err)) continue;
+      float* so = (slot < 0 ? out.o_row : out.o_part) + at * D;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        if constexpr (E8) {
+          *reinterpret_cast<float2*>(so + 16 * k + 2 * gid) = make_float2(acc[k][e], acc[k][2 + e]);
+        } else {
+          so[16 * k + gid] = acc[k][e];
+          so[16 * k + 8 + gid] = acc[k][2 + e];
+        }
+      }
+      if (gid == 0) {
+        (slot < 0 ? out.m_row : out.m_part)[at] = M;
+        (slot < 0 ? out.l_row : out.l_part)[at] = L;
+      }
+    }
+  };
 
   int used = 0;      // stages consumed
   bool dead = false; // a wait gave up: results are void, the error word says so
   const int v_row = 8 * ((lane >> 3) & 1) + (lane & 7), v_dc = lane >> 4;
 
-  do {  // ---- one unit of the run ----
+  while (have) {  // ---- one unit of the run ----
+    if (cw.hi <= cw.lo) {  // the run ends before the unit's first page
+      have = walk_next(cw, rw, s_len);
+      continue;
+    }
     const int kvh = cw.u / n_gb, gb = cw.u % n_gb;
     const int hq0 = kvh * g + gb * 8;     // first query head of the block
     const int nh = min(8, g - gb * 8);    // heads in the block
@@ -432,21 +518,21 @@ __global__ void __launch_bounds__(NW * 32, 2)
 
     // State of heads 2tq, 2tq + 1: normaliser share l of this lane's keys
     // relative to 2^m, accumulators relative to 2^r.
-    float m0 = kNone, m1 = kNone, r0 = kNone, r1 = kNone, l0 = 0.f, l1 = 0.f;
-    float acc[KS][4];
+    m0 = m1 = kNone;
+    l0 = l1 = 0.f;
+    float r0 = kNone, r1 = kNone;
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
-    const int span = cw.hi - cw.lo;
-    for (int i = warp; i < span; i += NW) {
+    for (int i = cw.lo; i < cw.hi; ++i) {
       const int st = used % NST;
       if (!dead && !mbar_wait(bars + st * 8, (used / NST) & 1, &g_decode_runs_err)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       if (dead) break;
       const uint32_t kp = ring + st * C::STAGE_BYTES, vp = kp + C::PAGE_BYTES;
-      const int valid = min(kPage, cw.len - (cw.lo + i) * kPage);
+      const int valid = min(kPage, cw.len - i * kPage);
       if (valid < kPage) {
         // Slots past the row's end hold whatever the cache holds there (NaN
         // codes among it); their weights are 0, but 0 * NaN is not.
@@ -585,27 +671,15 @@ __global__ void __launch_bounds__(NW * 32, 2)
       issue_next();
     }
 
-    // ---- join the warps' states ----
+    // ---- the unit's state: normaliser over all keys, accumulators relative
+    // to 2^m ----
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, off);
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
-    if (gid == 0) {
-      ms[warp * 8 + 2 * tq] = m0;
-      ms[warp * 8 + 2 * tq + 1] = m1;
-      ls[warp * 8 + 2 * tq] = l0;
-      ls[warp * 8 + 2 * tq + 1] = l1;
-    }
-    __syncthreads();
-    float M0 = kNone, M1 = kNone;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      M0 = fmaxf(M0, ms[w * 8 + 2 * tq]);
-      M1 = fmaxf(M1, ms[w * 8 + 2 * tq + 1]);
-    }
-    {
-      const float f0 = ex2_approx((E8 ? r0 : m0) - M0), f1 = ex2_approx((E8 ? r1 : m1) - M1);
+    if constexpr (E8) {
+      const float f0 = ex2_approx(r0 - m0), f1 = ex2_approx(r1 - m1);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         acc[k][0] *= f0;
@@ -614,66 +688,53 @@ __global__ void __launch_bounds__(NW * 32, 2)
         acc[k][3] *= f1;
       }
     }
+    const size_t row0 = static_cast<size_t>(cw.b) * h + hq0;
+    const bool begins = cw.lo == 0, ends = cw.hi == cw.np;
+    if (begins && ends) {
+      emit(-1, row0, nh);
+    } else if (begins || (warp == 0 && !ends)) {  // the run's last unit
+      own = begins ? 1 : 2;
+      own_row = row0;
+      own_nh = nh;
+    } else if (warp == 0) {  // began before the CTA, ends here
+      emit(2ll * blockIdx.x, row0, nh);
+    } else {  // for the warp that has the unit's first part in this CTA
 #pragma unroll
-    for (int half = NW / 2; half >= 1; half >>= 1) {
-      if (warp >= half && warp < 2 * half) {
-#pragma unroll
-        for (int i = 0; i < C::NREG; ++i)
-          join[((warp - half) * C::NREG + i) * 32 + lane] = acc[i >> 2][i & 3];
+      for (int i = 0; i < C::NREG; ++i) join[(warp * C::NREG + i) * 32 + lane] = acc[i >> 2][i & 3];
+      if (gid == 0) {
+        ms[warp * 8 + 2 * tq] = m0;
+        ms[warp * 8 + 2 * tq + 1] = m1;
+        ls[warp * 8 + 2 * tq] = l0;
+        ls[warp * 8 + 2 * tq + 1] = l1;
       }
-      __syncthreads();
-      if (warp < half) {
-#pragma unroll
-        for (int i = 0; i < C::NREG; ++i) acc[i >> 2][i & 3] += join[(warp * C::NREG + i) * 32 + lane];
-      }
-      if (half > 1) __syncthreads();
+      if (lane == 0) s_kind[warp] = ends ? 2 : 1;
     }
-    if (warp == 0) {
-      float L0 = 0.f, L1 = 0.f;
+    have = walk_next(cw, rw, s_len);
+  }
+
+  // ---- join the units cut between this CTA's warps ----
+  __syncthreads();
+  if (own != 0) {
+    bool ends = false;
+    for (int w = warp + 1; w < NW && !ends; ++w) {
+      const int kind = s_kind[w];
+      if (kind == 0) break;  // (only after a wait that gave up)
+      ends = kind == 2;
+      const float n0 = ms[w * 8 + 2 * tq], n1 = ms[w * 8 + 2 * tq + 1];
+      const float M0 = fmaxf(m0, n0), M1 = fmaxf(m1, n1);
+      const float a0 = ex2_approx(m0 - M0), a1 = ex2_approx(m1 - M1);
+      const float c0 = ex2_approx(n0 - M0), c1 = ex2_approx(n1 - M1);
+      l0 = l0 * a0 + ls[w * 8 + 2 * tq] * c0;
+      l1 = l1 * a1 + ls[w * 8 + 2 * tq + 1] * c1;
+      m0 = M0;
+      m1 = M1;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        L0 = fmaf(ls[w * 8 + 2 * tq], ex2_approx(ms[w * 8 + 2 * tq] - M0), L0);
-        L1 = fmaf(ls[w * 8 + 2 * tq + 1], ex2_approx(ms[w * 8 + 2 * tq + 1] - M1), L1);
-      }
-      const bool whole = cw.lo == 0 && cw.hi == cw.np;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int head = 2 * tq + e;
-        if (head >= nh) continue;
-        const float L = e ? L1 : L0, M = e ? M1 : M0;
-        const size_t row = static_cast<size_t>(cw.b) * h + hq0 + head;
-        if (!ATTN_GUARD(row < static_cast<size_t>(rw.B) * h, &g_decode_runs_err)) continue;
-        if (E8 && whole) {
-          const bool empty = L == 0.f;  // every logit -inf
-          const float inv = empty ? 0.f : 1.f / L;
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-            *reinterpret_cast<uint32_t*>(out.o + row * D + 16 * k + 2 * gid) =
-                empty ? 0u : pack_bf16x2(acc[k][e] * inv, acc[k][2 + e] * inv);
-          if (out.lse != nullptr && gid == 0) out.lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
-          continue;
-        }
-        const size_t slot =
-            whole ? row : (2 * static_cast<size_t>(blockIdx.x) + (cw.lo == 0 ? 1 : 0)) * 8 + head;
-        if (!ATTN_GUARD(whole || slot < static_cast<size_t>(gridDim.x) * 16, &g_decode_runs_err)) continue;
-        float* so = (whole ? out.o_row : out.o_part) + slot * D;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          if constexpr (E8) {
-            *reinterpret_cast<float2*>(so + 16 * k + 2 * gid) = make_float2(acc[k][e], acc[k][2 + e]);
-          } else {
-            so[16 * k + gid] = acc[k][e];
-            so[16 * k + 8 + gid] = acc[k][2 + e];
-          }
-        }
-        if (gid == 0) {
-          (whole ? out.m_row : out.m_part)[slot] = M;
-          (whole ? out.l_row : out.l_part)[slot] = L;
-        }
-      }
+      for (int i = 0; i < C::NREG; ++i)
+        acc[i >> 2][i & 3] = acc[i >> 2][i & 3] * ((i & 1) ? a1 : a0) +
+                             join[(w * C::NREG + i) * 32 + lane] * ((i & 1) ? c1 : c0);
     }
-    __syncthreads();  // join, ms and ls are free for the next unit
-  } while (walk_next(cw, rw));
+    emit(own == 2 ? 2ll * blockIdx.x : ends ? -1ll : 2ll * blockIdx.x + 1, own_row, own_nh);
+  }
   if (dead) {
     // Bounded chance for the copies in flight to land before the CTA exits.
     for (int j = used; j < issued; ++j)
@@ -696,17 +757,17 @@ __global__ void __launch_bounds__(128)
   pdl_wait();
   pdl_trigger();
   const long long per = __ldcg(plan), at = __ldcg(plan + 1 + b);
-  const long long np = __ldcg(plan + 2 + b) - at;
+  const long long wu = __ldcg(plan + 2 + b) - at;  // weight of one unit: its pages + kUnit
   const size_t row = static_cast<size_t>(b) * h + hq;
-  if (np == 0) {
+  if (wu == 0) {
     for (int i = threadIdx.x; i < D / 2; i += 128) reinterpret_cast<uint32_t*>(o + row * D)[i] = 0u;
     if (lse != nullptr && threadIdx.x == 0) lse[row] = -INFINITY;
     return;
   }
   const int u = (hq / g) * n_gb + (hq % g) / 8;
-  const long long s = at * upr + u * np;
-  const long long c0 = s / per;
-  const int n = static_cast<int>((s + np - 1) / per - c0) + 1;
+  const long long s = at * upr + u * wu;
+  const long long c0 = (s + kUnit) / per;  // CTAs of the unit's first and last page
+  const int n = static_cast<int>((s + wu - 1) / per - c0) + 1;
   if (n == 1) return;  // finished by its CTA
   float M = kNone, L = 0.f, acc[VEC];
 #pragma unroll
@@ -803,7 +864,7 @@ cudaError_t launch_cfg(const DecodeRunsArgs& a, int sms, cudaStream_t stream) {
   auto kern = decode_runs_kernel<E8, D, NW, NST>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * sms < kRunsMaxCtas ? 2 * sms : kRunsMaxCtas;
+  const int grid = C::CTAS * sms < kRunsMaxCtas ? C::CTAS * sms : kRunsMaxCtas;
   const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
   const Rows rw{a.seq_lens, a.B, a.max_blocks * kPage, a.h_kv * n_gb};
   const RunOut out{a.plan,  a.o_part, a.m_part, a.l_part, a.o_row,
@@ -841,8 +902,8 @@ cudaError_t launch_decode_runs_bf16(const DecodeRunsArgs& a, cudaStream_t stream
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  return a.d_h == 128 ? launch_cfg<false, 128, 4, 3>(a, sms, stream)
-                      : launch_cfg<false, 64, 4, 6>(a, sms, stream);
+  return a.d_h == 128 ? launch_cfg<false, 128, 8, 3>(a, sms, stream)
+                      : launch_cfg<false, 64, 8, 4>(a, sms, stream);
 }
 
 unsigned int decode_runs_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {

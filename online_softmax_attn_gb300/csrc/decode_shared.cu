@@ -508,13 +508,13 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a) {
   }
   // Own states.
   const long long per = __ldcg(a.plan), at = __ldcg(a.plan + 1 + b);
-  const long long np = __ldcg(a.plan + 2 + b) - at;
+  const long long wu = __ldcg(a.plan + 2 + b) - at;  // weight of one unit
   int n_own = 0;
   long long c0 = 0;
-  if (np > 0) {
-    const long long s = at * a.upr + kvh * np;
-    c0 = s / per;
-    n_own = static_cast<int>((s + np - 1) / per - c0) + 1;
+  if (wu > 0) {
+    const long long s = at * a.upr + kvh * wu;
+    c0 = (s + kRunsUnit) / per;
+    n_own = static_cast<int>((s + wu - 1) / per - c0) + 1;
   }
   const int n = n_pre + n_own;
   float M = kNone, L = 0.f, acc[VEC];

@@ -98,7 +98,8 @@ unsigned int cache8_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
 
 // decode_runs.cu -------------------------------------------------------------
 constexpr int kRunsMaxCtas = 320;  // bounds the workspace; two CTAs on each of 160 SMs
-// Plan (int64: pages per CTA, then the rows' first pages [B + 1]), then two
+constexpr int kRunsUnit = 1;       // weight of a unit beside its pages (decode_runs.cu)
+// Plan (int64: weight per CTA, then the rows' weights' prefix sums [B + 1]), then two
 // partial states per CTA: O~ [2 * 320, 8, d_h], m and l [2 * 320, 8].
 struct RunsLayout {
   size_t o_off, m_off, l_off, total;
