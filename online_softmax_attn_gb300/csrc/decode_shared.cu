@@ -28,9 +28,13 @@
 // same tiles at the same time, so the L2 serves all but one of them. A run that
 // crosses a head border gives two states.
 //
-// P = P_hi + P_lo in bf16 (two MMAs), as for the prefill's V tiles that stay
-// bf16. The reference of the weights moves only when a row's maximum passes it
-// by kSlack.
+// P V is one fp16 MMA chain where V's tile fits fp16: two warps convert each V
+// tile in shared memory as it lands (bf16 has 8 significant bits, so values in
+// [2^-14, 2^16) convert exactly and smaller ones within 2^-25) and zero the
+// slots past the last key. A tile holding a magnitude of 2^16 or more, inf or
+// NaN, or nothing above 2^-6 (whose small values would lose bits) is loaded
+// again and stays bf16, with P = P_hi + P_lo in two MMAs. With the two-term P
+// everywhere the prefix of 256 rows over 32768 keys took 205 us.
 #include "common.cuh"
 #include "internal.h"
 #include "pdl.cuh"
@@ -45,7 +49,10 @@ namespace {
 constexpr int kPage = 16;
 constexpr int kBM = 128, kBN = 128;
 constexpr float kNone = -1e30f;  // reference before the first key
-constexpr float kSlack = 8.0f;
+// Weights reach at most 2^15 (fp16's largest finite number is 65504): a row's
+// reference is set kTop below a new maximum and moves when a score passes it by
+// kTop + kSlack. Weights down to 2^-27 of the largest are normal fp16 numbers.
+constexpr float kTop = 13.0f, kSlack = 2.0f;
 
 template <int D, int NT>
 struct SpCfg {
@@ -58,16 +65,18 @@ struct SpCfg {
   static constexpr int K_OFF = Q_OFF + NT * TILE;
   static constexpr int V_OFF = K_OFF + NSK * TILE;
   static constexpr int BAR_OFF = V_OFF + NSV * TILE;
-  // q_full, q_empty, k_full[], k_empty[], v_full[], v_empty[], s_full[2],
+  // q_full, q_empty, k_full[], k_empty[], v_full[] (landed), v_ready[]
+  // (converted), v_empty[], v_again (a tile loaded once more), s_full[2],
   // p_full[2], o_final[2], mma_done
-  static constexpr int B_KF = 2, B_KE = B_KF + NSK, B_VF = B_KE + NSK, B_VE = B_VF + NSV,
-                       B_SF = B_VE + NSV, B_PF = B_SF + 2, B_OF = B_PF + 2, B_DONE = B_OF + 2,
-                       NBAR = B_DONE + 1;
+  static constexpr int B_KF = 2, B_KE = B_KF + NSK, B_VF = B_KE + NSK, B_VR = B_VF + NSV,
+                       B_VE = B_VR + NSV, B_VA = B_VE + NSV, B_SF = B_VA + 1, B_PF = B_SF + 2,
+                       B_OF = B_PF + 2, B_DONE = B_OF + 2, NBAR = B_DONE + 1;
   static_assert(NBAR <= 32, "one warp initialises the barriers, one per lane");
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr int SMEM = MISC_OFF + 16 + 1024;
+  static constexpr int SMEM = MISC_OFF + 32 + 1024;  // tensor-memory slot, abort flag, wide[NSV]
   static constexpr int THREADS = 384;  // two softmax warpgroups, one of control
-  static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;
+  static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, CONV_WARP = 10;  // to 11
+  static constexpr int CONV_THREADS = 64;
   static constexpr int REG_LAUNCH = 168, REG_CONTROL = 120, REG_SOFTMAX = 192;
   static_assert(2 * 128 * REG_SOFTMAX + 128 * REG_CONTROL <= THREADS * REG_LAUNCH,
                 "register split exceeds the launch allocation");
@@ -95,6 +104,66 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity,
       return false;
     }
   }
+}
+
+// Packed fp32 pairs.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Weights of a key tile whose V stays bf16: P_hi (upper 16 bits) in columns
+// 0-63 of the S tile, P_lo = bf16(p - P_hi) in columns 64-127. Reads the S tile
+// again (keys from lim on masked) and returns the weights' sum. Such tiles are
+// rare, so this stays out of line. Warp-collective.
+__device__ __noinline__ float two_term_weights(uint32_t tS, int lim, float scale_log2, float ref) {
+  float sum0 = 0.f, sum1 = 0.f;
+  uint32_t sr[4][32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
+  tc::wait_ld();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t hi[32], lo[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int key = 64 * half + 2 * i;
+      float x0 = __uint_as_float(sr[key >> 5][key & 31]);
+      float x1 = __uint_as_float(sr[key >> 5][(key & 31) + 1]);
+      if (key >= lim) x0 = -INFINITY;
+      if (key + 1 >= lim) x1 = -INFINITY;
+      const float p0 = ex2_approx(fmaf(x0, scale_log2, -ref));
+      const float p1 = ex2_approx(fmaf(x1, scale_log2, -ref));
+      sum0 += p0;
+      sum1 += p1;
+      const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+      asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(hi[i]) : "r"(u0), "r"(u1));
+      lo[i] = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u),
+                          p1 - __uint_as_float(u1 & 0xffff0000u));
+    }
+    tc::st32(tS + 32 * half, hi);
+    tc::st32(tS + 64 + 32 * half, lo);
+  }
+  return sum0 + sum1;
 }
 
 struct PrefixArgs {
@@ -134,6 +203,7 @@ __global__ void __launch_bounds__(384, 1)
   auto bar = [&](int i) { return sbase + C::BAR_OFF + 8 * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  volatile int* wide = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);  // [NSV]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rb = blockIdx.x % a.n_rb, group = blockIdx.x / a.n_rb;
 
@@ -144,7 +214,9 @@ __global__ void __launch_bounds__(384, 1)
     *abort_flag = 0;
   }
   if (warp == 0 && lane < C::NBAR) {
-    mbar_init(bar(lane), lane == C::B_PF || lane == C::B_PF + 1 ? 128u : 1u);
+    mbar_init(bar(lane), lane == C::B_PF || lane == C::B_PF + 1          ? 128u
+                         : lane >= C::B_VR && lane < C::B_VR + C::NSV ? uint32_t(C::CONV_THREADS)
+                                                                      : 1u);
     fence_barrier_init();
   }
   if (warp == C::MMA_WARP) tc::alloc(smem_u32(tmem_slot), 512);
@@ -175,79 +247,78 @@ __global__ void __launch_bounds__(384, 1)
   auto n_steps = [](const Seg& s) { return NT == 2 ? 2 * s.nt : s.nt; };
   auto tile_of = [](int e) { return NT == 2 ? e >> 1 : e; };
   auto n_of = [&](const Seg& s, int t) { return (n_steps(s) + 1 - t) >> 1; };
+  const int n_pages = (run.len + kPage - 1) / kPage;
+  // Table entries of the 32 pages from `page` on, one per lane; -1 (reads as
+  // zeros) behind the prefix.
+  auto entries = [&](int page) { return page + lane < n_pages ? __ldcg(a.table + page + lane) : -1; };
+  // Key tile of 8 pages into dst: lane i < 8 * SUBS issues the box of page
+  // i % 8, half i / 8 (one thread issuing all of them took 90 cycles a box).
+  // `ent` holds the tile's entries in lanes at .. at + 7. Whole warp.
+  auto load_tile = [&](uint32_t dst, const CUtensorMap* map, uint32_t b, int kvh, int ent, int at,
+                       int page0) {
+    int phys = __shfl_sync(0xffffffffu, ent, at + (lane & 7));
+    if (phys < 0 || phys >= a.num_blocks) {
+      if (page0 + (lane & 7) < n_pages) atomicOr(&g_shared_err, ATTN_DEVERR_BAD_PAGE);
+      phys = -1;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(b, C::TILE);
+    if (lane < 8 * C::SUBS)
+      tma_load_4d(dst + (lane >> 3) * C::SUB_BYTES + (lane & 7) * kPage * 128, map, b,
+                  (lane >> 3) * 64, kvh, 0, phys);
+    __syncwarp();
+  };
 
   if (warp >= C::PRODUCER_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_CONTROL));
     if (warp == C::PRODUCER_WARP) {
       // ---------------------------------------------------------- producer
-      if (lane == 0) {
-        int it = 0, g0 = 0, q_issued = 0, k_issued = 0, v_issued = 0;
-        bool ok = true;
-        const int n_pages = (run.len + kPage - 1) / kPage;
-        for (long long p = run.lo; ok && p < run.hi; ++it) {
-          const Seg s = seg_at(p);
-          p += s.nt;
-          if (it > 0 && !wait_or_abort(bar(1), (it - 1) & 1, abort_flag)) break;
-          mbar_arrive_expect_tx(bar(0), NT * C::TILE);
-          for (int t = 0; t < NT; ++t)
-            for (int u = 0; u < C::SUBS; ++u)
-              tma_load_4d(sbase + C::Q_OFF + t * C::TILE + u * C::SUB_BYTES, &tmap_q, bar(0), u * 64,
-                          0, s.kvh, (rb * NT + t) * tok_per_tile);
-          q_issued = it + 1;
-          int pg[8];
-          auto pages = [&](int j) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int page = (s.t0 + j) * 8 + i;
-              int phys = -1;  // reads as zeros
-              if (page < n_pages) {
-                phys = __ldcg(a.table + page);
-                if (phys < 0 || phys >= a.num_blocks) {
-                  atomicOr(&g_shared_err, ATTN_DEVERR_BAD_PAGE);
-                  phys = -1;
-                }
-              }
-              pg[i] = phys;
-            }
-          };
-          auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t b) {
-#pragma unroll
-            for (int u = 0; u < C::SUBS; ++u)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                tma_load_4d(dst + u * C::SUB_BYTES + i * kPage * 128, map, b, u * 64, s.kvh, 0, pg[i]);
-          };
-          for (int j = 0; j < s.nt; ++j) {
-            const int g = g0 + j, sk = g % C::NSK, sv = g % C::NSV;
-            pages(j);
-            if (g >= C::NSK &&
-                !wait_or_abort(bar(C::B_KE + sk), (g / C::NSK - 1) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(bar(C::B_KF + sk), C::TILE);
-            load(sbase + C::K_OFF + sk * C::TILE, &tmap_k, bar(C::B_KF + sk));
-            k_issued = g + 1;
-            if (g >= C::NSV &&
-                !wait_or_abort(bar(C::B_VE + sv), (g / C::NSV - 1) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(bar(C::B_VF + sv), C::TILE);
-            load(sbase + C::V_OFF + sv * C::TILE, &tmap_v, bar(C::B_VF + sv));
-            v_issued = g + 1;
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_or_abort(b, parity, abort_flag));
+      };
+      int it = 0, g0 = 0, q_issued = 0, k_issued = 0, v_issued = 0;
+      bool ok = true;
+      for (long long p = run.lo; ok && p < run.hi; ++it) {
+        const Seg s = seg_at(p);
+        p += s.nt;
+        int ent = entries(s.t0 * 8), next = -1;
+        if (it > 0 && !wait(bar(1), (it - 1) & 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(0), NT * C::TILE);
+        if (lane < NT * C::SUBS)
+          tma_load_4d(sbase + C::Q_OFF + lane * C::SUB_BYTES, &tmap_q, bar(0), (lane % C::SUBS) * 64, 0,
+                      s.kvh, (rb * NT + lane / C::SUBS) * tok_per_tile);
+        __syncwarp();
+        q_issued = it + 1;
+        for (int j = 0; j < s.nt; ++j) {
+          const int g = g0 + j, sk = g % C::NSK, sv = g % C::NSV, page0 = (s.t0 + j) * 8;
+          if ((j & 3) == 0) {  // entries four tiles at a time, fetched four tiles ahead
+            if (j > 0) ent = next;
+            next = entries(page0 + 32);
           }
-          g0 += s.nt;
+          if (g >= C::NSK && !wait(bar(C::B_KE + sk), (g / C::NSK - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          load_tile(sbase + C::K_OFF + sk * C::TILE, &tmap_k, bar(C::B_KF + sk), s.kvh, ent, (j & 3) * 8,
+                    page0);
+          k_issued = g + 1;
+          if (g >= C::NSV && !wait(bar(C::B_VE + sv), (g / C::NSV - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          load_tile(sbase + C::V_OFF + sv * C::TILE, &tmap_v, bar(C::B_VF + sv), s.kvh, ent, (j & 3) * 8,
+                    page0);
+          v_issued = g + 1;
         }
-        if (*abort_flag) {
-          // Drain: the newest load of each stage is the only one that can
-          // still be in flight. Bounded waits, error already recorded.
-          if (q_issued > 0) (void)mbar_wait(bar(0), (q_issued - 1) & 1, &g_shared_err);
-          for (int g = max(0, k_issued - C::NSK); g < k_issued; ++g)
-            (void)mbar_wait(bar(C::B_KF + g % C::NSK), (g / C::NSK) & 1, &g_shared_err);
-          for (int g = max(0, v_issued - C::NSV); g < v_issued; ++g)
-            (void)mbar_wait(bar(C::B_VF + g % C::NSV), (g / C::NSV) & 1, &g_shared_err);
-        }
+        g0 += s.nt;
+      }
+      if (*abort_flag) {
+        // Drain: the newest load of each stage is the only one that can still
+        // be in flight. Bounded waits, error already recorded.
+        if (q_issued > 0) (void)mbar_wait(bar(0), (q_issued - 1) & 1, &g_shared_err);
+        for (int g = max(0, k_issued - C::NSK); g < k_issued; ++g)
+          (void)mbar_wait(bar(C::B_KF + g % C::NSK), (g / C::NSK) & 1, &g_shared_err);
+        for (int g = max(0, v_issued - C::NSV); g < v_issued; ++g)
+          (void)mbar_wait(bar(C::B_VF + g % C::NSV), (g / C::NSV) & 1, &g_shared_err);
       }
     } else if (warp == C::MMA_WARP) {
       // -------------------------------------------------------- MMA issuer
@@ -266,14 +337,22 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc::commit_elect(bar(C::B_SF + t));
       };
-      auto issue_pv = [&](int t, int st, bool acc) {
+      constexpr uint32_t idO16 = tc::idesc_f16_f32(kBM, D, false, true);
+      auto issue_pv = [&](int t, int st, bool acc, bool two) {
         const uint64_t db = dv0 + uint64_t((st * C::TILE) >> 4);
         const uint32_t dO = tmem + t * 256 + 128, aP = tmem + t * 256;
+        if (!two) {
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk) {
-          const uint64_t b = db + uint64_t((kk * 16 * 128) >> 4);
-          tc::mma_ts_elect(dO, aP + kk * 8, b, idO, (acc || kk > 0) ? 1u : 0u);
-          tc::mma_ts_elect(dO, aP + 64 + kk * 8, b, idO, 1u);
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            tc::mma_ts_elect(dO, aP + kk * 8, db + uint64_t((kk * 16 * 128) >> 4), idO16,
+                             (acc || kk > 0) ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk) {
+            const uint64_t b = db + uint64_t((kk * 16 * 128) >> 4);
+            tc::mma_ts_elect(dO, aP + kk * 8, b, idO, (acc || kk > 0) ? 1u : 0u);
+            tc::mma_ts_elect(dO, aP + 64 + kk * 8, b, idO, 1u);
+          }
         }
       };
       auto wait = [&](uint32_t b, uint32_t parity) {
@@ -302,10 +381,10 @@ __global__ void __launch_bounds__(384, 1)
         for (int e = 0; ok && e < n; ++e) {
           const int t = e & 1, g = g0 + tile_of(e), sv = g % C::NSV;
           ok = wait(bar(C::B_PF + t), (base[t] + (e >> 1)) & 1) &&
-               wait(bar(C::B_VF + sv), (g / C::NSV) & 1);
+               wait(bar(C::B_VR + sv), (g / C::NSV) & 1);
           if (!ok) break;
           tc::fence_after();
-          issue_pv(t, sv, e >= 2);
+          issue_pv(t, sv, e >= 2, __shfl_sync(0xffffffffu, wide[sv], 0) != 0);
           if (NT == 1 || t == 1) tc::commit_elect(bar(C::B_VE + sv));
           if (e + 2 >= n) tc::commit_elect(bar(C::B_OF + t));  // the stream's last step
           if (e + 2 < n) ok = s_step(e + 2);
@@ -316,6 +395,115 @@ __global__ void __launch_bounds__(384, 1)
       }
       tc::commit_elect(bar(C::B_DONE));
       (void)__all_sync(0xffffffffu, mbar_wait(bar(C::B_DONE), 0, &g_shared_err));
+    } else {
+      // -------------------------------------------------------- V to fp16
+      const int ct = threadIdx.x - C::CONV_WARP * 32;  // 0 .. 63
+      constexpr int CHUNKS = C::TILE / 16, PER = CHUNKS / C::CONV_THREADS, UN = 8;
+      int g0 = 0, again = 0;
+      bool ok = true;
+      for (long long p = run.lo; ok && p < run.hi;) {
+        const Seg s = seg_at(p);
+        p += s.nt;
+        for (int j = 0; j < s.nt; ++j) {
+          const int g = g0 + j, sv = g % C::NSV;
+          if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_VF + sv), (g / C::NSV) & 1, abort_flag)))
+            ok = false;
+          const uint32_t base = sbase + C::V_OFF + sv * C::TILE + ct * 16;
+          const int lim = min(kBN, run.len - (s.t0 + j) * kBN);  // keys that exist
+          // 0 * h sums to NaN once a number does not fit fp16 (inf or NaN there);
+          // the sum of squares reaches 2^-12 where a magnitude reaches 2^-6.
+          __half2 bad = __floats2half2_rn(0.f, 0.f), big = bad;
+          if (ok) {
+#pragma unroll 1
+            for (int i0 = 0; i0 < PER; i0 += UN) {
+              uint4 x[UN];
+#pragma unroll
+              for (int u = 0; u < UN; ++u)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[u].x), "=r"(x[u].y), "=r"(x[u].z), "=r"(x[u].w)
+                             : "r"(base + (i0 + u) * (C::CONV_THREADS * 16)));
+#pragma unroll
+              for (int u = 0; u < UN; ++u) {
+                // Chunk index (i0 + u) * 64 + ct, 8 chunks per 128-byte row.
+                const int row = (((i0 + u) * C::CONV_THREADS + ct) >> 3) & (kBN - 1);
+                if (row >= lim) x[u] = make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                __half2 hh[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  hh[k] = __floats2half2_rn(bf16lo(w[k]), bf16hi(w[k]));
+                  bad = __hfma2(hh[k], __floats2half2_rn(0.f, 0.f), bad);
+                  big = __hfma2(hh[k], hh[k], big);
+                }
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 base + (i0 + u) * (C::CONV_THREADS * 16)),
+                             "r"(*reinterpret_cast<uint32_t*>(&hh[0])),
+                             "r"(*reinterpret_cast<uint32_t*>(&hh[1])),
+                             "r"(*reinterpret_cast<uint32_t*>(&hh[2])),
+                             "r"(*reinterpret_cast<uint32_t*>(&hh[3]))
+                             : "memory");
+              }
+            }
+          }
+          const bool too_big = !(__low2float(bad) == 0.f && __high2float(bad) == 0.f);
+          const bool fits = __low2float(big) >= 0x1p-12f || __high2float(big) >= 0x1p-12f;
+          int some_big, some_ok;
+          asm volatile(
+              "{\n\t.reg .pred p, q;\n\t"
+              "setp.ne.s32 p, %2, 0;\n\t"
+              "barrier.cta.red.or.pred q, 1, 64, p;\n\t"
+              "selp.s32 %0, 1, 0, q;\n\t"
+              "setp.ne.s32 p, %3, 0;\n\t"
+              "barrier.cta.red.or.pred q, 1, 64, p;\n\t"
+              "selp.s32 %1, 1, 0, q;\n\t}"
+              : "=r"(some_big), "=r"(some_ok)
+              : "r"(too_big ? 1 : 0), "r"(fits ? 1 : 0)
+              : "memory");
+          const int two = some_big | (some_ok ^ 1);
+          if (two) {
+            // The tile as it was. The generic writes above come before the
+            // copy engine's.
+            fence_proxy_async_smem();
+            asm volatile("barrier.cta.sync 1, 64;" ::: "memory");
+            if (warp == C::CONV_WARP && __all_sync(0xffffffffu, ok)) {
+              const int page0 = (s.t0 + j) * 8;
+              load_tile(sbase + C::V_OFF + sv * C::TILE, &tmap_v, bar(C::B_VA), s.kvh, entries(page0), 0,
+                        page0);
+            }
+            if (ok && !__all_sync(0xffffffffu, wait_or_abort(bar(C::B_VA), again & 1, abort_flag))) {
+              ok = false;
+              (void)mbar_wait(bar(C::B_VA), again & 1, &g_shared_err);  // bounded: let it land
+            }
+            ++again;
+            // Slots past the last key hold whatever the cache holds (possibly
+            // NaN or inf); their weights are 0, but 0 * NaN is not.
+            if (lim < kBN)
+              for (int c = lim * 8 + ct; c < kBN * 8; c += C::CONV_THREADS)
+#pragma unroll
+                for (int u = 0; u < C::SUBS; ++u)
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                   sbase + C::V_OFF + sv * C::TILE + u * C::SUB_BYTES + c * 16),
+                               "r"(0u)
+                               : "memory");
+          }
+          if (ct == 0) wide[sv] = two;
+          fence_proxy_async_smem();  // the MMA reads V through the async proxy
+          mbar_arrive(bar(C::B_VR + sv));
+          // Agreed by both warps before either goes on (an abort ends both).
+          int all_ok;
+          asm volatile(
+              "{\n\t.reg .pred p, q;\n\t"
+              "setp.ne.s32 p, %1, 0;\n\t"
+              "barrier.cta.red.and.pred q, 1, 64, p;\n\t"
+              "selp.s32 %0, 1, 0, q;\n\t}"
+              : "=r"(all_ok)
+              : "r"(ok ? 1 : 0)
+              : "memory");
+          ok = all_ok != 0;
+          if (!ok) break;
+        }
+        g0 += s.nt;
+      }
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -338,25 +526,6 @@ __global__ void __launch_bounds__(384, 1)
           break;
         }
         const int lim = min(kBN, run.len - (s.t0 + j) * kBN);  // keys that exist
-        if (lim < kBN && (NT == 1 || t == 0) && (lim & 15)) {
-          // Slots of the last page past the last key hold whatever the cache
-          // holds (possibly NaN or inf). Their weights are 0, but 0 * NaN is
-          // not, so they are zeroed before the arrival that lets the MMA warp
-          // issue the tile's first P V.
-          const int g = g0 + j, sv = g % C::NSV;
-          if (wait_or_abort(bar(C::B_VF + sv), (g / C::NSV) & 1, abort_flag)) {
-            if ((r >> 3) < 16 - (lim & 15)) {
-              const uint32_t at = sbase + C::V_OFF + sv * C::TILE + (lim + (r >> 3)) * 128 + (r & 7) * 16;
-#pragma unroll
-              for (int u = 0; u < C::SUBS; ++u)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + u * C::SUB_BYTES),
-                             "r"(0u)
-                             : "memory");
-            }
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-        }
         tc::fence_after();
         uint32_t sr[4][32];
 #pragma unroll
@@ -369,56 +538,73 @@ __global__ void __launch_bounds__(384, 1)
             for (int i2 = 0; i2 < 32; ++i2)
               if (c * 32 + i2 >= lim) sr[c][i2] = __float_as_uint(-INFINITY);
         }
-        float mx = -INFINITY;
+        float cm[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float cm = -INFINITY;
+          auto x = [&](int k) { return __uint_as_float(sr[c][k]); };
+          float m8[8];
 #pragma unroll
-          for (int i2 = 0; i2 < 32; i2 += 2)
-            cm = max3(cm, __uint_as_float(sr[c][i2]), __uint_as_float(sr[c][i2 + 1]));
-          mx = fmaxf(mx, cm);
+          for (int k = 0; k < 8; ++k) m8[k] = max3(x(4 * k), x(4 * k + 1), fmaxf(x(4 * k + 2), x(4 * k + 3)));
+          cm[c] = fmaxf(max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), m8[6]), m8[7]);
         }
-        const float cand = mx * scale_log2;
+        const float cand = fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]) * scale_log2;
         float alpha = 1.f;
-        if (cand > ref + kSlack) {
-          alpha = ex2_approx(ref - cand);
+        if (cand > ref + (kTop + kSlack)) {
+          alpha = ex2_approx(ref - (cand - kTop));
           l *= alpha;
-          ref = cand;
+          ref = cand - kTop;
         }
         const bool rescale = i > 0 && __any_sync(0xffffffffu, alpha != 1.f);
-        // P_hi (upper 16 bits of the weight) in columns 0-63, P_lo = bf16(p -
-        // P_hi) in columns 64-127.
-        float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t hi[32], lo[32];
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i2 = 0; i2 < 16; ++i2) {
-              const float p0 = ex2_approx(fmaf(__uint_as_float(sr[2 * half + c][2 * i2]), scale_log2, -ref));
-              const float p1 =
-                  ex2_approx(fmaf(__uint_as_float(sr[2 * half + c][2 * i2 + 1]), scale_log2, -ref));
-              sum0 += p0;
-              sum1 += p1;
-              const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-              asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(hi[16 * c + i2]) : "r"(u0), "r"(u1));
-              lo[16 * c + i2] = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u),
-                                            p1 - __uint_as_float(u1 & 0xffff0000u));
-            }
-          tc::st32(tS + 32 * half, hi);
-          tc::st32(tS + 64 + 32 * half, lo);
+        const int g = g0 + j, sv = g % C::NSV;
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_VR + sv), (g / C::NSV) & 1, abort_flag))) {
+          ok = false;
+          break;
         }
-        l += sum0 + sum1;
+        if (__shfl_sync(0xffffffffu, wide[sv], 0) == 0) {
+          // fp16 weights: key pair (2k, 2k + 1) of chunk c in column 16c + k,
+          // staged in registers whose scores are used up.
+          const uint64_t c2 = f2(scale_log2, scale_log2), n2 = f2(-ref, -ref);
+          uint64_t sumA = f2(0.f, 0.f), sumB = f2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float y0, y1;
+              unf2(fma2(f2(__uint_as_float(sr[c][2 * k]), __uint_as_float(sr[c][2 * k + 1])), c2, n2), y0, y1);
+              const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+              if (k & 1) sumB = add2(sumB, f2(p0, p1)); else sumA = add2(sumA, f2(p0, p1));
+              sr[c][k] = pack_f16x2(p0, p1);
+            }
+          uint32_t pw[32];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              pw[k] = sr[2 * half][k];
+              pw[16 + k] = sr[2 * half + 1][k];
+            }
+            tc::st32(tS + 32 * half, pw);
+          }
+          float s0, s1;
+          unf2(add2(sumA, sumB), s0, s1);
+          l += s0 + s1;
+        } else {
+          l += two_term_weights(tS, lim, scale_log2, ref);
+        }
         if (rescale) {
+          const uint64_t a2 = f2(alpha, alpha);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) tc::ld32(tO + c * 32, sr[c]);
           tc::wait_ld();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
 #pragma unroll
-            for (int i2 = 0; i2 < 32; ++i2)
-              sr[c][i2] = __float_as_uint(__uint_as_float(sr[c][i2]) * alpha);
+            for (int k = 0; k < 16; ++k) {
+              float x0, x1;
+              unf2(mul2(f2(__uint_as_float(sr[c][2 * k]), __uint_as_float(sr[c][2 * k + 1])), a2), x0, x1);
+              sr[c][2 * k] = __float_as_uint(x0);
+              sr[c][2 * k + 1] = __float_as_uint(x1);
+            }
             tc::st32(tO + c * 32, sr[c]);
           }
         }
@@ -433,9 +619,12 @@ __global__ void __launch_bounds__(384, 1)
         tc::fence_after();
       }
       // The state of this row over the segment (m in log2 units).
+      // Accumulators as [d_h / 4][128 rows][4], so that a warp stores 512
+      // contiguous bytes.
       const size_t slot =
           ((static_cast<size_t>(s.kvh) * a.s_cap + touch) * a.n_rb + rb) * 2 + t;
       const size_t pi = slot * kBM + r;
+      float* so = a.o + slot * kBM * D + r * 4;
       const bool store = row < a.rows && touch >= 0 && touch < a.s_cap;
       ATTN_DCHECK(touch >= 0 && touch < a.s_cap, &g_shared_err);
 #pragma unroll
@@ -448,7 +637,7 @@ __global__ void __launch_bounds__(384, 1)
         if (store && n > 0) {
 #pragma unroll
           for (int i2 = 0; i2 < 8; ++i2)
-            *reinterpret_cast<uint4*>(a.o + pi * D + c * 32 + i2 * 4) =
+            *reinterpret_cast<uint4*>(so + (c * 8 + i2) * (kBM * 4)) =
                 make_uint4(ov[4 * i2], ov[4 * i2 + 1], ov[4 * i2 + 2], ov[4 * i2 + 3]);
         }
       }
@@ -469,9 +658,11 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == C::MMA_WARP) tc::dealloc(tmem, 512);
 }
 
-// One CTA per (row, query head): the prefix's states (per CTA that had a part
-// of the head's tiles, two with NT = 1), then the row's own, joined in that
-// order.
+// Joins a row's states: the prefix's (one per CTA that had a part of the head's
+// tiles, two with NT = 1), then its own, in that order, and divides once. A CTA
+// takes kMergeRows neighbouring (token, head) rows of a KV head; a thread has 4
+// dims of one row over all its states, kMergeUnroll of them in flight.
+constexpr int kMergeRows = 8, kMergeUnroll = 8;
 struct MergeArgs {
   PrefixArgs p;
   int NT, h, g, upr;
@@ -482,33 +673,29 @@ struct MergeArgs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a) {
-  constexpr int VEC = D / 32, U = 4, NW = 4;
-  __shared__ float sm[NW], sl[NW], so[NW][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x / a.h, hq = blockIdx.x % a.h;
+__global__ void __launch_bounds__(kMergeRows* D / 4) shared_merge_kernel(const MergeArgs a) {
+  constexpr int U = kMergeUnroll;
+  const int kvh = blockIdx.y, c = threadIdx.x / kMergeRows;
+  const long long pr = static_cast<long long>(blockIdx.x) * kMergeRows + threadIdx.x % kMergeRows;
   pdl_wait();
   pdl_trigger();
-  const size_t row = static_cast<size_t>(b) * a.h + hq;
-  const int kvh = hq / a.g, hh = hq % a.g;
-  // Prefix states.
+  if (pr >= a.p.rows) return;
+  const int b = static_cast<int>(pr / a.g), hh = static_cast<int>(pr % a.g);
+  const size_t row = static_cast<size_t>(b) * a.h + kvh * a.g + hh;
+  // Own states' place (loads first: the prefix's length is one round trip too).
+  const long long per = __ldcg(a.plan), at = __ldcg(a.plan + 1 + b);
+  const long long wu = __ldcg(a.plan + 2 + b) - at;  // weight of one unit
   const PrefixRun run = prefix_run(a.p, 0);
-  int n_pre = 0;
-  size_t pre0 = 0, pre_step = 0;
-  int per_touch = 1;
+  int n_pre = 0, per_touch = 1;
+  size_t pre0 = 0;
   if (run.tiles > 0) {
     const long long s = static_cast<long long>(kvh) * run.tiles;
     n_pre = static_cast<int>((s + run.tiles - 1) / run.per - s / run.per) + 1;
-    const long long pr = static_cast<long long>(b) * a.g + hh;  // row of the KV head
     const int rb = static_cast<int>(pr / (a.NT * kBM)), rt = static_cast<int>(pr % (a.NT * kBM));
     pre0 = ((static_cast<size_t>(kvh) * a.p.s_cap * a.p.n_rb + rb) * 2 + rt / kBM) * kBM + rt % kBM;
-    pre_step = static_cast<size_t>(a.p.n_rb) * 2 * kBM;
     per_touch = a.NT == 1 ? 2 : 1;
     n_pre *= per_touch;
   }
-  // Own states.
-  const long long per = __ldcg(a.plan), at = __ldcg(a.plan + 1 + b);
-  const long long wu = __ldcg(a.plan + 2 + b) - at;  // weight of one unit
   int n_own = 0;
   long long c0 = 0;
   if (wu > 0) {
@@ -517,44 +704,30 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a) {
     n_own = static_cast<int>((s + wu - 1) / per - c0) + 1;
   }
   const int n = n_pre + n_own;
-  float M = kNone, L = 0.f, acc[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  for (int base = warp; base < n; base += NW * U) {
-    float m[U], l[U], x[U][VEC];
+  float M = kNone, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = 0; base < n; base += U) {
+    float m[U], l[U];
+    float4 x[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int j = base + i * NW;
+      const int j = base + i;
       m[i] = kNone;
       l[i] = 0.f;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[i][e] = 0.f;
-      if (j < n) {
-        const float *po, *pm, *pl;
-        size_t idx;
-        if (j < n_pre) {
-          po = a.p.o; pm = a.p.m; pl = a.p.l;
-          idx = pre0 + (j / per_touch) * pre_step + (j % per_touch) * kBM;
-        } else if (n_own == 1) {
-          po = a.o_row; pm = a.m_row; pl = a.l_row;
-          idx = row;
-        } else {
-          po = a.o_part; pm = a.m_part; pl = a.l_part;
-          idx = (2 * (c0 + j - n_pre) + (j == n_pre ? 1 : 0)) * 8 + hh;
-        }
-        l[i] = __ldcg(pl + idx);
-        const float mi = __ldcg(pm + idx);
-        if (mi != kNone) {  // (a stream without key tiles stores no O~)
-          m[i] = mi;
-          const float* src = po + idx * D + lane * VEC;
-          if constexpr (VEC == 4) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
-            x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
-          } else {
-            const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
-            x[i][0] = t.x; x[i][1] = t.y;
-          }
-        }
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < n_pre) {
+        const size_t idx = pre0 + ((j / per_touch) * static_cast<size_t>(a.p.n_rb) * 2 + j % per_touch) * kBM;
+        m[i] = __ldcg(a.p.m + idx);
+        l[i] = __ldcg(a.p.l + idx);
+        // (a stream without key tiles stores no accumulators: not used then)
+        x[i] = __ldcg(reinterpret_cast<const float4*>(a.p.o + (idx - idx % kBM) * D + (idx % kBM) * 4 +
+                                                      c * (kBM * 4)));
+      } else if (j < n) {
+        const bool cut = n_own > 1;
+        const size_t idx = cut ? (2 * (c0 + j - n_pre) + (j == n_pre ? 1 : 0)) * 8 + hh : row;
+        m[i] = __ldcg((cut ? a.m_part : a.m_row) + idx);
+        l[i] = __ldcg((cut ? a.l_part : a.l_row) + idx);
+        x[i] = __ldcg(reinterpret_cast<const float4*>((cut ? a.o_part : a.o_row) + idx * D + c * 4));
       }
     }
     float Mn = M;
@@ -563,37 +736,28 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const MergeArgs a) {
     const float sc = ex2_approx(M - Mn);
     M = Mn;
     L *= sc;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] *= sc;
+    acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const float w = ex2_approx(m[i] - Mn);
       L = fmaf(w, l[i], L);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
+      if (m[i] != kNone) {
+        acc.x = fmaf(w, x[i].x, acc.x);
+        acc.y = fmaf(w, x[i].y, acc.y);
+        acc.z = fmaf(w, x[i].z, acc.z);
+        acc.w = fmaf(w, x[i].w, acc.w);
+      }
     }
   }
-  if (lane == 0) {
-    sm[warp] = M;
-    sl[warp] = L;
+  const bool empty = L == 0.f;
+  const float inv = empty ? 0.f : 1.f / L;
+  uint2 y = make_uint2(0u, 0u);
+  if (!empty) {
+    y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   }
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) so[warp][lane * VEC + e] = acc[e];
-  __syncthreads();
-  float Mt = kNone, Lt = 0.f;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) Mt = fmaxf(Mt, sm[w]);
-#pragma unroll
-  for (int w = 0; w < NW; ++w) Lt = fmaf(sl[w], ex2_approx(sm[w] - Mt), Lt);
-  const bool empty = Lt == 0.f;
-  const float inv = empty ? 0.f : 1.f / Lt;
-  for (int e = threadIdx.x; e < D; e += 128) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) v = fmaf(so[w][e], ex2_approx(sm[w] - Mt), v);
-    a.out[row * D + e] = __float2bfloat16(empty ? 0.f : v * inv);
-  }
-  if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = empty ? -INFINITY : Mt * kLn2 + logf(Lt);
+  *reinterpret_cast<uint2*>(a.out + row * D + c * 4) = y;
+  if (a.lse != nullptr && c == 0) a.lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
 }
 
 template <int D, int NT>
@@ -669,7 +833,8 @@ cudaError_t launch_shared(const SharedArgs& s, cudaStream_t stream) {
   m.out = static_cast<__nv_bfloat16*>(r.o);
   m.lse = r.lse;
   auto merge = r.d_h == 128 ? shared_merge_kernel<128> : shared_merge_kernel<64>;
-  return launch_pdl(merge, dim3(unsigned(r.B) * r.h), dim3(128), 0, stream, m);
+  return launch_pdl(merge, dim3(unsigned((a.rows + kMergeRows - 1) / kMergeRows), unsigned(r.h_kv)),
+                    dim3(unsigned(kMergeRows * r.d_h / 4)), 0, stream, m);
 }
 
 unsigned int shared_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {
