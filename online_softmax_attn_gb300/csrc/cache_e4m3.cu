@@ -8,9 +8,17 @@
 // [num_blocks, h_kv, 16] exponent bytes, so the keys that one decode CTA reads
 // (a page of one KV head) are one run of 16 * d_h bytes.
 //
-// Both kernels move bytes and compute almost nothing: a group of d_h / 8 lanes
-// takes one row (8 numbers a lane: 16 or 32 bytes on the wide side, 8 on the
-// code side), the largest magnitude is a shuffle over the group.
+// Both kernels move bytes and compute little: what bounds them is the bytes in
+// flight and, once those are there, the instructions per value. A group of
+// d_h / 16 lanes takes one row (one token of one head of K or V), two 8-number
+// chunks a lane d_h / 2 numbers apart, so that every load and store of a warp is
+// contiguous; the largest magnitude is a shuffle over the group. A thread has U
+// rows in flight. Rows are ordered (block of 16 tokens, K heads then V heads,
+// token): neighbouring groups then write (read) neighbouring slots of one page
+// and head, runs of 16 * d_h bytes with their exponents, while the tensors'
+// side comes in whole rows of 128 bytes or more. A CTA's first threads look its
+// tokens up (a binary search over cu and the block table) while the others'
+// loads are under way.
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "internal.h"
@@ -65,169 +73,283 @@ __device__ __forceinline__ bool locate(const TokenMap& m, int t, int* page, int*
   return true;
 }
 
+struct RowStrides {
+  long long tok, head;  // elements
+};
+
+// Place of a CTA's tokens: page and slot; page -1: no place, -2: a page outside
+// the cache.
+constexpr int kBlk = 16;  // tokens per block
+constexpr int kThreads = 128;  // 256 and 512: 12.7 and 14.9 us for the write of 8192 tokens, 128: 12.4
+// Rows in flight per thread: 2 measured best for both (write of 8192 tokens 13.0,
+// 12.5, 13.9 us a call and read of 32768 tokens 41.0, 34.8, 36.7 us with 1, 2
+// and 4).
+constexpr int kU = 2;
+
+template <int D, int U>
+struct Cta {
+  static constexpr int L = D / 16;        // lanes per row
+  static constexpr int G = kThreads / L;       // rows at a time
+  static constexpr int ROWS = U * G;      // rows per CTA
+  static constexpr int TOKENS = (ROWS / (2 * kBlk) + 2) * kBlk;  // at least two rows per token
+};
+
+template <int D, int U>
+__device__ __forceinline__ void locate_tokens(const TokenMap& m, int total, int h_kv, int* s_page,
+                                              int* s_slot) {
+  using C = Cta<D, U>;
+  const int span = 2 * h_kv * kBlk;  // rows per block
+  const long long r0 = static_cast<long long>(blockIdx.x) * C::ROWS;
+  const long long t0 = r0 / span * kBlk, t1 = ((r0 + C::ROWS - 1) / span + 1) * kBlk;
+  const int n = static_cast<int>(min(static_cast<long long>(total), t1) - t0);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    int page = -1, slot = 0;
+    bool bad_page = false;
+    if (!locate(m, static_cast<int>(t0) + i, &page, &slot, &bad_page)) page = -1;
+    s_page[i] = bad_page ? -2 : page;
+    s_slot[i] = slot;
+  }
+}
+
+// Row `it` of a CTA's rows: its token's index within the CTA, K or V, head.
+struct RowId {
+  int t, ti, head;
+  bool is_v;
+};
+template <int D, int U>
+__device__ __forceinline__ RowId row_id(int it, int h_kv) {
+  using C = Cta<D, U>;
+  const int span = 2 * h_kv * kBlk;
+  const long long r0 = static_cast<long long>(blockIdx.x) * C::ROWS;
+  const long long blk0 = r0 / span;
+  const int r = static_cast<int>(r0 - blk0 * span) + it, blk = r / span, rem = r - blk * span;
+  RowId x;
+  x.ti = blk * kBlk + rem % kBlk;
+  // Tokens behind the last count up from `total` at most by a block.
+  x.t = static_cast<int>(min(blk0 * kBlk + x.ti, 0x7fffffffll));
+  x.head = rem / kBlk;
+  x.is_v = x.head >= h_kv;
+  if (x.is_v) x.head -= h_kv;
+  return x;
+}
+
+// 16 numbers of a row (two chunks) as loaded.
 template <bool BF16>
-__device__ __forceinline__ void load_row8(const void* base, long long off, float (&x)[8]) {
+struct Raw {
+  uint4 w[BF16 ? 2 : 4];
+};
+
+// Exponent byte from the row's largest finite magnitude (fp32 bits), codes of
+// 8 numbers.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+  uint2 w;
+  w.x = e4m3::encode2(x[0] * inv, x[1] * inv) | (e4m3::encode2(x[2] * inv, x[3] * inv) << 16);
+  w.y = e4m3::encode2(x[4] * inv, x[5] * inv) | (e4m3::encode2(x[6] * inv, x[7] * inv) << 16);
+  return w;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const Raw<BF16>& r, int c, float (&x)[8]) {
   if constexpr (BF16) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.w[c].x, r.w[c].y, r.w[c].z, r.w[c].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = bf16lo(w[i]);
       x[2 * i + 1] = bf16hi(w[i]);
     }
   } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[4 * i] = __uint_as_float(r.w[2 * c + i].x);
+      x[4 * i + 1] = __uint_as_float(r.w[2 * c + i].y);
+      x[4 * i + 2] = __uint_as_float(r.w[2 * c + i].z);
+      x[4 * i + 3] = __uint_as_float(r.w[2 * c + i].w);
+    }
   }
 }
 
-struct RowStrides {
-  long long tok, head;  // elements
-};
+// fp32 bits of the largest magnitude among a lane's 16 numbers (NaN and
+// infinities count, as the largest).
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_bits(const Raw<BF16>& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 2 : 4); ++i) {
+    const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (BF16)
+        asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7fff7fffu));
+      else
+        m = max(m, w[k] & 0x7fffffffu);
+    }
+  }
+  return BF16 ? max(m & 0xffffu, m >> 16) << 16 : m;
+}
 
-// One group of D / 8 lanes quantises U tokens of one head of K or V.
 template <int D, bool BF16, int U>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
     cache_write_kernel(const void* __restrict__ k, const void* __restrict__ v, RowStrides sk,
                        RowStrides sv, TokenMap m, int total, int h_kv, uint8_t* __restrict__ kc,
                        uint8_t* __restrict__ vc, uint8_t* __restrict__ ks,
                        uint8_t* __restrict__ vs) {
-  constexpr int L = D / 8;  // lanes per row
-  const int sub = threadIdx.x % L;
-  const long long gid = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / L;
-  const int rows = 2 * h_kv;
-  const int t0 = static_cast<int>(gid / rows) * U;
-  const int r = static_cast<int>(gid % rows);
-  const bool is_v = r >= h_kv;
-  const int head = is_v ? r - h_kv : r;
-  const void* src = is_v ? v : k;
-  const RowStrides st = is_v ? sv : sk;
-  uint8_t* codes = is_v ? vc : kc;
-  uint8_t* exps = is_v ? vs : ks;
+  using C = Cta<D, U>;
+  __shared__ int s_page[C::TOKENS], s_slot[C::TOKENS];
+  const int sub = threadIdx.x % C::L, grp = threadIdx.x / C::L;
   pdl_wait();
   pdl_trigger();
 
-  float x[U][8];
+  Raw<BF16> x[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    const RowId id = row_id<D, U>(u * C::G + grp, h_kv);
+    if (id.t < total) {
+      const RowStrides st = id.is_v ? sv : sk;
+      const long long off = id.t * st.tok + id.head * st.head + sub * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-    if (t0 + u < total) load_row8<BF16>(src, (t0 + u) * st.tok + head * st.head + sub * 8, x[u]);
+      for (int c = 0; c < 2; ++c) {
+        if constexpr (BF16) {
+          x[u].w[c] = __ldg(reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(id.is_v ? v : k) + off + c * (D / 2)));
+        } else {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(id.is_v ? v : k) +
+                                                          off + c * (D / 2));
+          x[u].w[2 * c] = __ldg(p);
+          x[u].w[2 * c + 1] = __ldg(p + 1);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < (BF16 ? 2 : 4); ++c) x[u].w[c] = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
+  locate_tokens<D, U>(m, total, h_kv, s_page, s_slot);
+  __syncthreads();
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    // Largest finite magnitude over the row, as bits (ordered like the
-    // numbers). A NaN or an infinity has no e4m3 code of its own: it is
-    // stored as NaN, so that it cannot turn into a finite key, and does not
-    // take part in the scale.
-    uint32_t a = 0;
-    bool odd = false;
+    uint32_t a = max_bits<BF16>(x[u]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = __float_as_uint(x[u][i]) & 0x7fffffffu;
-      odd |= b >= 0x7f800000u;
-      a = max(a, b >= 0x7f800000u ? 0u : b);
+    for (int o = 1; o < C::L; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    float y[2][8];
+    unpack8<BF16>(x[u], 0, y[0]);
+    unpack8<BF16>(x[u], 1, y[1]);
+    if (__any_sync(0xffffffffu, a >= 0x7f800000u)) {
+      // A NaN or an infinity has no e4m3 code of its own: it is stored as NaN,
+      // so that it cannot turn into a finite key, and has no part in the scale.
+      a = 0;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t b = __float_as_uint(y[c][i]) & 0x7fffffffu;
+          if (b >= 0x7f800000u)
+            y[c][i] = __uint_as_float(0x7fffffffu);
+          else
+            a = max(a, b);
+        }
+#pragma unroll
+      for (int o = 1; o < C::L; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
     }
-    if (odd) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if ((__float_as_uint(x[u][i]) & 0x7f800000u) == 0x7f800000u)
-          x[u][i] = __uint_as_float(0x7fffffffu);
-    }
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
     const uint32_t e = e4m3::scale_byte(a);
     const float inv = e4m3::inv_scale_of(e);
-    uint2 w;
-    w.x = e4m3::encode2(x[u][0] * inv, x[u][1] * inv) |
-          (e4m3::encode2(x[u][2] * inv, x[u][3] * inv) << 16);
-    w.y = e4m3::encode2(x[u][4] * inv, x[u][5] * inv) |
-          (e4m3::encode2(x[u][6] * inv, x[u][7] * inv) << 16);
-    int page, slot;
-    bool bad_page;
-    if (t0 + u >= total || !locate(m, t0 + u, &page, &slot, &bad_page) || bad_page) continue;
-    const size_t row = (static_cast<size_t>(page) * h_kv + head) * kPage + slot;
+    const RowId id = row_id<D, U>(u * C::G + grp, h_kv);
+    if (id.t >= total || s_page[id.ti] < 0) continue;
+    const size_t row =
+        (static_cast<size_t>(s_page[id.ti]) * h_kv + id.head) * kPage + s_slot[id.ti];
     if (!ATTN_GUARD(row < static_cast<size_t>(m.num_blocks) * h_kv * kPage, &g_cache8_err)) continue;
-    *reinterpret_cast<uint2*>(codes + row * D + sub * 8) = w;
-    if (sub == 0) exps[row] = static_cast<uint8_t>(e);
+    uint8_t* dst = (id.is_v ? vc : kc) + row * D + sub * 8;
+    *reinterpret_cast<uint2*>(dst) = encode8(y[0], inv);
+    *reinterpret_cast<uint2*>(dst + D / 2) = encode8(y[1], inv);
+    if (sub == 0) (id.is_v ? vs : ks)[row] = static_cast<uint8_t>(e);
   }
 }
 
-// The reverse: one group of D / 8 lanes reads U tokens of one head back.
+// The reverse. fp32 results: four chunks of 4 numbers a lane, so that each store
+// of a warp fills its sectors (two halves of a sector in two stores took 28.1 us
+// for 86 MB of them, 40 rows of up to 1999 tokens).
 template <int D, bool BF16, int U>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
     cache_read_kernel(const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
                       const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs, TokenMap m,
                       int total, int h_kv, void* __restrict__ k, void* __restrict__ v,
                       RowStrides sk, RowStrides sv) {
-  constexpr int L = D / 8;
-  const int sub = threadIdx.x % L;
-  const long long gid = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / L;
-  const int rows = 2 * h_kv;
-  const int t0 = static_cast<int>(gid / rows) * U;
-  const int r = static_cast<int>(gid % rows);
-  const bool is_v = r >= h_kv;
-  const int head = is_v ? r - h_kv : r;
-  const uint8_t* codes = is_v ? vc : kc;
-  const uint8_t* exps = is_v ? vs : ks;
-  const RowStrides st = is_v ? sv : sk;
+  using C = Cta<D, U>;
+  __shared__ int s_page[C::TOKENS], s_slot[C::TOKENS];
+  const int sub = threadIdx.x % C::L, grp = threadIdx.x / C::L;
   pdl_wait();
   pdl_trigger();
-  uint2 w[U];
+  locate_tokens<D, U>(m, total, h_kv, s_page, s_slot);
+  __syncthreads();
+  uint32_t w[U][4];  // codes: two chunks of 8, or four of 4
   uint32_t e[U];
-  bool live[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    int page = 0, slot = 0;
-    bool bad_page = false;
-    live[u] = t0 + u < total && locate(m, t0 + u, &page, &slot, &bad_page);
-    w[u] = make_uint2(0u, 0u);  // a page outside the cache reads as zeros
+    const RowId id = row_id<D, U>(u * C::G + grp, h_kv);
+    w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0u;  // a page outside the cache reads as zeros
     e[u] = 127u;
-    if (live[u] && !bad_page) {
-      const size_t row = (static_cast<size_t>(page) * h_kv + head) * kPage + slot;
-      w[u] = __ldg(reinterpret_cast<const uint2*>(codes + row * D + sub * 8));
-      e[u] = __ldg(exps + row);
+    if (id.t < total && s_page[id.ti] >= 0) {
+      const size_t row =
+          (static_cast<size_t>(s_page[id.ti]) * h_kv + id.head) * kPage + s_slot[id.ti];
+      const uint8_t* src = (id.is_v ? vc : kc) + row * D + sub * (BF16 ? 8 : 4);
+      if constexpr (BF16) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(src));
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(src + D / 2));
+        w[u][0] = a.x; w[u][1] = a.y; w[u][2] = b.x; w[u][3] = b.y;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[u][c] = __ldg(reinterpret_cast<const uint32_t*>(src + c * (D / 4)));
+      }
+      e[u] = __ldg((id.is_v ? vs : ks) + row);
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (!live[u]) continue;
+    const RowId id = row_id<D, U>(u * C::G + grp, h_kv);
+    if (id.t >= total || s_page[id.ti] == -1) continue;
     const float sc = e4m3::scale_of(e[u]);
-    float x[8];
+    const RowStrides st = id.is_v ? sv : sk;
+    const long long off = id.t * st.tok + id.head * st.head + sub * (BF16 ? 8 : 4);
+    float x[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t c = ((i & 2) ? w[u].y : w[u].x) >> ((i & 1) * 16);
-      const uint32_t hh = e4m3::decode2(static_cast<uint16_t>(c & 0xffffu));
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t hh = e4m3::decode2(static_cast<uint16_t>(w[u][i >> 1] >> ((i & 1) * 16)));
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
       x[2 * i] = f.x * sc;
       x[2 * i + 1] = f.y * sc;
     }
-    const long long off = (t0 + u) * st.tok + head * st.head + sub * 8;
-    void* dst = is_v ? v : k;
     if constexpr (BF16) {
-      uint4 y;
-      y.x = pack_bf16x2(x[0], x[1]);
-      y.y = pack_bf16x2(x[2], x[3]);
-      y.z = pack_bf16x2(x[4], x[5]);
-      y.w = pack_bf16x2(x[6], x[7]);
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + off) = y;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(id.is_v ? v : k) + off;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<uint4*>(dst + c * (D / 2)) =
+            make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
+                       pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
     } else {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + off);
-      p[0] = make_float4(x[0], x[1], x[2], x[3]);
-      p[1] = make_float4(x[4], x[5], x[6], x[7]);
+      float* dst = static_cast<float*>(id.is_v ? v : k) + off;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<float4*>(dst + c * (D / 4)) =
+            make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
     }
   }
 }
 
+template <int D, int U>
+cudaError_t grid_of(const CacheTokens& a, dim3* grid) {
+  const long long rows = (static_cast<long long>(a.total) + kBlk - 1) / kBlk * kBlk * 2 * a.h_kv;
+  const long long blocks = (rows + Cta<D, U>::ROWS - 1) / Cta<D, U>::ROWS;
+  if (blocks > 0x7fffffffll) return cudaErrorNotSupported;
+  *grid = dim3(static_cast<unsigned>(blocks));
+  return cudaSuccess;
+}
+
 template <int D, bool BF16, int U>
 cudaError_t launch_write_u(const CacheTokens& a, cudaStream_t stream) {
-  const long long groups = (static_cast<long long>(a.total) + U - 1) / U * 2 * a.h_kv;
-  const long long blocks = (groups * (D / 8) + 255) / 256;
-  if (blocks > 0x7fffffffll) return cudaErrorNotSupported;
+  dim3 grid;
+  const cudaError_t e = grid_of<D, U>(a, &grid);
+  if (e != cudaSuccess) return e;
   const TokenMap m{a.block_table, a.cu, a.seq_lens, a.B, a.max_blocks, a.num_blocks};
-  return launch_pdl(cache_write_kernel<D, BF16, U>, dim3(unsigned(blocks)), dim3(256), 0, stream,
+  return launch_pdl(cache_write_kernel<D, BF16, U>, grid, dim3(kThreads), 0, stream,
                     static_cast<const void*>(a.k), static_cast<const void*>(a.v),
                     RowStrides{a.k_tok, a.k_head}, RowStrides{a.v_tok, a.v_head}, m, a.total,
                     a.h_kv, a.k_codes, a.v_codes, a.k_exp, a.v_exp);
@@ -235,11 +357,11 @@ cudaError_t launch_write_u(const CacheTokens& a, cudaStream_t stream) {
 
 template <int D, bool BF16, int U>
 cudaError_t launch_read_u(const CacheTokens& a, cudaStream_t stream) {
-  const long long groups = (static_cast<long long>(a.total) + U - 1) / U * 2 * a.h_kv;
-  const long long blocks = (groups * (D / 8) + 255) / 256;
-  if (blocks > 0x7fffffffll) return cudaErrorNotSupported;
+  dim3 grid;
+  const cudaError_t e = grid_of<D, U>(a, &grid);
+  if (e != cudaSuccess) return e;
   const TokenMap m{a.block_table, a.cu, a.seq_lens, a.B, a.max_blocks, a.num_blocks};
-  return launch_pdl(cache_read_kernel<D, BF16, U>, dim3(unsigned(blocks)), dim3(256), 0, stream,
+  return launch_pdl(cache_read_kernel<D, BF16, U>, grid, dim3(kThreads), 0, stream,
                     static_cast<const uint8_t*>(a.k_codes), static_cast<const uint8_t*>(a.v_codes),
                     static_cast<const uint8_t*>(a.k_exp), static_cast<const uint8_t*>(a.v_exp), m,
                     a.total, a.h_kv, a.k, a.v, RowStrides{a.k_tok, a.k_head},
@@ -251,15 +373,15 @@ cudaError_t launch_read_u(const CacheTokens& a, cudaStream_t stream) {
 cudaError_t launch_cache_write(const CacheTokens& a, cudaStream_t stream) {
   const bool bf = a.dtype == ATTN_DTYPE_BF16;
   if (a.d_h == 128)
-    return bf ? launch_write_u<128, true, 4>(a, stream) : launch_write_u<128, false, 4>(a, stream);
-  return bf ? launch_write_u<64, true, 4>(a, stream) : launch_write_u<64, false, 4>(a, stream);
+    return bf ? launch_write_u<128, true, kU>(a, stream) : launch_write_u<128, false, kU>(a, stream);
+  return bf ? launch_write_u<64, true, kU>(a, stream) : launch_write_u<64, false, kU>(a, stream);
 }
 
 cudaError_t launch_cache_read(const CacheTokens& a, cudaStream_t stream) {
   const bool bf = a.dtype == ATTN_DTYPE_BF16;
   if (a.d_h == 128)
-    return bf ? launch_read_u<128, true, 4>(a, stream) : launch_read_u<128, false, 4>(a, stream);
-  return bf ? launch_read_u<64, true, 4>(a, stream) : launch_read_u<64, false, 4>(a, stream);
+    return bf ? launch_read_u<128, true, kU>(a, stream) : launch_read_u<128, false, kU>(a, stream);
+  return bf ? launch_read_u<64, true, kU>(a, stream) : launch_read_u<64, false, kU>(a, stream);
 }
 
 unsigned int cache8_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {
