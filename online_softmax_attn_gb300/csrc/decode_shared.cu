@@ -6,14 +6,16 @@
 // once: the B * g query rows of a KV head are the M rows of dense products
 // against each key tile, and the prefix is read once for all of them.
 //
-//   1. shared_prefix_kernel (here): tcgen05, states of every row over the
-//      prefix, cut along the keys.
-//   2. decode_runs_kernel (decode_runs.cu, bf16 form): states over the rows'
-//      own pages.
-//   3. shared_merge_kernel (here): the states of a row, joined in a fixed
-//      order and divided once.
+//   shared_kernel: in two phases, the prefix's states of every row by tcgen05,
+//     and the states over the rows' own pages (runs_body of decode_runs.cuh on
+//     the softmax warps). Every other group of CTAs takes the phases in the
+//     other order, so that the products of one half run beside the memory
+//     traffic of the other; as kernels behind each other the two took 127 +
+//     66 us for 256 rows over 32768 keys and up to 700 of their own.
+//   shared_merge_kernel: the states of a row, joined in a fixed order and
+//     divided once.
 //
-// Prefix kernel. Query rows of a KV head are ordered (token, head of the
+// Prefix phase. Query rows of a KV head are ordered (token, head of the
 // group), so a 128-row tile is one TMA box of 128 / g tokens x g heads. A CTA
 // has two softmax warpgroups ("streams"; thread = row), a TMA warp and an MMA
 // warp. NT = 2 (more than 128 rows): the streams are two row tiles that share
@@ -35,8 +37,7 @@
 // NaN, or nothing above 2^-6 (whose small values would lose bits) is loaded
 // again and stays bf16, with P = P_hi + P_lo in two MMAs. With the two-term P
 // everywhere the prefix of 256 rows over 32768 keys took 205 us.
-#include "common.cuh"
-#include "internal.h"
+#include "decode_runs.cuh"
 #include "pdl.cuh"
 #include "tc.cuh"
 
@@ -46,13 +47,9 @@ static __device__ unsigned int g_shared_err;
 
 namespace {
 
-constexpr int kPage = 16;
 constexpr int kBM = 128, kBN = 128;
-constexpr float kNone = -1e30f;  // reference before the first key
-// Weights reach at most 2^15 (fp16's largest finite number is 65504): a row's
-// reference is set kTop below a new maximum and moves when a score passes it by
-// kTop + kSlack. Weights down to 2^-27 of the largest are normal fp16 numbers.
-constexpr float kTop = 13.0f, kSlack = 2.0f;
+// kTop, kSlack (decode_runs.cuh): a row's reference is set kTop below a new
+// maximum and moves when a score passes it by kTop + kSlack.
 
 template <int D, int NT>
 struct SpCfg {
@@ -64,7 +61,6 @@ struct SpCfg {
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = Q_OFF + NT * TILE;
   static constexpr int V_OFF = K_OFF + NSK * TILE;
-  static constexpr int BAR_OFF = V_OFF + NSV * TILE;
   // q_full, q_empty, k_full[], k_empty[], v_full[] (landed), v_ready[]
   // (converted), v_empty[], v_again (a tile loaded once more), s_full[2],
   // p_full[2], o_final[2], mma_done
@@ -72,8 +68,13 @@ struct SpCfg {
                        B_VE = B_VR + NSV, B_VA = B_VE + NSV, B_SF = B_VA + 1, B_PF = B_SF + 2,
                        B_OF = B_PF + 2, B_DONE = B_OF + 2, NBAR = B_DONE + 1;
   static_assert(NBAR <= 32, "one warp initialises the barriers, one per lane");
-  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr int SMEM = MISC_OFF + 32 + 1024;  // tensor-memory slot, abort flag, wide[NSV]
+  static constexpr int NST = D == 128 ? 3 : 4;
+  using Own = Cfg<false, D, 8, NST>;  // the other phase, from offset 0
+  static constexpr int TILES_END = V_OFF + NSV * TILE;
+  static constexpr int BAR_OFF = TILES_END > Own::SMEM ? TILES_END : Own::SMEM;
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;  // tensor-memory slot, abort flag, wide[NSV]
+  static constexpr int SMEM = MISC_OFF + 32 + 1024;
+  static_assert(SMEM + sizeof(RunShared<8>) <= 227 * 1024, "shared memory of an SM");
   static constexpr int THREADS = 384;  // two softmax warpgroups, one of control
   static constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, CONV_WARP = 10;  // to 11
   static constexpr int CONV_THREADS = 64;
@@ -189,14 +190,26 @@ __device__ __forceinline__ PrefixRun prefix_run(const PrefixArgs& a, int group) 
   return r;
 }
 
+// The rows' own pages (runs_body's arguments).
+struct OwnArgs {
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const __nv_bfloat16* q;
+  const int32_t* block_table;
+  Rows rw;
+  int h, g, max_blocks;
+  RunOut out;
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(384, 1)
-    shared_prefix_kernel(const __grid_constant__ CUtensorMap tmap_q,
-                         const __grid_constant__ CUtensorMap tmap_k,
-                         const __grid_constant__ CUtensorMap tmap_v, const PrefixArgs a,
-                         int tok_per_tile, float scale_log2) {
+    shared_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                  const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v, const PrefixArgs a,
+                  const OwnArgs own, int tok_per_tile, float scale_log2) {
   using C = SpCfg<D, NT>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  extern __shared__ __align__(16) uint8_t smem_raw[];  // (1024 would pad the static part)
+  __shared__ RunShared<8> sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -224,8 +237,10 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();     // q, the prefix's length, table and pages are earlier kernels' output
-  pdl_trigger();
+  // q, the prefix's length, table and pages are earlier kernels' output. The
+  // merge is not let in before this kernel's end (its waiting CTAs took SMs from
+  // running ones: 57 us instead of 49 for 64 rows over 8192 keys).
+  pdl_wait();
   const PrefixRun run = prefix_run(a, group);
   if (blockIdx.x == 0 && threadIdx.x == 0)
     (void)clamp_seq_len(__ldcg(a.len), a.max_blocks * kPage, &g_shared_err);
@@ -268,8 +283,27 @@ __global__ void __launch_bounds__(384, 1)
     __syncwarp();
   };
 
+  // The rows' own pages, before the prefix in every other group of CTAs (the
+  // row blocks of a group read the same key tiles and stay together). Both
+  // phases use the same shared memory: all warps meet between them, and the
+  // generic accesses of one come before the copies of the other.
+  const bool own_first = group & 1;
+  auto own_phase = [&] {
+    const int n_cta = min(int(gridDim.x), kRunsMaxCtas);
+    if (int(blockIdx.x) < n_cta)
+      runs_body<false, D, 8, C::NST>(own.kc, own.vc, nullptr, nullptr, own.q, own.block_table, own.rw,
+                                     own.h, a.h_kv, own.g, own.max_blocks, a.num_blocks, scale_log2,
+                                     own.out, smem, sh, blockIdx.x, n_cta, &g_shared_err,
+                                     [] { asm volatile("barrier.cta.sync 2, 256;" ::: "memory"); });
+  };
+  auto meet = [] {
+    fence_proxy_async_smem();
+    __syncthreads();
+  };
+
   if (warp >= C::PRODUCER_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_CONTROL));
+    if (own_first) meet();
     if (warp == C::PRODUCER_WARP) {
       // ---------------------------------------------------------- producer
       auto wait = [&](uint32_t b, uint32_t parity) {
@@ -505,9 +539,14 @@ __global__ void __launch_bounds__(384, 1)
         g0 += s.nt;
       }
     }
+    if (!own_first) meet();
   } else {
     // ------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_SOFTMAX));
+    if (own_first) {
+      own_phase();
+      meet();
+    }
     const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t tS = tmem + (uint32_t(wq * 32) << 16) + t * 256, tO = tS + 128;
     const long long row = (static_cast<long long>(rb) * NT + (NT == 2 ? t : 0)) * kBM + r;
@@ -650,6 +689,10 @@ __global__ void __launch_bounds__(384, 1)
       tc::fence_before();
       g0 += s.nt;
     }
+    if (!own_first) {
+      meet();
+      own_phase();
+    }
   }
 
   tc::fence_before();
@@ -678,7 +721,12 @@ __global__ void __launch_bounds__(kMergeRows* D / 4) shared_merge_kernel(const M
   const int kvh = blockIdx.y, c = threadIdx.x / kMergeRows;
   const long long pr = static_cast<long long>(blockIdx.x) * kMergeRows + threadIdx.x % kMergeRows;
   pdl_wait();
-  pdl_trigger();
+  // The next kernel may start once every CTA of this one runs. With more CTAs
+  // than the GPU holds at a time (three per SM) it would come in on whichever
+  // SMs fall free: the next call's row blocks, neighbours that share key tiles,
+  // then lie scattered (256 rows over 32768 keys: 220 us a call, else 178),
+  // while 64 rows over 8192 keys gain (54 us without, 49.5 with).
+  if (gridDim.x * gridDim.y <= 3 * 152) pdl_trigger();
   if (pr >= a.p.rows) return;
   const int b = static_cast<int>(pr / a.g), hh = static_cast<int>(pr % a.g);
   const size_t row = static_cast<size_t>(b) * a.h + kvh * a.g + hh;
@@ -761,7 +809,7 @@ __global__ void __launch_bounds__(kMergeRows* D / 4) shared_merge_kernel(const M
 }
 
 template <int D, int NT>
-cudaError_t launch_prefix(const SharedArgs& s, const SharedPlan& pl, const PrefixArgs& a,
+cudaError_t launch_states(const SharedArgs& s, const SharedPlan& pl, const PrefixArgs& a,
                           cudaStream_t stream) {
   using C = SpCfg<D, NT>;
   const DecodeRunsArgs& r = s.own;
@@ -783,11 +831,21 @@ cudaError_t launch_prefix(const SharedArgs& s, const SharedPlan& pl, const Prefi
       encode_tensor_map(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(r.v_cache), dims,
                         strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  auto kern = shared_prefix_kernel<D, NT>;
+  OwnArgs own;
+  own.kc = static_cast<const uint8_t*>(r.k_cache);
+  own.vc = static_cast<const uint8_t*>(r.v_cache);
+  own.q = static_cast<const __nv_bfloat16*>(r.q);
+  own.block_table = r.block_table;
+  own.rw = Rows{r.seq_lens, r.B, r.max_blocks * kPage, r.h_kv};
+  own.h = r.h;
+  own.g = g;
+  own.max_blocks = r.max_blocks;
+  own.out = RunOut{r.plan, r.o_part, r.m_part, r.l_part, r.o_row, r.m_row, r.l_row, nullptr, nullptr};
+  auto kern = shared_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(unsigned(pl.groups) * pl.n_rb), dim3(C::THREADS), size_t(C::SMEM), stream,
-                    tq, tk, tv, a, kBM / g, r.scale * kLog2e);
+                    tq, tk, tv, a, own, kBM / g, r.scale * kLog2e);
 }
 
 }  // namespace
@@ -811,11 +869,9 @@ cudaError_t launch_shared(const SharedArgs& s, cudaStream_t stream) {
   a.l = s.pre_l;
   cudaError_t e;
   if (r.d_h == 128)
-    e = pl.nt == 2 ? launch_prefix<128, 2>(s, pl, a, stream) : launch_prefix<128, 1>(s, pl, a, stream);
+    e = pl.nt == 2 ? launch_states<128, 2>(s, pl, a, stream) : launch_states<128, 1>(s, pl, a, stream);
   else
-    e = pl.nt == 2 ? launch_prefix<64, 2>(s, pl, a, stream) : launch_prefix<64, 1>(s, pl, a, stream);
-  if (e != cudaSuccess) return e;
-  e = launch_decode_runs_bf16(r, stream);
+    e = pl.nt == 2 ? launch_states<64, 2>(s, pl, a, stream) : launch_states<64, 1>(s, pl, a, stream);
   if (e != cudaSuccess) return e;
   MergeArgs m;
   m.p = a;

@@ -133,7 +133,6 @@ struct DecodeRunsArgs {
   float* lse = nullptr;
 };
 cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream);  // and its merge
-cudaError_t launch_decode_runs_bf16(const DecodeRunsArgs& a, cudaStream_t stream);  // states only
 unsigned int decode_runs_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
 
 // decode_shared.cu -----------------------------------------------------------
