@@ -15,7 +15,7 @@ import os
 
 import torch
 
-from .build import LIB_PATH
+from .build import CALLS_PATH, LIB_PATH
 
 __all__ = [
     "AttnError",
@@ -536,62 +536,33 @@ def attn_merge_lse_pair(o_a, lse_a, o_b, lse_b, out_dtype=torch.bfloat16, o=None
     return o, lse
 
 
-# The calls below are as short as a kernel launch on small inputs, so their
-# checks are written for the host's time: one pass of cheap tests, and the
-# stream handle without a torch.cuda.Stream object.
-_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_calls_mod = None
 
 
-def _same_device(*ts):
-    """Every tensor on the current CUDA device (kernels launch there); its index."""
-    dev = ts[0].get_device()
-    _need(dev >= 0 and dev == torch._C._cuda_getDevice(), "tensors must be on the current CUDA device")
-    for t in ts:
-        if t.get_device() != dev:
-            raise ValueError("tensors must be on one CUDA device")
-    return dev
+def _calls():
+    """The compiled binding (csrc/binding.cpp) of the calls below, which on small
+    inputs are as short as their checks and argument conversion in Python."""
+    global _calls_mod
+    if _calls_mod is None:
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"compiled binding not built: {CALLS_PATH} is missing "
+                               "(run `python -m online_softmax_attn_gb300.build`)")
+        import importlib.util
+
+        spec = importlib.util.spec_from_file_location(__name__ + "._calls", CALLS_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _calls_mod = mod
+    return _calls_mod
 
 
-def _contiguous(*ts):
-    for t in ts:
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-
-
-def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _cache_e4m3(k_cache, v_cache, k_scale, v_scale):
-    """Shape (num_blocks, h_kv, page, d) of a checked 8-bit cache."""
-    shape = k_cache.shape
-    if not (k_cache.dtype is _E4M3 and v_cache.dtype is _E4M3 and k_scale.dtype is _U8 and v_scale.dtype is _U8):
-        raise ValueError("caches must be float8_e4m3fn and scales uint8 exponents")
-    if not (len(shape) == 4 and v_cache.shape == shape and k_scale.shape == shape[:3] and
-            v_scale.shape == shape[:3]):
-        raise ValueError("caches [num_blocks,h_kv,16,d] and scales [num_blocks,h_kv,16] expected")
-    _contiguous(k_cache, v_cache, k_scale, v_scale)
-    return shape
-
-
-def _cache_tokens(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens):
-    dev = _same_device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens)
-    nb, h_kv, page, d = _cache_e4m3(k_cache, v_cache, k_scale, v_scale)
-    dt = k.dtype
-    if not (v.dtype is dt and (dt is _BF16 or dt is _F32)):
-        raise ValueError("k, v must share dtype bf16 or fp32")
-    shape, ks, vs = k.shape, k.stride(), v.stride()
-    if not (len(shape) == 3 and v.shape == shape and shape[1] == h_kv and shape[2] == d):
-        raise ValueError("k, v [total,h_kv,d] expected")
-    if not (ks[2] == 1 and vs[2] == 1):
-        raise ValueError("k, v must be contiguous in d")
-    if not (block_table.dtype is _I32 and cu_seqlens.dtype is _I32 and seq_lens.dtype is _I32):
-        raise ValueError("block_table, cu_seqlens and seq_lens must be int32")
-    tab, B = block_table.shape, seq_lens.numel()
-    if not (seq_lens.dim() == 1 and cu_seqlens.shape == (B + 1,) and len(tab) == 2 and tab[0] == B):
-        raise ValueError("block_table [B,max_blocks], cu_seqlens [B+1] and seq_lens [B] expected")
-    _contiguous(block_table, cu_seqlens, seq_lens)
-    return dev, ks, vs, ATTN_DTYPE_BF16 if dt is _BF16 else ATTN_DTYPE_F32, (B, shape[0], h_kv, d, page, nb, tab[1])
+def _where(t, stream):
+    """(library handle, current device, stream handle) for a call on t."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("tensors must be on the current CUDA device")
+    return (library()._handle, dev,
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
 def attn_cache_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens,
@@ -602,12 +573,10 @@ def attn_cache_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
     are the last of its seq_lens[b] positions. Caches [num_blocks, h_kv, 16, d]
     float8_e4m3fn and scales [num_blocks, h_kv, 16] uint8 are updated in place:
     value = code * 2^(byte - 127)."""
-    dev, ks, vs, dt, shape = _cache_tokens(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens)
-    st = library().attn_cache_write_e4m3(
-        k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], dt, block_table.data_ptr(),
-        cu_seqlens.data_ptr(), seq_lens.data_ptr(), *shape, k_cache.data_ptr(), v_cache.data_ptr(),
-        k_scale.data_ptr(), v_scale.data_ptr(), _raw_stream(stream, dev))
-    _check("attn_cache_write_e4m3", st)
+    st = _calls().cache_tokens(*_where(k, stream), k, v, k_cache, v_cache, k_scale, v_scale, block_table,
+                               cu_seqlens, seq_lens, True)
+    if st:
+        _check("attn_cache_write_e4m3", st)
 
 
 def attn_cache_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens, k, v,
@@ -616,35 +585,26 @@ def attn_cache_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, cu_seq
     (bf16 or fp32, strided as in attn_cache_write_e4m3): row b's last
     cu_seqlens[b+1] - cu_seqlens[b] positions go to its tokens, exactly.
     Returns (k, v)."""
-    dev, ks, vs, dt, shape = _cache_tokens(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens)
-    st = library().attn_cache_read_e4m3(
-        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        block_table.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), *shape, k.data_ptr(),
-        v.data_ptr(), ks[0], ks[1], vs[0], vs[1], dt, _raw_stream(stream, dev))
-    _check("attn_cache_read_e4m3", st)
+    st = _calls().cache_tokens(*_where(k, stream), k, v, k_cache, v_cache, k_scale, v_scale, block_table,
+                               cu_seqlens, seq_lens, False)
+    if st:
+        _check("attn_cache_read_e4m3", st)
     return k, v
 
 
-def _outputs(q, dev, B, h, need, workspace, o, lse, return_lse, stream):
-    """Workspace and outputs of a decode call: the caller's, checked, or new
-    ones, allocated for the stream that the call runs on."""
-    if workspace is not None:
-        if not (workspace.get_device() == dev and workspace.is_contiguous()):
-            raise ValueError("workspace must be contiguous and on q's device")
-    if o is not None:
-        if not (o.shape == q.shape and o.dtype is _BF16 and o.is_contiguous() and o.get_device() == dev):
-            raise ValueError("o must be like q")
-    if lse is not None:
-        if not (lse.shape == (B, h) and lse.dtype is _F32 and lse.is_contiguous() and lse.get_device() == dev):
-            raise ValueError("lse must be contiguous fp32 [B,h]")
-    if workspace is None or o is None or (lse is None and return_lse):
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            if workspace is None:
-                workspace = torch.empty(max(need, 256), dtype=_U8, device=q.device)
-            if o is None:
-                o = torch.empty_like(q)
-            if lse is None and return_lse:
-                lse = torch.empty((B, h), dtype=_F32, device=q.device)
+def _new_outputs(q, need, h_kv, workspace, o, lse, return_lse, stream):
+    """Fills in the workspace and outputs that the caller left out, allocated
+    for the stream that the call runs on."""
+    if q.dim() != 3:
+        raise ValueError("q [B,h,d] expected")
+    B, h, d = q.shape
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        if workspace is None:
+            workspace = torch.empty(max(need(B, h, h_kv, d), 256), dtype=torch.uint8, device=q.device)
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None and return_lse:
+            lse = torch.empty((B, h), dtype=torch.float32, device=q.device)
     return workspace, o, lse
 
 
@@ -661,25 +621,14 @@ def attn_decode_paged_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, s
     contiguous); any h / h_kv. The keys are divided over the GPU on the device,
     so the call can be captured and replayed with new lengths.
     Returns (o [B,h,d] bf16, lse [B,h] fp32 or None)."""
-    dev = _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
-    nb, h_kv, page, d = _cache_e4m3(k_cache, v_cache, k_scale, v_scale)
-    qs, tab = q.shape, block_table.shape
-    if not (q.dtype is _BF16 and len(qs) == 3 and qs[2] == d):
-        raise ValueError("q must be bf16 [B,h,d]")
-    B, h = qs[0], qs[1]
-    if not (block_table.dtype is _I32 and seq_lens.dtype is _I32 and len(tab) == 2 and tab[0] == B and
-            seq_lens.shape == (B,)):
-        raise ValueError("block_table [B,max_blocks] and seq_lens [B] must be int32")
-    _contiguous(q, block_table, seq_lens)
-    lib = library()
-    need = lib.attn_decode_e4m3_workspace_bytes(B, h, h_kv, d) if workspace is None else 0
-    workspace, o, lse = _outputs(q, dev, B, h, need, workspace, o, lse, return_lse, stream)
-    st = lib.attn_decode_paged_e4m3(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        block_table.data_ptr(), seq_lens.data_ptr(), B, h, h_kv, d, page, nb, tab[1],
-        1.0 / math.sqrt(d) if scale is None else scale, workspace.data_ptr(), workspace.nbytes, o.data_ptr(),
-        None if lse is None else lse.data_ptr(), _raw_stream(stream, dev))
-    _check("attn_decode_paged_e4m3", st)
+    where = _where(q, stream)
+    if workspace is None or o is None or (lse is None and return_lse):
+        workspace, o, lse = _new_outputs(q, attn_decode_e4m3_workspace_bytes, k_cache.shape[1], workspace, o,
+                                         lse, return_lse, stream)
+    st = _calls().decode_e4m3(*where, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
+                              workspace, o, lse)
+    if st:
+        _check("attn_decode_paged_e4m3", st)
     return o, lse
 
 
@@ -697,32 +646,14 @@ def attn_decode_paged_shared(q, k_cache, v_cache, prefix_table, prefix_len, bloc
     [B,h,d] bf16, caches [num_blocks,16,h_kv,d] bf16 (all CUDA, contiguous).
     The prefix is read once for all rows. Returns (o [B,h,d] bf16, lse [B,h]
     fp32 over all keys, or None)."""
-    dev = _same_device(q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens)
-    if not (q.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16):
-        raise ValueError("q and caches must be bf16")
-    qs, cs, tab = q.shape, k_cache.shape, block_table.shape
-    if not (len(qs) == 3 and len(cs) == 4 and v_cache.shape == cs and cs[3] == qs[2]):
-        raise ValueError("q [B,h,d] and caches [num_blocks,16,h_kv,d] expected")
-    if not (prefix_table.dtype is _I32 and prefix_len.dtype is _I32 and block_table.dtype is _I32 and
-            seq_lens.dtype is _I32):
-        raise ValueError("tables and lengths must be int32")
-    B, h, d = qs
-    nb, page, h_kv, _ = cs
-    if not (prefix_table.dim() == 1 and prefix_len.shape == (1,) and len(tab) == 2 and tab[0] == B and
-            seq_lens.shape == (B,)):
-        raise ValueError("prefix_table [max_prefix_blocks], prefix_len [1], block_table [B,max_blocks], "
-                         "seq_lens [B] expected")
-    _contiguous(q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens)
-    lib = library()
-    need = lib.attn_decode_shared_workspace_bytes(B, h, h_kv, d) if workspace is None else 0
-    workspace, o, lse = _outputs(q, dev, B, h, need, workspace, o, lse, return_lse, stream)
-    st = lib.attn_decode_paged_shared(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_table.data_ptr(),
-        prefix_len.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), B, h, h_kv, d, page, nb,
-        prefix_table.shape[0], tab[1], 1.0 / math.sqrt(d) if scale is None else scale,
-        workspace.data_ptr(), workspace.nbytes, o.data_ptr(), None if lse is None else lse.data_ptr(),
-        _raw_stream(stream, dev))
-    _check("attn_decode_paged_shared", st)
+    where = _where(q, stream)
+    if workspace is None or o is None or (lse is None and return_lse):
+        workspace, o, lse = _new_outputs(q, attn_decode_shared_workspace_bytes, k_cache.shape[2], workspace, o,
+                                         lse, return_lse, stream)
+    st = _calls().decode_shared(*where, q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens,
+                                scale, workspace, o, lse)
+    if st:
+        _check("attn_decode_paged_shared", st)
     return o, lse
 
 

@@ -1,9 +1,11 @@
-"""Compile the CUDA library for sm_103a, in-tree.
+"""Compile the CUDA library for sm_103a and its compiled binding, in-tree.
 
 Produces ``online_softmax_attn_gb300/libattn_gb300.so`` from the ``csrc/*.cu``
 translation units, compiled in parallel with nvcc (one ``-gencode``) and linked
 with the static CUDA runtime, so the library needs no libcuda at load time
-(driver entry points are resolved at run time).
+(driver entry points are resolved at run time). ``_calls.so``, the Python side of
+the calls whose host time matters (``csrc/binding.cpp``), is compiled beside it by
+g++ against the installed torch.
 
     python -m online_softmax_attn_gb300.build [--force] [--ptxas-verbose] [--debug]
 
@@ -28,6 +30,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+CALLS_PATH = os.path.join(PKG, "_calls.so")
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG, "libattn_gb300_debug.so")
 
@@ -73,6 +76,28 @@ def _compile(src: str, obj: str, ptxas_verbose: bool, debug: bool = False) -> st
     return res.stderr if ptxas_verbose else ""
 
 
+def _compile_calls(src: str, out: str) -> str:
+    """The compiled binding: a Python extension that uses torch's headers and
+    the torch libraries of this interpreter, and no CUDA."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = out + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in inc], src, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-ldl"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {os.path.basename(src)}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, out)
+    return ""
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
           debug: bool = False) -> str:
     """Compile (if stale) and link the library (the -DATTN_DEBUG variant with
@@ -90,10 +115,14 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
         if force or ptxas_verbose or _stale(obj, [src, *headers]):
             jobs.append((src, obj))
     logs = []
-    if jobs:
-        workers = min(len(jobs), max(1, os.cpu_count() or 1))
+    calls = os.path.join(CSRC, "binding.cpp")
+    calls_stale = force or _stale(CALLS_PATH, [calls, os.path.join(INCLUDE, "attn.h")])
+    if jobs or calls_stale:
+        workers = min(len(jobs) + 1, max(1, os.cpu_count() or 1))
         with concurrent.futures.ThreadPoolExecutor(workers) as ex:
             futs = [ex.submit(_compile, s, o, ptxas_verbose, debug) for s, o in jobs]
+            if calls_stale:
+                futs.append(ex.submit(_compile_calls, calls, CALLS_PATH))
             for f in futs:
                 logs.append(f.result())
     if force or jobs or _stale(lib_path, objs):

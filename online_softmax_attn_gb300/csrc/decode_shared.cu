@@ -289,11 +289,13 @@ __global__ void __launch_bounds__(384, 1)
   // generic accesses of one come before the copies of the other.
   const bool own_first = group & 1;
   auto own_phase = [&] {
-    const int n_cta = min(int(gridDim.x), kRunsMaxCtas);
-    if (int(blockIdx.x) < n_cta)
+    // Runs are handed out from the last CTA on: where there is little work of
+    // either kind, no CTA gets both.
+    const int n_cta = min(int(gridDim.x), kRunsMaxCtas), cta = int(gridDim.x) - 1 - int(blockIdx.x);
+    if (cta < n_cta)
       runs_body<false, D, 8, C::NST>(own.kc, own.vc, nullptr, nullptr, own.q, own.block_table, own.rw,
                                      own.h, a.h_kv, own.g, own.max_blocks, a.num_blocks, scale_log2,
-                                     own.out, smem, sh, blockIdx.x, n_cta, &g_shared_err,
+                                     own.out, smem, sh, cta, n_cta, &g_shared_err,
                                      [] { asm volatile("barrier.cta.sync 2, 256;" ::: "memory"); });
   };
   auto meet = [] {

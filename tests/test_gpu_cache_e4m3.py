@@ -203,3 +203,28 @@ def test_far_pages_beyond_32_bit_offsets():
     check_out(o[0], (np.einsum("hgn,nhd->hgd", p, want) / p.sum(-1)[..., None]).reshape(32, d), torch.bfloat16)
     check_lse(lse[0], (s.max(-1) + np.log(p.sum(-1))).reshape(32))
     assert attn.attn_get_device_error() == 0
+
+
+def test_binding_refuses():
+    """What the compiled binding checks before it calls the library."""
+    x = W.normal((20, 2, 64), 1, torch.bfloat16).cuda()
+    kc, vc, ks, vs = empty_cache(3, 2, 64)
+    good = dict(k=x, v=x, k_cache=kc, v_cache=vc, k_scale=ks, v_scale=vs, block_table=dev([[0, 2]]),
+                cu_seqlens=dev([0, 20]), seq_lens=dev([20]))
+    for fn in (attn.attn_cache_write_e4m3, attn.attn_cache_read_e4m3):
+        fn(**good)
+        wide = torch.zeros((20, 2, 128), dtype=torch.bfloat16, device="cuda")
+        for kw in (dict(k=x.half()), dict(v=x.float()), dict(k=x.cpu()), dict(k=x[:, :1]), dict(k=x[:10]),
+                   dict(k=wide[:, :, ::2], v=wide[:, :, ::2]), dict(k_cache=kc.view(torch.uint8)),
+                   dict(v_cache=vc[:2]), dict(k_scale=ks[:, :1]), dict(v_scale=vs.cpu()),
+                   dict(block_table=dev([0, 2])), dict(cu_seqlens=dev([0, 20, 20])), dict(cu_seqlens=dev([0, 20]).long()),
+                   dict(seq_lens=dev([[20]]))):
+            with pytest.raises(ValueError):
+                fn(**{**good, **kw})
+        odd = torch.zeros(20 * 2 * 64 + 8, dtype=torch.bfloat16, device="cuda")[4:4 + 2560].view(20, 2, 64)
+        with pytest.raises(attn.AttnError):  # rows not on 16 bytes
+            fn(**{**good, "k": odd})
+        loose = torch.zeros((20, 2, 68), dtype=torch.bfloat16, device="cuda")[:, :, :64]
+        with pytest.raises(attn.AttnError):
+            fn(**{**good, "v": loose})
+    assert attn.attn_get_device_error() == 0

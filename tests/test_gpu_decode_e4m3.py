@@ -311,3 +311,33 @@ def test_write_decode_and_read_together():
             assert (err <= 4e-3 + ob[0].float().abs() * 2.0 ** -7).all()
             assert (lse[b] - lb[0]).abs().max() <= 2e-4
     assert attn.attn_get_device_error() == 0
+
+
+def test_binding_refuses():
+    """What the compiled binding checks before it calls the library."""
+    lens = [20, 33]
+    good = dict(zip(("q", "kc", "vc", "ks", "vs", "table", "lens"), cuda(*decode_case(lens, 2, 4, 64, seed=20))))
+    call = lambda **kw: attn.attn_decode_paged_e4m3(**{**dict(
+        q=good["q"], k_cache=good["kc"], v_cache=good["vc"], k_scale=good["ks"], v_scale=good["vs"],
+        block_table=good["table"], seq_lens=good["lens"]), **kw})
+    call()
+    bad = [dict(q=good["q"].float()), dict(q=good["q"][0]), dict(q=good["q"].transpose(0, 1)), dict(q=good["q"].cpu()),
+           dict(k_cache=good["kc"].view(torch.uint8)), dict(k_cache=good["kc"][:, :1]), dict(k_cache=good["kc"][:-1]),
+           dict(v_scale=good["vs"].int()), dict(k_scale=good["ks"][:, :, :8]), dict(k_scale=good["ks"].cpu()),
+           dict(block_table=good["table"].long()), dict(block_table=good["table"][:1]),
+           dict(block_table=good["table"].t()), dict(seq_lens=good["lens"].long()), dict(seq_lens=good["lens"][:1]),
+           dict(o=torch.empty_like(good["q"], dtype=torch.float32)), dict(o=torch.empty_like(good["q"]).cpu()),
+           dict(lse=torch.empty((2, 8), dtype=torch.bfloat16, device="cuda")),
+           dict(lse=torch.empty((8, 2), device="cuda").t()), dict(lse=torch.empty((2, 7), device="cuda")),
+           dict(workspace=torch.empty(1 << 24, dtype=torch.uint8))]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw in (dict(scale=0.0), dict(scale=float("nan")), dict(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(attn.AttnError):
+            call(**kw)
+    with pytest.raises((TypeError, ValueError)):
+        call(scale="x")
+    with pytest.raises((TypeError, ValueError, AttributeError)):
+        call(block_table=None)
+    assert attn.attn_get_device_error() == 0

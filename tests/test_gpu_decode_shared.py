@@ -317,3 +317,21 @@ def test_prefix_read_back_from_the_8_bit_cache():
     assert ((o.float() - o8.float()).abs() <= 4e-3 + o8.float().abs() * 2.0 ** -7).all()
     assert (lse - l8).abs().max() <= 2e-4
     assert attn.attn_get_device_error() == 0
+
+
+def test_binding_refuses():
+    """What the compiled binding checks before it calls the library."""
+    q, k, v, ptab, plen, tab, n = [t.cuda() for t in case(40, [3, 20], 2, 4, 64, seed=21)]
+    good = dict(q=q, k_cache=k, v_cache=v, prefix_table=ptab, prefix_len=plen, block_table=tab, seq_lens=n)
+    attn.attn_decode_paged_shared(**good)
+    for kw in (dict(q=q.float()), dict(q=q[0]), dict(k_cache=k.float()), dict(v_cache=v[:2]), dict(k_cache=k[..., :32]),
+               dict(prefix_table=ptab[None]), dict(prefix_table=ptab.long()), dict(prefix_len=plen[0]),
+               dict(prefix_len=torch.cat([plen, plen])), dict(prefix_len=plen.cpu()), dict(block_table=tab[:1]),
+               dict(seq_lens=n[:1]), dict(o=q.float()), dict(lse=torch.empty((2, 9), device="cuda"))):
+        with pytest.raises(ValueError):
+            attn.attn_decode_paged_shared(**{**good, **kw})
+    with pytest.raises(attn.AttnError):
+        attn.attn_decode_paged_shared(**good, scale=-1.0)
+    with pytest.raises(attn.AttnError):
+        attn.attn_decode_paged_shared(**good, workspace=torch.empty(4096, dtype=torch.uint8, device="cuda"))
+    assert attn.attn_get_device_error() == 0
