@@ -9,9 +9,12 @@ static __device__ unsigned int g_decode_runs_err;
 
 namespace {
 
-// 8 warps a CTA, two CTAs per SM.
+// 8 warps and one CTA per SM, 4 stages (d_h = 128). Two CTAs of 2 stages took
+// 22.4 instead of 20.9 us for a row of 32768 keys (twice as many parts to join)
+// and 170.8 instead of 173.0 for 66 rows of up to 16384; 12 warps of 3 stages
+// 21.5 and 173.4, 16 of 2 24.0 and 170.7.
 template <int D, int NST>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, 1)
     decode_runs_kernel(const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
                        const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs, const __nv_bfloat16* __restrict__ q,
                        const int32_t* __restrict__ block_table, Rows rw, int h, int h_kv, int g,
@@ -124,11 +127,11 @@ template <int D, int NST>
 cudaError_t launch_cfg(const DecodeRunsArgs& a, int sms, cudaStream_t stream) {
   using C = Cfg<true, D, 8, NST>;
   constexpr int kSmem = C::SMEM + 1024;
-  static_assert(2 * (kSmem + sizeof(RunShared<8>) + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kSmem + sizeof(RunShared<8>) <= 227 * 1024, "shared memory of an SM");
   auto kern = decode_runs_kernel<D, NST>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * sms < kRunsMaxCtas ? 2 * sms : kRunsMaxCtas;
+  const int grid = sms < kRunsMaxCtas ? sms : kRunsMaxCtas;
   const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
   const Rows rw{a.seq_lens, a.B, a.max_blocks * kPage, a.h_kv * n_gb};
   const RunOut out{a.plan,  a.o_part, a.m_part, a.l_part, nullptr,
@@ -152,8 +155,8 @@ cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  e = a.d_h == 128 ? launch_cfg<128, 2>(a, sms, stream)
-                   : launch_cfg<64, 3>(a, sms, stream);
+  e = a.d_h == 128 ? launch_cfg<128, 4>(a, sms, stream)
+                   : launch_cfg<64, 6>(a, sms, stream);
   if (e != cudaSuccess) return e;
   const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
   auto merge = a.d_h == 128 ? decode_runs_merge_kernel<128> : decode_runs_merge_kernel<64>;
