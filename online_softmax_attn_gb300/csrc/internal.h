@@ -97,10 +97,10 @@ cudaError_t launch_cache_read(const CacheTokens& a, cudaStream_t stream);
 unsigned int cache8_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
 
 // decode_runs.cu -------------------------------------------------------------
-constexpr int kRunsMaxCtas = 320;  // bounds the workspace; two CTAs on each of 160 SMs
+constexpr int kRunsMaxCtas = 160;  // bounds the workspace; one CTA per SM
 constexpr int kRunsUnit = 1;       // weight of a unit beside its pages (decode_runs.cu)
 // Plan (int64: weight per CTA, then the rows' weights' prefix sums [B + 1]), then two
-// partial states per CTA: O~ [2 * 320, 8, d_h], m and l [2 * 320, 8].
+// partial states per CTA: O~ [2 * 160, 8, d_h], m and l [2 * 160, 8].
 struct RunsLayout {
   size_t o_off, m_off, l_off, total;
 };

@@ -79,10 +79,10 @@ def test_decode_refuses(lib):
 
 
 def test_decode_workspace_bytes(lib):
-    """Plan (int64: B + 2), then 640 states of 8 heads: d_h + 2 floats each."""
+    """Plan (int64: B + 2), then 320 states of 8 heads: d_h + 2 floats each."""
     a = lambda x: -(-x // 256) * 256
     for B, d in ((0, 128), (1, 64), (66, 128), (65535, 64)):
-        assert attn.attn_decode_e4m3_workspace_bytes(B, 32, 8, d) == a((B + 2) * 8) + 640 * 8 * (d + 2) * 4
+        assert attn.attn_decode_e4m3_workspace_bytes(B, 32, 8, d) == a((B + 2) * 8) + 320 * 8 * (d + 2) * 4
     for bad in ((-1, 32, 8, 128), (2, 0, 8, 128), (2, 30, 8, 128), (2, 32, 0, 128), (2, 32, 8, 96)):
         assert attn.attn_decode_e4m3_workspace_bytes(*bad) == 0
 

@@ -39,7 +39,7 @@ def test_workspace_bytes(lib):
     f = attn.attn_decode_shared_workspace_bytes
     a = lambda x: -(-x // 256) * 256
     # 64 rows x 4 heads: one block of two tiles, 152 runs, at most 152 / 8 + 2 on a head
-    own = a(a(66 * 8) + 640 * 8 * 130 * 4) + 64 * 32 * 512 + 2 * a(64 * 32 * 4)
+    own = a(a(66 * 8) + 320 * 8 * 130 * 4) + 64 * 32 * 512 + 2 * a(64 * 32 * 4)
     assert f(64, 32, 8, 128) == own + 8 * 21 * 256 * 130 * 4
     assert f(0, 32, 8, 128) == f(1, 32, 8, 128) > 0
     assert f(65535, 8, 1, 64) > f(256, 8, 1, 64)
