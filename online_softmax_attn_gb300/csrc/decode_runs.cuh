@@ -268,46 +268,87 @@ __device__ __forceinline__ void runs_body(
   auto tail_of = [&](int w) { return reinterpret_cast<float*>(smem + w * NST * C::STAGE_BYTES); };
 
   // ---- the runs: prefix sums of the rows' weights (per unit) ----
-  const int per_t = (rw.B + NW * 32 - 1) / (NW * 32);
-  const int b0 = min(tid * per_t, rw.B), b1 = min(b0 + per_t, rw.B);
-  long long sum = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int raw = __ldcg(rw.seq_lens + b);
-    const int len = min(max(raw, 0), rw.max_len);
-    if (cta == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
-    if (b < kLenCache) s_len[b] = len;
-    sum += row_weight(len);
-  }
-  long long incl = sum;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
-  }
-  if (lane == 31) s_warp[warp] = incl;
-  if (tid < NW) s_kind[tid] = s_own[tid] = 0;
-  sync();
-  long long before = incl - sum, total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
-  }
-  const long long all = total * rw.upr;
   const long long n_runs = static_cast<long long>(n_cta) * NW;
-  const long long per = max(static_cast<long long>(kMinRun), div_ll(all + n_runs - 1, n_runs));
-  const long long cta0 = per * NW * cta;
-  if (cta == 0) {  // for the merge
-    if (tid == 0) out.plan[0] = per * NW;
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      out.plan[1 + b] = at;
-      at += row_weight(row_len(rw, s_len, b));
-      if (b == rw.B - 1) out.plan[1 + rw.B] = at;
+  auto per_of = [&](long long all) {
+    return max(static_cast<long long>(kMinRun), div_ll(all + n_runs - 1, n_runs));
+  };
+  if (lane == 0) s_kind[warp] = s_own[warp] = 0;  // read behind the join's barrier
+  long long all, per, p0;
+  bool have;
+  Walk cw;
+  long long off;  // weight between the first row of this warp's run and the run
+  if (rw.B <= 32) {
+    // A row per lane: every warp plans for itself, without a barrier (9.0 us a
+    // call for a row of 1000 keys; the form below 9.4).
+    int len = 0;
+    if (lane < rw.B) {
+      const int raw = __ldcg(rw.seq_lens + lane);
+      len = min(max(raw, 0), rw.max_len);
+      if (cta == 0 && warp == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
     }
-  }
-  if (cta0 >= all) return;
-  {
+    s_len[lane] = len;  // (every warp writes the same)
+    const uint32_t w = row_weight(len);
+    uint32_t incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    all = static_cast<long long>(__shfl_sync(0xffffffffu, incl, 31)) * rw.upr;
+    per = per_of(all);
+    if (cta == 0 && warp == 0) {  // for the merge
+      if (lane == 0) out.plan[0] = per * NW;
+      if (lane < rw.B) out.plan[1 + lane] = incl - w;
+      if (lane == rw.B - 1) out.plan[1 + rw.B] = incl;
+    }
+    if (per * NW * cta >= all) return;
+    p0 = per * (static_cast<long long>(NW) * cta + warp);
+    have = p0 < all;
+    const long long at = static_cast<long long>(incl - w) * rw.upr;
+    const uint32_t mine =
+        __ballot_sync(0xffffffffu, p0 >= at && p0 < static_cast<long long>(incl) * rw.upr);
+    cw.b = have ? __ffs(mine) - 1 : 0;
+    off = have ? p0 - __shfl_sync(0xffffffffu, at, cw.b) : 0;
+    cw.len = __shfl_sync(0xffffffffu, len, cw.b);
+    __syncwarp();
+  } else {
+    const int per_t = (rw.B + NW * 32 - 1) / (NW * 32);
+    const int b0 = min(tid * per_t, rw.B), b1 = min(b0 + per_t, rw.B);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int raw = __ldcg(rw.seq_lens + b);
+      const int len = min(max(raw, 0), rw.max_len);
+      if (cta == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
+      if (b < kLenCache) s_len[b] = len;
+      sum += row_weight(len);
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    sync();
+    long long before = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before += s_warp[w];
+      total += s_warp[w];
+    }
+    all = total * rw.upr;
+    per = per_of(all);
+    const long long cta0 = per * NW * cta;
+    if (cta == 0) {  // for the merge
+      if (tid == 0) out.plan[0] = per * NW;
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        out.plan[1 + b] = at;
+        at += row_weight(row_len(rw, s_len, b));
+        if (b == rw.B - 1) out.plan[1 + rw.B] = at;
+      }
+    }
+    if (cta0 >= all) return;
     long long at = before * rw.upr;
     const long long end = (before + sum) * rw.upr;
     if (cta0 + per * NW > at && cta0 < end) {
@@ -324,18 +365,16 @@ __device__ __forceinline__ void runs_body(
         at = next;
       }
     }
+    sync();
+    p0 = cta0 + per * warp;
+    have = p0 < all;
+    cw.b = have ? s_b[warp] : 0;
+    off = have ? s_off[warp] : 0;
+    cw.len = row_len(rw, s_len, cw.b);
   }
-  sync();
-  const long long p0 = cta0 + per * warp;
-  bool have = p0 < all;
-  Walk cw;
-  cw.b = have ? s_b[warp] : 0;
-  cw.len = row_len(rw, s_len, cw.b);
   cw.np = (cw.len + kPage - 1) / kPage;
   cw.rem = have ? min(per, all - p0) : 0;
-  cw.u = 0;
   {
-    const long long off = have ? s_off[warp] : 0;
     const int wu = cw.np + kUnit;
     cw.u = static_cast<int>(div_ll(off, wu));
     walk_open(cw, off - static_cast<long long>(cw.u) * wu);
