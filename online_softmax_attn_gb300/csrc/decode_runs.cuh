@@ -111,6 +111,14 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live,
                "r"(live ? 16 : 0), "l"(policy)
                : "memory");
 }
+// The same for exponents: a page's bytes of 8 heads fill a 128-byte line, which
+// is fetched whole and kept for the other heads' runs. (As 16-byte reads that L2
+// drops first they cost a DRAM access each, as many as the codes' slabs.)
+__device__ __forceinline__ void copy16_line(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest N groups of this thread's copies have landed.
 template <int N>
@@ -431,7 +439,7 @@ __device__ __forceinline__ void runs_body(
         copy16(chunk_at<E8, D>(vd, j * RPI + r, c), vc + off + j * RPI * row_bytes, live, policy);
       if constexpr (E8) {
         if (lane < 2)
-          copy16(exps + st * 32 + lane * 16, (lane ? vs : ks) + (page * h_kv + kvh) * kPage, live, policy);
+          copy16_line(exps + st * 32 + lane * 16, (lane ? vs : ks) + (page * h_kv + kvh) * kPage, live);
       }
       ++issued;
       ++bt_i;
