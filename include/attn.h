@@ -631,7 +631,7 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
  * prefix_len[0] keys and to its own seq_lens[b] ones; both live in the same
  * bf16 caches. The prefix is read once for all rows: its scores are dense
  * products on the tensor cores with the B * h / h_kv query rows of a KV head
- * as their rows. The three kernels' launches depend on B, h and h_kv only
+ * as their rows. Two kernels, whose launches depend on B, h and h_kv only
  * (capturable, replayable with new lengths and tables); the result does not
  * depend on timing.
  *   q            [B, h, d_h] bf16                                     (read)

@@ -335,3 +335,22 @@ def test_binding_refuses():
     with pytest.raises(attn.AttnError):
         attn.attn_decode_paged_shared(**good, workspace=torch.empty(4096, dtype=torch.uint8, device="cuda"))
     assert attn.attn_get_device_error() == 0
+
+
+def test_far_pages_beyond_32_bit_offsets():
+    """Prefix and own pages whose elements lie past 2^31."""
+    nb, h_kv, d = 140000, 8, 128
+    assert nb * h_kv * 16 * d > 2 ** 31
+    args = case(40, [20, 0], h_kv, 4, d, seed=22)
+    q, k, v, ptab, plen, tab, n = args
+    far_k = torch.empty((nb, 16, h_kv, d), dtype=torch.bfloat16, device="cuda")
+    far_v = torch.empty_like(far_k)
+    move = lambda t: torch.where(t < 0, t, nb - 1 - t)
+    for page in range(k.shape[0]):
+        far_k[nb - 1 - page] = k[page].cuda()
+        far_v[nb - 1 - page] = v[page].cuda()
+    O, L = reference(*args)
+    o, lse = attn.attn_decode_paged_shared(q.cuda(), far_k, far_v, move(ptab).cuda(), plen.cuda(), move(tab).cuda(), n.cuda())
+    check_out(o, O, torch.bfloat16)
+    check_lse(lse, L)
+    assert attn.attn_get_device_error() == 0
