@@ -20,7 +20,10 @@
 // the normaliser (a running max of s) and r for the accumulator (a running max
 // of s + f, the log2 weight with which a code of V enters). Any common shift
 // is legal, and a weight 2^(s + f - r) fits fp16 whatever the values'
-// magnitudes are, so P V is one fp16 product against the codes themselves. q
+// magnitudes are, so P V is one fp16 product against the codes themselves. r is
+// held as d = r - m and scores enter as rounded products minus m: both are
+// exact for the heaviest keys at any magnitude of the logits, where the spacing
+// of fp32 numbers passes 2^15's exponent (from 2^27 on). q
 // is scaled per head by a power of two to a largest magnitude in
 // [2^14, 2^15), where fp16 holds bf16's 8 significant bits down to 2^-28 of
 // that maximum. ldmatrix moves byte pairs (two dims of a key); one prmt puts
@@ -65,7 +68,7 @@ using e4m3::kPage;
 // fp16 numbers, and what fp16 drops below 2^-38 of it is under 2^-20 of the sum
 // even for 2^18 keys.
 constexpr float kTop = 13.0f, kSlack = 2.0f;
-constexpr float kNone = -1e30f;  // reference before the first key
+constexpr float kNone = -3.402823466e38f;  // reference before the first key: below every score
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -567,7 +570,7 @@ __device__ __forceinline__ void runs_body(
     // relative to 2^m, accumulators relative to 2^r.
     m0 = m1 = kNone;
     l0 = l1 = 0.f;
-    float r0 = kNone, r1 = kNone, c0 = 1.f, c1 = 1.f;  // c: 2^(m - r)
+    float d0 = 0.f, d1 = 0.f, c0 = 1.f, c1 = 1.f;  // d: r - m, c: 2^-d
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -592,7 +595,7 @@ __device__ __forceinline__ void runs_body(
       }
 
       // ---- S^T = K q^T: keys gid and gid + 8, heads 2tq and 2tq + 1 ----
-      // s[2 i + e]: key gid + 8 i, head 2 tq + e, before the factor hk.
+      // s[2 i + e]: key gid + 8 i, head 2 tq + e.
       float s[4] = {0.f, 0.f, 0.f, 0.f}, hk[4] = {hc0, hc1, hc0, hc1};
       uint32_t fa = 0, fb = 0;  // exponent bytes of the values
       if constexpr (E8) {
@@ -633,11 +636,13 @@ __device__ __forceinline__ void runs_body(
         for (int i = 0; i < 4; ++i) s[i] += s2[i];
       }
 
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] *= hk[i];
+
       // ---- weights: p relative to m, w (8-bit) relative to r ----
       float p0, p1, p2, p3, w0, w1, w2, w3;
       auto weights = [&] {
-        float x[4] = {fmaf(s[0], hk[0], -m0), fmaf(s[1], hk[1], -m1), fmaf(s[2], hk[2], -m0),
-                      fmaf(s[3], hk[3], -m1)};
+        float x[4] = {s[0] - m0, s[1] - m1, s[2] - m0, s[3] - m1};
         float va = e4m3::scale_of(fa), vb = e4m3::scale_of(fb);
         if (valid < kPage) {  // slots past the row's end: weight 0, whatever they hold
           if (gid >= valid) x[0] = x[1] = -INFINITY, va = 0.f;
@@ -647,11 +652,11 @@ __device__ __forceinline__ void runs_body(
         p1 = ex2_approx(x[1]);
         p2 = ex2_approx(x[2]);
         p3 = ex2_approx(x[3]);
-        if constexpr (E8) {  // 2^(s + f - r) = p * 2^f * 2^(m - r)
-          w0 = p0 * (va * c0);
-          w1 = p1 * (va * c1);
-          w2 = p2 * (vb * c0);
-          w3 = p3 * (vb * c1);
+        if constexpr (E8) {  // 2^(s + f - r) = p * 2^-d * 2^f, in the order whose
+          w0 = (p0 * c0) * va;  // first product is finite (2^f 2^-d may not be)
+          w1 = (p1 * c1) * va;
+          w2 = (p2 * c0) * vb;
+          w3 = (p3 * c1) * vb;
         }
       };
       weights();
@@ -661,41 +666,40 @@ __device__ __forceinline__ void runs_body(
       if constexpr (E8) up = up || fmaxf(fmaxf(w0, w1), fmaxf(w2, w3)) > 32768.f;
       if (__any_sync(0xffffffffu, up)) {
         const bool la = gid < valid, lb = gid + 8 < valid;
-        const float s0 = la ? s[0] * hk[0] : -INFINITY, s1 = la ? s[1] * hk[1] : -INFINITY;
-        const float s2 = lb ? s[2] * hk[2] : -INFINITY, s3 = lb ? s[3] * hk[3] : -INFINITY;
+        const float s0 = la ? s[0] : -INFINITY, s1 = la ? s[1] : -INFINITY;
+        const float s2 = lb ? s[2] : -INFINITY, s3 = lb ? s[3] : -INFINITY;
         const float ga = static_cast<float>(static_cast<int>(fa) - 127);
         const float gb2 = static_cast<float>(static_cast<int>(fb) - 127);
         float n0 = fmaxf(s0, s2), n1 = fmaxf(s1, s3);
-        float t0 = fmaxf(s0 + ga, s2 + gb2), t1 = fmaxf(s1 + ga, s3 + gb2);
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
           n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
           n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-          if constexpr (E8) {
-            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
-            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
-          }
         }
         n0 = fmaxf(n0, m0);
         n1 = fmaxf(n1, m1);
         float a0 = ex2_approx(m0 - n0), a1 = ex2_approx(m1 - n1);
         l0 *= a0;
         l1 *= a1;
+        if constexpr (E8) {
+          float t0 = fmaxf(s0 - n0 + ga, s2 - n0 + gb2), t1 = fmaxf(s1 - n1 + ga, s3 - n1 + gb2);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
+          }
+          // d stays above -120, so that 2^-d is finite: values all below 2^-107
+          // (rows of zeros among them) then have weights up to 2^3 instead of 2^13.
+          const float b0 = d0 + (m0 - n0), b1 = d1 + (m1 - n1);  // the old r, from the new m
+          d0 = fmaxf(fmaxf(t0 - kTop, b0), -120.f);
+          d1 = fmaxf(fmaxf(t1 - kTop, b1), -120.f);
+          a0 = ex2_approx(b0 - d0);
+          a1 = ex2_approx(b1 - d1);
+          c0 = ex2_approx(-d0);
+          c1 = ex2_approx(-d1);
+        }
         m0 = n0;
         m1 = n1;
-        if constexpr (E8) {
-          // r stays within 2^120 of m, so that 2^(m - r) is finite: values all
-          // below 2^-107 (rows of zeros among them) then have weights up to 2^3
-          // instead of 2^13.
-          t0 = fmaxf(fmaxf(t0 - kTop, r0), m0 - 120.f);
-          t1 = fmaxf(fmaxf(t1 - kTop, r1), m1 - 120.f);
-          a0 = ex2_approx(r0 - t0);
-          a1 = ex2_approx(r1 - t1);
-          r0 = t0;
-          r1 = t1;
-          c0 = ex2_approx(m0 - r0);
-          c1 = ex2_approx(m1 - r1);
-        }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           acc[k][0] *= a0;
@@ -751,7 +755,7 @@ __device__ __forceinline__ void runs_body(
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
     if constexpr (E8) {
-      const float f0 = ex2_approx(r0 - m0), f1 = ex2_approx(r1 - m1);
+      const float f0 = ex2_approx(d0), f1 = ex2_approx(d1);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         acc[k][0] *= f0;

@@ -132,11 +132,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Weights of a key tile whose V stays bf16: P_hi (upper 16 bits) in columns
-// 0-63 of the S tile, P_lo = bf16(p - P_hi) in columns 64-127. Reads the S tile
-// again (keys from lim on masked) and returns the weights' sum. Such tiles are
-// rare, so this stays out of line. Warp-collective.
-__device__ __noinline__ float two_term_weights(uint32_t tS, int lim, float scale_log2, float ref) {
+// Weights of a key tile in the rare cases, out of line: where V stays bf16
+// (`two`) P_hi (upper 16 bits) in columns 0-63 of the S tile and P_lo =
+// bf16(p - P_hi) in columns 64-127, else fp16 as in the common case. The scores
+// enter as rounded products minus the reference, which is exact near it at any
+// magnitude of the logits. Reads the S tile again (keys from lim on masked) and
+// returns the weights' sum. Warp-collective.
+__device__ __noinline__ float rare_weights(uint32_t tS, int lim, float scale_log2, float ref, bool two) {
   float sum0 = 0.f, sum1 = 0.f;
   uint32_t sr[4][32];
 #pragma unroll
@@ -152,17 +154,22 @@ __device__ __noinline__ float two_term_weights(uint32_t tS, int lim, float scale
       float x1 = __uint_as_float(sr[key >> 5][(key & 31) + 1]);
       if (key >= lim) x0 = -INFINITY;
       if (key + 1 >= lim) x1 = -INFINITY;
-      const float p0 = ex2_approx(fmaf(x0, scale_log2, -ref));
-      const float p1 = ex2_approx(fmaf(x1, scale_log2, -ref));
+      const float p0 = ex2_approx(__fsub_rn(__fmul_rn(x0, scale_log2), ref));
+      const float p1 = ex2_approx(__fsub_rn(__fmul_rn(x1, scale_log2), ref));
       sum0 += p0;
       sum1 += p1;
+      if (!two) {
+        hi[i] = pack_f16x2(p0, p1);
+        lo[i] = 0u;
+        continue;
+      }
       const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
       asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(hi[i]) : "r"(u0), "r"(u1));
       lo[i] = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u),
                           p1 - __uint_as_float(u1 & 0xffff0000u));
     }
     tc::st32(tS + 32 * half, hi);
-    tc::st32(tS + 64 + 32 * half, lo);
+    if (two) tc::st32(tS + 64 + 32 * half, lo);
   }
   return sum0 + sum1;
 }
@@ -590,10 +597,12 @@ __global__ void __launch_bounds__(384, 1)
         }
         const float cand = fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]) * scale_log2;
         float alpha = 1.f;
-        if (cand > ref + (kTop + kSlack)) {
-          alpha = ex2_approx(ref - (cand - kTop));
+        if (cand - ref > kTop + kSlack) {
+          float next = cand - kTop;  // where fp32's spacing is too wide for that, cand itself
+          if (cand - next > kTop + kSlack) next = cand;
+          alpha = ex2_approx(ref - next);
           l *= alpha;
-          ref = cand - kTop;
+          ref = next;
         }
         const bool rescale = i > 0 && __any_sync(0xffffffffu, alpha != 1.f);
         const int g = g0 + j, sv = g % C::NSV;
@@ -601,7 +610,10 @@ __global__ void __launch_bounds__(384, 1)
           ok = false;
           break;
         }
-        if (__shfl_sync(0xffffffffu, wide[sv], 0) == 0) {
+        // Below 2^20 the products' and the reference's roundings cannot take a
+        // weight past fp16's range.
+        const bool two = __shfl_sync(0xffffffffu, wide[sv], 0) != 0;
+        if (!two && !__any_sync(0xffffffffu, fabsf(ref) >= 0x1p20f)) {
           // fp16 weights: key pair (2k, 2k + 1) of chunk c in column 16c + k,
           // staged in registers whose scores are used up.
           const uint64_t c2 = f2(scale_log2, scale_log2), n2 = f2(-ref, -ref);
@@ -630,7 +642,7 @@ __global__ void __launch_bounds__(384, 1)
           unf2(add2(sumA, sumB), s0, s1);
           l += s0 + s1;
         } else {
-          l += two_term_weights(tS, lim, scale_log2, ref);
+          l += rare_weights(tS, lim, scale_log2, ref, two);
         }
         if (rescale) {
           const uint64_t a2 = f2(alpha, alpha);

@@ -228,3 +228,33 @@ def test_binding_refuses():
         with pytest.raises(attn.AttnError):
             fn(**{**good, "v": loose})
     assert attn.attn_get_device_error() == 0
+
+
+def test_offsets_lengths_and_table_rewritten_just_before():
+    """The kernel in front lets the write (the read) start at once and rewrites
+    one of table, offsets and lengths 50 us later."""
+    lens, h_kv, d = [40, 100, 7], 2, 128
+    table, nb = W.paged_layout(lens, seed=31)
+    cu = torch.tensor([0, 40, 140, 147], dtype=torch.int32)
+    where = [table.cuda(), cu.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()]
+    k, v = (W.normal((147, h_kv, d), 40 + i, torch.bfloat16).cuda() for i in range(2))
+    cache = empty_cache(nb, h_kv, d)
+    attn.attn_cache_write_e4m3(k, v, *cache, *where)
+    back = attn.attn_cache_read_e4m3(*cache, *where, torch.empty_like(k), torch.empty_like(v))
+    for i in range(3):
+        for read in (False, True):
+            old = torch.zeros_like(where[i])
+            now = where[:i] + [old] + where[i + 1:]
+            fresh = empty_cache(nb, h_kv, d)
+            out = [torch.zeros_like(k), torch.zeros_like(v)]
+            attn.attn_cache_read_e4m3(*cache, *now, torch.empty_like(k), torch.empty_like(v))  # warm
+            attn.attn_get_device_error()
+            attn.attn_selftest_delayed_copy(old.view(-1), where[i].view(-1), delay_us=50)
+            if read:
+                attn.attn_cache_read_e4m3(*cache, *now, *out)
+                assert torch.equal(out[0], back[0]) and torch.equal(out[1], back[1])
+            else:
+                attn.attn_cache_write_e4m3(k, v, *fresh, *now)
+                for a, b in zip(fresh, cache):
+                    assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+            assert attn.attn_get_device_error() == 0

@@ -8,7 +8,7 @@ import torch
 import online_softmax_attn_gb300 as attn
 import oracle
 import workloads as W
-from e4m3_cases import decode_case, empty_cache, values
+from e4m3_cases import cache_from, decode_case, empty_cache, values
 from parity import check_lse, check_out
 
 pytestmark = pytest.mark.gpu
@@ -98,8 +98,6 @@ def test_zero_value_rows_of_a_dominant_key():
     page, slot = int(table[0, 40]), 5
     one = q[0, 0].double().numpy() * 2.0
     k64[page, slot, 0] = one
-    from e4m3_cases import cache_from
-
     kc, ks = cache_from(k64.transpose(0, 2, 1, 3))
     v64 = values(vc, vs)
     v64[page, slot, 0] = 0.0
@@ -122,8 +120,6 @@ def test_flat_tail_under_a_heavy_key():
     k64 = np.zeros_like(values(kc, ks))
     page = int(table[0, 17])
     k64[page, 3, 0, 0] = 8.0 * 17 * np.log(2.0) * 1.0
-    from e4m3_cases import cache_from
-
     kc, ks = cache_from(k64.transpose(0, 2, 1, 3))
     v64 = np.ones_like(k64)
     v64[page, 3] = -1.0
@@ -340,4 +336,73 @@ def test_binding_refuses():
         call(scale="x")
     with pytest.raises((TypeError, ValueError, AttributeError)):
         call(block_table=None)
+    assert attn.attn_get_device_error() == 0
+
+
+def one_hot_keys(shape, seed, shift):
+    """Keys of small integers (each one e4m3 and bf16 number) along dim 0 only,
+    from -8 to 7 and shifted; the caller places the largest, 8 + shift."""
+    x = np.zeros(shape)
+    x[..., 0] = np.random.default_rng(seed).integers(-8, 8, shape[:-1]) + shift
+    return x
+
+
+@pytest.mark.parametrize("shift", [0, -16])
+@pytest.mark.parametrize("v_mult", [1.0, 2.0 ** 30, 2.0 ** -40])
+@pytest.mark.parametrize("exp", [16, 24, 27, 30, 40, 110])
+def test_logits_beyond_the_precision_of_differences(exp, v_mult, shift):
+    """Logits up to 2^exp in magnitude, exact up to the factor log2(e): one key
+    leads by 2^(exp - 3) or more, so the row is that key's value. In fp32 the
+    logits' spacing passes the weights' range (2^15) from 2^27 on."""
+    lens = [1000, 33]
+    q, kc, vc, ks, vs, table, n = decode_case(lens, 2, 4, 64, seed=11, v_mult=v_mult)
+    q = torch.zeros_like(q)
+    q[:, :, 0] = 2.0 ** exp  # scale 1/8: the leading key's logit is 2^exp (or -2^exp)
+    k64 = one_hot_keys(values(kc, ks).shape, 12, shift)
+    lead = [(int(table[0, 31]), 7), (int(table[1, 1]), 15)]
+    for page, slot in lead:
+        k64[page, slot, :, 0] = 8 + shift
+    kc, ks = cache_from(k64.transpose(0, 2, 1, 3))
+    args = (q, kc, vc, ks, vs, table, n)
+    O, L = reference(*args)
+    o, lse = attn.attn_decode_paged_e4m3(*cuda(*args))
+    # The weights besides the leading one's are 0; the output rounds once, the
+    # leading weight and the fp32 accumulation below 2^-20.
+    assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -8 * np.abs(O)).all()
+    # Factor, product, ln 2 and the product with it: 5 roundings of 2^-24.
+    assert (np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -21 * np.abs(L)).all()
+
+
+def test_large_values_under_a_dominant_key_without_value():
+    """Pages of zero values (the smallest exponent) with a key that leaves the
+    others no weight, then pages of large values: 0, not 0 * inf."""
+    lens = [60000]  # six pages a run
+    q, kc, vc, ks, vs, table, n = decode_case(lens, 2, 2, 64, seed=13, v_mult=2.0 ** 20)
+    q = torch.zeros_like(q)
+    q[:, :, 0] = 16.0
+    k64, v64 = np.zeros_like(values(kc, ks)), values(vc, vs)
+    pages = table[0, ::4].long().numpy()
+    k64[pages, 2, :, 0] = 96.0  # logit 192
+    v64[pages] = 0.0
+    kc, ks = cache_from(k64.transpose(0, 2, 1, 3))
+    vc, vs = cache_from(v64.transpose(0, 2, 1, 3))
+    o, lse = attn.attn_decode_paged_e4m3(*cuda(q, kc, vc, ks, vs, table, n))
+    assert (o == 0).all()  # exp(-192) * 2^20 is no fp32 number
+    assert (np.abs(lse.double().cpu().numpy() - (192 + np.log(len(pages)))) <= 1e-4).all()
+
+
+def test_lengths_and_table_rewritten_just_before():
+    """The kernel in front lets the decode start at once and rewrites lengths and
+    table 50 us later."""
+    args = decode_case([900, 40, 300], 2, 4, 128, seed=14)
+    O, L = reference(*args)
+    dev = cuda(*args)
+    for i in (5, 6):
+        old = torch.zeros_like(dev[i])
+        now = dev[:i] + [old] + dev[i + 1:]
+        attn.attn_decode_paged_e4m3(*now)  # warm: lines of the old contents
+        attn.attn_selftest_delayed_copy(old.view(-1), dev[i].view(-1), delay_us=50)
+        o, lse = attn.attn_decode_paged_e4m3(*now)
+        check_out(o, O, torch.bfloat16)
+        check_lse(lse, L)
     assert attn.attn_get_device_error() == 0

@@ -354,3 +354,51 @@ def test_far_pages_beyond_32_bit_offsets():
     check_out(o, O, torch.bfloat16)
     check_lse(lse, L)
     assert attn.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("where", ["prefix", "own"])
+@pytest.mark.parametrize("v_mult", [1.0, 1e6])
+@pytest.mark.parametrize("shift", [0, -16])
+@pytest.mark.parametrize("exp", [16, 21, 24, 27, 30, 40, 110])
+def test_logits_beyond_the_precision_of_differences(exp, shift, v_mult, where):
+    """Logits up to 2^exp in magnitude, exact up to the factor log2(e): one key
+    leads by 2^(exp - 3) or more, so the row is that key's value. In fp32 the
+    logits' spacing passes the weights' range (2^15) from 2^27 on."""
+    prefix, lens = 700, [500, 20]
+    args = case(prefix, lens, 2, 4, 64, seed=23)
+    q, k, v, ptab, plen, tab, n = args
+    q.zero_()
+    q[:, :, 0] = 2.0 ** exp  # scale 1/8: the leading key's logit is 2^exp (or -2^exp)
+    k.zero_()
+    g = torch.Generator().manual_seed(1)
+    k[..., 0] = torch.randint(-8, 8, k.shape[:-1], generator=g).to(torch.bfloat16) + shift
+    v *= v_mult
+    if where == "prefix":
+        k[int(ptab[20]), 3, :, 0] = 8 + shift
+    else:
+        for b in range(2):
+            k[int(tab[b, 1]), 3, :, 0] = 8 + shift
+    O, L = reference(*args)
+    o, lse = run(args)
+    # The weights besides the leading one's are 0; the output rounds once, and V
+    # (fp16 in the prefix: within 2^-25) and the accumulation far below that.
+    assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -8 * np.abs(O) + 2.0 ** -24).all()
+    # Factor, product, ln 2 and the product with it: 5 roundings of 2^-24.
+    assert (np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -21 * np.abs(L)).all()
+
+
+def test_lengths_and_tables_rewritten_just_before():
+    """The kernel in front lets the decode start at once and rewrites one of
+    lengths and tables 50 us later."""
+    args = case(300, [200, 0, 33], 2, 4, 128, seed=24)
+    O, L = reference(*args)
+    dev = [t.cuda() for t in args]
+    for i in (3, 4, 5, 6):
+        old = torch.zeros_like(dev[i])
+        now = dev[:i] + [old] + dev[i + 1:]
+        attn.attn_decode_paged_shared(*now)  # warm: lines of the old contents
+        attn.attn_selftest_delayed_copy(old.view(-1), dev[i].view(-1), delay_us=50)
+        o, lse = attn.attn_decode_paged_shared(*now)
+        check_out(o, O, torch.bfloat16)
+        check_lse(lse, L)
+    assert attn.attn_get_device_error() == 0
