@@ -246,6 +246,137 @@ __device__ __forceinline__ bool walk_next(Walk& w, const Rows& rw, const int* ca
   return true;
 }
 
+// A warp's run: weight (0: none; -1: none for the whole CTA), first row and its
+// length, weight between that row's first unit and the run.
+struct RunPlan {
+  long long rem, off;
+  int b, len;
+};
+
+// Plans the runs, one per warp; CTA 0 leaves the plan for the merge.
+template <int NW, class Sync>
+__device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, RunShared<NW>& sh, int cta,
+                                          int n_cta, unsigned int* err, Sync sync) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // ---- the runs: prefix sums of the rows' weights (per unit) ----
+  const long long n_runs = static_cast<long long>(n_cta) * NW;
+  auto per_of = [&](long long all) {
+    return max(static_cast<long long>(kMinRun), div_ll(all + n_runs - 1, n_runs));
+  };
+  if (lane == 0) sh.kind[warp] = sh.own[warp] = 0;  // read behind the join's barrier
+  long long all, per, p0;
+  bool have;
+  RunPlan r;
+  if (rw.B <= 32) {
+    // A row per lane: every warp plans for itself, without a barrier (9.0 us a
+    // call for a row of 1000 keys; the form below 9.4).
+    int len = 0;
+    if (lane < rw.B) {
+      const int raw = __ldcg(rw.seq_lens + lane);
+      len = min(max(raw, 0), rw.max_len);
+      if (cta == 0 && warp == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
+    }
+    sh.len[lane] = len;  // (every warp writes the same)
+    const uint32_t w = row_weight(len);
+    uint32_t incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    all = static_cast<long long>(__shfl_sync(0xffffffffu, incl, 31)) * rw.upr;
+    per = per_of(all);
+    if (cta == 0 && warp == 0) {  // for the merge
+      if (lane == 0) plan[0] = per * NW;
+      if (lane < rw.B) plan[1 + lane] = incl - w;
+      if (lane == rw.B - 1) plan[1 + rw.B] = incl;
+    }
+    if (per * NW * cta >= all) return RunPlan{-1, 0, 0, 0};
+    p0 = per * (static_cast<long long>(NW) * cta + warp);
+    have = p0 < all;
+    const long long at = static_cast<long long>(incl - w) * rw.upr;
+    const uint32_t mine =
+        __ballot_sync(0xffffffffu, p0 >= at && p0 < static_cast<long long>(incl) * rw.upr);
+    r.b = have ? __ffs(mine) - 1 : 0;
+    r.off = have ? p0 - __shfl_sync(0xffffffffu, at, r.b) : 0;
+    r.len = __shfl_sync(0xffffffffu, len, r.b);
+    __syncwarp();
+  } else {
+    const int per_t = (rw.B + NW * 32 - 1) / (NW * 32);
+    const int b0 = min(tid * per_t, rw.B), b1 = min(b0 + per_t, rw.B);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int raw = __ldcg(rw.seq_lens + b);
+      const int len = min(max(raw, 0), rw.max_len);
+      if (cta == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
+      if (b < kLenCache) sh.len[b] = len;
+      sum += row_weight(len);
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh.warp[warp] = incl;
+    sync();
+    long long before = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before += sh.warp[w];
+      total += sh.warp[w];
+    }
+    all = total * rw.upr;
+    per = per_of(all);
+    const long long cta0 = per * NW * cta;
+    if (cta == 0) {  // for the merge
+      if (tid == 0) plan[0] = per * NW;
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        plan[1 + b] = at;
+        at += row_weight(row_len(rw, sh.len, b));
+        if (b == rw.B - 1) plan[1 + rw.B] = at;
+      }
+    }
+    if (cta0 >= all) return RunPlan{-1, 0, 0, 0};
+    long long at = before * rw.upr;
+    const long long end = (before + sum) * rw.upr;
+    if (cta0 + per * NW > at && cta0 < end) {
+      for (int b = b0; b < b1; ++b) {
+        const long long next = at + static_cast<long long>(row_weight(row_len(rw, sh.len, b))) * rw.upr;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const long long p = cta0 + per * w;
+          if (p >= at && p < next) {
+            sh.b[w] = b;
+            sh.off[w] = p - at;
+          }
+        }
+        at = next;
+      }
+    }
+    sync();
+    p0 = cta0 + per * warp;
+    have = p0 < all;
+    r.b = have ? sh.b[warp] : 0;
+    r.off = have ? sh.off[warp] : 0;
+    r.len = row_len(rw, sh.len, r.b);
+  }
+  r.rem = have ? min(per, all - p0) : 0;
+  return r;
+}
+
+// The same out of line, for shared_kernel, whose two phases miss the instruction
+// cache as it is (a third of its warps' waits with 64 rows over 8192 keys). With
+// the plan inlined 256 rows over a prefix of 32768 keys took 192 us instead of
+// 182, 64 over 8192 50.9 instead of 50.3; the 8-bit decode takes it inlined (a row
+// of 32768 keys 20.7 us, this way 20.9).
+template <int NW, class Sync>
+__device__ __noinline__ RunPlan plan_runs_apart(const Rows rw, long long* plan, RunShared<NW>& sh,
+                                                int cta, int n_cta, unsigned int* err, Sync sync) {
+  return plan_runs(rw, plan, sh, cta, n_cta, err, sync);
+}
+
 // The whole of CTA `cta` of `n_cta`, by NW warps (threads 0 .. NW * 32 - 1), which
 // `sync` joins; `smem` starts at a 1024-byte boundary. Returns with every copy
 // landed.
@@ -266,9 +397,6 @@ __device__ __forceinline__ void runs_body(
   float* join = reinterpret_cast<float*>(smem + C::JOIN_OFF);
   float* ms = reinterpret_cast<float*>(smem + C::ML_OFF);  // [warp][8]
   float* ls = ms + NW * 8;
-  auto& s_warp = sh.warp;
-  auto& s_off = sh.off;
-  auto& s_b = sh.b;
   auto& s_kind = sh.kind;
   auto& s_own = sh.own;
   auto& s_own_row = sh.own_row;
@@ -278,113 +406,19 @@ __device__ __forceinline__ void runs_body(
   // the warp's ring, free by then.
   auto tail_of = [&](int w) { return reinterpret_cast<float*>(smem + w * NST * C::STAGE_BYTES); };
 
-  // ---- the runs: prefix sums of the rows' weights (per unit) ----
-  const long long n_runs = static_cast<long long>(n_cta) * NW;
-  auto per_of = [&](long long all) {
-    return max(static_cast<long long>(kMinRun), div_ll(all + n_runs - 1, n_runs));
-  };
-  if (lane == 0) s_kind[warp] = s_own[warp] = 0;  // read behind the join's barrier
-  long long all, per, p0;
-  bool have;
+  RunPlan plan;
+  if constexpr (E8)
+    plan = plan_runs(rw, out.plan, sh, cta, n_cta, err, sync);
+  else
+    plan = plan_runs_apart(rw, out.plan, sh, cta, n_cta, err, sync);
+  if (plan.rem < 0) return;  // nothing for this CTA
+  bool have = plan.rem > 0;
   Walk cw;
-  long long off;  // weight between the first row of this warp's run and the run
-  if (rw.B <= 32) {
-    // A row per lane: every warp plans for itself, without a barrier (9.0 us a
-    // call for a row of 1000 keys; the form below 9.4).
-    int len = 0;
-    if (lane < rw.B) {
-      const int raw = __ldcg(rw.seq_lens + lane);
-      len = min(max(raw, 0), rw.max_len);
-      if (cta == 0 && warp == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
-    }
-    s_len[lane] = len;  // (every warp writes the same)
-    const uint32_t w = row_weight(len);
-    uint32_t incl = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    all = static_cast<long long>(__shfl_sync(0xffffffffu, incl, 31)) * rw.upr;
-    per = per_of(all);
-    if (cta == 0 && warp == 0) {  // for the merge
-      if (lane == 0) out.plan[0] = per * NW;
-      if (lane < rw.B) out.plan[1 + lane] = incl - w;
-      if (lane == rw.B - 1) out.plan[1 + rw.B] = incl;
-    }
-    if (per * NW * cta >= all) return;
-    p0 = per * (static_cast<long long>(NW) * cta + warp);
-    have = p0 < all;
-    const long long at = static_cast<long long>(incl - w) * rw.upr;
-    const uint32_t mine =
-        __ballot_sync(0xffffffffu, p0 >= at && p0 < static_cast<long long>(incl) * rw.upr);
-    cw.b = have ? __ffs(mine) - 1 : 0;
-    off = have ? p0 - __shfl_sync(0xffffffffu, at, cw.b) : 0;
-    cw.len = __shfl_sync(0xffffffffu, len, cw.b);
-    __syncwarp();
-  } else {
-    const int per_t = (rw.B + NW * 32 - 1) / (NW * 32);
-    const int b0 = min(tid * per_t, rw.B), b1 = min(b0 + per_t, rw.B);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      const int raw = __ldcg(rw.seq_lens + b);
-      const int len = min(max(raw, 0), rw.max_len);
-      if (cta == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
-      if (b < kLenCache) s_len[b] = len;
-      sum += row_weight(len);
-    }
-    long long incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    sync();
-    long long before = incl - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      if (w < warp) before += s_warp[w];
-      total += s_warp[w];
-    }
-    all = total * rw.upr;
-    per = per_of(all);
-    const long long cta0 = per * NW * cta;
-    if (cta == 0) {  // for the merge
-      if (tid == 0) out.plan[0] = per * NW;
-      long long at = before;
-      for (int b = b0; b < b1; ++b) {
-        out.plan[1 + b] = at;
-        at += row_weight(row_len(rw, s_len, b));
-        if (b == rw.B - 1) out.plan[1 + rw.B] = at;
-      }
-    }
-    if (cta0 >= all) return;
-    long long at = before * rw.upr;
-    const long long end = (before + sum) * rw.upr;
-    if (cta0 + per * NW > at && cta0 < end) {
-      for (int b = b0; b < b1; ++b) {
-        const long long next = at + static_cast<long long>(row_weight(row_len(rw, s_len, b))) * rw.upr;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const long long p = cta0 + per * w;
-          if (p >= at && p < next) {
-            s_b[w] = b;
-            s_off[w] = p - at;
-          }
-        }
-        at = next;
-      }
-    }
-    sync();
-    p0 = cta0 + per * warp;
-    have = p0 < all;
-    cw.b = have ? s_b[warp] : 0;
-    off = have ? s_off[warp] : 0;
-    cw.len = row_len(rw, s_len, cw.b);
-  }
+  cw.b = plan.b;
+  cw.len = plan.len;
+  const long long off = plan.off;
   cw.np = (cw.len + kPage - 1) / kPage;
-  cw.rem = have ? min(per, all - p0) : 0;
+  cw.rem = plan.rem;
   {
     const int wu = cw.np + kUnit;
     cw.u = static_cast<int>(div_ll(off, wu));

@@ -419,17 +419,17 @@ __global__ void __launch_bounds__(384, 1)
           if (e == n - 1) tc::commit_elect(bar(1));  // Q's last reader
           return true;
         };
-        if (ok) ok = s_step(0);
-        if (ok && n > 1) ok = s_step(1);
-        for (int e = 0; ok && e < n; ++e) {
-          const int t = e & 1, g = g0 + tile_of(e), sv = g % C::NSV;
-          ok = wait(bar(C::B_PF + t), (base[t] + (e >> 1)) & 1) &&
-               wait(bar(C::B_VR + sv), (g / C::NSV) & 1);
-          if (!ok) break;
-          tc::fence_after();
-          issue_pv(t, sv, e >= 2, __shfl_sync(0xffffffffu, wide[sv], 0) != 0);
-          if (NT == 1 || t == 1) tc::commit_elect(bar(C::B_VE + sv));
-          if (e + 2 >= n) tc::commit_elect(bar(C::B_OF + t));  // the stream's last step
+        for (int e = -2; ok && e < n; ++e) {
+          if (e >= 0) {
+            const int t = e & 1, g = g0 + tile_of(e), sv = g % C::NSV;
+            ok = wait(bar(C::B_PF + t), (base[t] + (e >> 1)) & 1) &&
+                 wait(bar(C::B_VR + sv), (g / C::NSV) & 1);
+            if (!ok) break;
+            tc::fence_after();
+            issue_pv(t, sv, e >= 2, __shfl_sync(0xffffffffu, wide[sv], 0) != 0);
+            if (NT == 1 || t == 1) tc::commit_elect(bar(C::B_VE + sv));
+            if (e + 2 >= n) tc::commit_elect(bar(C::B_OF + t));  // the stream's last step
+          }
           if (e + 2 < n) ok = s_step(e + 2);
         }
         g0 += s.nt;
