@@ -197,7 +197,7 @@ struct RunShared {
 
 struct Rows {
   const int32_t* seq_lens;
-  int B, max_len, upr;  // upr: units per row
+  int B, max_len, upr, n_gb;  // units per row, and per (row, KV head)
 };
 
 // A warp's run, unit by unit. Warp-uniform.
@@ -253,7 +253,8 @@ struct RunPlan {
   int b, len;
 };
 
-// Plans the runs, one per warp; CTA 0 leaves the plan for the merge.
+// Plans the runs, one per warp; CTA 0 leaves the plan for the merge (none: nullptr,
+// up to 32 rows).
 template <int NW, class Sync>
 __device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, RunShared<NW>& sh, int cta,
                                           int n_cta, unsigned int* err, Sync sync) {
@@ -286,7 +287,7 @@ __device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, Run
     }
     all = static_cast<long long>(__shfl_sync(0xffffffffu, incl, 31)) * rw.upr;
     per = per_of(all);
-    if (cta == 0 && warp == 0) {  // for the merge
+    if (cta == 0 && warp == 0 && plan != nullptr) {  // for the merge
       if (lane == 0) plan[0] = per * NW;
       if (lane < rw.B) plan[1 + lane] = incl - w;
       if (lane == rw.B - 1) plan[1 + rw.B] = incl;
@@ -391,7 +392,7 @@ __device__ __forceinline__ void runs_body(
   constexpr int KS = D / 16;  // MMA steps over d_h
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tq = lane & 3;
-  const int n_gb = rw.upr / h_kv;
+  const int n_gb = rw.n_gb;
 
   const uint32_t sbase = smem_u32(smem);
   float* join = reinterpret_cast<float*>(smem + C::JOIN_OFF);

@@ -850,7 +850,7 @@ cudaError_t launch_states(const SharedArgs& s, const SharedPlan& pl, const Prefi
   own.vc = static_cast<const uint8_t*>(r.v_cache);
   own.q = static_cast<const __nv_bfloat16*>(r.q);
   own.block_table = r.block_table;
-  own.rw = Rows{r.seq_lens, r.B, r.max_blocks * kPage, r.h_kv};
+  own.rw = Rows{r.seq_lens, r.B, r.max_blocks * kPage, r.h_kv, 1};
   own.h = r.h;
   own.g = g;
   own.max_blocks = r.max_blocks;
