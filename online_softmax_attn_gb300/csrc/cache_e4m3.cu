@@ -19,8 +19,8 @@
 // side comes in whole rows of 128 bytes or more. A CTA's first threads look its
 // tokens up (a binary search over cu and the block table) while the others'
 // loads are under way. Both sides' inputs are read once and marked so (streaming
-// loads: write of 8192 tokens 11.0 us a call, 11.9 without; read of 32768 tokens
-// 32.8, 34.1 without).
+// loads took 7% off the write of 8192 tokens, now 9.6 us a call, and 4% off the
+// read of 32768, 33.1).
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "internal.h"
@@ -83,56 +83,54 @@ struct RowStrides {
 // Place of a CTA's tokens: page and slot; page -1: no place, -2: a page outside
 // the cache.
 constexpr int kBlk = 16;  // tokens per block
-constexpr int kThreads = 128;  // 256 and 512: 12.7 and 14.9 us for the write of 8192 tokens, 128: 12.4
-// Rows in flight per thread: 2 measured best for both (write of 8192 tokens 13.0,
-// 12.5, 13.9 us a call and read of 32768 tokens 41.0, 34.8, 36.7 us with 1, 2
-// and 4).
-constexpr int kU = 2;
+// Threads per CTA and rows in flight per thread, us a call for the write of 8192
+// tokens (bf16, 8 heads of 128) and the read of 32768: 64 and 2 9.8, 34.6; 128 and
+// 2 10.3, 33.1; 256 and 2 10.5, 35.8; 64 and 4 11.0, 33.1; 128 and 4 10.8, 33.1
+// (and 40 rows of heads of 64 read in fp32 22.0, else 20.9).
+constexpr int kWriteThreads = 64, kReadThreads = 128, kU = 2;
 
-template <int D, int U>
+// A CTA's rows lie in one block of 16 tokens: grid (parts of a block, blocks in y
+// and z), so that no index needs a division (with rows numbered through and
+// divided by a block's, the write of 8192 tokens took 10.9 us, else 10.2).
+template <int D, int U, int T>
 struct Cta {
-  static constexpr int L = D / 16;        // lanes per row
-  static constexpr int G = kThreads / L;       // rows at a time
-  static constexpr int ROWS = U * G;      // rows per CTA
-  static constexpr int TOKENS = (ROWS / (2 * kBlk) + 2) * kBlk;  // at least two rows per token
+  static constexpr int L = D / 16;         // lanes per row
+  static constexpr int G = T / L;   // rows at a time
+  static constexpr int ROWS = U * G;       // rows per CTA
+  static_assert(ROWS % kBlk == 0, "whole heads");
 };
 
-template <int D, int U>
-__device__ __forceinline__ void locate_tokens(const TokenMap& m, int total, int h_kv, int* s_page,
-                                              int* s_slot) {
-  using C = Cta<D, U>;
-  const int span = 2 * h_kv * kBlk;  // rows per block
-  const long long r0 = static_cast<long long>(blockIdx.x) * C::ROWS;
-  const long long t0 = r0 / span * kBlk, t1 = ((r0 + C::ROWS - 1) / span + 1) * kBlk;
-  const int n = static_cast<int>(min(static_cast<long long>(total), t1) - t0);
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+__device__ __forceinline__ long long block_of() {
+  return static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
+}
+
+__device__ __forceinline__ void locate_tokens(const TokenMap& m, int total, int* s_page, int* s_slot) {
+  const long long t = block_of() * kBlk + threadIdx.x;
+  if (threadIdx.x < kBlk && t < total) {
     int page = -1, slot = 0;
     bool bad_page = false;
-    if (!locate(m, static_cast<int>(t0) + i, &page, &slot, &bad_page)) page = -1;
-    s_page[i] = bad_page ? -2 : page;
-    s_slot[i] = slot;
+    if (!locate(m, static_cast<int>(t), &page, &slot, &bad_page)) page = -1;
+    s_page[threadIdx.x] = bad_page ? -2 : page;
+    s_slot[threadIdx.x] = slot;
   }
 }
 
-// Row `it` of a CTA's rows: its token's index within the CTA, K or V, head.
+// Row `it` of a CTA's rows: its token, that token's index within the CTA, head,
+// K or V.
 struct RowId {
-  int t, ti, head;
-  bool is_v;
+  long long t;
+  int ti, head;
+  bool is_v, live;
 };
-template <int D, int U>
-__device__ __forceinline__ RowId row_id(int it, int h_kv) {
-  using C = Cta<D, U>;
-  const int span = 2 * h_kv * kBlk;
-  const long long r0 = static_cast<long long>(blockIdx.x) * C::ROWS;
-  const long long blk0 = r0 / span;
-  const int r = static_cast<int>(r0 - blk0 * span) + it, blk = r / span, rem = r - blk * span;
+template <int D, int U, int T>
+__device__ __forceinline__ RowId row_id(int it, int total, int h_kv) {
   RowId x;
-  x.ti = blk * kBlk + rem % kBlk;
-  // Tokens behind the last count up from `total` at most by a block.
-  x.t = static_cast<int>(min(blk0 * kBlk + x.ti, 0x7fffffffll));
-  x.head = rem / kBlk;
+  x.ti = it % kBlk;
+  x.t = block_of() * kBlk + x.ti;
+  x.head = static_cast<int>(blockIdx.x) * (Cta<D, U, T>::ROWS / kBlk) + it / kBlk;
   x.is_v = x.head >= h_kv;
   if (x.is_v) x.head -= h_kv;
+  x.live = x.t < total && x.head < h_kv;
   return x;
 }
 
@@ -142,33 +140,27 @@ struct Raw {
   uint4 w[BF16 ? 2 : 4];
 };
 
-// Exponent byte from the row's largest finite magnitude (fp32 bits), codes of
-// 8 numbers.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
-  uint2 w;
-  w.x = e4m3::encode2(x[0] * inv, x[1] * inv) | (e4m3::encode2(x[2] * inv, x[3] * inv) << 16);
-  w.y = e4m3::encode2(x[4] * inv, x[5] * inv) | (e4m3::encode2(x[6] * inv, x[7] * inv) << 16);
-  return w;
-}
-
+// Codes of chunk c of a lane's numbers, times 2^-e. Exact in bf16 too, whose
+// exponents are fp32's.
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const Raw<BF16>& r, int c, float (&x)[8]) {
-  if constexpr (BF16) {
-    const uint32_t w[4] = {r.w[c].x, r.w[c].y, r.w[c].z, r.w[c].w};
+__device__ __forceinline__ uint2 encode8(const Raw<BF16>& r, int c, uint32_t e) {
+  uint32_t y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16lo(w[i]);
-      x[2 * i + 1] = bf16hi(w[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      x[4 * i] = __uint_as_float(r.w[2 * c + i].x);
-      x[4 * i + 1] = __uint_as_float(r.w[2 * c + i].y);
-      x[4 * i + 2] = __uint_as_float(r.w[2 * c + i].z);
-      x[4 * i + 3] = __uint_as_float(r.w[2 * c + i].w);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      const uint32_t w[4] = {r.w[c].x, r.w[c].y, r.w[c].z, r.w[c].w};
+      const uint32_t inv = (254u - e) * 0x00800080u;  // 2^-e twice
+      const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&inv));
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(&p);
+      y[i] = e4m3::encode2(bf16lo(u), bf16hi(u));
+    } else {
+      const uint4 q = r.w[2 * c + (i >> 1)];
+      const float inv = e4m3::inv_scale_of(e);
+      y[i] = e4m3::encode2(__uint_as_float(i & 1 ? q.z : q.x) * inv, __uint_as_float(i & 1 ? q.w : q.y) * inv);
     }
   }
+  return make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
 }
 
 // fp32 bits of the largest magnitude among a lane's 16 numbers (NaN and
@@ -191,13 +183,14 @@ __device__ __forceinline__ uint32_t max_bits(const Raw<BF16>& r) {
 }
 
 template <int D, bool BF16, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kWriteThreads)
     cache_write_kernel(const void* __restrict__ k, const void* __restrict__ v, RowStrides sk,
                        RowStrides sv, TokenMap m, int total, int h_kv, uint8_t* __restrict__ kc,
                        uint8_t* __restrict__ vc, uint8_t* __restrict__ ks,
                        uint8_t* __restrict__ vs) {
-  using C = Cta<D, U>;
-  __shared__ int s_page[C::TOKENS], s_slot[C::TOKENS];
+  constexpr int T = kWriteThreads;
+  using C = Cta<D, U, T>;
+  __shared__ int s_page[kBlk], s_slot[kBlk];
   const int sub = threadIdx.x % C::L, grp = threadIdx.x / C::L;
   pdl_wait();
   pdl_trigger();
@@ -205,8 +198,8 @@ __global__ void __launch_bounds__(kThreads)
   Raw<BF16> x[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const RowId id = row_id<D, U>(u * C::G + grp, h_kv);
-    if (id.t < total) {
+    const RowId id = row_id<D, U, T>(u * C::G + grp, total, h_kv);
+    if (id.live) {
       const RowStrides st = id.is_v ? sv : sk;
       const long long off = id.t * st.tok + id.head * st.head + sub * 8;
 #pragma unroll
@@ -226,43 +219,52 @@ __global__ void __launch_bounds__(kThreads)
       for (int c = 0; c < (BF16 ? 2 : 4); ++c) x[u].w[c] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  locate_tokens<D, U>(m, total, h_kv, s_page, s_slot);
+  locate_tokens(m, total, s_page, s_slot);
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     uint32_t a = max_bits<BF16>(x[u]);
 #pragma unroll
     for (int o = 1; o < C::L; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-    float y[2][8];
-    unpack8<BF16>(x[u], 0, y[0]);
-    unpack8<BF16>(x[u], 1, y[1]);
     if (__any_sync(0xffffffffu, a >= 0x7f800000u)) {
       // A NaN or an infinity has no e4m3 code of its own: it is stored as NaN,
       // so that it cannot turn into a finite key, and has no part in the scale.
       a = 0;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < (BF16 ? 2 : 4); ++c) {
+        uint32_t* const w[4] = {&x[u].w[c].x, &x[u].w[c].y, &x[u].w[c].z, &x[u].w[c].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t b = __float_as_uint(y[c][i]) & 0x7fffffffu;
-          if (b >= 0x7f800000u)
-            y[c][i] = __uint_as_float(0x7fffffffu);
-          else
-            a = max(a, b);
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (BF16) {
+#pragma unroll
+            for (int s = 0; s < 32; s += 16) {
+              const uint32_t b = (*w[i] >> s) & 0x7fffu;
+              if (b >= 0x7f80u)
+                *w[i] |= 0x7fffu << s;
+              else
+                a = max(a, b << 16);
+            }
+          } else {
+            const uint32_t b = *w[i] & 0x7fffffffu;
+            if (b >= 0x7f800000u)
+              *w[i] |= 0x7fffffffu;
+            else
+              a = max(a, b);
+          }
         }
+      }
 #pragma unroll
       for (int o = 1; o < C::L; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
     }
     const uint32_t e = e4m3::scale_byte(a);
-    const float inv = e4m3::inv_scale_of(e);
-    const RowId id = row_id<D, U>(u * C::G + grp, h_kv);
-    if (id.t >= total || s_page[id.ti] < 0) continue;
+    const RowId id = row_id<D, U, T>(u * C::G + grp, total, h_kv);
+    if (!id.live || s_page[id.ti] < 0) continue;
     const size_t row =
         (static_cast<size_t>(s_page[id.ti]) * h_kv + id.head) * kPage + s_slot[id.ti];
     if (!ATTN_GUARD(row < static_cast<size_t>(m.num_blocks) * h_kv * kPage, &g_cache8_err)) continue;
     uint8_t* dst = (id.is_v ? vc : kc) + row * D + sub * 8;
-    *reinterpret_cast<uint2*>(dst) = encode8(y[0], inv);
-    *reinterpret_cast<uint2*>(dst + D / 2) = encode8(y[1], inv);
+    *reinterpret_cast<uint2*>(dst) = encode8<BF16>(x[u], 0, e);
+    *reinterpret_cast<uint2*>(dst + D / 2) = encode8<BF16>(x[u], 1, e);
     if (sub == 0) (id.is_v ? vs : ks)[row] = static_cast<uint8_t>(e);
   }
 }
@@ -271,26 +273,27 @@ __global__ void __launch_bounds__(kThreads)
 // of a warp fills its sectors (two halves of a sector in two stores took 28.1 us
 // for 86 MB of them, 40 rows of up to 1999 tokens).
 template <int D, bool BF16, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kReadThreads)
     cache_read_kernel(const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
                       const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs, TokenMap m,
                       int total, int h_kv, void* __restrict__ k, void* __restrict__ v,
                       RowStrides sk, RowStrides sv) {
-  using C = Cta<D, U>;
-  __shared__ int s_page[C::TOKENS], s_slot[C::TOKENS];
+  constexpr int T = kReadThreads;
+  using C = Cta<D, U, T>;
+  __shared__ int s_page[kBlk], s_slot[kBlk];
   const int sub = threadIdx.x % C::L, grp = threadIdx.x / C::L;
   pdl_wait();
   pdl_trigger();
-  locate_tokens<D, U>(m, total, h_kv, s_page, s_slot);
+  locate_tokens(m, total, s_page, s_slot);
   __syncthreads();
   uint32_t w[U][4];  // codes: two chunks of 8, or four of 4
   uint32_t e[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const RowId id = row_id<D, U>(u * C::G + grp, h_kv);
+    const RowId id = row_id<D, U, T>(u * C::G + grp, total, h_kv);
     w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0u;  // a page outside the cache reads as zeros
     e[u] = 127u;
-    if (id.t < total && s_page[id.ti] >= 0) {
+    if (id.live && s_page[id.ti] >= 0) {
       const size_t row =
           (static_cast<size_t>(s_page[id.ti]) * h_kv + id.head) * kPage + s_slot[id.ti];
       const uint8_t* src = (id.is_v ? vc : kc) + row * D + sub * (BF16 ? 8 : 4);
@@ -307,8 +310,8 @@ __global__ void __launch_bounds__(kThreads)
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const RowId id = row_id<D, U>(u * C::G + grp, h_kv);
-    if (id.t >= total || s_page[id.ti] == -1) continue;
+    const RowId id = row_id<D, U, T>(u * C::G + grp, total, h_kv);
+    if (!id.live || s_page[id.ti] == -1) continue;
     const float sc = e4m3::scale_of(e[u]);
     const RowStrides st = id.is_v ? sv : sk;
     const long long off = id.t * st.tok + id.head * st.head + sub * (BF16 ? 8 : 4);
@@ -337,22 +340,22 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <int D, int U>
+template <int D, int U, int T>
 cudaError_t grid_of(const CacheTokens& a, dim3* grid) {
-  const long long rows = (static_cast<long long>(a.total) + kBlk - 1) / kBlk * kBlk * 2 * a.h_kv;
-  const long long blocks = (rows + Cta<D, U>::ROWS - 1) / Cta<D, U>::ROWS;
-  if (blocks > 0x7fffffffll) return cudaErrorNotSupported;
-  *grid = dim3(static_cast<unsigned>(blocks));
+  constexpr int kHeads = Cta<D, U, T>::ROWS / kBlk;  // per CTA, K and V counted apart
+  const long long blocks = (static_cast<long long>(a.total) + kBlk - 1) / kBlk;
+  const unsigned y = static_cast<unsigned>(blocks < 65535 ? blocks : 65535);
+  *grid = dim3(unsigned((2 * a.h_kv + kHeads - 1) / kHeads), y, unsigned((blocks + y - 1) / y));
   return cudaSuccess;
 }
 
 template <int D, bool BF16, int U>
 cudaError_t launch_write_u(const CacheTokens& a, cudaStream_t stream) {
   dim3 grid;
-  const cudaError_t e = grid_of<D, U>(a, &grid);
+  const cudaError_t e = grid_of<D, U, kWriteThreads>(a, &grid);
   if (e != cudaSuccess) return e;
   const TokenMap m{a.block_table, a.cu, a.seq_lens, a.B, a.max_blocks, a.num_blocks};
-  return launch_pdl(cache_write_kernel<D, BF16, U>, grid, dim3(kThreads), 0, stream,
+  return launch_pdl(cache_write_kernel<D, BF16, U>, grid, dim3(kWriteThreads), 0, stream,
                     static_cast<const void*>(a.k), static_cast<const void*>(a.v),
                     RowStrides{a.k_tok, a.k_head}, RowStrides{a.v_tok, a.v_head}, m, a.total,
                     a.h_kv, a.k_codes, a.v_codes, a.k_exp, a.v_exp);
@@ -361,10 +364,10 @@ cudaError_t launch_write_u(const CacheTokens& a, cudaStream_t stream) {
 template <int D, bool BF16, int U>
 cudaError_t launch_read_u(const CacheTokens& a, cudaStream_t stream) {
   dim3 grid;
-  const cudaError_t e = grid_of<D, U>(a, &grid);
+  const cudaError_t e = grid_of<D, U, kReadThreads>(a, &grid);
   if (e != cudaSuccess) return e;
   const TokenMap m{a.block_table, a.cu, a.seq_lens, a.B, a.max_blocks, a.num_blocks};
-  return launch_pdl(cache_read_kernel<D, BF16, U>, grid, dim3(kThreads), 0, stream,
+  return launch_pdl(cache_read_kernel<D, BF16, U>, grid, dim3(kReadThreads), 0, stream,
                     static_cast<const uint8_t*>(a.k_codes), static_cast<const uint8_t*>(a.v_codes),
                     static_cast<const uint8_t*>(a.k_exp), static_cast<const uint8_t*>(a.v_exp), m,
                     a.total, a.h_kv, a.k, a.v, RowStrides{a.k_tok, a.k_head},

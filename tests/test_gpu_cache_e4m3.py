@@ -258,3 +258,25 @@ def test_offsets_lengths_and_table_rewritten_just_before():
                 for a, b in zip(fresh, cache):
                     assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
             assert attn.attn_get_device_error() == 0
+
+
+def test_more_tokens_than_one_grid_dimension_holds():
+    """Two rows of over half a million tokens each, the same thousand repeated:
+    written and read back through blocks beyond 65535."""
+    base, n = 1000, 65535 * 16 + 1000
+    k0, v0 = (W.normal((base, 1, 64), 60 + i, torch.bfloat16) for i in range(2))
+    k, v = (t.repeat(n // base + 1, 1, 1)[:n].contiguous().cuda() for t in (k0, v0))
+    lens = [n // 2 + 3, n - n // 2 - 3]
+    pages = [(x + 15) // 16 for x in lens]
+    table = torch.full((2, max(pages)), -1, dtype=torch.int32)
+    table[0, :pages[0]] = torch.arange(pages[0], dtype=torch.int32)
+    table[1, :pages[1]] = torch.arange(pages[0], sum(pages), dtype=torch.int32).flip(0)
+    cache = empty_cache(sum(pages), 1, 64)
+    where = (table.cuda(), torch.tensor([0, lens[0], n], dtype=torch.int32).cuda(),
+             torch.tensor(lens, dtype=torch.int32).cuda())
+    attn.attn_cache_write_e4m3(k, v, *cache, *where)
+    outs = attn.attn_cache_read_e4m3(*cache, *where, torch.empty_like(k), torch.empty_like(v))
+    for x0, out in zip((k0, v0), outs):
+        want = torch.from_numpy(ref.values_ref(*ref.quantise_ref(x0.double().numpy()))).to(torch.bfloat16).cuda()
+        assert torch.equal(out, want.repeat(n // base + 1, 1, 1)[:n])
+    assert attn.attn_get_device_error() == 0
