@@ -739,8 +739,8 @@ __global__ void __launch_bounds__(kMergeRows* D / 4) shared_merge_kernel(const M
   // The next kernel may start once every CTA of this one runs. With more CTAs
   // than the GPU holds at a time (three per SM) it would come in on whichever
   // SMs fall free: the next call's row blocks, neighbours that share key tiles,
-  // then lie scattered (256 rows over 32768 keys: 220 us a call, else 178),
-  // while 64 rows over 8192 keys gain (54 us without, 49.5 with).
+  // then lie scattered (256 rows over 32768 keys: 215 us a call, else 181),
+  // while 64 rows over 8192 keys gain (55.0 us without, 50.0 with).
   if (gridDim.x * gridDim.y <= 3 * 152) pdl_trigger();
   if (pr >= a.p.rows) return;
   const int b = static_cast<int>(pr / a.g), hh = static_cast<int>(pr % a.g);
