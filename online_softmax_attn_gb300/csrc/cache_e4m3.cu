@@ -16,11 +16,15 @@
 // rows in flight. Rows are ordered (block of 16 tokens, K heads then V heads,
 // token): neighbouring groups then write (read) neighbouring slots of one page
 // and head, runs of 16 * d_h bytes with their exponents, while the tensors'
-// side comes in whole rows of 128 bytes or more. A CTA's first threads look its
-// tokens up (a binary search over cu and the block table) while the others'
-// loads are under way. Both sides' inputs are read once and marked so (streaming
-// loads took 7% off the write of 8192 tokens, now 9.6 us a call, and 4% off the
-// read of 32768, 33.1).
+// side comes in whole rows of 128 bytes or more. A CTA's first warp looks its
+// tokens up (cu, lengths, block table) while the others' loads are under way. Both
+// sides' inputs are read once and marked so (streaming loads took 7% off the write
+// of 8192 tokens, now 9.7 us a call, and 4% off the read of 32768, 33.6).
+//
+// Both kernels may become resident while the kernel in front still writes what
+// they read, so that none of it is constant for their lifetime: nothing is read
+// before pdl_wait, and no load is a non-coherent one. Offsets, lengths, table and
+// exponents come from L2.
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "internal.h"
@@ -34,10 +38,6 @@ namespace {
 
 using e4m3::kPage;
 
-// Flat slot (page * h_kv + head) * 16 + slot of token t, or -1 where it has
-// none: a token before or behind the sequences (silently: padding), one whose
-// position lies outside its table row, or one on a page outside the cache
-// (both with an error bit; *bad_page tells the latter apart).
 struct TokenMap {
   const int32_t* block_table;
   const int32_t* cu;
@@ -45,28 +45,65 @@ struct TokenMap {
   int B, max_blocks, num_blocks;
 };
 
-__device__ __forceinline__ int last_row_at(const TokenMap& m, int t) {
-  int lo = 0, hi = m.B;  // rows [0, lo) start at or before t's row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(m.cu + mid) <= t) lo = mid; else hi = mid;
+// Offsets and lengths of 32 rows from `lo` on, one per lane; a token's row is
+// among them or behind them. Everything of the lookup comes from L2, so round
+// trips count: these are one, the table another (each lane searching its row for
+// itself took 31.9 us for the write of 24 ragged rows, 33000 tokens of 64 in fp32,
+// this way 24.3). Beyond 32 rows it is one more for each factor of 32.
+struct NearRows {
+  int lo, cu, len;
+};
+__device__ __forceinline__ NearRows near_rows(const TokenMap& m, int t0) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = m.B;  // t0's row is one of [lo, lo + n)
+  while (n > 32) {
+    const int step = (n + 31) >> 5, i = lane * step;
+    const bool le = lane == 0 || (i < n && __ldcg(m.cu + lo + i) <= t0);
+    const int k = __ffs(~__ballot_sync(0xffffffffu, le));  // lanes 0 .. k - 2, or all (0)
+    const int at = ((k == 0 ? 33 : k) - 2) * step;
+    lo += at;
+    n = min(step, n - at);
   }
-  return lo;
+  NearRows x;
+  x.lo = lo;
+  x.cu = lo + lane <= m.B ? __ldcg(m.cu + lo + lane) : 0x7fffffff;
+  x.len = lo + lane < m.B ? __ldcg(m.seq_lens + lo + lane) : 0;
+  return x;
 }
 
-__device__ __forceinline__ bool locate(const TokenMap& m, int t, int* page, int* slot,
-                                       bool* bad_page) {
+// Page and slot of token t, false where it has none: a token before or behind the
+// sequences (silently: padding) or one whose position lies outside its table row.
+// One on a page outside the cache has a slot, and *bad_page (both of these with an
+// error bit). By a whole warp, each lane with a token at or behind x's.
+__device__ __forceinline__ bool locate(const TokenMap& m, const NearRows& x, int t, int* page,
+                                       int* slot, bool* bad_page) {
   *bad_page = false;
-  const int b = last_row_at(m, t);
-  // One round trip: the length is loaded beside the offsets it is used with.
-  const int begin = __ldg(m.cu + b), end = __ldg(m.cu + b + 1), len = __ldg(m.seq_lens + b);
+  int r = 0;  // the last of the 32 rows that starts at or before t
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    if (s >= m.B) continue;
+    const int v = __shfl_sync(0xffffffffu, x.cu, r + s);
+    if (x.lo + r + s < m.B && v <= t) r += s;
+  }
+  int begin = __shfl_sync(0xffffffffu, x.cu, r), end = __shfl_sync(0xffffffffu, x.cu, (r + 1) & 31);
+  int len = __shfl_sync(0xffffffffu, x.len, r), b = x.lo + r;
+  if (r == 31) {  // its end, or its row, lies behind them (empty rows between the tokens)
+    int hi = m.B;
+    while (hi - b > 1) {
+      const int mid = b + ((hi - b) >> 1);
+      if (__ldcg(m.cu + mid) <= t) b = mid; else hi = mid;
+    }
+    begin = __ldcg(m.cu + b);
+    end = __ldcg(m.cu + b + 1);
+    len = __ldcg(m.seq_lens + b);
+  }
   const long long pos = static_cast<long long>(len) - end + t;
   if (t < begin || t >= end) return false;  // no sequence's token
   if (pos < 0 || pos >= static_cast<long long>(m.max_blocks) * kPage) {
     atomicOr(&g_cache8_err, ATTN_DEVERR_BAD_SEQ_LEN);
     return false;
   }
-  const int p = __ldg(m.block_table + static_cast<size_t>(b) * m.max_blocks + pos / kPage);
+  const int p = __ldcg(m.block_table + static_cast<size_t>(b) * m.max_blocks + pos / kPage);
   *slot = static_cast<int>(pos % kPage);
   *page = p;
   if (p < 0 || p >= m.num_blocks) {
@@ -83,11 +120,11 @@ struct RowStrides {
 // Place of a CTA's tokens: page and slot; page -1: no place, -2: a page outside
 // the cache.
 constexpr int kBlk = 16;  // tokens per block
-// Threads per CTA and rows in flight per thread, us a call for the write of 8192
-// tokens (bf16, 8 heads of 128) and the read of 32768: 64 and 2 9.8, 34.6; 128 and
-// 2 10.3, 33.1; 256 and 2 10.5, 35.8; 64 and 4 11.0, 33.1; 128 and 4 10.8, 33.1
-// (and 40 rows of heads of 64 read in fp32 22.0, else 20.9).
-constexpr int kWriteThreads = 64, kReadThreads = 128, kU = 2;
+// Threads per CTA and rows in flight per thread. Write of 8192 tokens (bf16, 8
+// heads of 128), us a call: 64 and 2 10.3, 128 and 2 9.7, 256 and 2 10.6. Read of
+// 32768: 64 and 2 34.6, 128 and 2 33.6, 256 and 2 35.8; 4 rows no faster (and
+// 40 rows of heads of 64 read in fp32 22.0, else 20.9).
+constexpr int kWriteThreads = 128, kReadThreads = 128, kU = 2;
 
 // A CTA's rows lie in one block of 16 tokens: grid (parts of a block, blocks in y
 // and z), so that no index needs a division (with rows numbered through and
@@ -104,15 +141,22 @@ __device__ __forceinline__ long long block_of() {
   return static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
 }
 
-__device__ __forceinline__ void locate_tokens(const TokenMap& m, int total, int* s_page, int* s_slot) {
-  const long long t = block_of() * kBlk + threadIdx.x;
-  if (threadIdx.x < kBlk && t < total) {
-    int page = -1, slot = 0;
-    bool bad_page = false;
-    if (!locate(m, static_cast<int>(t), &page, &slot, &bad_page)) page = -1;
-    s_page[threadIdx.x] = bad_page ? -2 : page;
-    s_slot[threadIdx.x] = slot;
-  }
+// Both by a CTA's first warp: the lookup's first loads, and what is left of it.
+__device__ __forceinline__ NearRows tokens_near(const TokenMap& m, int total) {
+  const long long t0 = block_of() * kBlk;
+  return threadIdx.x < 32 && t0 < total ? near_rows(m, static_cast<int>(t0)) : NearRows{0, 0, 0};
+}
+__device__ __forceinline__ void locate_tokens(const TokenMap& m, const NearRows& x, int total,
+                                              int* s_page, int* s_slot) {
+  const long long t0 = block_of() * kBlk;
+  if (threadIdx.x >= 32 || t0 >= total) return;
+  // Lanes without a token of their own have the last one's place.
+  const int i = min(static_cast<int>(threadIdx.x), min(kBlk, static_cast<int>(total - t0)) - 1);
+  int page = -1, slot = 0;
+  bool bad_page = false;
+  if (!locate(m, x, static_cast<int>(t0) + i, &page, &slot, &bad_page)) page = -1;
+  s_page[i] = bad_page ? -2 : page;  // (lanes of one token write the same)
+  s_slot[i] = slot;
 }
 
 // Row `it` of a CTA's rows: its token, that token's index within the CTA, head,
@@ -184,10 +228,9 @@ __device__ __forceinline__ uint32_t max_bits(const Raw<BF16>& r) {
 
 template <int D, bool BF16, int U>
 __global__ void __launch_bounds__(kWriteThreads)
-    cache_write_kernel(const void* __restrict__ k, const void* __restrict__ v, RowStrides sk,
-                       RowStrides sv, TokenMap m, int total, int h_kv, uint8_t* __restrict__ kc,
-                       uint8_t* __restrict__ vc, uint8_t* __restrict__ ks,
-                       uint8_t* __restrict__ vs) {
+    cache_write_kernel(const void* k, const void* v, RowStrides sk, RowStrides sv, TokenMap m,
+                       int total, int h_kv, uint8_t* __restrict__ kc, uint8_t* __restrict__ vc,
+                       uint8_t* __restrict__ ks, uint8_t* __restrict__ vs) {
   constexpr int T = kWriteThreads;
   using C = Cta<D, U, T>;
   __shared__ int s_page[kBlk], s_slot[kBlk];
@@ -219,7 +262,7 @@ __global__ void __launch_bounds__(kWriteThreads)
       for (int c = 0; c < (BF16 ? 2 : 4); ++c) x[u].w[c] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  locate_tokens(m, total, s_page, s_slot);
+  locate_tokens(m, tokens_near(m, total), total, s_page, s_slot);
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -274,9 +317,8 @@ __global__ void __launch_bounds__(kWriteThreads)
 // for 86 MB of them, 40 rows of up to 1999 tokens).
 template <int D, bool BF16, int U>
 __global__ void __launch_bounds__(kReadThreads)
-    cache_read_kernel(const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
-                      const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs, TokenMap m,
-                      int total, int h_kv, void* __restrict__ k, void* __restrict__ v,
+    cache_read_kernel(const uint8_t* kc, const uint8_t* vc, const uint8_t* ks, const uint8_t* vs,
+                      TokenMap m, int total, int h_kv, void* __restrict__ k, void* __restrict__ v,
                       RowStrides sk, RowStrides sv) {
   constexpr int T = kReadThreads;
   using C = Cta<D, U, T>;
@@ -284,7 +326,7 @@ __global__ void __launch_bounds__(kReadThreads)
   const int sub = threadIdx.x % C::L, grp = threadIdx.x / C::L;
   pdl_wait();
   pdl_trigger();
-  locate_tokens(m, total, s_page, s_slot);
+  locate_tokens(m, tokens_near(m, total), total, s_page, s_slot);
   __syncthreads();
   uint32_t w[U][4];  // codes: two chunks of 8, or four of 4
   uint32_t e[U];
@@ -305,7 +347,7 @@ __global__ void __launch_bounds__(kReadThreads)
 #pragma unroll
         for (int c = 0; c < 4; ++c) w[u][c] = __ldcs(reinterpret_cast<const uint32_t*>(src + c * (D / 4)));
       }
-      e[u] = __ldg((id.is_v ? vs : ks) + row);
+      e[u] = __ldcg((id.is_v ? vs : ks) + row);
     }
   }
 #pragma unroll
