@@ -49,7 +49,14 @@ namespace {
 
 constexpr int kBM = 128, kBN = 128;
 // kTop, kSlack (decode_runs.cuh): a row's reference is set kTop below a new
-// maximum and moves when a score passes it by kTop + kSlack.
+// maximum and moves when a score passes it by kTop + kSlack. fp16 weights need
+// that room below them. With weights of up to 2^15 a sum over V passes fp32's
+// range from |v| = 2^113 on, where its result need not: once a tile holds a
+// magnitude of 2^kHuge the segment's rows go on with the maximum itself as
+// reference, and its tiles stay bf16 with the two-term P. Up to 2^kHuge sums over
+// 2^30 keys stay below 2^109.
+constexpr int kHuge = 64;
+constexpr int kVFp16 = 0, kVWide = 1, kVHuge = 2;  // a V tile's format (wide[])
 
 template <int D, int NT>
 struct SpCfg {
@@ -448,15 +455,18 @@ __global__ void __launch_bounds__(384, 1)
       for (long long p = run.lo; ok && p < run.hi;) {
         const Seg s = seg_at(p);
         p += s.nt;
+        bool huge = false;  // a tile of the segment so far
         for (int j = 0; j < s.nt; ++j) {
           const int g = g0 + j, sv = g % C::NSV;
           if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_VF + sv), (g / C::NSV) & 1, abort_flag)))
             ok = false;
           const uint32_t base = sbase + C::V_OFF + sv * C::TILE + ct * 16;
           const int lim = min(kBN, run.len - (s.t0 + j) * kBN);  // keys that exist
-          // 0 * h sums to NaN once a number does not fit fp16 (inf or NaN there);
-          // the sum of squares reaches 2^-12 where a magnitude reaches 2^-6.
-          __half2 bad = __floats2half2_rn(0.f, 0.f), big = bad;
+          // The largest magnitude, as bits below the sign's (a NaN counts as one),
+          // pairs as signed halves behind a set sign bit; the sum of squares
+          // reaches 2^-12 where a magnitude reaches 2^-6.
+          uint32_t top = 0x80008000u;
+          __half2 big = __floats2half2_rn(0.f, 0.f);
           if (ok) {
 #pragma unroll 1
             for (int i0 = 0; i0 < PER; i0 += UN) {
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   hh[k] = __floats2half2_rn(bf16lo(w[k]), bf16hi(w[k]));
-                  bad = __hfma2(hh[k], __floats2half2_rn(0.f, 0.f), bad);
+                  asm("max.s16x2 %0, %0, %1;" : "+r"(top) : "r"(w[k] | 0x80008000u));
                   big = __hfma2(hh[k], hh[k], big);
                 }
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
@@ -489,7 +499,8 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
           }
-          const bool too_big = !(__low2float(bad) == 0.f && __high2float(bad) == 0.f);
+          const uint32_t most = max(top & 0x7fffu, (top >> 16) & 0x7fffu);
+          const bool too_big = most >= ((127u + 16) << 7);
           const bool fits = __low2float(big) >= 0x1p-12f || __high2float(big) >= 0x1p-12f;
           int some_big, some_ok;
           asm volatile(
@@ -503,8 +514,18 @@ __global__ void __launch_bounds__(384, 1)
               : "=r"(some_big), "=r"(some_ok)
               : "r"(too_big ? 1 : 0), "r"(fits ? 1 : 0)
               : "memory");
-          const int two = some_big | (some_ok ^ 1);
+          const int two = some_big | (some_ok ^ 1) | (huge ? 1 : 0);
           if (two) {
+            int some_huge;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ge.u32 p, %1, %2;\n\t"
+                "barrier.cta.red.or.pred q, 1, 64, p;\n\t"
+                "selp.s32 %0, 1, 0, q;\n\t}"
+                : "=r"(some_huge)
+                : "r"(most), "r"((127u + kHuge) << 7)
+                : "memory");
+            huge = huge || some_huge;
             // The tile as it was. The generic writes above come before the
             // copy engine's.
             fence_proxy_async_smem();
@@ -530,7 +551,7 @@ __global__ void __launch_bounds__(384, 1)
                                "r"(0u)
                                : "memory");
           }
-          if (ct == 0) wide[sv] = two;
+          if (ct == 0) wide[sv] = two ? (huge ? kVHuge : kVWide) : kVFp16;
           fence_proxy_async_smem();  // the MMA reads V through the async proxy
           mbar_arrive(bar(C::B_VR + sv));
           // Agreed by both warps before either goes on (an abort ends both).
@@ -567,7 +588,7 @@ __global__ void __launch_bounds__(384, 1)
       const int touch = group - static_cast<int>((static_cast<long long>(s.kvh) * run.tiles) / run.per);
       p += s.nt;
       const int n = n_of(s, t);
-      float ref = kNone, l = 0.f;
+      float ref = kNone, l = 0.f, top = kTop;
       for (int i = 0; i < n; ++i, ++cnt) {
         const int j = NT == 2 ? i : 2 * i + t;  // key tile within the segment
         if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_SF + t), cnt & 1, abort_flag))) {
@@ -598,22 +619,29 @@ __global__ void __launch_bounds__(384, 1)
         }
         const float cand = fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]) * scale_log2;
         float alpha = 1.f;
-        if (cand - ref > kTop + kSlack) {
-          float next = cand - kTop;  // where fp32's spacing is too wide for that, cand itself
-          if (cand - next > kTop + kSlack) next = cand;
+        if (cand - ref > top + kSlack) {
+          float next = cand - top;  // where fp32's spacing is too wide for that, cand itself
+          if (cand - next > top + kSlack) next = cand;
           alpha = ex2_approx(ref - next);
           l *= alpha;
           ref = next;
         }
-        const bool rescale = i > 0 && __any_sync(0xffffffffu, alpha != 1.f);
         const int g = g0 + j, sv = g % C::NSV;
         if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_VR + sv), (g / C::NSV) & 1, abort_flag))) {
           ok = false;
           break;
         }
+        const int fmt = __shfl_sync(0xffffffffu, wide[sv], 0);
+        if (fmt == kVHuge && top != 0.f) {  // from here on weights of at most 2^kSlack
+          const float next = ref + top, down = ex2_approx(ref - next);
+          alpha *= down;
+          l *= down;
+          ref = next;
+          top = 0.f;
+        }
+        const bool two = fmt != kVFp16, rescale = i > 0 && __any_sync(0xffffffffu, alpha != 1.f);
         // Below 2^20 the products' and the reference's roundings cannot take a
         // weight past fp16's range.
-        const bool two = __shfl_sync(0xffffffffu, wide[sv], 0) != 0;
         if (!two && !__any_sync(0xffffffffu, fabsf(ref) >= 0x1p20f)) {
           // fp16 weights: key pair (2k, 2k + 1) of chunk c in column 16c + k,
           // staged in registers whose scores are used up.
