@@ -30,13 +30,13 @@
 // same tiles at the same time, so the L2 serves all but one of them. A run that
 // crosses a head border gives two states.
 //
-// P V is one fp16 MMA chain where V's tile fits fp16: two warps convert each V
-// tile in shared memory as it lands (bf16 has 8 significant bits, so values in
-// [2^-14, 2^16) convert exactly and smaller ones within 2^-25) and zero the
-// slots past the last key. A tile holding a magnitude of 2^16 or more, inf or
-// NaN, or nothing above 2^-6 (whose small values would lose bits) is loaded
-// again and stays bf16, with P = P_hi + P_lo in two MMAs. With the two-term P
-// everywhere the prefix of 256 rows over 32768 keys took 205 us.
+// P V is one fp16 MMA chain where V's tile is a tile of fp16 numbers: two warps
+// convert each V tile in shared memory as it lands, times a power of two, and put
+// ones into the slots past the last key. A tile with a number that does not convert
+// exactly (kVShift) is loaded again and stays bf16, with P = P_hi + P_lo in two MMAs;
+// so V enters as it is everywhere, however small a column's or a key's values are
+// beside the rest of their tile. With the two-term P everywhere the prefix of 256
+// rows over 32768 keys took 205 us.
 #include "decode_runs.cuh"
 #include "pdl.cuh"
 #include "tc.cuh"
@@ -50,12 +50,29 @@ namespace {
 constexpr int kBM = 128, kBN = 128;
 // kTop, kSlack (decode_runs.cuh): a row's reference is set kTop below a new
 // maximum and moves when a score passes it by kTop + kSlack. fp16 weights need
-// that room below them. With weights of up to 2^15 a sum over V passes fp32's
-// range from |v| = 2^113 on, where its result need not: once a tile holds a
-// magnitude of 2^kHuge the segment's rows go on with the maximum itself as
-// reference, and its tiles stay bf16 with the two-term P. Up to 2^kHuge sums over
-// 2^30 keys stay below 2^109.
+// that room below them. fp16 tiles hold V times 2^kVShift, and tiles that stay bf16
+// have it in their weights instead, so that one accumulator serves both. With
+// weights of up to 2^15 a sum over V passes fp32's range from |v| = 2^105 on, where
+// its result need not: once a tile holds a magnitude of 2^kHuge the segment's rows
+// go on with the maximum itself as reference and without kVShift, and its tiles
+// stay bf16 with the two-term P. Up to 2^kHuge sums over 2^30 keys stay below 2^117.
 constexpr int kHuge = 64;
+// fp16 holds a bf16 number's 8 bits, times 2^kVShift, from 2^(-17 - kVShift) (8 bits
+// above its smallest step, 2^-24) to below 2^(16 - kVShift). The lower 32 of these 33
+// binades, 2^-25 to below 128, are the window that tiles are checked for: with kVWindow
+// added the numbers in it, and no others, have 111 as their exponents' first bits, so
+// the check is an addition and half an AND a pair. Zero, which converts, lies outside:
+// a batch with anything outside is looked at again in the registers. (Exact limits for
+// every pair, as minima and maxima of magnitudes, took 188 us for 256 rows over 32768
+// keys, this way 186.6, without a check 182.3; rounding both to nearest and towards
+// zero, 182.5, misses what both take to zero. A tile that goes on as bf16 costs its CTA
+// 9 us.) Of tiles of 128 x 128 values from N(0, 1) one in 2500 holds a number that is
+// too small, of N(0, 0.02^2) one in 50.
+constexpr int kVShift = 8;
+constexpr float kVScale = 1 << kVShift;
+constexpr uint32_t kVLeast = (127 - 17 - kVShift) << 7, kVMost = (127 + 16 - kVShift) << 7;  // bits
+constexpr uint32_t kVWindow = (224 - (127 - 17 - kVShift)) * 0x00800080u;
+constexpr uint32_t kOnes = 0x3f803f80u;  // in slots past the last key, whose weights are 0
 constexpr int kVFp16 = 0, kVWide = 1, kVHuge = 2;  // a V tile's format (wide[])
 
 template <int D, int NT>
@@ -141,11 +158,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 
 // Weights of a key tile in the rare cases, out of line: where V stays bf16
 // (`two`) P_hi (upper 16 bits) in columns 0-63 of the S tile and P_lo =
-// bf16(p - P_hi) in columns 64-127, else fp16 as in the common case. The scores
-// enter as rounded products minus the reference, which is exact near it at any
-// magnitude of the logits. Reads the S tile again (keys from lim on masked) and
-// returns the weights' sum. Warp-collective.
-__device__ __noinline__ float rare_weights(uint32_t tS, int lim, float scale_log2, float ref, bool two) {
+// bf16(p - P_hi) in columns 64-127, of weights times v_scale (what fp16 tiles hold V
+// times), else fp16 as in the common case. The scores enter as rounded products
+// minus the reference, which is exact near it at any magnitude of the logits. Reads
+// the S tile again (keys from lim on masked) and returns the weights' sum (without
+// v_scale). Warp-collective.
+__device__ __noinline__ float rare_weights(uint32_t tS, int lim, float scale_log2, float ref, bool two,
+                                           float v_scale) {
   float sum0 = 0.f, sum1 = 0.f;
   uint32_t sr[4][32];
 #pragma unroll
@@ -170,15 +189,39 @@ __device__ __noinline__ float rare_weights(uint32_t tS, int lim, float scale_log
         lo[i] = 0u;
         continue;
       }
-      const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-      asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(hi[i]) : "r"(u0), "r"(u1));
-      lo[i] = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u),
-                          p1 - __uint_as_float(u1 & 0xffff0000u));
+      const float y0 = p0 * v_scale, y1 = p1 * v_scale;
+      hi[i] = split_hi(y0, y1);
+      lo[i] = split_lo(y0, y1);
     }
     tc::st32(tS + 32 * half, hi);
     if (two) tc::st32(tS + 64 + 32 * half, lo);
   }
   return sum0 + sum1;
+}
+
+// Bits, but the sign, of the largest magnitude in a converter thread's chunks of a V
+// tile (every 64th from `base` on, the thread's first), of keys before lim.
+template <int D>
+__device__ __noinline__ uint32_t largest_bits(uint32_t base, int ct, int lim) {
+  uint32_t m = 0x80008000u;  // behind a set sign bit the bits are in order as signed halves
+#pragma unroll 1
+  for (int i = 0; i < D / 4; ++i) {
+    if ((((i * 64 + ct) >> 3) & (kBN - 1)) >= lim) continue;
+    const uint4 x = lds128(base + i * (64 * 16));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm("max.s16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] | 0x80008000u));
+  }
+  return max(m & 0x7fffu, (m >> 16) & 0x7fffu);
+}
+
+// Two bf16 numbers times 2^kVShift as fp16 numbers.
+__device__ __forceinline__ __nv_bfloat162 v_scaled(uint32_t w) {
+  return __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __floats2bfloat162_rn(kVScale, kVScale));
+}
+__device__ __forceinline__ uint32_t v_fp16(__nv_bfloat162 y) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
+  return pack_f16x2(bf16lo(u), bf16hi(u));
 }
 
 struct PrefixArgs {
@@ -449,7 +492,7 @@ __global__ void __launch_bounds__(384, 1)
     } else {
       // -------------------------------------------------------- V to fp16
       const int ct = threadIdx.x - C::CONV_WARP * 32;  // 0 .. 63
-      constexpr int CHUNKS = C::TILE / 16, PER = CHUNKS / C::CONV_THREADS, UN = 8;
+      constexpr int CHUNKS = C::TILE / 16, PER = CHUNKS / C::CONV_THREADS, UN = 4;
       int g0 = 0, again = 0;
       bool ok = true;
       for (long long p = run.lo; ok && p < run.hi;) {
@@ -462,11 +505,8 @@ __global__ void __launch_bounds__(384, 1)
             ok = false;
           const uint32_t base = sbase + C::V_OFF + sv * C::TILE + ct * 16;
           const int lim = min(kBN, run.len - (s.t0 + j) * kBN);  // keys that exist
-          // The largest magnitude, as bits below the sign's (a NaN counts as one),
-          // pairs as signed halves behind a set sign bit; the sum of squares
-          // reaches 2^-12 where a magnitude reaches 2^-6.
-          uint32_t top = 0x80008000u;
-          __half2 big = __floats2half2_rn(0.f, 0.f);
+          bool off = false;
+          uint32_t in = 0xffffffffu;  // the window's bits: cleared by a number outside it
           if (ok) {
 #pragma unroll 1
             for (int i0 = 0; i0 < PER; i0 += UN) {
@@ -480,52 +520,54 @@ __global__ void __launch_bounds__(384, 1)
               for (int u = 0; u < UN; ++u) {
                 // Chunk index (i0 + u) * 64 + ct, 8 chunks per 128-byte row.
                 const int row = (((i0 + u) * C::CONV_THREADS + ct) >> 3) & (kBN - 1);
-                if (row >= lim) x[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (row >= lim) x[u] = make_uint4(kOnes, kOnes, kOnes, kOnes);
                 const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                __half2 hh[4];
+                uint32_t hh[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  hh[k] = __floats2half2_rn(bf16lo(w[k]), bf16hi(w[k]));
-                  asm("max.s16x2 %0, %0, %1;" : "+r"(top) : "r"(w[k] | 0x80008000u));
-                  big = __hfma2(hh[k], hh[k], big);
+                  hh[k] = v_fp16(v_scaled(w[k]));
+                  in &= w[k] + kVWindow;
                 }
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
                                  base + (i0 + u) * (C::CONV_THREADS * 16)),
-                             "r"(*reinterpret_cast<uint32_t*>(&hh[0])),
-                             "r"(*reinterpret_cast<uint32_t*>(&hh[1])),
-                             "r"(*reinterpret_cast<uint32_t*>(&hh[2])),
-                             "r"(*reinterpret_cast<uint32_t*>(&hh[3]))
+                             "r"(hh[0]), "r"(hh[1]), "r"(hh[2]), "r"(hh[3])
                              : "memory");
+              }
+              if ((in & 0x70007000u) != 0x70007000u) {  // zeros do convert
+                // Behind a set sign bit the bits are in order as signed halves; with 1
+                // taken off, zero becomes the largest.
+                uint32_t most = 0x80008000u, least = 0x7fff7fffu;
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                  const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t m = w[k] | 0x80008000u;
+                    asm("max.s16x2 %0, %0, %1;" : "+r"(most) : "r"(m));
+                    asm("min.s16x2 %0, %0, %1;" : "+r"(least) : "r"(m - 0x00010001u));
+                  }
+                }
+                off = off || min(least & 0x7fffu, (least >> 16) & 0x7fffu) + 1 < kVLeast ||
+                      max(most & 0x7fffu, (most >> 16) & 0x7fffu) >= kVMost;
+                in = 0xffffffffu;
               }
             }
           }
-          const uint32_t most = max(top & 0x7fffu, (top >> 16) & 0x7fffu);
-          const bool too_big = most >= ((127u + 16) << 7);
-          const bool fits = __low2float(big) >= 0x1p-12f || __high2float(big) >= 0x1p-12f;
-          int some_big, some_ok;
-          asm volatile(
-              "{\n\t.reg .pred p, q;\n\t"
-              "setp.ne.s32 p, %2, 0;\n\t"
-              "barrier.cta.red.or.pred q, 1, 64, p;\n\t"
-              "selp.s32 %0, 1, 0, q;\n\t"
-              "setp.ne.s32 p, %3, 0;\n\t"
-              "barrier.cta.red.or.pred q, 1, 64, p;\n\t"
-              "selp.s32 %1, 1, 0, q;\n\t}"
-              : "=r"(some_big), "=r"(some_ok)
-              : "r"(too_big ? 1 : 0), "r"(fits ? 1 : 0)
-              : "memory");
-          const int two = some_big | (some_ok ^ 1) | (huge ? 1 : 0);
-          if (two) {
-            int some_huge;
+          // Agreed by the 64 threads.
+          auto any = [](bool mine) {
+            int r;
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\t"
-                "setp.ge.u32 p, %1, %2;\n\t"
+                "setp.ne.s32 p, %1, 0;\n\t"
                 "barrier.cta.red.or.pred q, 1, 64, p;\n\t"
                 "selp.s32 %0, 1, 0, q;\n\t}"
-                : "=r"(some_huge)
-                : "r"(most), "r"((127u + kHuge) << 7)
+                : "=r"(r)
+                : "r"(mine ? 1 : 0)
                 : "memory");
-            huge = huge || some_huge;
+            return r != 0;
+          };
+          int fmt = kVFp16;
+          if (any(huge || off)) {
             // The tile as it was. The generic writes above come before the
             // copy engine's.
             fence_proxy_async_smem();
@@ -540,6 +582,8 @@ __global__ void __launch_bounds__(384, 1)
               (void)mbar_wait(bar(C::B_VA), again & 1, &g_shared_err);  // bounded: let it land
             }
             ++again;
+            huge = any(huge || largest_bits<D>(base, ct, lim) >= (127u + kHuge) << 7);
+            fmt = huge ? kVHuge : kVWide;
             // Slots past the last key hold whatever the cache holds (possibly
             // NaN or inf); their weights are 0, but 0 * NaN is not.
             if (lim < kBN)
@@ -551,7 +595,7 @@ __global__ void __launch_bounds__(384, 1)
                                "r"(0u)
                                : "memory");
           }
-          if (ct == 0) wide[sv] = two ? (huge ? kVHuge : kVWide) : kVFp16;
+          if (ct == 0) wide[sv] = fmt;
           fence_proxy_async_smem();  // the MMA reads V through the async proxy
           mbar_arrive(bar(C::B_VR + sv));
           // Agreed by both warps before either goes on (an abort ends both).
@@ -632,9 +676,9 @@ __global__ void __launch_bounds__(384, 1)
           break;
         }
         const int fmt = __shfl_sync(0xffffffffu, wide[sv], 0);
-        if (fmt == kVHuge && top != 0.f) {  // from here on weights of at most 2^kSlack
-          const float next = ref + top, down = ex2_approx(ref - next);
-          alpha *= down;
+        if (fmt == kVHuge && top != 0.f) {  // from here on weights of at most 2^kSlack,
+          const float next = ref + top, down = ex2_approx(ref - next);  // and V as it is
+          alpha *= down * (1.f / kVScale);
           l *= down;
           ref = next;
           top = 0.f;
@@ -671,7 +715,7 @@ __global__ void __launch_bounds__(384, 1)
           unf2(add2(sumA, sumB), s0, s1);
           l += s0 + s1;
         } else {
-          l += rare_weights(tS, lim, scale_log2, ref, two);
+          l += rare_weights(tS, lim, scale_log2, ref, two, top != 0.f ? kVScale : 1.f);
         }
         if (rescale) {
           const uint64_t a2 = f2(alpha, alpha);
@@ -708,6 +752,7 @@ __global__ void __launch_bounds__(384, 1)
       const size_t pi = slot * kBM + r;
       float* so = a.o + slot * kBM * D + r * 4;
       const bool store = row < a.rows && touch >= 0 && touch < a.s_cap;
+      const float v_inv = top != 0.f ? 1.f / kVScale : 1.f;
       ATTN_DCHECK(touch >= 0 && touch < a.s_cap, &g_shared_err);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -719,8 +764,9 @@ __global__ void __launch_bounds__(384, 1)
         if (store && n > 0) {
 #pragma unroll
           for (int i2 = 0; i2 < 8; ++i2)
-            *reinterpret_cast<uint4*>(so + (c * 8 + i2) * (kBM * 4)) =
-                make_uint4(ov[4 * i2], ov[4 * i2 + 1], ov[4 * i2 + 2], ov[4 * i2 + 3]);
+            *reinterpret_cast<float4*>(so + (c * 8 + i2) * (kBM * 4)) =
+                make_float4(__uint_as_float(ov[4 * i2]) * v_inv, __uint_as_float(ov[4 * i2 + 1]) * v_inv,
+                            __uint_as_float(ov[4 * i2 + 2]) * v_inv, __uint_as_float(ov[4 * i2 + 3]) * v_inv);
         }
       }
       if (store) {
