@@ -600,6 +600,7 @@ __device__ __forceinline__ void runs_body(
     }
     const float hc0 = __shfl_sync(0xffffffffu, hc, (2 * tq) * 4);
     const float hc1 = __shfl_sync(0xffffffffu, hc, (2 * tq + 1) * 4);
+    const float lo0 = fminf(hc0, 1.f), lo1 = fminf(hc1, 1.f), up0 = fmaxf(hc0, 1.f), up1 = fmaxf(hc1, 1.f);
 
     // State of heads 2tq, 2tq + 1: normaliser share l of this lane's keys
     // relative to 2^m, accumulators relative to 2^r.
@@ -631,7 +632,7 @@ __device__ __forceinline__ void runs_body(
 
       // ---- S^T = K q^T: keys gid and gid + 8, heads 2tq and 2tq + 1 ----
       // s[2 i + e]: key gid + 8 i, head 2 tq + e.
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, hk[4] = {hc0, hc1, hc0, hc1};
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t fa = 0, fb = 0;  // exponent bytes of the values
       if constexpr (E8) {
 #pragma unroll
@@ -653,10 +654,11 @@ __device__ __forceinline__ void runs_body(
         const float ka = e4m3::scale_of(lds_u8(ep + gid)), kb = e4m3::scale_of(lds_u8(ep + gid + 8));
         fa = lds_u8(ep + 16 + gid);
         fb = lds_u8(ep + 24 + gid);
-        hk[0] *= ka;
-        hk[1] *= ka;
-        hk[2] *= kb;
-        hk[3] *= kb;
+        // hc ka may be infinite where the score is not, its two parts' products cannot.
+        s[0] = s[0] * (lo0 * ka) * up0;
+        s[1] = s[1] * (lo1 * ka) * up1;
+        s[2] = s[2] * (lo0 * kb) * up0;
+        s[3] = s[3] * (lo1 * kb) * up1;
       } else {
         float s2[4] = {0.f, 0.f, 0.f, 0.f};  // two chains: half the latency
 #pragma unroll
@@ -668,11 +670,8 @@ __device__ __forceinline__ void runs_body(
           mma_bf16(s2, x.z, y.z, x.w, y.w, qb[2 * c + 1][0], qb[2 * c + 1][1]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] += s2[i];
+        for (int i = 0; i < 4; ++i) s[i] = (s[i] + s2[i]) * (i & 1 ? hc1 : hc0);
       }
-
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] *= hk[i];
 
       // ---- weights: p relative to m, w (8-bit) relative to r ----
       float p0, p1, p2, p3, w0, w1, w2, w3;
