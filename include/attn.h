@@ -544,8 +544,9 @@ attn_status_t attn_merge_lse_pair(const void* o_a, const float* lse_a, const voi
  * seq_lens[b] keys (the length after the write), position p in slot p % 16 of
  * page block_table[b][p / 16].
  *   k, v          [total, h_kv, d_h] dtype, d_h contiguous, token and head
- *                 strides in elements (each a multiple of 16 bytes; slices of
- *                 a fused projection's output need no copy)           (read)
+ *                 strides in elements (each a multiple of 16 bytes unless its
+ *                 dimension is 1; slices of a fused projection's output need
+ *                 no copy)                                            (read)
  *   block_table   [B, max_blocks_per_seq], cu_seqlens [B + 1] non-decreasing,
  *                 seq_lens [B], int32                                  (read)
  *   caches        as above; slots that no token maps to keep their

@@ -454,7 +454,9 @@ attn_status_t cache_tokens(const void* k, const void* v, long long k_tok, long l
       !v_scale)
     return ATTN_ERR_INVALID_ARG;
   const long long unit = dtype == ATTN_DTYPE_BF16 ? 8 : 4;  // elements in 16 bytes
-  if (k_tok % unit || k_head % unit || v_tok % unit || v_head % unit) return ATTN_ERR_INVALID_ARG;
+  // (The stride of a dimension of one element may be anything.)
+  if ((total > 1 && (k_tok % unit || v_tok % unit)) || (h_kv > 1 && (k_head % unit || v_head % unit)))
+    return ATTN_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(block_table, 4) ||
       !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4))

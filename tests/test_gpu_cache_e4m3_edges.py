@@ -91,3 +91,27 @@ def test_many_rows_with_and_without_tokens(B, most):
     assert torch.equal(k[:total], x[:total]) and torch.equal(v[:total], -x[:total])
     assert (k[total:] == 9).all() and (v[total:] == 9).all()
     assert attn.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("total,h_kv", [(1, 3), (20, 1), (1, 1)])
+def test_strides_of_dimensions_of_one_element(total, h_kv, dtype):
+    """Where there is one token (one head) its stride is never used: any value does,
+    as in a slice of a wider or padded tensor."""
+    d = 64
+    x = W.normal((total, h_kv, d), 5, dtype).cuda()
+    tok = h_kv * d if total > 1 else 1021
+    head = d if h_kv > 1 else 333
+    odd = lambda t: torch.as_strided(t, t.shape, (tok, head, 1))
+    where = (dev([[1, 0]]), dev([0, total]), dev([total]))
+    want, got = empty_cache(2, h_kv, d), empty_cache(2, h_kv, d)
+    attn.attn_cache_write_e4m3(x, -x, *want, *where)
+    attn.attn_cache_write_e4m3(odd(x.clone()), odd(-x), *got, *where)
+    for a, b in zip(want, got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    k, v = torch.empty_like(x), torch.empty_like(x)
+    attn.attn_cache_read_e4m3(*want, *where, k, v)
+    k2, v2 = torch.empty_like(x), torch.empty_like(x)
+    attn.attn_cache_read_e4m3(*want, *where, odd(k2), odd(v2))
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    assert attn.attn_get_device_error() == 0
