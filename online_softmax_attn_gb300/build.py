@@ -5,7 +5,9 @@ translation units, compiled in parallel with nvcc (one ``-gencode``) and linked
 with the static CUDA runtime, so the library needs no libcuda at load time
 (driver entry points are resolved at run time). ``_calls.so``, the Python side of
 the calls whose host time matters (``csrc/binding.cpp``), is compiled beside it by
-g++ against the installed torch.
+g++ against the installed torch, and again when torch or Python change. The library
+needs neither: where only the binding fails to compile, the library is linked before
+the error is raised.
 
     python -m online_softmax_attn_gb300.build [--force] [--ptxas-verbose] [--debug]
 
@@ -76,6 +78,22 @@ def _compile(src: str, obj: str, ptxas_verbose: bool, debug: bool = False) -> st
     return res.stderr if ptxas_verbose else ""
 
 
+def _calls_key() -> str:
+    """What a compiled binding depends on besides its sources."""
+    import torch
+
+    return "\n".join([torch.__version__, os.path.dirname(torch.__file__), sys.version,
+                      str(torch._C._GLIBCXX_USE_CXX11_ABI), os.environ.get("CXX", "g++")])
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _compile_calls(src: str, out: str) -> str:
     """The compiled binding: a Python extension that uses torch's headers and
     the torch libraries of this interpreter, and no CUDA."""
@@ -116,13 +134,17 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
             jobs.append((src, obj))
     logs = []
     calls = os.path.join(CSRC, "binding.cpp")
-    calls_stale = force or _stale(CALLS_PATH, [calls, os.path.join(INCLUDE, "attn.h")])
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    calls_key = os.path.join(BUILD_DIR, "calls.key")  # one binding for both variants
+    calls_stale = (force or _stale(CALLS_PATH, [calls, os.path.join(INCLUDE, "attn.h")])
+                   or _read(calls_key) != _calls_key())
+    calls_job = None
     if jobs or calls_stale:
         workers = min(len(jobs) + 1, max(1, os.cpu_count() or 1))
         with concurrent.futures.ThreadPoolExecutor(workers) as ex:
             futs = [ex.submit(_compile, s, o, ptxas_verbose, debug) for s, o in jobs]
             if calls_stale:
-                futs.append(ex.submit(_compile_calls, calls, CALLS_PATH))
+                calls_job = ex.submit(_compile_calls, calls, CALLS_PATH)
             for f in futs:
                 logs.append(f.result())
     if force or jobs or _stale(lib_path, objs):
@@ -132,6 +154,10 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, lib_path)
+    if calls_job is not None:
+        calls_job.result()
+        with open(calls_key, "w") as f:
+            f.write(_calls_key())
     if ptxas_verbose or not quiet:
         for log in logs:
             if log:
