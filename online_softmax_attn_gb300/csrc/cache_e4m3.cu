@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(kReadThreads)
   for (int u = 0; u < U; ++u) {
     const RowId id = row_id<D, U, T>(u * C::G + grp, total, h_kv);
     if (!id.live || s_page[id.ti] == -1) continue;
+    if (!ATTN_GUARD(id.t < total && id.head < h_kv && id.ti < kBlk, &g_cache8_err)) continue;
     const float sc = e4m3::scale_of(e[u]);
     const RowStrides st = id.is_v ? sv : sk;
     const long long off = id.t * st.tok + id.head * st.head + sub * (BF16 ? 8 : 4);

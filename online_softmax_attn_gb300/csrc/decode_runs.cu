@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(128)
   const long long per = __ldcg(plan), at = __ldcg(plan + 1 + b);
   const long long wu = __ldcg(plan + 2 + b) - at;  // weight of one unit: its pages + kUnit
   const size_t row = static_cast<size_t>(b) * h + hq;
+  if (!ATTN_GUARD(row < gridDim.x && per > 0 && wu >= 0, &g_decode_runs_err)) return;
   if (wu == 0) {
     for (int i = threadIdx.x; i < D / 2; i += 128) reinterpret_cast<uint32_t*>(o + row * D)[i] = 0u;
     if (lse != nullptr && threadIdx.x == 0) lse[row] = -INFINITY;
@@ -73,6 +74,7 @@ __global__ void __launch_bounds__(128)
       for (int e = 0; e < VEC; ++e) x[i][e] = 0.f;
       if (j < n) {
         const size_t slot = (2 * (c0 + j) + (j == 0 ? 1 : 0)) * 8 + (hq % g) % 8;
+        ATTN_DCHECK(slot < 2 * kRunsMaxCtas * 8, &g_decode_runs_err);
         m[i] = __ldcg(m_part + slot);
         l[i] = __ldcg(l_part + slot);
         const float* src = o_part + slot * D + lane * VEC;
@@ -171,6 +173,8 @@ __global__ void __launch_bounds__(256, 1) __cluster_dims__(kClusterCtas)
   if (cta >= nh || threadIdx.x >= 32) return;
   constexpr int VEC = D / 32;
   const int lane = threadIdx.x, wu = row_weight(row_len(rw, 0));
+  if (!ATTN_GUARD(row0 + cta < static_cast<size_t>(gridDim.x / (kClusterCtas * upr)) * h, &g_decode_runs_err))
+    return;
   if (wu == 0) {  // an empty row
     for (int i = lane; i < D / 2; i += 32) reinterpret_cast<uint32_t*>(mine.o + cta * D)[i] = 0u;
     if (mine.lse != nullptr && lane == 0) mine.lse[cta] = -INFINITY;

@@ -754,6 +754,7 @@ __global__ void __launch_bounds__(384, 1)
       const bool store = row < a.rows && touch >= 0 && touch < a.s_cap;
       const float v_inv = top != 0.f ? 1.f / kVScale : 1.f;
       ATTN_DCHECK(touch >= 0 && touch < a.s_cap, &g_shared_err);
+      ATTN_DCHECK(!store || pi < static_cast<size_t>(a.h_kv) * a.s_cap * a.n_rb * (2 * kBM), &g_shared_err);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t ov[32];
@@ -819,6 +820,7 @@ __global__ void __launch_bounds__(kMergeRows* D / 4) shared_merge_kernel(const M
   if (pr >= a.p.rows) return;
   const int b = static_cast<int>(pr / a.g), hh = static_cast<int>(pr % a.g);
   const size_t row = static_cast<size_t>(b) * a.h + kvh * a.g + hh;
+  if (!ATTN_GUARD(row < static_cast<size_t>(a.p.rows / a.g) * a.h, &g_shared_err)) return;
   // Own states' place (loads first: the prefix's length is one round trip too).
   const long long per = __ldcg(a.plan), at = __ldcg(a.plan + 1 + b);
   const long long wu = __ldcg(a.plan + 2 + b) - at;  // weight of one unit
