@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import online_softmax_attn_gb300 as attn
+import position_cases as PC
 from e4m3_cases import cache_from, decode_case, values
 from parity import check_lse
 from test_gpu_decode_e4m3 import cuda, reference
@@ -53,3 +54,24 @@ def test_queries_and_keys_far_from_one(qe, ke, d, call):
     assert (err <= 2.0 ** -8 * np.abs(O) + (2.0 ** -11 + 2.0 ** -13) * mag).all()
     check_lse(lse, L)
     assert attn.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("i", range(len(PC.E4M3)))
+def test_every_page_counts_once(i):
+    """Rows cut over the GPU, with values that carry their position."""
+    args = PC.e4m3_case(*PC.E4M3[i], seed=81 + i)
+    O, L = reference(*args)
+    o, lse = attn.attn_decode_paged_e4m3(*cuda(*args))
+    PC.check(o.double().cpu().numpy(), O)
+    check_lse(lse, L)
+    assert attn.attn_get_device_error() == 0
+
+
+@FORMS
+@pytest.mark.parametrize("length", [1000, 4096, 16])
+def test_every_page_counts_once_in_either_form(length, call):
+    args = PC.e4m3_case([length, 20], 2, 4, 64, seed=91)
+    O, L = reference(*args)
+    o, lse = call(*cuda(*args))
+    PC.check(o.double().cpu().numpy(), O)
+    check_lse(lse, L)

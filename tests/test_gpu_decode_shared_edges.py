@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import online_softmax_attn_gb300 as attn
+import position_cases as PC
 from parity import check_lse
 from test_gpu_decode_shared import case, reference, run
 
@@ -161,3 +162,16 @@ def test_every_bf16_number_as_a_value():
         o, _ = run([q, k, v, torch.arange(pages, dtype=torch.int32), i32([n]), torch.full((n, 1), -1, dtype=torch.int32),
                     torch.zeros(n, dtype=torch.int32)], scale=1.0)
         assert torch.equal(o.cpu().view(-1), vals)
+
+
+@pytest.mark.parametrize("i", range(len(PC.SHARED)))
+def test_every_page_counts_once(i):
+    """Long prefixes and rows cut over the GPU, with values that carry their position."""
+    args = PC.shared_case(*PC.SHARED[i], seed=71 + i)
+    B = args[0].shape[0]
+    rows = sorted({0, B // 2, B - 1, int(torch.argmax(args[6]))})
+    O, L = reference(*args, rows=rows)
+    o, lse = run(args)
+    PC.check(o[rows].double().cpu().numpy(), O[rows])
+    check_lse(lse[rows], L[rows])
+    assert attn.attn_get_device_error() == 0
