@@ -661,7 +661,7 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
  * prefix key is one fp16 number, within 2^-11 of itself down to 2^-27 of the
  * row's largest and within 2^-38 of the largest below that; where values of its
  * 128 keys reach 128, or are not zero and below 2^-25, and for the rows' own
- * keys, it is two bf16 terms, within 2^-16 of itself.
+ * keys, it is two bf16 terms, within 2^-15 of itself.
  * Errors: as attn_decode_paged_e4m3, plus INVALID_ARG for max_prefix_blocks < 1
  * or beyond 2^30 / 16; UNSUPPORTED also for h / h_kv not in {1, 2, 4, 8}.
  */

@@ -483,9 +483,6 @@ attn_status_t cache_tokens(const void* k, const void* v, long long k_tok, long l
   a->v_exp = const_cast<uint8_t*>(v_scale);
   return ATTN_OK;
 }
-attn_status_t from_launch(cudaError_t e) {
-  return e == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : from_cuda(e);
-}
 }  // namespace
 
 attn_status_t attn_cache_write_e4m3(const void* k, const void* v, long long k_stride_token,
@@ -502,7 +499,7 @@ attn_status_t attn_cache_write_e4m3(const void* k, const void* v, long long k_st
       cu_seqlens, seq_lens, B, total, h_kv, d_h, page_size, num_blocks, max_blocks_per_seq, k_cache,
       v_cache, k_scale, v_scale, &a);
   if (st != ATTN_OK || a.total == 0) return st;
-  return from_launch(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_cache_write(a, static_cast<cudaStream_t>(stream)));
 }
 
 attn_status_t attn_cache_read_e4m3(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
@@ -519,7 +516,7 @@ attn_status_t attn_cache_read_e4m3(const void* k_cache, const void* v_cache, con
       cu_seqlens, seq_lens, B, total, h_kv, d_h, page_size, num_blocks, max_blocks_per_seq, k_cache,
       v_cache, k_scale, v_scale, &a);
   if (st != ATTN_OK || a.total == 0) return st;
-  return from_launch(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t attn_decode_e4m3_workspace_bytes(int B, int h, int h_kv, int d_h) {

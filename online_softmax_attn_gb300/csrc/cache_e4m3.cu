@@ -384,21 +384,17 @@ __global__ void __launch_bounds__(kReadThreads)
 }
 
 template <int D, int U, int T>
-cudaError_t grid_of(const CacheTokens& a, dim3* grid) {
+dim3 grid_of(const CacheTokens& a) {
   constexpr int kHeads = Cta<D, U, T>::ROWS / kBlk;  // per CTA, K and V counted apart
   const long long blocks = (static_cast<long long>(a.total) + kBlk - 1) / kBlk;
   const unsigned y = static_cast<unsigned>(blocks < 65535 ? blocks : 65535);
-  *grid = dim3(unsigned((2 * a.h_kv + kHeads - 1) / kHeads), y, unsigned((blocks + y - 1) / y));
-  return cudaSuccess;
+  return dim3(unsigned((2 * a.h_kv + kHeads - 1) / kHeads), y, unsigned((blocks + y - 1) / y));
 }
 
 template <int D, bool BF16, int U>
 cudaError_t launch_write_u(const CacheTokens& a, cudaStream_t stream) {
-  dim3 grid;
-  const cudaError_t e = grid_of<D, U, kWriteThreads>(a, &grid);
-  if (e != cudaSuccess) return e;
   const TokenMap m{a.block_table, a.cu, a.seq_lens, a.B, a.max_blocks, a.num_blocks};
-  return launch_pdl(cache_write_kernel<D, BF16, U>, grid, dim3(kWriteThreads), 0, stream,
+  return launch_pdl(cache_write_kernel<D, BF16, U>, grid_of<D, U, kWriteThreads>(a), dim3(kWriteThreads), 0, stream,
                     static_cast<const void*>(a.k), static_cast<const void*>(a.v),
                     RowStrides{a.k_tok, a.k_head}, RowStrides{a.v_tok, a.v_head}, m, a.total,
                     a.h_kv, a.k_codes, a.v_codes, a.k_exp, a.v_exp);
@@ -406,11 +402,8 @@ cudaError_t launch_write_u(const CacheTokens& a, cudaStream_t stream) {
 
 template <int D, bool BF16, int U>
 cudaError_t launch_read_u(const CacheTokens& a, cudaStream_t stream) {
-  dim3 grid;
-  const cudaError_t e = grid_of<D, U, kReadThreads>(a, &grid);
-  if (e != cudaSuccess) return e;
   const TokenMap m{a.block_table, a.cu, a.seq_lens, a.B, a.max_blocks, a.num_blocks};
-  return launch_pdl(cache_read_kernel<D, BF16, U>, grid, dim3(kReadThreads), 0, stream,
+  return launch_pdl(cache_read_kernel<D, BF16, U>, grid_of<D, U, kReadThreads>(a), dim3(kReadThreads), 0, stream,
                     static_cast<const uint8_t*>(a.k_codes), static_cast<const uint8_t*>(a.v_codes),
                     static_cast<const uint8_t*>(a.k_exp), static_cast<const uint8_t*>(a.v_exp), m,
                     a.total, a.h_kv, a.k, a.v, RowStrides{a.k_tok, a.k_head},
