@@ -720,6 +720,14 @@ attn_status_t attn_selftest_wait_timeout(unsigned int limit_us, void* stream);
 attn_status_t attn_selftest_prefill_stall(int key_tile);
 
 /*
+ * attn_selftest_shared_stall -- the same for attn_decode_paged_shared: every
+ * CTA leaves out one load of the key_tile-th key tile of the prefix that it
+ * visits, K (what 0), V (1) or the second load of a V tile that stays bf16 (2).
+ * INVALID_ARG for any other `what`.
+ */
+attn_status_t attn_selftest_shared_stall(int key_tile, int what);
+
+/*
  * attn_selftest_delayed_copy -- test aid for the decode kernels' reads before
  * their dependency wait. The split-KV decode kernel reads seq_lens and the
  * block table before it waits for the previous kernel on its stream (to warm

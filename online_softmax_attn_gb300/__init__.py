@@ -35,6 +35,7 @@ __all__ = [
     "attn_get_device_error",
     "attn_get_last_device_error",
     "attn_selftest_prefill_stall",
+    "attn_selftest_shared_stall",
     "attn_status_string",
     "library",
     "ATTN_MAX_SPLITS",
@@ -130,6 +131,8 @@ def library() -> ctypes.CDLL:
     lib.attn_selftest_delayed_copy.restype = I
     lib.attn_selftest_prefill_stall.argtypes = [I]
     lib.attn_selftest_prefill_stall.restype = I
+    lib.attn_selftest_shared_stall.argtypes = [I, I]
+    lib.attn_selftest_shared_stall.restype = I
     lib.attn_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_uint)]
     lib.attn_get_device_error.restype = I
     lib.attn_get_last_device_error.argtypes = [P]
@@ -680,6 +683,13 @@ def attn_selftest_prefill_stall(key_tile: int) -> None:
     up and the kernel takes its abort path (key_tile < 0: off). Raises
     AttnError (UNSUPPORTED) on a release build."""
     _check("attn_selftest_prefill_stall", library().attn_selftest_prefill_stall(int(key_tile)))
+
+
+def attn_selftest_shared_stall(key_tile: int, what: int = 0) -> None:
+    """Debug builds only: the same for attn_decode_paged_shared, whose CTAs leave
+    out K (what 0), V (1) or V's second load (2) of the key_tile-th key tile of
+    the prefix that they visit. Raises AttnError (UNSUPPORTED) on a release build."""
+    _check("attn_selftest_shared_stall", library().attn_selftest_shared_stall(int(key_tile), int(what)))
 
 
 def attn_get_device_error(stream=None) -> int:

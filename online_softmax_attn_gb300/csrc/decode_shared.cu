@@ -44,6 +44,11 @@
 namespace attn {
 
 static __device__ unsigned int g_shared_err;
+#ifdef ATTN_DEBUG
+// The key tile, in each CTA's own order, and which of its loads is not requested
+// (attn_selftest_shared_stall): 0 K, 1 V, 2 V's second load.
+static __device__ int g_shared_stall[2] = {-1, 0};
+#endif
 
 namespace {
 
@@ -303,6 +308,13 @@ __global__ void __launch_bounds__(384, 1)
   if (blockIdx.x == 0 && threadIdx.x == 0)
     (void)clamp_seq_len(__ldcg(a.len), a.max_blocks * kPage, &g_shared_err);
 
+#ifdef ATTN_DEBUG
+  const int stall_tile = g_shared_stall[0], stall_what = g_shared_stall[1];
+  auto stalled = [=](int g, int what) { return g == stall_tile && what == stall_what; };
+#else
+  auto stalled = [](int, int) { return false; };
+#endif
+
   // A segment: key tiles [t0, t0 + nt) of KV head kvh. Every role walks the
   // same segments.
   struct Seg {
@@ -392,15 +404,17 @@ __global__ void __launch_bounds__(384, 1)
             ok = false;
             break;
           }
-          load_tile(sbase + C::K_OFF + sk * C::TILE, &tmap_k, bar(C::B_KF + sk), s.kvh, ent, (j & 3) * 8,
-                    page0);
+          if (!stalled(g, 0))
+            load_tile(sbase + C::K_OFF + sk * C::TILE, &tmap_k, bar(C::B_KF + sk), s.kvh, ent, (j & 3) * 8,
+                      page0);
           k_issued = g + 1;
           if (g >= C::NSV && !wait(bar(C::B_VE + sv), (g / C::NSV - 1) & 1)) {
             ok = false;
             break;
           }
-          load_tile(sbase + C::V_OFF + sv * C::TILE, &tmap_v, bar(C::B_VF + sv), s.kvh, ent, (j & 3) * 8,
-                    page0);
+          if (!stalled(g, 1))
+            load_tile(sbase + C::V_OFF + sv * C::TILE, &tmap_v, bar(C::B_VF + sv), s.kvh, ent, (j & 3) * 8,
+                      page0);
           v_issued = g + 1;
         }
         g0 += s.nt;
@@ -410,9 +424,9 @@ __global__ void __launch_bounds__(384, 1)
         // be in flight. Bounded waits, error already recorded.
         if (q_issued > 0) (void)mbar_wait(bar(0), (q_issued - 1) & 1, &g_shared_err);
         for (int g = max(0, k_issued - C::NSK); g < k_issued; ++g)
-          (void)mbar_wait(bar(C::B_KF + g % C::NSK), (g / C::NSK) & 1, &g_shared_err);
+          if (!stalled(g, 0)) (void)mbar_wait(bar(C::B_KF + g % C::NSK), (g / C::NSK) & 1, &g_shared_err);
         for (int g = max(0, v_issued - C::NSV); g < v_issued; ++g)
-          (void)mbar_wait(bar(C::B_VF + g % C::NSV), (g / C::NSV) & 1, &g_shared_err);
+          if (!stalled(g, 1)) (void)mbar_wait(bar(C::B_VF + g % C::NSV), (g / C::NSV) & 1, &g_shared_err);
       }
     } else if (warp == C::MMA_WARP) {
       // -------------------------------------------------------- MMA issuer
@@ -572,7 +586,7 @@ __global__ void __launch_bounds__(384, 1)
             // copy engine's.
             fence_proxy_async_smem();
             asm volatile("barrier.cta.sync 1, 64;" ::: "memory");
-            if (warp == C::CONV_WARP && __all_sync(0xffffffffu, ok)) {
+            if (warp == C::CONV_WARP && !stalled(g, 2) && __all_sync(0xffffffffu, ok)) {
               const int page0 = (s.t0 + j) * 8;
               load_tile(sbase + C::V_OFF + sv * C::TILE, &tmap_v, bar(C::B_VA), s.kvh, entries(page0), 0,
                         page0);
@@ -982,6 +996,17 @@ cudaError_t launch_shared(const SharedArgs& s, cudaStream_t stream) {
   auto merge = r.d_h == 128 ? shared_merge_kernel<128> : shared_merge_kernel<64>;
   return launch_pdl(merge, dim3(unsigned((a.rows + kMergeRows - 1) / kMergeRows), unsigned(r.h_kv)),
                     dim3(unsigned(kMergeRows * r.d_h / 4)), 0, stream, m);
+}
+
+cudaError_t shared_set_stall(int key_tile, int what) {
+#ifdef ATTN_DEBUG
+  const int v[2] = {key_tile, what};
+  return cudaMemcpyToSymbol(g_shared_stall, v, sizeof(v));
+#else
+  (void)key_tile;
+  (void)what;
+  return cudaErrorNotSupported;
+#endif
 }
 
 unsigned int shared_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {

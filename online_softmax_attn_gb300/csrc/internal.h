@@ -189,6 +189,9 @@ struct SharedArgs {
 };
 cudaError_t launch_shared(const SharedArgs& a, cudaStream_t stream);
 unsigned int shared_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
+// Debug builds: the load (0 K, 1 V, 2 V's second) of the key tile that each CTA does
+// not request (-1: none); cudaErrorNotSupported in release builds.
+cudaError_t shared_set_stall(int key_tile, int what);
 
 // prefill_simt.cu ----------------------------------------------------------
 cudaError_t launch_prefill_f32(const float* q, const float* k, const float* v, float* o,

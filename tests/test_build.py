@@ -64,3 +64,13 @@ def test_the_binding_is_compiled_again_for_another_torch(sandbox, monkeypatch):
     assert sandbox == ["binding"]
     b.build()
     assert sandbox == ["binding"]
+
+
+def test_shared_stall_selftest_is_debug_only():
+    """The release library refuses it without touching the device."""
+    import online_softmax_attn_gb300 as attn
+
+    b.build()
+    lib = attn.library()
+    assert lib.attn_selftest_shared_stall(2, 0) == lib.attn_selftest_shared_stall(-1, 2) == attn.ATTN_ERR_UNSUPPORTED
+    assert lib.attn_selftest_shared_stall(0, 3) == lib.attn_selftest_shared_stall(0, -1) == attn.ATTN_ERR_INVALID_ARG
