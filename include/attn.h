@@ -612,6 +612,10 @@ attn_status_t attn_cache_read_e4m3(const void* k_cache, const void* v_cache,
  * clamped (ATTN_DEVERR_BAD_SEQ_LEN), pages outside the cache read as zeros
  * (ATTN_DEVERR_BAD_PAGE). NaN codes reach the rows that attend them; slots
  * past a row's length never do.
+ * q enters as fp16 times a power of two per head: exact down to 2^-28 of the
+ * head's largest magnitude, within 2^-39 of it below that. A key's weight (times
+ * its value's scale) is one fp16 number, within 2^-11 of itself down to 2^-27 of
+ * the row's largest and within 2^-38 of the largest below that.
  * Errors: INVALID_ARG for NULL or misaligned pointers, B outside [0, 65535],
  * bad sizes, num_blocks * h_kv or B * h beyond int32, scale not finite and
  * > 0, a small workspace; UNSUPPORTED for d_h other than 64 / 128 or page_size
