@@ -615,7 +615,8 @@ attn_status_t attn_cache_read_e4m3(const void* k_cache, const void* v_cache,
  * q enters as fp16 times a power of two per head: exact down to 2^-28 of the
  * head's largest magnitude, within 2^-39 of it below that. A key's weight (times
  * its value's scale) is one fp16 number, within 2^-11 of itself down to 2^-27 of
- * the row's largest and within 2^-38 of the largest below that.
+ * the row's largest and within 2^-38 of the largest below that. A row's sum of
+ * exp(s - max) |v| has to stay below 2^126.
  * Errors: INVALID_ARG for NULL or misaligned pointers, B outside [0, 65535],
  * bad sizes, num_blocks * h_kv or B * h beyond int32, scale not finite and
  * > 0, a small workspace; UNSUPPORTED for d_h other than 64 / 128 or page_size
@@ -661,7 +662,7 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
  * a row; non-finite keys and values that are attended do, as in
  * attn_decode_paged.
  * Keys and values enter as they are, whatever their magnitudes, as long as a
- * row's sum of exp(s - max) |v| is a fp32 number. A weight exp(s - max) of a
+ * row's sum of exp(s - max) |v| stays below 2^126. A weight exp(s - max) of a
  * prefix key is one fp16 number, within 2^-11 of itself down to 2^-27 of the
  * row's largest and within 2^-38 of the largest below that; where values of its
  * 128 keys reach 128, or are not zero and below 2^-25, and for the rows' own

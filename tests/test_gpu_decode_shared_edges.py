@@ -175,3 +175,26 @@ def test_every_page_counts_once(i):
     PC.check(o[rows].double().cpu().numpy(), O[rows])
     check_lse(lse[rows], L[rows])
     assert attn.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("shift", [0, -16])
+@pytest.mark.parametrize("exp", [16, 21, 24, 27, 28, 30, 110])
+@pytest.mark.parametrize("at", [5, 400])
+def test_large_logits_and_large_values(at, exp, shift):
+    """Logits up to 2^exp, of which one key leads by 2^(exp - 3), and values around 2^100
+    from the second key tile on: the row is the leading key's value."""
+    args = case(700, [50, 20], 2, 4, 64, seed=44)
+    q, k, v, ptab = args[:4]
+    q.zero_()
+    q[:, :, 0] = 2.0 ** exp
+    k.zero_()
+    k[..., 0] = torch.randint(-8, 8, k.shape[:-1], generator=torch.Generator().manual_seed(2)).to(torch.bfloat16) + shift
+    for p in range(8, 44):
+        v[int(ptab[p])] *= 2.0 ** 100
+    page, slot = int(ptab[at // 16]), at % 16
+    k[page, slot, :, 0] = 8 + shift
+    o, lse = run(args)
+    assert torch.equal(o.cpu(), v[page, slot].repeat_interleave(4, 0).expand(2, -1, -1))
+    L = reference(*args)[1]
+    # factor, product, ln 2 and the product with it: 5 roundings of 2^-24
+    assert (np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -21 * np.abs(L)).all()
