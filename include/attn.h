@@ -680,6 +680,56 @@ attn_status_t attn_decode_paged_shared(const void* q, const void* k_cache, const
                                        void* stream);
 
 /*
+ * attn_decode_paged_window -- attn_decode_paged with a sliding window and a few
+ * first tokens that stay visible (sinks): one query token per row, at its last
+ * position seq_lens[b] - 1, that sees key j iff j >= seq_lens[b] - window or
+ * j < sinks ([DEC] paged addressing, [MRG] for the parts; the pages name no
+ * window, its bounds are this library's). The window counts the query's own
+ * position; window >= seq_lens[b] is plain causal decode, sinks 0 a plain window.
+ * attn_prefill_paged_window has the same mask. Only pages that hold a visible key
+ * are read, and only their table entries: a program may give the others back and
+ * leave anything in the table. The visible pages of all rows, laid end to end, are
+ * cut into equal runs on the device (as in attn_decode_paged_e4m3): no split count,
+ * any mix of lengths is balanced, the launch depends on no length (capturable,
+ * replayable with new lengths and tables), the result not on timing (no atomics).
+ *   q            [B, h, d_h] bf16                                    (read)
+ *   k_cache,
+ *   v_cache      [num_blocks, page_size, h_kv, d_h] bf16             (read)
+ *   block_table  [B, max_blocks_per_seq], seq_lens [B], int32        (read)
+ *   window       >= 1, sinks >= 0: the same for every row
+ *   workspace    256-byte aligned, attn_decode_window_workspace_bytes(B, h, h_kv,
+ *                d_h) bytes, overwritten; calls (and captured graphs) that share
+ *                one must not overlap on the GPU
+ *   o            [B, h, d_h] bf16                                    (written)
+ *   lse          [B, h] fp32, natural log, may be NULL               (written)
+ * Any h / h_kv; more than 8 query heads per KV head read its keys once per 8. A row
+ * of length 0 gives o = 0, lse = -inf. Lengths outside the table row are clamped
+ * (ATTN_DEVERR_BAD_SEQ_LEN); a visible page outside the cache reads as zeros
+ * (ATTN_DEVERR_BAD_PAGE). Slots out of sight never reach a row, whatever they hold.
+ * q, K and V enter as they are; a weight is two bf16 terms, within 2^-15 of itself.
+ * A row's sum of exp(s - max) |v| has to stay below 2^126.
+ * Errors: as attn_decode_paged_e4m3, plus INVALID_ARG for window < 1 or sinks < 0.
+ *
+ * attn_decode_paged_window_e4m3 -- the same over the 8-bit cache (arguments, number
+ * formats and limits of attn_decode_paged_e4m3).
+ */
+size_t attn_decode_window_workspace_bytes(int B, int h, int h_kv, int d_h);
+attn_status_t attn_decode_paged_window(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_table, const int32_t* seq_lens, int B,
+                                       int h, int h_kv, int d_h, int page_size, int num_blocks,
+                                       int max_blocks_per_seq, int window, int sinks, float scale,
+                                       void* workspace, size_t workspace_bytes, void* o, float* lse,
+                                       void* stream);
+attn_status_t attn_decode_paged_window_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                            const uint8_t* k_scale, const uint8_t* v_scale,
+                                            const int32_t* block_table, const int32_t* seq_lens,
+                                            int B, int h, int h_kv, int d_h, int page_size,
+                                            int num_blocks, int max_blocks_per_seq, int window,
+                                            int sinks, float scale, void* workspace,
+                                            size_t workspace_bytes, void* o, float* lse,
+                                            void* stream);
+
+/*
  * attn_get_device_error -- synchronise `stream`, then read and clear the
  * device error word of every kernel module (ATTN_DEVERR_* bits, 0 = none)
  * into *bits. Returns ATTN_ERR_CUDA if the synchronisation fails.

@@ -30,6 +30,9 @@ __all__ = [
     "attn_cache_read_e4m3",
     "attn_decode_paged_e4m3",
     "attn_decode_e4m3_workspace_bytes",
+    "attn_decode_paged_window",
+    "attn_decode_paged_window_e4m3",
+    "attn_decode_window_workspace_bytes",
     "attn_decode_paged_shared",
     "attn_decode_shared_workspace_bytes",
     "attn_get_device_error",
@@ -123,6 +126,12 @@ def library() -> ctypes.CDLL:
     lib.attn_decode_e4m3_workspace_bytes.restype = S
     lib.attn_decode_paged_e4m3.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, S, P, P, P]
     lib.attn_decode_paged_e4m3.restype = I
+    lib.attn_decode_window_workspace_bytes.argtypes = [I, I, I, I]
+    lib.attn_decode_window_workspace_bytes.restype = S
+    lib.attn_decode_paged_window.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, P, S, P, P, P]
+    lib.attn_decode_paged_window.restype = I
+    lib.attn_decode_paged_window_e4m3.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, P, S, P, P, P]
+    lib.attn_decode_paged_window_e4m3.restype = I
     lib.attn_decode_shared_workspace_bytes.argtypes = [I, I, I, I]
     lib.attn_decode_shared_workspace_bytes.restype = S
     lib.attn_decode_paged_shared.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, P, S, P, P, P]
@@ -633,6 +642,51 @@ def attn_decode_paged_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, s
     if st:
         _check("attn_decode_paged_e4m3", st)
     return o, lse
+
+
+def attn_decode_window_workspace_bytes(B: int, h: int, h_kv: int, d_h: int) -> int:
+    """Workspace bytes of attn_decode_paged_window and attn_decode_paged_window_e4m3."""
+    return int(library().attn_decode_window_workspace_bytes(int(B), int(h), int(h_kv), int(d_h)))
+
+
+def _decode_window(name, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, window, sinks, scale,
+                   workspace, o, lse, return_lse, stream):
+    where = _where(q, stream)
+    if workspace is None or o is None or (lse is None and return_lse):
+        h_kv = k_cache.shape[2 if k_scale is None else 1]
+        workspace, o, lse = _new_outputs(q, attn_decode_window_workspace_bytes, h_kv, workspace, o, lse,
+                                         return_lse, stream)
+    st = _calls().decode_window(*where, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, window,
+                                sinks, scale, workspace, o, lse)
+    if st:
+        _check(name, st)
+    return o, lse
+
+
+def attn_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, window: int, sinks: int = 0,
+                             scale: float | None = None, workspace=None, o=None, lse=None,
+                             return_lse: bool = True, stream=None):
+    """Paged decode with a sliding window: row b's query, at position
+    seq_lens[b] - 1, sees its last ``window`` keys (its own among them) and the
+    first ``sinks``. q [B,h,d] bf16, caches [num_blocks,16,h_kv,d] bf16,
+    block_table [B,max_blocks] int32, seq_lens [B] int32 (all CUDA, contiguous);
+    any h / h_kv. Table entries of pages without a visible key are not read. The
+    keys are divided over the GPU on the device, so the call can be captured and
+    replayed with new lengths. Returns (o [B,h,d] bf16, lse [B,h] fp32 or None)."""
+    return _decode_window("attn_decode_paged_window", q, k_cache, v_cache, None, None, block_table, seq_lens,
+                          window, sinks, scale, workspace, o, lse, return_lse, stream)
+
+
+def attn_decode_paged_window_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, window: int,
+                                  sinks: int = 0, scale: float | None = None, workspace=None, o=None, lse=None,
+                                  return_lse: bool = True, stream=None):
+    """attn_decode_paged_window over the 8-bit cache of attn_cache_write_e4m3
+    (caches [num_blocks,h_kv,16,d] float8_e4m3fn, scales [num_blocks,h_kv,16]
+    uint8). Returns (o [B,h,d] bf16, lse [B,h] fp32 or None)."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale expected")
+    return _decode_window("attn_decode_paged_window_e4m3", q, k_cache, v_cache, k_scale, v_scale, block_table,
+                          seq_lens, window, sinks, scale, workspace, o, lse, return_lse, stream)
 
 
 def attn_decode_shared_workspace_bytes(B: int, h: int, h_kv: int, d_h: int) -> int:

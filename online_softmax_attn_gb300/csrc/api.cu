@@ -524,12 +524,14 @@ size_t attn_decode_e4m3_workspace_bytes(int B, int h, int h_kv, int d_h) {
   return runs_layout(B, d_h).total;
 }
 
-attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const void* v_cache,
-                                     const uint8_t* k_scale, const uint8_t* v_scale,
-                                     const int32_t* block_table, const int32_t* seq_lens, int B,
-                                     int h, int h_kv, int d_h, int page_size, int num_blocks,
-                                     int max_blocks_per_seq, float scale, void* workspace,
-                                     size_t workspace_bytes, void* o, float* lse, void* stream) {
+namespace {
+// The run decodes: the 8-bit cache (eight_bit; with window = 0 the whole rows), or
+// the bf16 cache with a window.
+attn_status_t decode_runs(const void* q, const void* k_cache, const void* v_cache, bool eight_bit,
+                          const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                          const int32_t* seq_lens, int B, int h, int h_kv, int d_h, int page_size,
+                          int num_blocks, int max_blocks_per_seq, int window, int sinks, float scale,
+                          void* workspace, size_t workspace_bytes, void* o, float* lse, void* stream) {
   if (B < 0 || B > 65535 || h < 1 || h_kv < 1 || h_kv > 65535 || h % h_kv != 0 || num_blocks < 1 ||
       max_blocks_per_seq < 1 || !std::isfinite(scale) || !(scale > 0.f))
     return ATTN_ERR_INVALID_ARG;
@@ -540,8 +542,8 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
       static_cast<long long>(B) * h > 0x7fffffffll)
     return ATTN_ERR_INVALID_ARG;
   if (B == 0) return ATTN_OK;
-  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens ||
-      !workspace || !o)
+  if (!q || !k_cache || !v_cache || (eight_bit && (!k_scale || !v_scale)) || !block_table ||
+      !seq_lens || !workspace || !o)
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
       !aligned(v_scale, 16) || !aligned(o, 16) || !aligned(block_table, 4) ||
@@ -571,7 +573,52 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
   a.l_part = reinterpret_cast<float*>(ws + L.l_off);
   a.o = o;
   a.lse = lse;
-  return from_cuda(launch_decode8(a, static_cast<cudaStream_t>(stream)));
+  a.window = window;
+  a.sinks = sinks;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(window > 0 ? launch_decode_window(a, s) : launch_decode8(a, s));
+}
+}  // namespace
+
+attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                     const uint8_t* k_scale, const uint8_t* v_scale,
+                                     const int32_t* block_table, const int32_t* seq_lens, int B,
+                                     int h, int h_kv, int d_h, int page_size, int num_blocks,
+                                     int max_blocks_per_seq, float scale, void* workspace,
+                                     size_t workspace_bytes, void* o, float* lse, void* stream) {
+  return decode_runs(q, k_cache, v_cache, true, k_scale, v_scale, block_table, seq_lens, B, h, h_kv,
+                     d_h, page_size, num_blocks, max_blocks_per_seq, 0, 0, scale, workspace,
+                     workspace_bytes, o, lse, stream);
+}
+
+size_t attn_decode_window_workspace_bytes(int B, int h, int h_kv, int d_h) {
+  return attn_decode_e4m3_workspace_bytes(B, h, h_kv, d_h);
+}
+
+attn_status_t attn_decode_paged_window(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_table, const int32_t* seq_lens, int B,
+                                       int h, int h_kv, int d_h, int page_size, int num_blocks,
+                                       int max_blocks_per_seq, int window, int sinks, float scale,
+                                       void* workspace, size_t workspace_bytes, void* o, float* lse,
+                                       void* stream) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return decode_runs(q, k_cache, v_cache, false, nullptr, nullptr, block_table, seq_lens, B, h, h_kv,
+                     d_h, page_size, num_blocks, max_blocks_per_seq, window, sinks, scale, workspace,
+                     workspace_bytes, o, lse, stream);
+}
+
+attn_status_t attn_decode_paged_window_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                            const uint8_t* k_scale, const uint8_t* v_scale,
+                                            const int32_t* block_table, const int32_t* seq_lens,
+                                            int B, int h, int h_kv, int d_h, int page_size,
+                                            int num_blocks, int max_blocks_per_seq, int window,
+                                            int sinks, float scale, void* workspace,
+                                            size_t workspace_bytes, void* o, float* lse,
+                                            void* stream) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return decode_runs(q, k_cache, v_cache, true, k_scale, v_scale, block_table, seq_lens, B, h, h_kv,
+                     d_h, page_size, num_blocks, max_blocks_per_seq, window, sinks, scale, workspace,
+                     workspace_bytes, o, lse, stream);
 }
 
 size_t attn_decode_shared_workspace_bytes(int B, int h, int h_kv, int d_h) {

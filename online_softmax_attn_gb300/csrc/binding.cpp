@@ -1,6 +1,6 @@
 // binding.cpp -- the Python binding of the calls whose host time matters: the
-// 8-bit cache's write and read, its decode, and the shared-prefix decode run in
-// a few microseconds on small inputs, as long as ctypes and checks written in
+// 8-bit cache's write and read, its decode, the decodes with a window or a shared
+// prefix run in a few microseconds on small inputs, as long as ctypes and checks written in
 // Python take (of 10.2 us a call for the write of one token, 6.3 were checks and
 // argument conversion). Each function checks its tensors, as the other
 // entry points of the package do in Python, and calls the C entry point of the
@@ -22,6 +22,8 @@ struct Fns {
   decltype(&attn_cache_read_e4m3) read;
   decltype(&attn_decode_paged_e4m3) decode;
   decltype(&attn_decode_paged_shared) shared;
+  decltype(&attn_decode_paged_window) window;
+  decltype(&attn_decode_paged_window_e4m3) window8;
 };
 
 // Entry points of the library `handle` (guarded by the interpreter lock).
@@ -41,6 +43,8 @@ const Fns& entries(PyObject* handle) {
     n.read = reinterpret_cast<decltype(n.read)>(sym("attn_cache_read_e4m3"));
     n.decode = reinterpret_cast<decltype(n.decode)>(sym("attn_decode_paged_e4m3"));
     n.shared = reinterpret_cast<decltype(n.shared)>(sym("attn_decode_paged_shared"));
+    n.window = reinterpret_cast<decltype(n.window)>(sym("attn_decode_paged_window"));
+    n.window8 = reinterpret_cast<decltype(n.window8)>(sym("attn_decode_paged_window_e4m3"));
     f = n;
     loaded = h;
   }
@@ -191,6 +195,50 @@ PyObject* decode_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+int whole(PyObject* o, const char* what) {
+  const long n = PyLong_AsLong(o);
+  if (n == -1 && PyErr_Occurred()) throw std::invalid_argument(what);
+  need(n >= INT32_MIN && n <= INT32_MAX, what);
+  return static_cast<int>(n);
+}
+
+// (handle, device, stream, q, k_cache, v_cache, k_scale, v_scale (None, None: bf16
+//  caches), block_table, seq_lens, window, sinks, scale, workspace, o, lse) -> status
+PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> long {
+    args(n, 16);
+    const Fns& f = entries(a[0]);
+    const long dev = PyLong_AsLong(a[1]);
+    void* stream = PyLong_AsVoidPtr(a[2]);
+    const at::Tensor &q = tensor(a[3]), &kc = tensor(a[4]), &vc = tensor(a[5]), &table = tensor(a[8]),
+                     &lens = tensor(a[9]);
+    on_device(dev, {&q, &kc, &vc, &table, &lens});
+    const bool eight = a[6] != Py_None;
+    need(q.scalar_type() == at::kBFloat16 && q.dim() == 3 && kc.dim() == 4 && q.size(2) == kc.size(3),
+         "q must be bf16 [B,h,d]");
+    check_rows(q, table, lens);
+    const int B = small(q.size(0)), h = small(q.size(1)), d = small(q.size(2)), nb = small(kc.size(0)),
+              mb = small(table.size(1)), window = whole(a[10], "window"), sinks = whole(a[11], "sinks");
+    const float scale = scale_of(a[12], q.size(2));
+    const at::Tensor &ws = tensor(a[13]), &o = tensor(a[14]);
+    float* lse = check_outputs(dev, q, ws, o, a[15]);
+    if (eight) {
+      const at::Tensor &ks = tensor(a[6]), &vs = tensor(a[7]);
+      on_device(dev, {&ks, &vs});
+      check_cache8(kc, vc, ks, vs);
+      return f.window8(ptr(q), ptr(kc), ptr(vc), bptr(ks), bptr(vs), iptr(table), iptr(lens), B, h,
+                       small(kc.size(1)), d, small(kc.size(2)), nb, mb, window, sinks, scale, ptr(ws),
+                       ws.nbytes(), ptr(o), lse, stream);
+    }
+    need(kc.scalar_type() == at::kBFloat16 && vc.scalar_type() == at::kBFloat16 && vc.sizes() == kc.sizes(),
+         "caches must be bf16 [num_blocks,16,h_kv,d]");
+    contiguous({&kc, &vc});
+    return f.window(ptr(q), ptr(kc), ptr(vc), iptr(table), iptr(lens), B, h, small(kc.size(2)), d,
+                    small(kc.size(1)), nb, mb, window, sinks, scale, ptr(ws), ws.nbytes(), ptr(o), lse,
+                    stream);
+  });
+}
+
 // (handle, device, stream, q, k_cache, v_cache, prefix_table, prefix_len,
 //  block_table, seq_lens, scale, workspace, o, lse) -> status
 PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -228,6 +276,8 @@ PyMethodDef methods[] = {
      "attn_decode_paged_e4m3"},
     {"decode_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_shared)),
      METH_FASTCALL, "attn_decode_paged_shared"},
+    {"decode_window", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_window)),
+     METH_FASTCALL, "attn_decode_paged_window and attn_decode_paged_window_e4m3"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr,
                       nullptr};

@@ -1,6 +1,7 @@
 // decode_runs.cu -- attn_decode_paged_e4m3: the run decode (decode_runs.cuh) over
 // the 8-bit cache, and the merge of the rows that its runs cut; for few keys both
-// in one kernel.
+// in one kernel. attn_decode_paged_window and attn_decode_paged_window_e4m3 are the
+// same kernels over the pages that a row's window and its first tokens leave.
 #include "decode_runs.cuh"
 #include "pdl.cuh"
 
@@ -14,11 +15,11 @@ namespace {
 // 22.4 instead of 20.9 us for a row of 32768 keys (twice as many parts to join)
 // and 170.8 instead of 173.0 for 66 rows of up to 16384; 12 warps of 3 stages
 // 21.5 and 173.4, 16 of 2 24.0 and 170.7.
-template <int D, int NST>
+template <bool E8, int D, int NST, class R>
 __global__ void __launch_bounds__(256, 1)
     decode_runs_kernel(const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
                        const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs, const __nv_bfloat16* __restrict__ q,
-                       const int32_t* __restrict__ block_table, Rows rw, int h, int h_kv, int g,
+                       const int32_t* __restrict__ block_table, R rw, int h, int h_kv, int g,
                        int max_blocks, int num_blocks, float qscale, const RunOut out) {
   extern __shared__ __align__(16) uint8_t smem_raw[];  // (1024 would pad the static part)
   __shared__ RunShared<8> sh;
@@ -26,9 +27,9 @@ __global__ void __launch_bounds__(256, 1)
                                              ~uintptr_t(1023));
   pdl_wait();     // lengths, table, q and the cache are earlier kernels' output
   pdl_trigger();
-  runs_body<true, D, 8, NST>(kc, vc, ks, vs, q, block_table, rw, h, h_kv, g, max_blocks,
-                             num_blocks, qscale, out, smem, sh, blockIdx.x, gridDim.x,
-                             &g_decode_runs_err, [] { __syncthreads(); });
+  runs_body<E8, D, 8, NST>(kc, vc, ks, vs, q, block_table, rw, h, h_kv, g, max_blocks,
+                           num_blocks, qscale, out, smem, sh, blockIdx.x, gridDim.x,
+                           &g_decode_runs_err, [] { __syncthreads(); });
 }
 
 // Joins the partial states of each (row, head) that a run border cut, and
@@ -138,13 +139,14 @@ __global__ void __launch_bounds__(128)
 constexpr int kClusterCtas = 8;
 constexpr int kUnitMost = 14, kUnitBlocks = 256;
 static_assert(kUnitMost * kClusterCtas <= kRunsMaxCtas, "workspace of the partial states");
-template <int D, int NST>
+template <bool E8, int D, int NST, class R>
 __global__ void __launch_bounds__(256, 1) __cluster_dims__(kClusterCtas)
     decode_unit_kernel(const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
                        const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs, const __nv_bfloat16* __restrict__ q,
-                       const int32_t* __restrict__ block_table, const int32_t* __restrict__ seq_lens, int h, int h_kv,
-                       int g, int n_gb, int max_blocks, int num_blocks, float qscale, const RunOut out) {
-  using C = Cfg<true, D, 8, NST>;
+                       const int32_t* __restrict__ block_table, R rw, int h, int h_kv, int g, int n_gb,
+                       int max_blocks, int num_blocks, float qscale, const RunOut out) {
+  using C = Cfg<E8, D, 8, NST>;
+  constexpr size_t kHead = E8 ? C::PAGE_BYTES : D * 2;  // bytes from one head of a page to the next
   extern __shared__ __align__(16) uint8_t smem_raw[];  // (1024 would pad the static part)
   __shared__ RunShared<8> sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -162,17 +164,16 @@ __global__ void __launch_bounds__(256, 1) __cluster_dims__(kClusterCtas)
   if (mine.lse != nullptr) mine.lse += row0;
   pdl_wait();     // lengths, table, q and the cache are earlier kernels' output
   pdl_trigger();
-  const Rows rw{seq_lens + b, 1, max_blocks * kPage, 1, 1};
-  runs_body<true, D, 8, NST>(kc + static_cast<size_t>(kvh) * C::PAGE_BYTES,
-                             vc + static_cast<size_t>(kvh) * C::PAGE_BYTES, ks + kvh * kPage,
-                             vs + kvh * kPage, q + row0 * D,
-                             block_table + static_cast<size_t>(b) * max_blocks, rw, h, h_kv, nh,
-                             max_blocks, num_blocks, qscale, mine, smem, sh, cta, kClusterCtas,
-                             &g_decode_runs_err, [] { __syncthreads(); });
+  rw.seq_lens += b;
+  rw.B = rw.upr = rw.n_gb = 1;
+  runs_body<E8, D, 8, NST>(kc + kvh * kHead, vc + kvh * kHead, ks + kvh * kPage, vs + kvh * kPage,
+                           q + row0 * D, block_table + static_cast<size_t>(b) * max_blocks, rw, h,
+                           h_kv, nh, max_blocks, num_blocks, qscale, mine, smem, sh, cta, kClusterCtas,
+                           &g_decode_runs_err, [] { __syncthreads(); });
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   if (cta >= nh || threadIdx.x >= 32) return;
   constexpr int VEC = D / 32;
-  const int lane = threadIdx.x, wu = row_weight(row_len(rw, 0));
+  const int lane = threadIdx.x, wu = row_weight(rw, row_len(rw, 0));
   if (!ATTN_GUARD(row0 + cta < static_cast<size_t>(gridDim.x / (kClusterCtas * upr)) * h, &g_decode_runs_err))
     return;
   if (wu == 0) {  // an empty row
@@ -224,38 +225,49 @@ __global__ void __launch_bounds__(256, 1) __cluster_dims__(kClusterCtas)
   if (mine.lse != nullptr && lane == 0) mine.lse[cta] = empty ? -INFINITY : M * kLn2 + logf(L);
 }
 
-template <int D, int NST>
+template <class R>
+R rows_of(const DecodeRunsArgs& a) {
+  const int n_gb = (a.h / a.h_kv + 7) / 8;
+  R rw{};
+  static_cast<Rows&>(rw) = Rows{a.seq_lens, a.B, a.max_blocks * kPage, a.h_kv * n_gb, n_gb};
+  if constexpr (R::kWindow) {
+    rw.window = a.window;
+    rw.sinks = a.sinks;
+  }
+  return rw;
+}
+
+template <bool E8, int D, int NST, class R>
 cudaError_t launch_unit(const DecodeRunsArgs& a, cudaStream_t stream) {
-  constexpr int kSmem = Cfg<true, D, 8, NST>::SMEM + 1024;
-  auto kern = decode_unit_kernel<D, NST>;
+  constexpr int kSmem = Cfg<E8, D, 8, NST>::SMEM + 1024;
+  static_assert(kSmem + sizeof(RunShared<8>) <= 227 * 1024, "shared memory of an SM");
+  auto kern = decode_unit_kernel<E8, D, NST, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
+  const R rw = rows_of<R>(a);
   const RunOut out{nullptr, a.o_part, a.m_part, a.l_part, nullptr,
                    nullptr, nullptr,  static_cast<__nv_bfloat16*>(a.o), a.lse};
-  return launch_pdl(kern, dim3(unsigned(a.B * a.h_kv * n_gb * kClusterCtas)), dim3(256), size_t(kSmem), stream,
+  return launch_pdl(kern, dim3(unsigned(a.B * rw.upr * kClusterCtas)), dim3(256), size_t(kSmem), stream,
                     static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache), a.k_exp, a.v_exp,
-                    static_cast<const __nv_bfloat16*>(a.q), a.block_table, a.seq_lens, a.h, a.h_kv, g, n_gb,
+                    static_cast<const __nv_bfloat16*>(a.q), a.block_table, rw, a.h, a.h_kv, a.h / a.h_kv, rw.n_gb,
                     a.max_blocks, a.num_blocks, a.scale * kLog2e, out);
 }
 
-template <int D, int NST>
+template <bool E8, int D, int NST, class R>
 cudaError_t launch_cfg(const DecodeRunsArgs& a, int sms, cudaStream_t stream) {
-  using C = Cfg<true, D, 8, NST>;
+  using C = Cfg<E8, D, 8, NST>;
   constexpr int kSmem = C::SMEM + 1024;
   static_assert(kSmem + sizeof(RunShared<8>) <= 227 * 1024, "shared memory of an SM");
-  auto kern = decode_runs_kernel<D, NST>;
+  auto kern = decode_runs_kernel<E8, D, NST, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int grid = sms < kRunsMaxCtas ? sms : kRunsMaxCtas;
-  const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
-  const Rows rw{a.seq_lens, a.B, a.max_blocks * kPage, a.h_kv * n_gb, n_gb};
   const RunOut out{a.plan,  a.o_part, a.m_part, a.l_part, nullptr,
                    nullptr, nullptr,  static_cast<__nv_bfloat16*>(a.o), a.lse};
   return launch_pdl(kern, dim3(grid), dim3(256), size_t(kSmem), stream,
                     static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache), a.k_exp, a.v_exp,
-                    static_cast<const __nv_bfloat16*>(a.q), a.block_table, rw, a.h, a.h_kv, g,
-                    a.max_blocks, a.num_blocks, a.scale * kLog2e, out);
+                    static_cast<const __nv_bfloat16*>(a.q), a.block_table, rows_of<R>(a), a.h, a.h_kv,
+                    a.h / a.h_kv, a.max_blocks, a.num_blocks, a.scale * kLog2e, out);
 }
 
 cudaError_t sm_count(int* sms) {
@@ -267,15 +279,18 @@ cudaError_t sm_count(int* sms) {
 
 }  // namespace
 
-cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream) {
+namespace {
+// `most`: pages that a row can have, known on the host.
+template <bool E8, int NST128, int NST64, class R>
+cudaError_t launch_runs(const DecodeRunsArgs& a, int most, cudaStream_t stream) {
   const long long units = static_cast<long long>(a.B) * a.h_kv * ((a.h / a.h_kv + 7) / 8);
-  if (units <= kUnitMost && a.max_blocks <= kUnitBlocks)
-    return a.d_h == 128 ? launch_unit<128, 4>(a, stream) : launch_unit<64, 6>(a, stream);
+  if (units <= kUnitMost && most <= kUnitBlocks)
+    return a.d_h == 128 ? launch_unit<E8, 128, NST128, R>(a, stream) : launch_unit<E8, 64, NST64, R>(a, stream);
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  e = a.d_h == 128 ? launch_cfg<128, 4>(a, sms, stream)
-                   : launch_cfg<64, 6>(a, sms, stream);
+  e = a.d_h == 128 ? launch_cfg<E8, 128, NST128, R>(a, sms, stream)
+                   : launch_cfg<E8, 64, NST64, R>(a, sms, stream);
   if (e != cudaSuccess) return e;
   const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
   auto merge = a.d_h == 128 ? decode_runs_merge_kernel<128> : decode_runs_merge_kernel<64>;
@@ -283,6 +298,19 @@ cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream) {
                     static_cast<const float*>(a.o_part), static_cast<const float*>(a.m_part),
                     static_cast<const float*>(a.l_part), static_cast<const long long*>(a.plan), a.h,
                     g, n_gb, a.h_kv * n_gb, static_cast<__nv_bfloat16*>(a.o), a.lse);
+}
+}  // namespace
+
+cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream) {
+  return launch_runs<true, 4, 6, Rows>(a, a.max_blocks, stream);
+}
+
+cudaError_t launch_decode_window(const DecodeRunsArgs& a, cudaStream_t stream) {
+  // The window's pages (one more where it starts inside a page) and the sinks'.
+  const long long seen = (a.window + 14ll) / kPage + 1 + (a.sinks + 15ll) / kPage;
+  const int most = seen < a.max_blocks ? static_cast<int>(seen) : a.max_blocks;
+  return a.k_exp != nullptr ? launch_runs<true, 4, 6, WindowRows>(a, most, stream)
+                            : launch_runs<false, 3, 6, WindowRows>(a, most, stream);
 }
 
 unsigned int decode_runs_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {

@@ -1,6 +1,8 @@
 // decode_runs.cuh -- paged decode attention with the keys of the whole batch cut
-// into equal runs: over the 8-bit cache (attn_decode_paged_e4m3), and over the
-// rows' own bf16 pages in attn_decode_paged_shared.
+// into equal runs: over the 8-bit cache (attn_decode_paged_e4m3), over the rows' own
+// bf16 pages in attn_decode_paged_shared, and over the pages that a sliding window
+// and a few first tokens leave of a row, of either cache (attn_decode_paged_window,
+// attn_decode_paged_window_e4m3).
 //
 // One query token per row; the online recurrence of "Naive attention and the
 // online softmax" in base 2. Both contractions are mma.m16n8k16 with the keys
@@ -198,6 +200,36 @@ struct RunShared {
 struct Rows {
   const int32_t* seq_lens;
   int B, max_len, upr, n_gb;  // units per row, and per (row, KV head)
+  static constexpr bool kWindow = false;
+  __device__ __forceinline__ int pages(int len) const { return (len + kPage - 1) / kPage; }
+  __device__ __forceinline__ int page_at(int, int i) const { return i; }
+};
+// Rows that see their last `window` keys and the first `sinks`. What the kernel
+// walks are the pages that hold such keys, laid end to end: sink_pages of them,
+// then the window's from page first on. Every one of them holds a visible key, so
+// no page's scores are all masked, and pages in between are never looked up.
+struct WindowRows : Rows {
+  int window, sinks;
+  static constexpr bool kWindow = true;
+  __device__ __forceinline__ int first_key(int len) const { return max(len - window, 0); }
+  __device__ __forceinline__ int sink_pages(int len) const {
+    return (min(sinks, len) + kPage - 1) / kPage;
+  }
+  __device__ __forceinline__ int skipped(int len) const {  // pages between the two parts
+    return max(first_key(len) / kPage - sink_pages(len), 0);
+  }
+  __device__ __forceinline__ int pages(int len) const {
+    return (len + kPage - 1) / kPage - skipped(len);
+  }
+  __device__ __forceinline__ int page_at(int len, int i) const {
+    return i < sink_pages(len) ? i : i + skipped(len);
+  }
+  // Which of the 16 slots of page p a row of len keys sees, one bit each.
+  __device__ __forceinline__ uint32_t visible(int len, int p) const {
+    auto below = [](int n) { return (1u << min(max(n, 0), kPage)) - 1u; };  // slots 0 .. n - 1
+    const int at = p * kPage;
+    return below(len - at) & (~below(first_key(len) - at) | below(min(sinks, len) - at));
+  }
 };
 
 // A warp's run, unit by unit. Warp-uniform.
@@ -214,8 +246,9 @@ __device__ __forceinline__ int row_len(const Rows& rw, int b) {
 __device__ __forceinline__ int row_len(const Rows& rw, const int* cached, int b) {
   return rw.B <= kLenCache ? cached[b] : row_len(rw, b);
 }
-__device__ __forceinline__ int row_weight(int len) {  // of one unit of the row
-  return len > 0 ? (len + kPage - 1) / kPage + kUnit : 0;
+template <class R>
+__device__ __forceinline__ int row_weight(const R& rw, int len) {  // of one unit of the row
+  return len > 0 ? rw.pages(len) + kUnit : 0;
 }
 // a / b for a >= 0, b > 0: in 32 bits where both fit (64-bit division costs
 // several hundred cycles).
@@ -231,7 +264,8 @@ __device__ __forceinline__ void walk_open(Walk& w, long long off) {
   w.rem -= take;
 }
 // Next unit of the run; false at its end.
-__device__ __forceinline__ bool walk_next(Walk& w, const Rows& rw, const int* cached) {
+template <class R>
+__device__ __forceinline__ bool walk_next(Walk& w, const R& rw, const int* cached) {
   if (w.rem <= 0) return false;
   if (++w.u == rw.upr) {
     w.u = 0;
@@ -240,7 +274,7 @@ __device__ __forceinline__ bool walk_next(Walk& w, const Rows& rw, const int* ca
       if (w.b >= rw.B) return false;
       w.len = row_len(rw, cached, w.b);
     } while (w.len == 0);
-    w.np = (w.len + kPage - 1) / kPage;
+    w.np = rw.pages(w.len);
   }
   walk_open(w, 0);
   return true;
@@ -255,8 +289,8 @@ struct RunPlan {
 
 // Plans the runs, one per warp; CTA 0 leaves the plan for the merge (none: nullptr,
 // up to 32 rows).
-template <int NW, class Sync>
-__device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, RunShared<NW>& sh, int cta,
+template <int NW, class R, class Sync>
+__device__ __forceinline__ RunPlan plan_runs(const R rw, long long* plan, RunShared<NW>& sh, int cta,
                                           int n_cta, unsigned int* err, Sync sync) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // ---- the runs: prefix sums of the rows' weights (per unit) ----
@@ -278,7 +312,7 @@ __device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, Run
       if (cta == 0 && warp == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
     }
     sh.len[lane] = len;  // (every warp writes the same)
-    const uint32_t w = row_weight(len);
+    const uint32_t w = row_weight(rw, len);
     uint32_t incl = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -311,7 +345,7 @@ __device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, Run
       const int len = min(max(raw, 0), rw.max_len);
       if (cta == 0 && raw != len) atomicOr(err, ATTN_DEVERR_BAD_SEQ_LEN);
       if (b < kLenCache) sh.len[b] = len;
-      sum += row_weight(len);
+      sum += row_weight(rw, len);
     }
     long long incl = sum;
 #pragma unroll
@@ -335,7 +369,7 @@ __device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, Run
       long long at = before;
       for (int b = b0; b < b1; ++b) {
         plan[1 + b] = at;
-        at += row_weight(row_len(rw, sh.len, b));
+        at += row_weight(rw, row_len(rw, sh.len, b));
         if (b == rw.B - 1) plan[1 + rw.B] = at;
       }
     }
@@ -344,7 +378,7 @@ __device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, Run
     const long long end = (before + sum) * rw.upr;
     if (cta0 + per * NW > at && cta0 < end) {
       for (int b = b0; b < b1; ++b) {
-        const long long next = at + static_cast<long long>(row_weight(row_len(rw, sh.len, b))) * rw.upr;
+        const long long next = at + static_cast<long long>(row_weight(rw, row_len(rw, sh.len, b))) * rw.upr;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
           const long long p = cta0 + per * w;
@@ -372,8 +406,8 @@ __device__ __forceinline__ RunPlan plan_runs(const Rows rw, long long* plan, Run
 // the plan inlined 256 rows over a prefix of 32768 keys took 192 us instead of
 // 182, 64 over 8192 50.9 instead of 50.3; the 8-bit decode takes it inlined (a row
 // of 32768 keys 20.7 us, this way 20.9).
-template <int NW, class Sync>
-__device__ __noinline__ RunPlan plan_runs_apart(const Rows rw, long long* plan, RunShared<NW>& sh,
+template <int NW, class R, class Sync>
+__device__ __noinline__ RunPlan plan_runs_apart(const R rw, long long* plan, RunShared<NW>& sh,
                                                 int cta, int n_cta, unsigned int* err, Sync sync) {
   return plan_runs(rw, plan, sh, cta, n_cta, err, sync);
 }
@@ -381,14 +415,16 @@ __device__ __noinline__ RunPlan plan_runs_apart(const Rows rw, long long* plan, 
 // The whole of CTA `cta` of `n_cta`, by NW warps (threads 0 .. NW * 32 - 1), which
 // `sync` joins; `smem` starts at a 1024-byte boundary. Returns with every copy
 // landed.
-template <bool E8, int D, int NW, int NST, class Sync>
+template <bool E8, int D, int NW, int NST, class R, class Sync>
 __device__ __forceinline__ void runs_body(
     const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc, const uint8_t* __restrict__ ks,
     const uint8_t* __restrict__ vs, const __nv_bfloat16* __restrict__ q,
-    const int32_t* __restrict__ block_table, const Rows rw, int h, int h_kv, int g, int max_blocks,
+    const int32_t* __restrict__ block_table, const R rw, int h, int h_kv, int g, int max_blocks,
     int num_blocks, float qscale, const RunOut& out, uint8_t* smem, RunShared<NW>& sh, int cta,
     int n_cta, unsigned int* err, Sync sync) {
   using C = Cfg<E8, D, NW, NST>;
+  constexpr bool WIN = R::kWindow;
+  constexpr bool FINAL = E8 || WIN;  // units that no border cuts: o and lse, else row states
   constexpr int KS = D / 16;  // MMA steps over d_h
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tq = lane & 3;
@@ -408,7 +444,7 @@ __device__ __forceinline__ void runs_body(
   auto tail_of = [&](int w) { return reinterpret_cast<float*>(smem + w * NST * C::STAGE_BYTES); };
 
   RunPlan plan;
-  if constexpr (E8)
+  if constexpr (FINAL)
     plan = plan_runs(rw, out.plan, sh, cta, n_cta, err, sync);
   else
     plan = plan_runs_apart(rw, out.plan, sh, cta, n_cta, err, sync);
@@ -418,7 +454,7 @@ __device__ __forceinline__ void runs_body(
   cw.b = plan.b;
   cw.len = plan.len;
   const long long off = plan.off;
-  cw.np = (cw.len + kPage - 1) / kPage;
+  cw.np = rw.pages(cw.len);
   cw.rem = plan.rem;
   {
     const int wu = cw.np + kUnit;
@@ -434,7 +470,7 @@ __device__ __forceinline__ void runs_body(
   int issued = 0;
   auto load_bt = [&](int i) {
     bt = i + lane < pw.hi
-             ? __ldcg(block_table + static_cast<size_t>(pw.b) * max_blocks + i + lane)
+             ? __ldcg(block_table + static_cast<size_t>(pw.b) * max_blocks + rw.page_at(pw.len, i + lane))
              : -1;
   };
   const uint32_t ring = sbase + warp * NST * C::STAGE_BYTES;
@@ -502,11 +538,16 @@ __device__ __forceinline__ void runs_body(
       const float L = e ? L1 : L0, M = e ? M1 : M0;
       const size_t row = row0 + head;
       if (!ATTN_GUARD(row < static_cast<size_t>(rw.B) * h, err)) continue;
-      if (E8 && slot < 0) {
+      if (FINAL && slot < 0) {
         const bool empty = L == 0.f;  // every logit -inf
         const float inv = empty ? 0.f : 1.f / L;
-        *reinterpret_cast<uint32_t*>(out.o + row * D + 16 * k + 2 * gid) =
-            empty ? 0u : pack_bf16x2(x[e] * inv, x[2 + e] * inv);
+        if constexpr (E8) {
+          *reinterpret_cast<uint32_t*>(out.o + row * D + 16 * k + 2 * gid) =
+              empty ? 0u : pack_bf16x2(x[e] * inv, x[2 + e] * inv);
+        } else {
+          out.o[row * D + 16 * k + gid] = __float2bfloat16(empty ? 0.f : x[e] * inv);
+          out.o[row * D + 16 * k + 8 + gid] = __float2bfloat16(empty ? 0.f : x[2 + e] * inv);
+        }
         if (k == 0 && out.lse != nullptr && gid == 0)
           out.lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
         continue;
@@ -617,16 +658,22 @@ __device__ __forceinline__ void runs_body(
       copies_wait<NST - 1>();
       __syncwarp();
       const uint32_t kp = ring + st * C::STAGE_BYTES, vp = kp + C::PAGE_BYTES;
-      const int valid = min(kPage, cw.len - i * kPage);
-      if (valid < kPage) {
-        // Slots past the row's end hold whatever the cache holds there (NaN
-        // codes among it); their weights are 0, but 0 * NaN is not.
+      // Slots that the row sees: below `valid`, or (window) the bits of `vis`.
+      const int valid = WIN ? kPage : min(kPage, cw.len - i * kPage);
+      uint32_t vis = 0xffffu;
+      if constexpr (WIN) vis = rw.visible(cw.len, rw.page_at(cw.len, i));
+      const bool partial = WIN ? vis != 0xffffu : valid < kPage;
+      auto live = [&](int slot) { return WIN ? ((vis >> slot) & 1u) != 0u : slot < valid; };
+      if (partial) {
+        // Slots out of sight hold whatever the cache holds there (NaN codes
+        // among it); their weights are 0, but 0 * NaN is not.
         constexpr int CPR = C::PAGE_BYTES / (kPage * 16);
-        for (int c = lane; c < (kPage - valid) * CPR; c += 32)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                           chunk_at<E8, D>(vp, valid + c / CPR, c % CPR)),
-                       "r"(0u)
-                       : "memory");
+        for (int c = lane; c < (WIN ? kPage : kPage - valid) * CPR; c += 32)
+          if (!WIN || !live(c / CPR))
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             chunk_at<E8, D>(vp, (WIN ? 0 : valid) + c / CPR, c % CPR)),
+                         "r"(0u)
+                         : "memory");
         __syncwarp();
       }
 
@@ -678,9 +725,9 @@ __device__ __forceinline__ void runs_body(
       auto weights = [&] {
         float x[4] = {s[0] - m0, s[1] - m1, s[2] - m0, s[3] - m1};
         float va = e4m3::scale_of(fa), vb = e4m3::scale_of(fb);
-        if (valid < kPage) {  // slots past the row's end: weight 0, whatever they hold
-          if (gid >= valid) x[0] = x[1] = -INFINITY, va = 0.f;
-          if (gid + 8 >= valid) x[2] = x[3] = -INFINITY, vb = 0.f;
+        if (partial) {  // slots out of sight: weight 0, whatever they hold
+          if (!live(gid)) x[0] = x[1] = -INFINITY, va = 0.f;
+          if (!live(gid + 8)) x[2] = x[3] = -INFINITY, vb = 0.f;
         }
         p0 = ex2_approx(x[0]);
         p1 = ex2_approx(x[1]);
@@ -699,7 +746,7 @@ __device__ __forceinline__ void runs_body(
       bool up = fmaxf(fmaxf(p0, p1), fmaxf(p2, p3)) > 4.f;
       if constexpr (E8) up = up || fmaxf(fmaxf(w0, w1), fmaxf(w2, w3)) > 32768.f;
       if (__any_sync(0xffffffffu, up)) {
-        const bool la = gid < valid, lb = gid + 8 < valid;
+        const bool la = live(gid), lb = live(gid + 8);
         const float s0 = la ? s[0] : -INFINITY, s1 = la ? s[1] : -INFINITY;
         const float s2 = lb ? s[2] : -INFINITY, s3 = lb ? s[3] : -INFINITY;
         const float ga = static_cast<float>(static_cast<int>(fa) - 127);

@@ -129,10 +129,14 @@ struct DecodeRunsArgs {
   float* o_row = nullptr;  // bf16 only: states of units that no run border cuts
   float* m_row = nullptr;
   float* l_row = nullptr;
-  void* o = nullptr;       // 8-bit cache only
+  void* o = nullptr;       // 8-bit cache and windows
   float* lse = nullptr;
+  int window = 0, sinks = 0;  // windows only
 };
 cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream);  // and its merge
+// The same over each row's last `window` keys and first `sinks`, of the 8-bit cache
+// (k_exp given) or of the bf16 one.
+cudaError_t launch_decode_window(const DecodeRunsArgs& a, cudaStream_t stream);
 unsigned int decode_runs_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
 
 // decode_shared.cu -----------------------------------------------------------
