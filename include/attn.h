@@ -730,6 +730,60 @@ attn_status_t attn_decode_paged_window_e4m3(const void* q, const void* k_cache, 
                                             void* stream);
 
 /*
+ * attn_decode_paged_tree -- attention of drafted tokens over the paged cache:
+ * speculative decoding, where each row verifies the drafts of a tree in one call.
+ * Row b has the n_b = cu_seqlens_q[b+1] - cu_seqlens_q[b] query tokens
+ * cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 of q (packed as in attn_prefill_paged),
+ * whose keys and values are the last n_b of its seq_lens[b] in the cache ([DEC]
+ * paged addressing). All of them see the seq_lens[b] - n_b keys in front; token i
+ * of the row sees draft t of the row (at position seq_lens[b] - n_b + t) iff bit
+ * t % 32 of tree_mask[token][t / 32] is set: its ancestors and itself, for a tree
+ * (a chain is the causal mask). The masks are taken as they are; bits from n_b on
+ * are ignored. The query rows of a KV head (drafts times heads of the group) share
+ * its keys, which are read once per 256 / (h / h_kv) drafts. The work is divided over
+ * the GPU on the device (any mix of lengths and of drafts); two kernels, whose
+ * launches depend on h, h_kv and max_q_len only (capturable, replayable with new
+ * offsets, lengths, masks and tables); no atomics, the result does not depend on
+ * timing.
+ *   q            [total_q, h, d_h] bf16                               (read)
+ *   k_cache,
+ *   v_cache      [num_blocks, page_size, h_kv, d_h] bf16              (read)
+ *   block_table  [B, max_blocks_per_seq] int32                        (read)
+ *   cu_seqlens_q [B + 1] int32, non-decreasing; rows without a draft are allowed,
+ *                tokens in front of the first or behind the last row are left
+ *                as they are                                          (read)
+ *   seq_lens     [B] int32, the drafts among them                     (read)
+ *   tree_mask    [total_q, mask_words] int32 (bits)                   (read)
+ *   max_q_len    host bound on every n_b; mask_words * 32 >= max_q_len
+ *   workspace    256-byte aligned, attn_decode_tree_workspace_bytes(B, h, h_kv, d_h)
+ *                bytes (about 42 MB at d_h = 128, whatever B), overwritten; calls
+ *                (and captured graphs) that share one must not overlap on the GPU
+ *   o            [total_q, h, d_h] bf16                               (written)
+ *   lse          [total_q, h] fp32, natural log, may be NULL          (written)
+ * A token that sees no key gives o = 0, lse = -inf. Keys that a token does not see,
+ * slots behind the row's end among them, never reach it, whatever they and their
+ * values hold; a non-finite value of a draft that it does see makes its column NaN.
+ * Offsets outside [0, total_q], n_b outside [0, min(max_q_len, max_blocks_per_seq *
+ * 16)] set ATTN_DEVERR_BAD_SEQ_LEN and the row's outputs are not written; seq_lens
+ * outside [n_b, max_blocks_per_seq * 16] set it and are clamped; pages outside the
+ * cache read as zeros (ATTN_DEVERR_BAD_PAGE).
+ * q, K and V enter as they are; a weight is two bf16 terms, within 2^-15 of itself.
+ * A row's sum of exp(s - max) |v| has to stay below 2^118.
+ * Errors: INVALID_ARG for NULL or misaligned pointers, negative or zero sizes, h %
+ * h_kv != 0, B > 65535, total_q * h beyond int32, max_q_len < 1 or mask_words * 32 <
+ * max_q_len, scale not finite and > 0, a small workspace; UNSUPPORTED for d_h other
+ * than 64 / 128, page_size != 16 or h / h_kv > 128. B == 0 or total_q == 0 is a no-op.
+ */
+size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int d_h);
+attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                     const int32_t* seq_lens, const int32_t* tree_mask, int B,
+                                     int total_q, int h, int h_kv, int d_h, int page_size,
+                                     int num_blocks, int max_blocks_per_seq, int max_q_len,
+                                     int mask_words, float scale, void* workspace,
+                                     size_t workspace_bytes, void* o, float* lse, void* stream);
+
+/*
  * attn_get_device_error -- synchronise `stream`, then read and clear the
  * device error word of every kernel module (ATTN_DEVERR_* bits, 0 = none)
  * into *bits. Returns ATTN_ERR_CUDA if the synchronisation fails.

@@ -30,6 +30,8 @@ __all__ = [
     "attn_cache_read_e4m3",
     "attn_decode_paged_e4m3",
     "attn_decode_e4m3_workspace_bytes",
+    "attn_decode_paged_tree",
+    "attn_decode_tree_workspace_bytes",
     "attn_decode_paged_window",
     "attn_decode_paged_window_e4m3",
     "attn_decode_window_workspace_bytes",
@@ -126,6 +128,10 @@ def library() -> ctypes.CDLL:
     lib.attn_decode_e4m3_workspace_bytes.restype = S
     lib.attn_decode_paged_e4m3.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, S, P, P, P]
     lib.attn_decode_paged_e4m3.restype = I
+    lib.attn_decode_tree_workspace_bytes.argtypes = [I, I, I, I]
+    lib.attn_decode_tree_workspace_bytes.restype = S
+    lib.attn_decode_paged_tree.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, S, P, P, P]
+    lib.attn_decode_paged_tree.restype = I
     lib.attn_decode_window_workspace_bytes.argtypes = [I, I, I, I]
     lib.attn_decode_window_workspace_bytes.restype = S
     lib.attn_decode_paged_window.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, P, S, P, P, P]
@@ -711,6 +717,34 @@ def attn_decode_paged_shared(q, k_cache, v_cache, prefix_table, prefix_len, bloc
                                 scale, workspace, o, lse)
     if st:
         _check("attn_decode_paged_shared", st)
+    return o, lse
+
+
+def attn_decode_tree_workspace_bytes(B: int, h: int, h_kv: int, d_h: int) -> int:
+    """Workspace bytes of attn_decode_paged_tree (the same for every B)."""
+    return int(library().attn_decode_tree_workspace_bytes(int(B), int(h), int(h_kv), int(d_h)))
+
+
+def attn_decode_paged_tree(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, tree_mask, max_q_len: int,
+                           scale: float | None = None, workspace=None, o=None, lse=None,
+                           return_lse: bool = True, stream=None):
+    """Attention of drafted tokens that form a tree (speculative decoding). q
+    [total_q,h,d] bf16 holds each row's drafts back to back (cu_seqlens_q [B+1]
+    int32); their keys are the last of the row's seq_lens[b] (int32) positions of
+    the caches [num_blocks,16,h_kv,d] bf16 through block_table [B,max_blocks] int32.
+    Every draft sees the keys in front of the row's drafts; token i sees draft t of
+    its row iff bit t % 32 of tree_mask[i, t // 32] is set (int32 [total_q, words],
+    words * 32 >= max_q_len, the most drafts of a row). All CUDA, contiguous. Can be
+    captured and replayed with new offsets, lengths and masks. Returns (o
+    [total_q,h,d] bf16, lse [total_q,h] fp32 or None)."""
+    where = _where(q, stream)
+    if workspace is None or o is None or (lse is None and return_lse):
+        workspace, o, lse = _new_outputs(q, attn_decode_tree_workspace_bytes, k_cache.shape[2], workspace, o, lse,
+                                         return_lse, stream)
+    st = _calls().decode_tree(*where, q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, tree_mask,
+                              max_q_len, scale, workspace, o, lse)
+    if st:
+        _check("attn_decode_paged_tree", st)
     return o, lse
 
 

@@ -38,7 +38,7 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libattn_gb300_debug.so")
 
 SOURCES = ["api.cu", "merge.cu", "decode.cu", "prefill_simt.cu", "prefill_tc.cu",
            "decode_static.cu", "host_prefill.cu", "cache_e4m3.cu", "decode_runs.cu",
-           "decode_shared.cu"]
+           "decode_shared.cu", "decode_tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -690,6 +690,60 @@ attn_status_t attn_decode_paged_shared(const void* q, const void* k_cache, const
   return from_cuda(launch_shared(s, static_cast<cudaStream_t>(stream)));
 }
 
+size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int d_h) {
+  if (B < 0 || h < 1 || h_kv < 1 || h % h_kv != 0 || h / h_kv > 128 || (d_h != 64 && d_h != 128)) return 0;
+  return tree_layout(d_h).total;
+}
+
+attn_status_t attn_decode_paged_tree(const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                     const int32_t* seq_lens, const int32_t* tree_mask, int B,
+                                     int total_q, int h, int h_kv, int d_h, int page_size,
+                                     int num_blocks, int max_blocks_per_seq, int max_q_len,
+                                     int mask_words, float scale, void* workspace,
+                                     size_t workspace_bytes, void* o, float* lse, void* stream) {
+  if (B < 0 || B > 65535 || total_q < 0 || h < 1 || h_kv < 1 || h_kv > 65535 || h % h_kv != 0 ||
+      num_blocks < 1 || max_blocks_per_seq < 1 || !std::isfinite(scale) || !(scale > 0.f))
+    return ATTN_ERR_INVALID_ARG;
+  if ((d_h != 64 && d_h != 128) || page_size != 16 || h / h_kv > 128) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_blocks_per_seq) * page_size > (1ll << 30) ||
+      static_cast<long long>(total_q) * h > 0x7fffffffll)
+    return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || total_q == 0) return ATTN_OK;
+  if (max_q_len < 1 || mask_words < 1 || static_cast<long long>(mask_words) * 32 < max_q_len)
+    return ATTN_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens_q || !seq_lens || !tree_mask ||
+      !workspace || !o)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
+      !aligned(block_table, 4) || !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) ||
+      !aligned(tree_mask, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < tree_layout(d_h).total) return ATTN_ERR_INVALID_ARG;
+  TreeDecode t;
+  t.q = q;
+  t.k_cache = k_cache;
+  t.v_cache = v_cache;
+  t.block_table = block_table;
+  t.cu_q = cu_seqlens_q;
+  t.seq_lens = seq_lens;
+  t.mask = tree_mask;
+  t.B = B;
+  t.total_q = total_q;
+  t.max_q_len = max_q_len;
+  t.words = mask_words;
+  t.h = h;
+  t.h_kv = h_kv;
+  t.d_h = d_h;
+  t.num_blocks = num_blocks;
+  t.max_blocks = max_blocks_per_seq;
+  t.scale = scale;
+  t.workspace = workspace;
+  t.o = o;
+  t.lse = lse;
+  return from_cuda(launch_decode_tree(t, static_cast<cudaStream_t>(stream)));
+}
+
 attn_status_t attn_selftest_wait_timeout(unsigned int limit_us, void* stream) {
   if (limit_us < 1 || limit_us > 1000000) return ATTN_ERR_INVALID_ARG;
   return from_cuda(launch_wait_timeout_selftest(uint64_t(limit_us) * 1000ull,
@@ -723,7 +777,7 @@ attn_status_t attn_get_device_error(void* stream, unsigned int* bits) {
   if (bits == nullptr) return ATTN_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess, e4 = cudaSuccess;
-  cudaError_t e5 = cudaSuccess, e6 = cudaSuccess, e7 = cudaSuccess;
+  cudaError_t e5 = cudaSuccess, e6 = cudaSuccess, e7 = cudaSuccess, e8 = cudaSuccess;
   unsigned int v = decode_read_and_clear_error(s, &e1);
   v |= merge_read_and_clear_error(s, &e2);
   v |= prefill_read_and_clear_error(s, &e3);
@@ -731,9 +785,10 @@ attn_status_t attn_get_device_error(void* stream, unsigned int* bits) {
   v |= cache8_read_and_clear_error(s, &e5);
   v |= decode_runs_read_and_clear_error(s, &e6);
   v |= shared_read_and_clear_error(s, &e7);
+  v |= tree_read_and_clear_error(s, &e8);
   *bits = v;
   if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess || e4 != cudaSuccess ||
-      e5 != cudaSuccess || e6 != cudaSuccess || e7 != cudaSuccess)
+      e5 != cudaSuccess || e6 != cudaSuccess || e7 != cudaSuccess || e8 != cudaSuccess)
     return ATTN_ERR_CUDA;
   return ATTN_OK;
 }

@@ -197,6 +197,39 @@ unsigned int shared_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
 // not request (-1: none); cudaErrorNotSupported in release builds.
 cudaError_t shared_set_stall(int key_tile, int what);
 
+// decode_tree.cu -------------------------------------------------------------
+// Per attention CTA which unit it leaves to the merge (16 bytes), then two partial
+// states per CTA: O~ [2 * 160, 2 tiles, d_h / 4, 128, 4], m and l [2 * 160, 2, 128].
+constexpr size_t kTreeCutBytes = 16;
+struct TreeLayout {
+  size_t o_off, m_off, l_off, total;
+};
+inline TreeLayout tree_layout(int d_h) {
+  constexpr size_t kRows = size_t(2 * kRunsMaxCtas) * 2 * 128;
+  TreeLayout L;
+  L.o_off = align256(kRunsMaxCtas * kTreeCutBytes);
+  L.m_off = L.o_off + kRows * d_h * sizeof(float);
+  L.l_off = L.m_off + kRows * sizeof(float);
+  L.total = L.l_off + kRows * sizeof(float);
+  return L;
+}
+struct TreeDecode {
+  const void* q;  // [total_q, h, d_h] bf16
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_table;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  const int32_t* mask;  // [total_q, words]
+  int B, total_q, max_q_len, words, h, h_kv, d_h, num_blocks, max_blocks;
+  float scale;
+  void* workspace;
+  void* o;
+  float* lse;
+};
+cudaError_t launch_decode_tree(const TreeDecode& t, cudaStream_t stream);  // and its merge
+unsigned int tree_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
+
 // prefill_simt.cu ----------------------------------------------------------
 cudaError_t launch_prefill_f32(const float* q, const float* k, const float* v, float* o,
                                float* lse, int T, int h, int h_kv, int d_h, int causal,
