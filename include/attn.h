@@ -730,6 +730,37 @@ attn_status_t attn_decode_paged_window_e4m3(const void* q, const void* k_cache, 
                                             void* stream);
 
 /*
+ * attn_prefill_paged_window -- attn_prefill_paged (causal, variable-length rows of
+ * queries over the paged cache) with the mask of attn_decode_paged_window: the query
+ * at position p of its row sees key j <= p where j > p - window or j < sinks. Key tiles
+ * between the sinks and a query block's windows are not visited; pages that no query
+ * of their row sees are not read, nor their table entries.
+ *   q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, max_q_len, o, lse
+ *                as in attn_prefill_paged; tokens in front of the first or behind the
+ *                last row are left as they are
+ *   window       >= 1, sinks >= 0: the same for every row
+ *   workspace    256-byte aligned, attn_prefill_window_workspace_bytes(B,
+ *                max_blocks_per_seq, h_kv, d_h) bytes (those of
+ *                attn_prefill_paged_v16_workspace_bytes; 0 where the fp16 copy of V
+ *                cannot be used), overwritten; calls that share one must not overlap
+ * Rows of one query run as 1-row query tiles; attn_decode_paged_window is made for
+ * them. Keys that a query does not see never reach it, whatever they and their values
+ * hold; a non-finite value that it does see makes its column NaN or that infinity.
+ * Errors, device errors and limits: as attn_prefill_paged, where offsets outside
+ * [0, total_q] also set ATTN_DEVERR_BAD_SEQ_LEN (the row is skipped); plus INVALID_ARG
+ * for B > 65535, window < 1, sinks < 0 and a workspace below its size, UNSUPPORTED
+ * where that size is 0.
+ */
+size_t attn_prefill_window_workspace_bytes(int B, int max_blocks_per_seq, int h_kv, int d_h);
+attn_status_t attn_prefill_paged_window(const void* q, const void* k_cache, const void* v_cache,
+                                        const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                        const int32_t* seq_lens, int B, int total_q, int h, int h_kv,
+                                        int d_h, int page_size, int num_blocks,
+                                        int max_blocks_per_seq, int max_q_len, int window, int sinks,
+                                        float scale, void* workspace, size_t workspace_bytes, void* o,
+                                        float* lse, void* stream);
+
+/*
  * attn_decode_paged_tree -- attention of drafted tokens over the paged cache:
  * speculative decoding, where each row verifies the drafts of a tree in one call.
  * Row b has the n_b = cu_seqlens_q[b+1] - cu_seqlens_q[b] query tokens

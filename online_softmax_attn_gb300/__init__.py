@@ -30,6 +30,8 @@ __all__ = [
     "attn_cache_read_e4m3",
     "attn_decode_paged_e4m3",
     "attn_decode_e4m3_workspace_bytes",
+    "attn_prefill_paged_window",
+    "attn_prefill_window_workspace_bytes",
     "attn_decode_paged_tree",
     "attn_decode_tree_workspace_bytes",
     "attn_decode_paged_window",
@@ -128,6 +130,10 @@ def library() -> ctypes.CDLL:
     lib.attn_decode_e4m3_workspace_bytes.restype = S
     lib.attn_decode_paged_e4m3.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, S, P, P, P]
     lib.attn_decode_paged_e4m3.restype = I
+    lib.attn_prefill_window_workspace_bytes.argtypes = [I, I, I, I]
+    lib.attn_prefill_window_workspace_bytes.restype = S
+    lib.attn_prefill_paged_window.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, F, P, S, P, P, P]
+    lib.attn_prefill_paged_window.restype = I
     lib.attn_decode_tree_workspace_bytes.argtypes = [I, I, I, I]
     lib.attn_decode_tree_workspace_bytes.restype = S
     lib.attn_decode_paged_tree.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, S, P, P, P]
@@ -717,6 +723,33 @@ def attn_decode_paged_shared(q, k_cache, v_cache, prefix_table, prefix_len, bloc
                                 scale, workspace, o, lse)
     if st:
         _check("attn_decode_paged_shared", st)
+    return o, lse
+
+
+def attn_prefill_window_workspace_bytes(B: int, max_blocks: int, h_kv: int, d_h: int) -> int:
+    """Workspace bytes of attn_prefill_paged_window (0: sizes that it refuses)."""
+    return int(library().attn_prefill_window_workspace_bytes(int(B), int(max_blocks), int(h_kv), int(d_h)))
+
+
+def attn_prefill_paged_window(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, window: int, sinks: int,
+                              max_q_len: int, scale: float | None = None, workspace=None, o=None, lse=None,
+                              return_lse: bool = True, stream=None):
+    """Causal attention of variable-length query rows over a paged cache with a
+    sliding window: the query at position p of its row sees key j <= p where j > p -
+    window or j < sinks. q [total_q,h,d] bf16 (rows packed back to back, row b's the
+    last of its seq_lens[b] positions), caches [num_blocks,16,h_kv,d] bf16,
+    block_table [B,max_blocks], cu_seqlens_q [B+1], seq_lens [B] int32 (all CUDA,
+    contiguous); no row has more than max_q_len queries. Table entries of pages that
+    no query of their row sees are not read. Returns (o [total_q,h,d] bf16, lse
+    [total_q,h] fp32 or None)."""
+    where = _where(q, stream)
+    if workspace is None or o is None or (lse is None and return_lse):
+        need = lambda _, h, h_kv, d: attn_prefill_window_workspace_bytes(seq_lens.shape[0], block_table.shape[1], h_kv, d)
+        workspace, o, lse = _new_outputs(q, need, k_cache.shape[2], workspace, o, lse, return_lse, stream)
+    st = _calls().prefill_window(*where, q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, window, sinks,
+                                 max_q_len, scale, workspace, o, lse)
+    if st:
+        _check("attn_prefill_paged_window", st)
     return o, lse
 
 

@@ -1,6 +1,6 @@
 // binding.cpp -- the Python binding of the calls whose host time matters: the
 // 8-bit cache's write and read, its decode, and the decodes with a window, a shared
-// prefix or a tree of drafts run in a few microseconds on small inputs, as long as ctypes and checks written in
+// prefix or a tree of drafts, and the prefill with a window, run in a few microseconds on small inputs, as long as ctypes and checks written in
 // Python take (of 10.2 us a call for the write of one token, 6.3 were checks and
 // argument conversion). Each function checks its tensors, as the other
 // entry points of the package do in Python, and calls the C entry point of the
@@ -25,6 +25,7 @@ struct Fns {
   decltype(&attn_decode_paged_window) window;
   decltype(&attn_decode_paged_window_e4m3) window8;
   decltype(&attn_decode_paged_tree) tree;
+  decltype(&attn_prefill_paged_window) prefill_window;
 };
 
 // Entry points of the library `handle` (guarded by the interpreter lock).
@@ -47,6 +48,7 @@ const Fns& entries(PyObject* handle) {
     n.window = reinterpret_cast<decltype(n.window)>(sym("attn_decode_paged_window"));
     n.window8 = reinterpret_cast<decltype(n.window8)>(sym("attn_decode_paged_window_e4m3"));
     n.tree = reinterpret_cast<decltype(n.tree)>(sym("attn_decode_paged_tree"));
+    n.prefill_window = reinterpret_cast<decltype(n.prefill_window)>(sym("attn_prefill_paged_window"));
     f = n;
     loaded = h;
   }
@@ -271,6 +273,21 @@ PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Rows of packed queries over bf16 caches.
+void check_packed(const at::Tensor& q, const at::Tensor& kc, const at::Tensor& vc,
+                  const at::Tensor& table, const at::Tensor& cu, const at::Tensor& lens) {
+  need(q.scalar_type() == at::kBFloat16 && kc.scalar_type() == at::kBFloat16 &&
+           vc.scalar_type() == at::kBFloat16,
+       "q and caches must be bf16");
+  need(q.dim() == 3 && kc.dim() == 4 && vc.sizes() == kc.sizes() && kc.size(3) == q.size(2),
+       "q [total_q,h,d] and caches [num_blocks,16,h_kv,d] expected");
+  int32({&table, &cu, &lens});
+  need(lens.dim() == 1 && cu.dim() == 1 && cu.size(0) == lens.size(0) + 1 && table.dim() == 2 &&
+           table.size(0) == lens.size(0),
+       "block_table [B,max_blocks], cu_seqlens_q [B+1] and seq_lens [B] expected");
+  contiguous({&q, &kc, &vc, &table, &cu, &lens});
+}
+
 // (handle, device, stream, q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens,
 //  tree_mask, max_q_len, scale, workspace, o, lse) -> status
 PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -282,16 +299,10 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &q = tensor(a[3]), &kc = tensor(a[4]), &vc = tensor(a[5]), &table = tensor(a[6]),
                      &cu = tensor(a[7]), &lens = tensor(a[8]), &mask = tensor(a[9]);
     on_device(dev, {&q, &kc, &vc, &table, &cu, &lens, &mask});
-    need(q.scalar_type() == at::kBFloat16 && kc.scalar_type() == at::kBFloat16 &&
-             vc.scalar_type() == at::kBFloat16,
-         "q and caches must be bf16");
-    need(q.dim() == 3 && kc.dim() == 4 && vc.sizes() == kc.sizes() && kc.size(3) == q.size(2),
-         "q [total_q,h,d] and caches [num_blocks,16,h_kv,d] expected");
-    int32({&table, &cu, &lens, &mask});
-    need(lens.dim() == 1 && cu.dim() == 1 && cu.size(0) == lens.size(0) + 1 && table.dim() == 2 &&
-             table.size(0) == lens.size(0) && mask.dim() == 2 && mask.size(0) == q.size(0),
-         "block_table [B,max_blocks], cu_seqlens_q [B+1], seq_lens [B] and tree_mask [total_q,words] expected");
-    contiguous({&q, &kc, &vc, &table, &cu, &lens, &mask});
+    check_packed(q, kc, vc, table, cu, lens);
+    int32({&mask});
+    need(mask.dim() == 2 && mask.size(0) == q.size(0), "tree_mask [total_q,words] expected");
+    contiguous({&mask});
     const at::Tensor &ws = tensor(a[12]), &o = tensor(a[13]);
     float* lse = check_outputs(dev, q, ws, o, a[14]);
     return f.tree(ptr(q), ptr(kc), ptr(vc), iptr(table), iptr(cu), iptr(lens), iptr(mask),
@@ -299,6 +310,28 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   small(q.size(2)), small(kc.size(1)), small(kc.size(0)), small(table.size(1)),
                   whole(a[10], "max_q_len"), small(mask.size(1)), scale_of(a[11], q.size(2)), ptr(ws),
                   ws.nbytes(), ptr(o), lse, stream);
+  });
+}
+
+// (handle, device, stream, q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens,
+//  window, sinks, max_q_len, scale, workspace, o, lse) -> status
+PyObject* prefill_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> long {
+    args(n, 16);
+    const Fns& f = entries(a[0]);
+    const long dev = PyLong_AsLong(a[1]);
+    void* stream = PyLong_AsVoidPtr(a[2]);
+    const at::Tensor &q = tensor(a[3]), &kc = tensor(a[4]), &vc = tensor(a[5]), &table = tensor(a[6]),
+                     &cu = tensor(a[7]), &lens = tensor(a[8]);
+    on_device(dev, {&q, &kc, &vc, &table, &cu, &lens});
+    check_packed(q, kc, vc, table, cu, lens);
+    const at::Tensor &ws = tensor(a[13]), &o = tensor(a[14]);
+    float* lse = check_outputs(dev, q, ws, o, a[15]);
+    return f.prefill_window(ptr(q), ptr(kc), ptr(vc), iptr(table), iptr(cu), iptr(lens),
+                            small(lens.size(0)), small(q.size(0)), small(q.size(1)), small(kc.size(2)),
+                            small(q.size(2)), small(kc.size(1)), small(kc.size(0)), small(table.size(1)),
+                            whole(a[11], "max_q_len"), whole(a[9], "window"), whole(a[10], "sinks"),
+                            scale_of(a[12], q.size(2)), ptr(ws), ws.nbytes(), ptr(o), lse, stream);
   });
 }
 
@@ -311,6 +344,8 @@ PyMethodDef methods[] = {
      METH_FASTCALL, "attn_decode_paged_shared"},
     {"decode_tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_tree)), METH_FASTCALL,
      "attn_decode_paged_tree"},
+    {"prefill_window", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prefill_window)),
+     METH_FASTCALL, "attn_prefill_paged_window"},
     {"decode_window", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_window)),
      METH_FASTCALL, "attn_decode_paged_window and attn_decode_paged_window_e4m3"},
     {nullptr, nullptr, 0, nullptr}};

@@ -40,6 +40,9 @@
 //   loads, loads the next Q once the current item's last S MMA is done, and
 //   runs the next item's first S MMAs while its softmax warps store O (staged
 //   in two V stages, not in Q), so set-up and drain overlap work.
+//   With a window (attn_prefill_paged_window) an item visits the key tiles that hold
+//   the first tokens (sinks), then those of its queries' windows; both parts' edges
+//   are masked per query.
 //   Every mbarrier wait is bounded; on a timeout the CTA raises the error
 //   word, drains its copies and MMAs (bounded), frees tensor memory and exits.
 #include <climits>
@@ -214,6 +217,8 @@ struct PagedArgs {
   const int32_t* tile_off;
   int B, max_blocks, num_blocks;
   int max_tiles;  // 128-key tiles per row in the fp16 V copy: ceil(max_blocks / 8)
+  const __nv_bfloat16* v_copy;  // WIN kernels: the V copy (flagged tiles: bf16)
+  int window, sinks;  // WIN kernels: the query at position p sees keys > p - window, and < sinks
 };
 
 // One work item: a 128-query block of NQ query heads that share a KV head.
@@ -224,7 +229,17 @@ struct Work {
   int nkv;       // key tiles the block visits
   int n_kv_all;  // key tiles of the KV head (contiguous) or row (paged)
   int pb, q_tok0, q_len, ctx, n_pages;  // paged rows only
+  int sink_tiles, skip, first;  // windows: tiles before the gap, tiles in it, first key behind it
 };
+
+// Windows: which of the keys kb .. kb + 31 a query sees that sees keys lo .. hi - 1 and
+// those below sinks, one bit each.
+__device__ __forceinline__ uint32_t window_bits(int kb, int lo, int hi, int sinks) {
+  auto below = [kb](int n) -> uint32_t {  // keys kb .. n - 1
+    return n >= kb + 32 ? 0xffffffffu : (1u << max(n - kb, 0)) - 1u;
+  };
+  return below(hi) & (~below(lo) | below(min(sinks, hi)));
+}
 
 // P of a key tile whose V stays bf16 (a value of magnitude 2^16 or more, an
 // inf or a NaN): P = P_hi + P_lo, both bf16, P_hi in columns 0-63 of the S
@@ -233,13 +248,22 @@ struct Work {
 // from tensor memory (the caller's registers hold it only up to the row max),
 // masks keys from lim on to -inf as the caller did, and returns the row sum of
 // the weights, added up in the same order as the fp16 path. Warp-collective.
+template <bool WIN>
 __device__ __noinline__ float softmax_p_two_term(uint32_t tS, int lim, float scale_log2,
-                                                 float bias) {
+                                                 float bias, int first, int sinks) {
   uint32_t sr[4][32];
 #pragma unroll
   for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
   tc::wait_ld();
-  if (lim < kBN) {
+  if constexpr (WIN) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t bits = window_bits(c * 32, first, lim, sinks);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(-INFINITY);
+    }
+  } else if (lim < kBN) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -296,10 +320,60 @@ __device__ __noinline__ float softmax_p_two_term(uint32_t tS, int lim, float sca
   return sa0 + sa1;
 }
 
+// Windows: a flagged V tile (bf16) at `base` that some query of the item sees only in
+// part, key `row` of it: non-finite numbers become zeros (0 * NaN is not 0), to come
+// back as NaN where they are seen. Returns whether there were any.
+template <int D>
+__device__ __noinline__ bool clean_wide_v(uint32_t base, int row) {
+  bool found = false;
+#pragma unroll 1
+  for (int i = 0; i < D / 8; ++i) {
+    const uint32_t at = base + (i >> 3) * (128 * 128) + row * 128 + (i & 7) * 16;
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at));
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, any = true;
+      if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu, any = true;
+    }
+    if (!any) continue;
+    found = true;
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3])
+                 : "memory");
+  }
+  return found;
+}
+// Dims that are non-finite in the values of a flagged tile (bf16 at v, `step` bf16
+// numbers from key to key) that a query sees: bits of window_bits. Rare.
+template <int D>
+__device__ __noinline__ void poisoned_dims(const __nv_bfloat16* v, size_t step, int lo, int hi, int sinks,
+                                           uint32_t (&out)[4]) {
+#pragma unroll 1
+  for (int j = 0; j < kBN; ++j) {
+    if (!(window_bits(j, lo, hi, sinks) & 1u)) continue;
+    const uint4* x = reinterpret_cast<const uint4*>(v + j * step);
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 y = __ldcg(x + c);
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((w[k] & 0x7f80u) == 0x7f80u) out[c >> 2] |= 1u << ((c & 3) * 8 + 2 * k);
+        if ((w[k] & 0x7f800000u) == 0x7f800000u) out[c >> 2] |= 2u << ((c & 3) * 8 + 2 * k);
+      }
+    }
+  }
+}
+
 // PAGED: variable-length rows over a paged cache. PCOPY (paged only): V is
 // read from the workspace copy that paged_v_to_f16_kernel made (fp16 bits
 // for normal tiles, bf16 bits for flagged ones), else from the cache itself.
-template <int D, int NQ, int NSK, int NSV, bool PAGED, bool PCOPY>
+// WIN (paged with the copy only): causal with a window and sinks.
+template <int D, int NQ, int NSK, int NSV, bool PAGED, bool PCOPY, bool WIN = false>
 __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     prefill_bf16_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const __grid_constant__ CUtensorMap tmap_k,
@@ -309,6 +383,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
                         int h_kv, int causal, float scale_log2, int n_qblk,
                         int* __restrict__ sched, const PagedArgs pa) {
   using C = PfCfg<D, NQ, NSK, NSV>;
+  static_assert(!WIN || (PAGED && PCOPY), "windows: paged rows with the V copy");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -368,7 +443,17 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     const int key_end = causal ? ctx - pw.q_len + q_hi : ctx;
     pw.nkv = (key_end + kBN - 1) / kBN;
     pw.n_kv_all = pw.nkv;
+    if constexpr (WIN) {
+      // First key of the first query's window; pages and tiles between the sinks
+      // and it are not looked at.
+      pw.first = max(ctx - pw.q_len + pw.qb * kBM + 1 - pa.window, 0);
+      pw.sink_tiles = (min(pa.sinks, key_end) + kBN - 1) / kBN;
+      pw.skip = max(pw.first / kBN - pw.sink_tiles, 0);
+      pw.nkv -= pw.skip;
+    }
   }
+  // The item's j-th key tile.
+  auto tile_at = [&](const Work& w, int j) { return WIN && j >= w.sink_tiles ? j + w.skip : j; };
   auto work_at = [&](int i) -> Work {
     if constexpr (PAGED) {
       return pw;
@@ -401,7 +486,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
   auto wide_bits = [&](const int* tile_wide, int j0, int n) -> uint32_t {
     if (!tile_wide) return 0xffffffffu;
     const int jj = j0 + (threadIdx.x & 31);
-    return __ballot_sync(0xffffffffu, jj < n && __ldg(tile_wide + jj) != 0);
+    return __ballot_sync(0xffffffffu, jj < n && __ldg(tile_wide + (WIN ? tile_at(pw, jj) : jj)) != 0);
   };
   // Whether any of key tiles 0 .. n-1 is wide. Warp-collective.
   auto item_has_wide = [&](const int* tile_wide, int n) -> bool {
@@ -434,6 +519,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         tail_info[0] = pw.ctx % 16 != 0 ? pw.ctx / kBN : -1;
         tail_info[1] = (pw.ctx % kBN) | ((16 - pw.ctx % 16) << 8);
       }
+      if constexpr (WIN) tail_info[0] = 0;  // non-finite values taken out of a V tile
     }
   }
   if (warp == C::MMA_WARP) tc::alloc(smem_u32(tmem_slot), C::TMEM_COLS);
@@ -512,7 +598,8 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
             for (int p = 0; p < 8; ++p) {
               const int page = j * 8 + p;
               int phys = -1;
-              if (page < w.n_pages) {
+              // (windows: pages that the item's queries do not see read as zeros too)
+              if (page < w.n_pages && (!WIN || page * 16 + 16 > w.first || page * 16 < pa.sinks)) {
                 phys = pa.block_table[size_t(w.pb) * pa.max_blocks + page];
                 if (phys < 0 || phys >= pa.num_blocks) {
                   atomicOr(&g_prefill_err, ATTN_DEVERR_BAD_PAGE);
@@ -541,14 +628,15 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         for (int j = 0; j < w.nkv; ++j) {
           const int g = g0 + j;
           const int sk = g % NSK, sv = g % NSV;
-          fetch_pages(j);
+          const int jt = tile_at(w, j);
+          fetch_pages(jt);
           if (g >= NSK && !wait_or_abort(bars.k_empty(sk), ((g / NSK) - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
           if (g != stall) {  // (the abort-path self-test requests nothing for one tile)
             mbar_arrive_expect_tx(bars.k_full(sk), C::KTILE);
-            load_tile(sbase + C::K_OFF + sk * C::KTILE, &tmap_k, bars.k_full(sk), j);
+            load_tile(sbase + C::K_OFF + sk * C::KTILE, &tmap_k, bars.k_full(sk), jt);
           }
           k_issued = g + 1;
           if (g >= NSV && !wait_or_abort(bars.v_empty(sv), ((g / NSV) - 1) & 1, abort_flag)) {
@@ -571,7 +659,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
             // 64-element column block instead of one box per page. It holds
             // fp16 bits, or bf16 bits for a flagged tile (a byte copy: the map's
             // fp16 type only sets the element size).
-            const int tok = w.pb * pa.max_tiles * kBN + j * kBN;
+            const int tok = w.pb * pa.max_tiles * kBN + jt * kBN;
             for (int s = 0; s < C::SUBS; ++s)
               tma_load_3d(sbase + C::V_OFF + sv * C::KTILE + s * C::SUB_BYTES, &tmap_v16,
                           bars.v_full(sv), s * 64, w.kvh, tok);
@@ -760,6 +848,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     const bool row_valid = PAGED ? row < w.q_len : row < T;
     const int key_end =
         !PAGED ? 0 : (!row_valid ? 0 : (causal ? w.ctx - w.q_len + row + 1 : w.ctx));
+    const int key_lo = WIN ? max(key_end - pa.window, 0) : 0;  // first key of its window
     // m_ref: exp2-domain reference that l, O~ and this tile's P are relative
     // to (the row max of some tile seen so far, within 2^15 of the running
     // max).
@@ -809,10 +898,27 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
           }
         }
       }
+      if constexpr (WIN && MAYBE_WIDE) {
+        if (wide && t == 0) {
+          // Keys that some query of the item does not see have weight 0 in its
+          // P V, but 0 * NaN is NaN. (Unflagged tiles hold finite values.)
+          const int k0 = tile_at(w, j) * kBN;
+          const int end = w.ctx - w.q_len + w.qb * kBM + 1;  // behind the first query's last key
+          const int lo = min(end + kBM - 1, w.ctx) - pa.window;  // the last query's first
+          if (k0 + kBN > end || (k0 < lo && k0 + kBN > pa.sinks)) {
+            const int sv = g % NSV;
+            if (wait_or_abort(bars.v_full(sv), (g / NSV) & 1, abort_flag) &&
+                clean_wide_v<D>(sbase + C::V_OFF + sv * C::KTILE, r))
+              *reinterpret_cast<volatile int*>(tail_info) = 1;
+            fence_proxy_async_smem();  // the MMA reads V through the async proxy
+          }
+        }
+      }
       tc::fence_after();
       int lim = kBN;
+      const int k0 = WIN ? tile_at(w, j) * kBN : 0;
       if constexpr (PAGED) {
-        lim = min(kBN, key_end - j * kBN);
+        lim = WIN ? key_end - k0 : min(kBN, key_end - j * kBN);
       } else {
         if (j * kBN + kBN > T) lim = T - j * kBN;
         if (causal && j == w.qb) lim = min(lim, r + 1);
@@ -822,7 +928,17 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
       tc::wait_ld();
-      if (lim < kBN) {
+      if constexpr (WIN) {
+        if (lim < kBN || (k0 < key_lo && k0 + kBN > pa.sinks)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = window_bits(c * 32, key_lo - k0, lim, pa.sinks - k0);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(-INFINITY);
+          }
+        }
+      } else if (lim < kBN) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -895,7 +1011,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         unf2(add2(sumA, sumB), sa0, sa1);
         psum = sa0 + sa1;
       } else {
-        psum = softmax_p_two_term(tS, lim, scale_log2, bias);
+        psum = softmax_p_two_term<WIN>(tS, lim, scale_log2, bias, key_lo - k0, pa.sinks - k0);
       }
       if (rescale) {
         // sr is free once P is stored (tcgen05.st reads its registers at
@@ -933,6 +1049,17 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       // and the LSE.
       const bool empty = l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
+      uint32_t bad[4] = {0u, 0u, 0u, 0u};  // windows: columns of non-finite values in sight
+      if constexpr (WIN) {
+        if (*reinterpret_cast<volatile int*>(tail_info) != 0)
+          for (int j = 0; j < w.nkv; ++j) {
+            const int jt = tile_at(w, j), k0 = jt * kBN;
+            if (!is_wide(tile_wide, jt)) continue;
+            const size_t tok = size_t(w.pb) * pa.max_tiles * kBN + k0;
+            poisoned_dims<D>(pa.v_copy + (tok * h_kv + w.kvh) * D, size_t(h_kv) * D, key_lo - k0,
+                             min(key_end - k0, kBN), pa.sinks - k0, bad);
+          }
+      }
       const size_t orow_idx = PAGED ? size_t(w.q_tok0 + row) * h + hq : size_t(hq) * T + row;
       // Output rows (debug checks): h * T, or h per packed query token.
       auto out_rows = [&]() -> size_t {
@@ -971,6 +1098,12 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         uint32_t ov[32];
         tc::ld32(tO + c * 32, ov);
         tc::wait_ld();
+        if constexpr (WIN) {
+          if (bad[c] != 0u)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((bad[c] >> i) & 1u) ov[i] = 0x7fc00000u;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint4 pk;
@@ -1084,12 +1217,16 @@ __global__ void __launch_bounds__(256)
 // is clamped as the attention kernel clamps it. One CTA per (tile, row, KV
 // head); each thread holds its CPR / 2 chunks of 16 bytes between the range
 // check and the store.
-template <int CPR>
+//
+// WIN: with a window, tiles that no query of the row sees are left alone, and keys
+// that none sees are zeros in the others; their pages are not looked up.
+template <int CPR, bool WIN>
 __global__ void __launch_bounds__(256)
     paged_v_to_f16_kernel(const uint4* __restrict__ vc, const int32_t* __restrict__ block_table,
                           const int32_t* __restrict__ cu_q, const int32_t* __restrict__ seq_lens,
                           int max_blocks, int num_blocks, int h_kv, int max_tiles,
-                          int skip_single, uint4* __restrict__ v16, int* __restrict__ vwide) {
+                          int skip_single, int window, int sinks, uint4* __restrict__ v16,
+                          int* __restrict__ vwide) {
   constexpr int PER = kBN * CPR / 256;  // chunks per thread
   const int jt = blockIdx.x, b = blockIdx.y, kvh = blockIdx.z;
   const int cap = max_blocks * 16;
@@ -1099,6 +1236,8 @@ __global__ void __launch_bounds__(256)
   if (ctx < q_len || ctx > cap) ctx = ctx < q_len ? q_len : cap;
   const int n_pages = (ctx + 15) / 16;
   if (jt * 8 >= n_pages) return;
+  const int first = WIN ? max(ctx - q_len + 1 - window, 0) : 0;  // the first query's first key
+  if (WIN && (q_len == 0 || (jt * kBN + kBN <= first && jt * kBN >= sinks))) return;
   uint4 x[PER];
   uint32_t mx = 0;
 #pragma unroll
@@ -1107,7 +1246,7 @@ __global__ void __launch_bounds__(256)
     const int tok = i / CPR, c = i % CPR;
     const int page = jt * 8 + (tok >> 4), slot = tok & 15;
     int phys = -1;
-    if (jt * kBN + tok < ctx) {
+    if (jt * kBN + tok < ctx && (!WIN || jt * kBN + tok >= first || jt * kBN + tok < sinks)) {
       phys = __ldg(block_table + size_t(b) * max_blocks + page);
       if (phys >= num_blocks) phys = -1;
     }
@@ -1221,6 +1360,35 @@ __global__ void paged_tiles_kernel(const int32_t* __restrict__ cu_q, int B, int 
   }
 }
 
+// The same for windows, by a warp, a row per lane. Rows whose tokens lie outside
+// [0, total_q) get no tiles either.
+__global__ void window_tiles_kernel(const int32_t* __restrict__ cu_q, int B, int total_q, int max_q_len,
+                                    int max_blocks, int32_t* __restrict__ tile_off) {
+  const int lane = threadIdx.x;
+  int acc = 0;
+  if (lane == 0) tile_off[0] = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane;
+    int n = 0;
+    if (b < B) {
+      const int begin = cu_q[b], end = cu_q[b + 1];
+      n = end - begin;
+      if (begin < 0 || end > total_q || end < begin || n > max_q_len || n > max_blocks * 16) {
+        atomicOr(&g_prefill_err, ATTN_DEVERR_BAD_SEQ_LEN);
+        n = 0;
+      }
+    }
+    int incl = (n + kBM - 1) / kBM;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (b < B) tile_off[b + 1] = acc + incl;
+    acc += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
 template <int D, int NQ, int NSK, int NSV>
 cudaError_t launch_paged(const PagedPrefill& a, cudaStream_t stream) {
   using C = PfCfg<D, NQ, NSK, NSV>;
@@ -1258,18 +1426,25 @@ cudaError_t launch_paged(const PagedPrefill& a, cudaStream_t stream) {
     if (encode_tensor_map(&tv16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, a.v16, dims, strides, box,
                           CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
-    paged_v_to_f16_kernel<D / 8><<<dim3(max_tiles, a.B, a.h_kv), 256, 0, stream>>>(
+    auto pass = a.window > 0 ? paged_v_to_f16_kernel<D / 8, true> : paged_v_to_f16_kernel<D / 8, false>;
+    pass<<<dim3(max_tiles, a.B, a.h_kv), 256, 0, stream>>>(
         static_cast<const uint4*>(a.v_cache), a.block_table, a.cu_q, a.seq_lens, a.max_blocks,
-        a.num_blocks, a.h_kv, max_tiles, a.decode_rows_apart, static_cast<uint4*>(a.v16), a.vwide);
+        a.num_blocks, a.h_kv, max_tiles, a.decode_rows_apart, a.window, a.sinks,
+        static_cast<uint4*>(a.v16), a.vwide);
     const cudaError_t e0 = cudaGetLastError();
     if (e0 != cudaSuccess) return e0;
   }
-  paged_tiles_kernel<<<1, 32, 0, stream>>>(a.cu_q, a.B, a.max_q_len, a.max_blocks,
-                                           a.decode_rows_apart, a.tile_off);
+  if (a.window > 0)
+    window_tiles_kernel<<<1, 32, 0, stream>>>(a.cu_q, a.B, a.total_q, a.max_q_len, a.max_blocks,
+                                              a.tile_off);
+  else
+    paged_tiles_kernel<<<1, 32, 0, stream>>>(a.cu_q, a.B, a.max_q_len, a.max_blocks,
+                                             a.decode_rows_apart, a.tile_off);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto kern = a.v16 ? prefill_bf16_kernel<D, NQ, NSK, NSV, true, true>
-                    : prefill_bf16_kernel<D, NQ, NSK, NSV, true, false>;
+  auto kern = a.window > 0 ? prefill_bf16_kernel<D, NQ, NSK, NSV, true, true, true>
+              : a.v16      ? prefill_bf16_kernel<D, NQ, NSK, NSV, true, true>
+                           : prefill_bf16_kernel<D, NQ, NSK, NSV, true, false>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   // At most one partial tile per row beyond ceil(total_q / 128), and no row
@@ -1280,8 +1455,9 @@ cudaError_t launch_paged(const PagedPrefill& a, cudaStream_t stream) {
   if (tiles <= 0) return cudaSuccess;
   if (tiles > 65535) return cudaErrorNotSupported;  // query tiles index grid y
   const dim3 grid(a.h / NQ, static_cast<unsigned>(tiles));
-  PagedArgs pa{a.block_table, a.cu_q,      a.seq_lens,   a.tile_off,
-               a.B,           a.max_blocks, a.num_blocks, max_tiles};
+  PagedArgs pa{a.block_table, a.cu_q,       a.seq_lens,   a.tile_off,
+               a.B,           a.max_blocks, a.num_blocks, max_tiles,
+               static_cast<const __nv_bfloat16*>(a.v16), a.window, a.sinks};
   kern<<<grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, tv16, a.v16 ? a.vwide : nullptr,
                                                static_cast<__nv_bfloat16*>(a.o), a.lse, 0, a.h,
                                                a.h_kv, a.causal, a.scale * kLog2e, 0, nullptr,
