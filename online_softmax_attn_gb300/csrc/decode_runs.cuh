@@ -653,6 +653,9 @@ __device__ __forceinline__ void runs_body(
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
+    int sink_pages = 0;
+    if constexpr (WIN) sink_pages = rw.sink_pages(cw.len);
+
     for (int i = cw.lo; i < cw.hi; ++i) {
       const int st = used % NST;
       copies_wait<NST - 1>();
@@ -661,7 +664,10 @@ __device__ __forceinline__ void runs_body(
       // Slots that the row sees: below `valid`, or (window) the bits of `vis`.
       const int valid = WIN ? kPage : min(kPage, cw.len - i * kPage);
       uint32_t vis = 0xffffu;
-      if constexpr (WIN) vis = rw.visible(cw.len, rw.page_at(cw.len, i));
+      if constexpr (WIN) {  // only a part's first and last page can be seen in part
+        if (i + 1 == sink_pages || i == sink_pages || i + 1 == cw.np)
+          vis = rw.visible(cw.len, rw.page_at(cw.len, i));
+      }
       const bool partial = WIN ? vis != 0xffffu : valid < kPage;
       auto live = [&](int slot) { return WIN ? ((vis >> slot) & 1u) != 0u : slot < valid; };
       if (partial) {
