@@ -14,13 +14,15 @@
 // tiles and the two-term P less), and a key is read once for all of them.
 //
 // A unit is (row, KV head, block of up to two 128-row tiles) and its key tiles. A
-// CTA has two softmax warpgroups ("streams"; thread = query row), a warp that loads
-// Q and K, one that loads V, and an MMA warp. Where the unit has two row tiles the
-// streams have one each and share every key tile; where it has one, the streams take
-// its key tiles in turn, each with an accumulator of its own, and stream 0 joins the
-// two at the end (it reads stream 1's accumulator from tensor memory: the same
-// lanes). Steps alternate between the streams; per step S = Q K^T (SS), weights over
-// S in tensor memory, O += P V (TS), with S of step e + 2 issued behind P V of step e.
+// CTA has two softmax warpgroups ("streams"; thread = query row), warps that load Q,
+// K and V, and an MMA warp. Where the unit has two row tiles the streams have one each
+// and share every key tile; where it has one, the streams take its key tiles in turn,
+// each with an accumulator of its own, and join the two at the end, half of the
+// dimensions each (either reads both accumulators from tensor memory: the same lanes).
+// Steps alternate between the streams; per step S = Q K^T (SS), weights over S in
+// tensor memory, O += P V (TS), with S of step e + 2 issued behind P V of step e. Q has
+// two slots, so that a unit's queries, like its first keys, land while the one in
+// front is still at work.
 //
 // V stays bf16 and P is the two-term bf16 split P_hi + P_lo, so q, K and V enter as
 // they are, whatever their magnitudes.
@@ -47,10 +49,31 @@ static __device__ unsigned int g_tree_err;
 namespace {
 
 constexpr int kBM = 128, kBN = 128;
-constexpr int kTreeUnit = 1;  // a unit's weight beside its key tiles: query, states, output
+constexpr int kTreeUnit = 3;  // a unit's weight beside its key tiles: query, states, output
 // A row's reference moves, to the largest score so far, when one passes it by more
 // than this (log2 units).
 constexpr float kRise = 8.0f;
+
+// A row: drafts, keys, first query token, key tiles, row blocks (0: no work).
+struct TreeRow {
+  int n, len, tok0, nt, n_rb;
+};
+// Where the CTA's run starts, and the warps' sums of the rows' weights.
+struct TreePlan {
+  long long sum[12];
+  long long off;
+  int b;
+  TreeRow row;
+};
+// A unit's key tiles [t0, t0 + nt) in a CTA's run.
+struct TreeSeg {
+  int b, kvh;         // row, KV head
+  int n, len, tok0;   // the row's drafts, keys and first query token
+  int first;          // first draft of the unit's query rows
+  int t0, nt, left;   // left: key tiles of the unit behind these; nt 0: the run has ended
+  int begins;         // the unit's first tile is among them
+  int two;            // more drafts than one 128-row tile holds
+};
 
 template <int D>
 struct TrCfg {
@@ -61,19 +84,22 @@ struct TrCfg {
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = Q_OFF + 2 * TILE;
   static constexpr int V_OFF = K_OFF + NSK * TILE;
-  static constexpr int ML_OFF = V_OFF + NSV * TILE;  // stream 1's (reference, sum) per row
-  // q_full, q_empty, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2],
-  // o_final[2], ml_full, ml_empty, mma_done
-  static constexpr int B_QF = 0, B_QE = 1, B_KF = 2, B_KE = B_KF + NSK, B_VF = B_KE + NSK,
-                       B_VE = B_VF + NSV, B_SF = B_VE + NSV, B_PF = B_SF + 2, B_OF = B_PF + 2,
-                       B_MF = B_OF + 2, B_ME = B_MF + 1, B_DONE = B_ME + 1, NBAR = B_DONE + 1;
-  static_assert(NBAR <= 32, "one warp initialises the barriers, one per lane");
-  static constexpr int BAR_OFF = ML_OFF + kBM * 8;
+  static constexpr int ML_OFF = V_OFF + NSV * TILE;  // (reference, sum) [stream][row]
+  // q_full[2], q_empty[2], seg_full[2], seg_empty[2], k_full[], k_empty[], v_full[],
+  // v_empty[], s_full[2], p_full[2], o_final[2], ml_full, ml_empty, mma_done
+  static constexpr int B_QF = 0, B_QE = 2, B_GF = 4, B_GE = 6, B_KF = 8, B_KE = B_KF + NSK,
+                       B_VF = B_KE + NSK, B_VE = B_VF + NSV, B_SF = B_VE + NSV, B_PF = B_SF + 2,
+                       B_OF = B_PF + 2, B_MF = B_OF + 2, B_ME = B_MF + 1, B_DONE = B_ME + 1,
+                       NBAR = B_DONE + 1;
+  static_assert(NBAR <= 384, "a thread initialises each barrier");
+  static constexpr int BAR_OFF = ML_OFF + 2 * kBM * 8;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;  // tensor-memory slot, abort flag, poison[2]
-  static constexpr int SMEM = MISC_OFF + 16 + 1024;
-  static_assert(SMEM + 256 <= 227 * 1024, "shared memory of an SM");
+  static constexpr int PLAN_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+  static constexpr int SEG_OFF = PLAN_OFF + (sizeof(TreePlan) + 15) / 16 * 16;  // two segments
+  static constexpr int SMEM = SEG_OFF + 2 * sizeof(TreeSeg);
+  static_assert(SMEM <= 227 * 1024, "shared memory of an SM");
   static constexpr int THREADS = 384;
-  static constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10;
+  static constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10, Q_WARP = 11;
   static constexpr int REG_LAUNCH = 168, REG_CONTROL = 120, REG_SOFTMAX = 192;
   static_assert(2 * 128 * REG_SOFTMAX + 128 * REG_CONTROL <= THREADS * REG_LAUNCH,
                 "register split exceeds the launch allocation");
@@ -131,15 +157,17 @@ struct TreeRows {
   int tpt;  // tokens per 128-row tile: 128 / g
 };
 
-// A row: drafts, keys, first query token, key tiles, row blocks (0: no work).
-struct TreeRow {
-  int n, len, tok0, nt, n_rb;
+struct TreeRaw {  // a row's offsets and length as they are
+  int begin, end, len;
 };
-__device__ __forceinline__ TreeRow tree_row(const TreeRows& a, int b, bool report) {
+__device__ __forceinline__ TreeRaw tree_raw(const TreeRows& a, int b) {
+  return TreeRaw{__ldcg(a.cu_q + b), __ldcg(a.cu_q + b + 1), __ldcg(a.seq_lens + b)};
+}
+__device__ __forceinline__ TreeRow tree_row(const TreeRows& a, const TreeRaw& raw, bool report) {
   TreeRow r;
-  r.tok0 = __ldcg(a.cu_q + b);
-  const int end = __ldcg(a.cu_q + b + 1);
-  r.len = __ldcg(a.seq_lens + b);
+  r.tok0 = raw.begin;
+  const int end = raw.end;
+  r.len = raw.len;
   const int cap = a.max_blocks * kPage;
   const long long n = static_cast<long long>(end) - r.tok0;
   if (r.tok0 < 0 || end > a.total_q || n < 0 || n > a.max_q_len || n > cap) {
@@ -160,34 +188,36 @@ __device__ __forceinline__ long long tree_weight(const TreeRows& a, const TreeRo
   return static_cast<long long>(r.n_rb) * a.h_kv * (r.nt + kTreeUnit);
 }
 
-// A unit's key tiles [t0, t0 + nt) in this CTA's run.
-struct TreeSeg {
-  TreeRow r;
-  int b, kvh, rb, t0, nt;
-  bool begins, ends;  // the unit's first, last tile is among them
-};
-// A CTA's run. Every role walks the same segments.
+// A CTA's run.
 struct TreeWalk {
   long long rem, off;  // weight of the run left; the run's start within the unit
   int b, u;            // row, unit within it
   TreeRow r;
+  TreeRaw ahead;       // row b + 1
+  __device__ __forceinline__ void look_ahead(const TreeRows& a) {
+    ahead = b + 1 < a.B ? tree_raw(a, b + 1) : TreeRaw{0, 0, 0};
+  }
   __device__ __forceinline__ bool next(const TreeRows& a, TreeSeg& s) {
     while (rem > 0) {
       while (u >= r.n_rb * a.h_kv) {
         if (++b >= a.B) return false;
-        r = tree_row(a, b, false);
+        r = tree_row(a, ahead, false);
         u = 0;
+        look_ahead(a);
       }
       const long long take = min(r.nt + kTreeUnit - off, rem);
       s.t0 = static_cast<int>(max(off - kTreeUnit, 0ll));
       const int hi = static_cast<int>(max(off + take - kTreeUnit, 0ll));
       s.nt = hi - s.t0;
-      s.r = r;
+      s.left = r.nt - hi;
       s.b = b;
       s.kvh = u / r.n_rb;
-      s.rb = u % r.n_rb;
+      s.n = r.n;
+      s.len = r.len;
+      s.tok0 = r.tok0;
+      s.first = (u % r.n_rb) * 2 * a.tpt;
       s.begins = s.t0 == 0;
-      s.ends = hi == r.nt;
+      s.two = r.n - s.first > a.tpt;
       rem -= take;
       off = 0;
       ++u;
@@ -211,68 +241,74 @@ struct TreeOut {
   float* lse;
 };
 
-// 32 bits of which of the keys kb .. kb + 31 the query row with mask words `mask`
-// sees: all of them below ctx, draft t where bit t is set (t < n).
-__device__ __forceinline__ uint32_t tree_bits(const int32_t* mask, int n, int ctx, int kb) {
-  const int rel = kb - ctx;
-  if (rel <= -32) return 0xffffffffu;
-  auto word = [&](int w) -> uint32_t {
-    if (w * 32 >= n) return 0u;
-    const uint32_t x = static_cast<uint32_t>(__ldcg(mask + w));
-    return n - w * 32 >= 32 ? x : x & ((1u << (n - w * 32)) - 1u);
-  };
-  if (rel < 0) return ((1u << -rel) - 1u) | (word(0) << -rel);
-  return __funnelshift_r(word(rel >> 5), word((rel >> 5) + 1), rel & 31);
+// Which keys the query row with mask words `mask` sees, 32 from key ctx + 32 w on, one
+// bit each: all of them in front of the drafts (w < 0), draft t where bit t is set
+// (t < n).
+__device__ __forceinline__ uint32_t tree_word(const int32_t* mask, int n, int w) {
+  if (w < 0) return 0xffffffffu;
+  if (w * 32 >= n) return 0u;
+  const uint32_t x = static_cast<uint32_t>(__ldcg(mask + w));
+  return n - w * 32 >= 32 ? x : x & ((1u << (n - w * 32)) - 1u);
 }
 
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {  // either of two bf16 numbers
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Chunk c of 16 bytes of key `row` of the V tile at `base`.
+__device__ __forceinline__ uint32_t v_chunk(uint32_t base, int row, int c) {
+  // (any order will do: eight neighbouring rows read distinct banks)
+  return base + (c >> 3) * (128 * 128) + row * 128 + (((c ^ row) & 7) << 4);
 }
-
+// Non-finite numbers of a V tile's key become zeros. Rare.
+template <int D>
+__device__ __noinline__ void drop_nonfinite(uint32_t base, int row) {
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    const uint32_t at = v_chunk(base, row, c);
+    const uint4 x = lds128(at);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
+      if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu;
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3])
+                 : "memory");
+  }
+}
 // The tile's V, in shared memory at `base`, before a P V that gives some of its keys
 // weight 0: key `row` of the tile. Keys from `lim` on become zeros. Non-finite numbers
-// of keys from `draft` on become zeros too; returns whether there were any.
+// of keys from `draft` on become zeros too; returns whether there were any. (Chunk by
+// chunk with a branch each this took 3 us, at every unit's end.)
 template <int D>
-__device__ __noinline__ bool clean_v(uint32_t base, int row, int draft, int lim) {
-  bool found = false;
-  if (row < draft) return false;
-#pragma unroll 1
-  for (int s = 0; s < D / 64; ++s) {
-    const uint32_t at = base + s * (128 * 128) + row * 128;
+__device__ __forceinline__ bool clean_v(uint32_t base, int row, int draft, int lim) {
+  if (row >= lim) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (row < lim) {
-        x = lds128(at + c * 16);
-        uint32_t* w = &x.x;
-        bool any = false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (!nonfinite2(w[k])) continue;
-          any = true;
-          if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
-          if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu;
-        }
-        if (!any) continue;
-        found = true;
-      }
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + c * 16), "r"(x.x), "r"(x.y),
-                   "r"(x.z), "r"(x.w)
-                   : "memory");
-    }
+    for (int c = 0; c < D / 8; ++c)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_chunk(base, row, c)), "r"(0u) : "memory");
+    return false;
   }
-  return found;
+  if (row < draft) return false;
+  uint32_t most = 0u;  // largest exponent fields, of either half
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = lds128(v_chunk(base, row, c));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(w[k] & 0x7f807f80u));
+  }
+  if ((most & 0xffffu) != 0x7f80u && (most >> 16) != 0x7f80u) return false;
+  drop_nonfinite<D>(base, row);
+  return true;
 }
 
 // Which dims are non-finite in the value of a draft that the row sees, among keys
 // k0 .. k1 - 1 (one bit each). Rare: the values are read again from the cache.
 template <int D>
-__device__ __noinline__ void poisoned_dims(const __nv_bfloat16* vc, const TreeRows& a, int b, int kvh,
-                                           const int32_t* mask, int n, int ctx, int k0, int k1,
-                                           uint32_t (&out)[4]) {
+__device__ __noinline__ uint4 poisoned_dims(const __nv_bfloat16* vc, const TreeRows& a, int b, int kvh,
+                                            const int32_t* mask, int n, int ctx, int k0, int k1) {
+  uint32_t out[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 1
   for (int j = max(k0, ctx); j < k1; ++j) {
-    if (!(tree_bits(mask, n, ctx, j) & 1u)) continue;
+    if (!((tree_word(mask, n, (j - ctx) >> 5) >> ((j - ctx) & 31)) & 1u)) continue;
     const int phys = __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + j / kPage);
     if (phys < 0 || phys >= a.num_blocks) continue;
     const uint4* v = reinterpret_cast<const uint4*>(
@@ -288,6 +324,7 @@ __device__ __noinline__ void poisoned_dims(const __nv_bfloat16* vc, const TreeRo
       }
     }
   }
+  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 template <int D>
@@ -296,12 +333,10 @@ __global__ void __launch_bounds__(384, 1)
                 const __grid_constant__ CUtensorMap tmap_v, const __nv_bfloat16* __restrict__ v_cache,
                 const TreeRows a, const TreeOut out, float scale_log2) {
   using C = TrCfg<D>;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  __shared__ long long s_sum[12];
-  __shared__ long long s_off;
-  __shared__ int s_b;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  // Aligned by its declaration (there is no room for slack, nor anything static in
+  // front of it).
+  extern __shared__ __align__(1024) uint8_t smem[];
+  TreePlan& plan = *reinterpret_cast<TreePlan*>(smem + C::PLAN_OFF);
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + C::BAR_OFF + 8 * i; };
   float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
@@ -309,9 +344,14 @@ __global__ void __launch_bounds__(384, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
   // Segment (counted from 1) whose V had non-finite drafts, by its count's parity.
   volatile int* poison = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);
+  // Segment i of the run lies in slot i & 1: the Q warp walks the run and leaves what
+  // the other warps need, which keeps the walk out of their registers (what they spill
+  // does not stay in the 28 KB of L1 that the tiles leave).
+  TreeSeg* segs = reinterpret_cast<TreeSeg*>(smem + C::SEG_OFF);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
 
+  ATTN_DCHECK((sbase & 1023u) == 0u, &g_tree_err);
   if (tid == 0) {
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
@@ -319,9 +359,10 @@ __global__ void __launch_bounds__(384, 1)
     *abort_flag = 0;
     poison[0] = poison[1] = 0;
   }
-  if (warp == 0 && lane < C::NBAR) {
-    const bool per_thread = (lane >= C::B_PF && lane < C::B_PF + 2) || lane == C::B_MF || lane == C::B_ME;
-    mbar_init(bar(lane), per_thread ? 128u : 1u);
+  if (tid < C::NBAR) {
+    const bool both = tid == C::B_MF || tid == C::B_ME, p = tid >= C::B_PF && tid < C::B_PF + 2;
+    const bool seg = tid >= C::B_GE && tid < C::B_GE + 2;  // eleven warps read a segment
+    mbar_init(bar(tid), both ? 256u : p ? 128u : seg ? 11u : 1u);
     fence_barrier_init();
   }
   if (warp == C::MMA_WARP) tc::alloc(smem_u32(tmem_slot), 512);
@@ -332,29 +373,35 @@ __global__ void __launch_bounds__(384, 1)
   const int per_t = (a.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(tid * per_t, a.B), b1 = min(b0 + per_t, a.B);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += tree_weight(a, tree_row(a, b, cta == 0));
+  TreeRow mine{0, 0, 0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    mine = tree_row(a, tree_raw(a, b), cta == 0);
+    sum += tree_weight(a, mine);
+  }
   long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) s_sum[warp] = incl;
+  if (lane == 31) plan.sum[warp] = incl;
   __syncthreads();
   long long at = incl - sum, all = 0;
 #pragma unroll
   for (int w = 0; w < 12; ++w) {
-    if (w < warp) at += s_sum[w];
-    all += s_sum[w];
+    if (w < warp) at += plan.sum[w];
+    all += plan.sum[w];
   }
   const long long per = max(1ll, div_ll(all + gridDim.x - 1, gridDim.x));
   const long long p0 = per * cta;
   if (p0 >= at && p0 < at + sum) {
     for (int b = b0; b < b1; ++b) {
-      const long long w = tree_weight(a, tree_row(a, b, false));
+      if (per_t > 1) mine = tree_row(a, tree_raw(a, b), false);
+      const long long w = tree_weight(a, mine);
       if (p0 >= at && p0 < at + w) {
-        s_b = b;
-        s_off = p0 - at;
+        plan.b = b;
+        plan.off = p0 - at;
+        plan.row = mine;
       }
       at += w;
     }
@@ -363,26 +410,12 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
-  TreeWalk walk;
-  walk.rem = p0 < all ? min(per, all - p0) : 0;
-  walk.off = 0;
-  walk.b = walk.u = 0;
-  walk.r = TreeRow{0, 0, 0, 0, 0};
-  if (walk.rem > 0) {
-    walk.b = s_b;
-    walk.r = tree_row(a, walk.b, false);
-    const long long wu = walk.r.nt + kTreeUnit;
-    walk.u = static_cast<int>(div_ll(s_off, wu));
-    walk.off = s_off - walk.u * wu;
-  }
-
-  // Two row tiles share the unit's key tiles, or its only one has them in turn.
-  auto shared = [&](const TreeSeg& s) { return s.r.n - s.rb * 2 * a.tpt > a.tpt; };
-  // Steps e = 0, 1, ... of a segment alternate between the streams: stream e & 1.
-  auto n_of = [&](const TreeSeg& s, int t) { return shared(s) ? s.nt : (s.nt + 1 - t) >> 1; };
+  // Steps e = 0, 1, ... of a segment alternate between the streams (stream e & 1), which
+  // share its key tiles, or have them in turn.
+  auto n_of = [](int nt, bool two, int t) { return two ? nt : (nt + 1 - t) >> 1; };
   // Key tile of 8 pages into dst: lane i < 8 * SUBS issues the box of page i % 8,
   // half i / 8. Whole warp.
-  auto load_tile = [&](uint32_t dst, const CUtensorMap* map, uint32_t b, const TreeSeg& s, int ent, int sel,
+  auto load_tile = [&](uint32_t dst, const CUtensorMap* map, uint32_t b, int kvh, int ent, int sel,
                        int page0, int n_pages) {
     int phys = __shfl_sync(0xffffffffu, ent, sel + (lane & 7));
     if (phys < 0 || phys >= a.num_blocks) {
@@ -393,11 +426,20 @@ __global__ void __launch_bounds__(384, 1)
     __syncwarp();
     if (lane < 8 * C::SUBS)
       tma_load_4d(dst + (lane >> 3) * C::SUB_BYTES + (lane & 7) * kPage * 128, map, b, (lane >> 3) * 64,
-                  s.kvh, 0, phys);
+                  kvh, 0, phys);
     __syncwarp();
   };
   auto warp_wait = [&](uint32_t b, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_or_abort(b, parity, abort_flag));
+  };
+  // Segment i, or false: none is left, or an abort. Once a warp has read what it needs
+  // it lets go of it. Whole warp.
+  auto open = [&](int i) {
+    return warp_wait(bar(C::B_GF + (i & 1)), (i >> 1) & 1) && segs[i & 1].nt > 0;
+  };
+  auto close = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::B_GE + (i & 1)));
   };
 
   if (warp >= C::K_WARP) {
@@ -409,26 +451,16 @@ __global__ void __launch_bounds__(384, 1)
                 empty = is_k ? C::B_KE : C::B_VE;
       const uint32_t ring = sbase + (is_k ? C::K_OFF : C::V_OFF);
       const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
-      int it = 0, g = 0, q_issued = 0;
+      int g = 0;
       bool ok = true;
-      TreeSeg s;
-      for (; ok && walk.next(a, s); ++it) {
-        const int n_pages = (s.r.len + kPage - 1) / kPage;
+      for (int it = 0; ok && open(it); ++it) {
+        const TreeSeg s = segs[it & 1];
+        close(it);
+        const int n_pages = (s.len + kPage - 1) / kPage;
         const int32_t* table = a.block_table + static_cast<size_t>(s.b) * a.max_blocks;
         // Table entries of the 32 pages from `page` on, one per lane.
         auto entries = [&](int page) { return page + lane < n_pages ? __ldcg(table + page + lane) : -1; };
         int ent = entries(s.t0 * 8), next = -1;
-        if (is_k) {
-          if (it > 0 && !warp_wait(bar(C::B_QE), (it - 1) & 1)) break;
-          const int tiles = shared(s) ? 2 : 1;
-          if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QF), tiles * C::SUBS * 128 * a.g * a.tpt);
-          __syncwarp();
-          if (lane < tiles * C::SUBS)
-            tma_load_4d(sbase + C::Q_OFF + lane * C::SUB_BYTES, &tmap_q, bar(C::B_QF), (lane % C::SUBS) * 64,
-                        0, s.kvh, s.r.tok0 + (s.rb * 2 + lane / C::SUBS) * a.tpt);
-          __syncwarp();
-          q_issued = it + 1;
-        }
         for (int j = 0; j < s.nt; ++j, ++g) {
           const int st = g % ns, page0 = (s.t0 + j) * 8;
           if ((j & 3) == 0) {  // entries four tiles at a time, fetched four tiles ahead
@@ -439,16 +471,61 @@ __global__ void __launch_bounds__(384, 1)
             ok = false;
             break;
           }
-          load_tile(ring + st * C::TILE, map, bar(full + st), s, ent, (j & 3) * 8, page0, n_pages);
+          load_tile(ring + st * C::TILE, map, bar(full + st), s.kvh, ent, (j & 3) * 8, page0, n_pages);
         }
       }
       if (*abort_flag) {
         // Drain: the newest load of each stage is the only one that can still be in
         // flight. Bounded waits, error already recorded.
-        if (q_issued > 0) (void)mbar_wait(bar(C::B_QF), (q_issued - 1) & 1, &g_tree_err);
         for (int i = max(0, g - ns); i < g; ++i)
           (void)mbar_wait(bar(full + i % ns), (i / ns) & 1, &g_tree_err);
       }
+    } else if (warp == C::Q_WARP) {
+      // The run's segments, and query tile q (counted over them) in slot q & 1.
+      TreeWalk walk;
+      walk.rem = p0 < all ? min(per, all - p0) : 0;
+      walk.off = 0;
+      walk.b = walk.u = 0;
+      walk.r = TreeRow{0, 0, 0, 0, 0};
+      walk.ahead = TreeRaw{0, 0, 0};
+      if (walk.rem > 0) {
+        walk.b = plan.b;
+        walk.r = plan.row;
+        walk.look_ahead(a);
+        const long long wu = walk.r.nt + kTreeUnit;
+        walk.u = static_cast<int>(div_ll(plan.off, wu));
+        walk.off = plan.off - walk.u * wu;
+      }
+      int q = 0;
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        TreeSeg s;
+        if (!walk.next(a, s)) s.nt = 0;
+        if (it >= 2 && !warp_wait(bar(C::B_GE + (it & 1)), ((it >> 1) - 1) & 1)) break;
+        if (lane == 0) {
+          segs[it & 1] = s;
+          mbar_arrive(bar(C::B_GF + (it & 1)));
+        }
+        __syncwarp();
+        if (s.nt == 0) break;
+        const int tiles = s.two ? 2 : 1;
+        for (int i = 0; i < tiles; ++i, ++q) {
+          const int slot = q & 1;
+          if (q >= 2 && !warp_wait(bar(C::B_QE + slot), ((q >> 1) - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QF + slot), C::SUBS * 128 * a.g * a.tpt);
+          __syncwarp();
+          if (lane < C::SUBS)
+            tma_load_4d(sbase + C::Q_OFF + slot * C::TILE + lane * C::SUB_BYTES, &tmap_q, bar(C::B_QF + slot),
+                        lane * 64, 0, s.kvh, s.tok0 + s.first + i * a.tpt);
+          __syncwarp();
+        }
+      }
+      if (*abort_flag)
+        for (int i = max(0, q - 2); i < q; ++i)
+          (void)mbar_wait(bar(C::B_QF + (i & 1)), (i >> 1) & 1, &g_tree_err);
     } else if (warp == C::MMA_WARP) {
       // -------------------------------------------------------- MMA issuer
       constexpr uint32_t idS = tc::idesc_bf16_f32(kBM, kBN, false, false);
@@ -457,18 +534,20 @@ __global__ void __launch_bounds__(384, 1)
       const uint64_t dk0 = tc::sw128_desc(sbase + C::K_OFF, 16, 1024);
       const uint64_t dv0 = tc::sw128_desc(sbase + C::V_OFF, C::SUB_BYTES, 1024);
       bool ok = true;
-      int g0 = 0, base[2] = {0, 0};
-      TreeSeg s;
-      for (int it = 0; ok && walk.next(a, s); ++it) {
-        const bool two = shared(s);
-        const int n = two ? 2 * s.nt : s.nt;
-        ok = warp_wait(bar(C::B_QF), it & 1);
+      int g0 = 0, q = 0, base[2] = {0, 0};
+      for (int it = 0; ok && open(it); ++it) {
+        const bool two = segs[it & 1].two;
+        const int nt = segs[it & 1].nt, n = two ? 2 * nt : nt;
+        close(it);
+        ok = warp_wait(bar(C::B_QF + (q & 1)), (q >> 1) & 1) &&
+             (!two || warp_wait(bar(C::B_QF + ((q + 1) & 1)), ((q + 1) >> 1) & 1));
         // S of step e once its K tile is there, then what it frees.
         auto s_step = [&](int e) {
           const int t = e & 1, g = g0 + (two ? e >> 1 : e), st = g % C::NSK;
           if (!warp_wait(bar(C::B_KF + st), (g / C::NSK) & 1)) return false;
           tc::fence_after();
-          const uint64_t da = dq0 + uint64_t(((two ? t : 0) * C::TILE) >> 4);
+          const int slot = (q + (two ? t : 0)) & 1;
+          const uint64_t da = dq0 + uint64_t((slot * C::TILE) >> 4);
           const uint64_t db = dk0 + uint64_t((st * C::TILE) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -477,7 +556,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           tc::commit_elect(bar(C::B_SF + t));
           if (!two || t == 1) tc::commit_elect(bar(C::B_KE + st));
-          if (e == n - 1) tc::commit_elect(bar(C::B_QE));  // Q's last reader
+          if (e == n - 1 || (two && e == n - 2)) tc::commit_elect(bar(C::B_QE + slot));  // its last reader
           return true;
         };
         for (int e = -2; ok && e < n; ++e) {
@@ -500,9 +579,10 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (e + 2 < n) ok = s_step(e + 2);
         }
-        g0 += s.nt;
-        base[0] += n_of(s, 0);
-        base[1] += n_of(s, 1);
+        g0 += nt;
+        q += two ? 2 : 1;
+        base[0] += n_of(nt, two, 0);
+        base[1] += n_of(nt, two, 1);
       }
       tc::commit_elect(bar(C::B_DONE));
       (void)__all_sync(0xffffffffu, mbar_wait(bar(C::B_DONE), 0, &g_tree_err));
@@ -512,40 +592,42 @@ __global__ void __launch_bounds__(384, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_SOFTMAX));
     const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t tS = tmem + (uint32_t(wq * 32) << 16) + t * 256, tO = tS + 128;
+    const int row_tok = r / a.g, hh = r % a.g;  // token of the tile, head of the group
     int g0 = 0, cnt = 0, fin[2] = {0, 0}, handed = 0;
     bool ok = true;
-    TreeSeg s;
-    for (int it = 1; ok && walk.next(a, s); ++it) {
-      const bool two = shared(s);
-      const int n = n_of(s, t), n1 = n_of(s, 1);
-      const int ctx = s.r.len - s.r.n;
-      // This thread's query row: token `tok` of the row, head hh of the group.
-      const int blk = s.rb * 2 + (two ? t : 0);
-      const int tok = blk * a.tpt + r / a.g, hh = r % a.g;
-      const bool valid = r < a.tpt * a.g && tok < s.r.n;
+    for (int it = 0; ok && open(it); ++it) {
+      const TreeSeg& s = segs[it & 1];
+      const bool two = s.two;
+      const int n = n_of(s.nt, two, t), n1 = n_of(s.nt, two, 1);
+      const int ctx = s.len - s.n;
+      // This thread's query row: draft `tok` of the row.
+      const int tok = s.first + (two ? t * a.tpt : 0) + row_tok;
+      const bool valid = row_tok < a.tpt && tok < s.n;
       const bool busy = __any_sync(0xffffffffu, valid);
-      const int32_t* mask = a.mask + static_cast<size_t>(s.r.tok0 + (valid ? tok : 0)) * a.words;
+      const int32_t* mask = a.mask + static_cast<size_t>(s.tok0 + (valid ? tok : 0)) * a.words;
       float ref = kNone, l = 0.f;
-      // Stream 1's accumulator and ml are stream 0's to read until it says so.
-      if (t == 1 && handed > 0 &&
+      // The accumulators and ml are the other stream's to read until it says so.
+      if (handed > 0 &&
           !__all_sync(0xffffffffu, wait_or_abort(bar(C::B_ME), (handed - 1) & 1, abort_flag)))
         break;
+      // The words that hold an edge tile's bits are asked for a step ahead: a load takes
+      // 2 us beside the pages' traffic.
+      uint32_t words[5];
+      auto fetch_words = [&](int i) {
+        const int key = (s.t0 + (two ? i : 2 * i + t)) * kBN;
+        if (i < n && key + kBN > ctx) {
+#pragma unroll
+          for (int k = 0; k < 5; ++k) words[k] = tree_word(mask, s.n, ((key - ctx) >> 5) + k);
+        }
+      };
+      fetch_words(0);
       for (int i = 0; i < n; ++i, ++cnt) {
         const int j = two ? i : 2 * i + t;  // key tile within the segment
         const int k0 = (s.t0 + j) * kBN;
+        const bool edge = k0 + kBN > ctx;  // drafts, and perhaps slots past the row's end
         if (!warp_wait(bar(C::B_SF + t), cnt & 1)) {
           ok = false;
           break;
-        }
-        const bool edge = k0 + kBN > ctx;  // drafts, and perhaps slots past the row's end
-        if (edge && (t == 0 || !two)) {
-          const int g = g0 + j, sv = g % C::NSV;
-          if (!warp_wait(bar(C::B_VF + sv), (g / C::NSV) & 1)) {
-            ok = false;
-            break;
-          }
-          if (clean_v<D>(sbase + C::V_OFF + sv * C::TILE, r, max(ctx - k0, 0), s.r.len - k0)) poison[it & 1] = it;
-          fence_proxy_async_smem();  // the MMA reads V through the async proxy
         }
         if (busy) {
           tc::fence_after();
@@ -556,7 +638,7 @@ __global__ void __launch_bounds__(384, 1)
           if (edge) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint32_t bits = tree_bits(mask, s.r.n, ctx, k0 + 32 * c);
+              const uint32_t bits = __funnelshift_r(words[c], words[c + 1], (k0 - ctx) & 31);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (!((bits >> k) & 1u)) sr[c][k] = __float_as_uint(-INFINITY);
@@ -627,88 +709,119 @@ __global__ void __launch_bounds__(384, 1)
           tc::wait_st();
           tc::fence_before();
         }
+        if (edge && (t == 0 || !two)) {
+          const int g = g0 + j, sv = g % C::NSV;
+          if (!warp_wait(bar(C::B_VF + sv), (g / C::NSV) & 1)) {
+            ok = false;
+            break;
+          }
+          if (clean_v<D>(sbase + C::V_OFF + sv * C::TILE, r, max(ctx - k0, 0), s.len - k0))
+            poison[it & 1] = it + 1;
+          fence_proxy_async_smem();  // the MMA reads V through the async proxy
+        }
         mbar_arrive(bar(C::B_PF + t));
+        fetch_words(i + 1);
       }
       g0 += s.nt;
       if (!ok) break;
-      if (!two && t == 1) {  // hand the state to stream 0
-        ml[r] = make_float2(ref, l);
-        mbar_arrive(bar(C::B_MF));
-        ++handed;
-        if (n1 > 0) ++fin[1];
-        continue;
-      }
-      // This stream's P V are done (n > 0: a stream-0 segment has a tile at least).
-      if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_OF + t), fin[t] & 1, abort_flag))) break;
+      // The P V that this thread reads are done. (n > 0 but for stream 1 of a single
+      // tile; stream 0 has one at least.)
       float w0 = 1.f, w1 = 0.f;
-      bool join = false;
+      uint32_t acc = tO;             // what w0 weighs
+      int c0 = 0, c1 = D / 32;       // 32-column blocks of the output that this thread has
+      const bool join = !two && n1 > 0;
       if (!two) {
+        ml[t * kBM + r] = make_float2(ref, l);
+        mbar_arrive(bar(C::B_MF));
         if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_MF), handed & 1, abort_flag))) break;
         ++handed;
-        join = n1 > 0;
-        if (join && !__all_sync(0xffffffffu, wait_or_abort(bar(C::B_OF + 1), fin[1] & 1, abort_flag))) break;
-        const float2 o = ml[r];
-        const float m = fmaxf(ref, o.x);
-        w0 = ex2_approx(ref - m);
-        w1 = ex2_approx(o.x - m);
-        l = l * w0 + o.y * w1;
+        const float2 x = ml[r], y = ml[kBM + r];
+        const float m = fmaxf(x.x, y.x);
+        w0 = ex2_approx(x.x - m);
+        w1 = ex2_approx(y.x - m);
+        l = x.y * w0 + y.y * w1;
         ref = m;
+        acc = tmem + (uint32_t(wq * 32) << 16) + 128;
+        c0 = t * (D / 64);
+        c1 = c0 + D / 64;
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_OF), fin[0] & 1, abort_flag))) break;
+        if (join && !__all_sync(0xffffffffu, wait_or_abort(bar(C::B_OF + 1), fin[1] & 1, abort_flag))) break;
+      } else if (!__all_sync(0xffffffffu, wait_or_abort(bar(C::B_OF + t), fin[t] & 1, abort_flag))) {
+        break;
       }
       ++fin[0];
       if (n1 > 0) ++fin[1];
       tc::fence_after();
-      const bool whole = s.begins && s.ends;
-      uint32_t bad[4] = {0u, 0u, 0u, 0u};
-      if (busy && poison[it & 1] == it && valid)
-        poisoned_dims<D>(v_cache, a, s.b, s.kvh, mask, s.r.n, ctx, s.t0 * kBN,
-                         min((s.t0 + s.nt) * kBN, s.r.len), bad);
+      const bool whole = s.begins && s.left == 0;
+      uint4 bad = make_uint4(0u, 0u, 0u, 0u);
+      if (busy && poison[it & 1] == it + 1 && valid)
+        bad = poisoned_dims<D>(v_cache, a, s.b, s.kvh, mask, s.n, ctx, s.t0 * kBN,
+                               min((s.t0 + s.nt) * kBN, s.len));
       const int slot = 2 * cta + (s.begins ? 1 : 0);
       const size_t pt = static_cast<size_t>(slot) * 2 + (two ? t : 0);
       const bool empty = l == 0.f;
       const float inv = whole ? (empty ? 0.f : 1.f / l) : 1.f;
-      const size_t row = static_cast<size_t>(s.r.tok0 + tok) * a.h + s.kvh * a.g + hh;
+      const size_t row = static_cast<size_t>(s.tok0 + tok) * a.h + s.kvh * a.g + hh;
       const bool store = valid && ATTN_GUARD(row < static_cast<size_t>(a.total_q) * a.h, &g_tree_err) &&
                          ATTN_GUARD(slot < 2 * kRunsMaxCtas, &g_tree_err);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      const int out_row = store ? static_cast<int>(row) : -1;
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) {
         if (!busy) break;
         uint32_t ov[32];
         float x[32];
-        tc::ld32(tO + c * 32, ov);
+        tc::ld32(acc + c * 32, ov);
         tc::wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(ov[k]) * w0;
         if (join) {
-          tc::ld32(tO + 256 + c * 32, ov);
+          tc::ld32(acc + 256 + c * 32, ov);
           tc::wait_ld();
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = fmaf(__uint_as_float(ov[k]), w1, x[k]);
         }
+        const uint32_t nan = c < 2 ? (c == 0 ? bad.x : bad.y) : (c == 2 ? bad.z : bad.w);
+        if (nan != 0u)
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if ((bad[c] >> k) & 1u) x[k] = __uint_as_float(0x7fc00000u);
-        if (!store) continue;
+          for (int k = 0; k < 32; ++k)
+            if ((nan >> k) & 1u) x[k] = __uint_as_float(0x7fc00000u);
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(out.o + row * D + c * 32);
+          // 64 bytes of a row per thread; turned among four lanes so that they store
+          // 64 contiguous bytes, of the four lanes' rows in turn.
+          uint32_t y[4][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              y[k][w] = empty ? 0u : pack_bf16x2(x[8 * k + 2 * w] * inv, x[8 * k + 2 * w + 1] * inv);
+#pragma unroll
+          for (int bit = 1; bit < 4; bit <<= 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k & bit) continue;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const bool up = lane & bit;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? y[k][w] : y[k | bit][w], bit);
+                y[k][w] = up ? got : y[k][w];
+                y[k | bit][w] = up ? y[k | bit][w] : got;
+              }
+            }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint4 y = make_uint4(0u, 0u, 0u, 0u);
-            if (!empty) {
-              y.x = pack_bf16x2(x[8 * k] * inv, x[8 * k + 1] * inv);
-              y.y = pack_bf16x2(x[8 * k + 2] * inv, x[8 * k + 3] * inv);
-              y.z = pack_bf16x2(x[8 * k + 4] * inv, x[8 * k + 5] * inv);
-              y.w = pack_bf16x2(x[8 * k + 6] * inv, x[8 * k + 7] * inv);
-            }
-            dst[k] = y;
+            const int to = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + k);
+            if (to >= 0)
+              *reinterpret_cast<uint4*>(out.o + static_cast<size_t>(to) * D + c * 32 + (lane & 3) * 8) =
+                  make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
           }
-        } else {
+        } else if (store) {
           float4* dst = reinterpret_cast<float4*>(out.o_part + pt * (kBM * D)) + r;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             dst[(c * 8 + k) * kBM] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
       }
-      if (store) {
+      if (store && (two || t == 0)) {
         if (whole) {
           if (out.lse != nullptr) out.lse[row] = empty ? -INFINITY : ref * kLn2 + logf(l);
         } else {
@@ -716,13 +829,12 @@ __global__ void __launch_bounds__(384, 1)
           out.l_part[pt * kBM + r] = l;
         }
       }
-      if (tid == 0 && s.begins && !s.ends) {
-        const long long left = s.r.nt - s.nt;  // key tiles in the CTAs behind
-        out.cut[cta] = TreeCut{static_cast<int>(1 + (left + per - 1) / per),
-                               s.r.tok0 + s.rb * 2 * a.tpt, min(2 * a.tpt, s.r.n - s.rb * 2 * a.tpt), s.kvh};
-      }
+      if (tid == 0 && s.begins && s.left > 0)
+        out.cut[cta] = TreeCut{static_cast<int>(1 + div_ll(s.left + per - 1, per)), s.tok0 + s.first,
+                               min(2 * a.tpt, s.n - s.first), s.kvh};
+      close(it);
       // O is read out before the next segment's first P V, which waits for this
-      // thread's next P (stream 1's, behind ml_empty, where stream 0 read it).
+      // thread's next P (behind ml_empty, where the other stream read it too).
       tc::fence_before();
       if (!two) mbar_arrive(bar(C::B_ME));
     }

@@ -328,7 +328,7 @@ __device__ __noinline__ bool clean_wide_v(uint32_t base, int row) {
   bool found = false;
 #pragma unroll 1
   for (int i = 0; i < D / 8; ++i) {
-    const uint32_t at = base + (i >> 3) * (128 * 128) + row * 128 + (i & 7) * 16;
+    const uint32_t at = base + (i >> 3) * (128 * 128) + row * 128 + ((i ^ row) & 7) * 16;
     uint32_t w[4];
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
