@@ -741,15 +741,17 @@ attn_status_t attn_decode_paged_window_e4m3(const void* q, const void* k_cache, 
  *   window       >= 1, sinks >= 0: the same for every row
  *   workspace    256-byte aligned, attn_prefill_window_workspace_bytes(B,
  *                max_blocks_per_seq, h_kv, d_h) bytes (those of
- *                attn_prefill_paged_v16_workspace_bytes; 0 where the fp16 copy of V
- *                cannot be used), overwritten; calls that share one must not overlap
+ *                attn_prefill_paged_v16_workspace_bytes and a counter; 0 where the
+ *                fp16 copy of V cannot be used), overwritten; calls that share one
+ *                must not overlap
  * Rows of one query run as 1-row query tiles; attn_decode_paged_window is made for
  * them. Keys that a query does not see never reach it, whatever they and their values
  * hold; a non-finite value that it does see makes its column NaN or that infinity.
  * Errors, device errors and limits: as attn_prefill_paged, where offsets outside
  * [0, total_q] also set ATTN_DEVERR_BAD_SEQ_LEN (the row is skipped); plus INVALID_ARG
  * for B > 65535, window < 1, sinks < 0 and a workspace below its size, UNSUPPORTED
- * where that size is 0.
+ * where that size is 0 or (total_q / 128 + B + 1) * h is 2^30 or more (there is no
+ * limit of 65535 query tiles).
  */
 size_t attn_prefill_window_workspace_bytes(int B, int max_blocks_per_seq, int h_kv, int d_h);
 attn_status_t attn_prefill_paged_window(const void* q, const void* k_cache, const void* v_cache,

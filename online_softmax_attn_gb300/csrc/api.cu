@@ -691,7 +691,8 @@ attn_status_t attn_decode_paged_shared(const void* q, const void* k_cache, const
 }
 
 size_t attn_prefill_window_workspace_bytes(int B, int max_blocks_per_seq, int h_kv, int d_h) {
-  return attn_prefill_paged_v16_workspace_bytes(B, max_blocks_per_seq, h_kv, d_h);
+  const size_t n = attn_prefill_paged_v16_workspace_bytes(B, max_blocks_per_seq, h_kv, d_h);
+  return n == 0 ? 0 : align256(n) + 256;  // the counter of the attention kernel's items
 }
 
 attn_status_t attn_prefill_paged_window(const void* q, const void* k_cache, const void* v_cache,
@@ -717,7 +718,9 @@ attn_status_t attn_prefill_paged_window(const void* q, const void* k_cache, cons
     return ATTN_ERR_INVALID_ARG;
   const PagedV16Layout L = paged_v16_layout(B, max_blocks_per_seq, h_kv, d_h);
   if (L.total == 0) return ATTN_ERR_UNSUPPORTED;
-  if (workspace_bytes < L.total) return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < align256(L.total) + 256) return ATTN_ERR_INVALID_ARG;
+  // Query tiles times heads are counted in 32 bits.
+  if ((static_cast<long long>(total_q) / 128 + B + 1) * h > 0x3fffffffll) return ATTN_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PagedPrefill a;
   a.q = q;
@@ -743,8 +746,8 @@ attn_status_t attn_prefill_paged_window(const void* q, const void* k_cache, cons
   a.lse = lse;
   a.window = window;
   a.sinks = sinks;
-  const cudaError_t e = launch_prefill_paged(a, static_cast<cudaStream_t>(stream));
-  return e == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : from_cuda(e);
+  a.sched = reinterpret_cast<int*>(ws + align256(L.total));
+  return from_cuda(launch_prefill_paged(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int d_h) {

@@ -263,6 +263,7 @@ struct PagedPrefill {
   float* lse;                  // [total_q, h] or nullptr
   int decode_rows_apart = 0;   // nonzero: rows of one query get no query tiles
   int window = 0, sinks = 0;   // window > 0: causal with a window and sinks (v16 given)
+  int* sched = nullptr;        // windows: workspace of the item counter
 };
 cudaError_t launch_prefill_paged(const PagedPrefill& a, cudaStream_t stream);
 unsigned int prefill_read_and_clear_error(cudaStream_t stream, cudaError_t* st);

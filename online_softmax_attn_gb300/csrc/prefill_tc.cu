@@ -42,7 +42,8 @@
 //   in two V stages, not in Q), so set-up and drain overlap work.
 //   With a window (attn_prefill_paged_window) an item visits the key tiles that hold
 //   the first tokens (sinks), then those of its queries' windows; both parts' edges
-//   are masked per query.
+//   are masked per query. Its items are short, so these paged rows run a persistent
+//   grid too: warp 10 claims the items, finds their rows and publishes them.
 //   Every mbarrier wait is bounded; on a timeout the CTA raises the error
 //   word, drains its copies and MMAs (bounded), frees tensor memory and exits.
 #include <climits>
@@ -229,7 +230,9 @@ struct Work {
   int nkv;       // key tiles the block visits
   int n_kv_all;  // key tiles of the KV head (contiguous) or row (paged)
   int pb, q_tok0, q_len, ctx, n_pages;  // paged rows only
-  int sink_tiles, skip, first;  // windows: tiles before the gap, tiles in it, first key behind it
+  // Windows: tiles before the gap, tiles in it, first key behind it; keys that all of
+  // the item's queries see: from all_lo (and below sinks) to all_hi - 1.
+  int sink_tiles, skip, first, all_lo, all_hi;
 };
 
 // Windows: which of the keys kb .. kb + 31 a query sees that sees keys lo .. hi - 1 and
@@ -248,22 +251,13 @@ __device__ __forceinline__ uint32_t window_bits(int kb, int lo, int hi, int sink
 // from tensor memory (the caller's registers hold it only up to the row max),
 // masks keys from lim on to -inf as the caller did, and returns the row sum of
 // the weights, added up in the same order as the fp16 path. Warp-collective.
-template <bool WIN>
 __device__ __noinline__ float softmax_p_two_term(uint32_t tS, int lim, float scale_log2,
-                                                 float bias, int first, int sinks) {
+                                                 float bias) {
   uint32_t sr[4][32];
 #pragma unroll
   for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
   tc::wait_ld();
-  if constexpr (WIN) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t bits = window_bits(c * 32, first, lim, sinks);
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(-INFINITY);
-    }
-  } else if (lim < kBN) {
+  if (lim < kBN) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -320,6 +314,25 @@ __device__ __noinline__ float softmax_p_two_term(uint32_t tS, int lim, float sca
   return sa0 + sa1;
 }
 
+// Windows: masks an S tile in tensor memory: -inf for the keys that the row does not
+// see (as window_bits, from the tile's first key on). Out of line, so that the softmax
+// loop holds neither its code nor its registers (with the bits tested in the loop it
+// spilled, which cost every tile: 8 x 1024 queries, window 4096, 457 us). Warp-collective.
+__device__ __noinline__ void mask_window(uint32_t tS, int lo, int hi, int sinks) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t s[32];
+    tc::ld32(tS + c * 32, s);
+    tc::wait_ld();
+    const uint32_t bits = window_bits(c * 32, lo, hi, sinks);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!((bits >> i) & 1u)) s[i] = __float_as_uint(-INFINITY);
+    tc::st32(tS + c * 32, s);
+  }
+  tc::wait_st();
+}
+
 // Windows: a flagged V tile (bf16) at `base` that some query of the item sees only in
 // part, key `row` of it: non-finite numbers become zeros (0 * NaN is not 0), to come
 // back as NaN where they are seen. Returns whether there were any.
@@ -350,8 +363,8 @@ __device__ __noinline__ bool clean_wide_v(uint32_t base, int row) {
 // Dims that are non-finite in the values of a flagged tile (bf16 at v, `step` bf16
 // numbers from key to key) that a query sees: bits of window_bits. Rare.
 template <int D>
-__device__ __noinline__ void poisoned_dims(const __nv_bfloat16* v, size_t step, int lo, int hi, int sinks,
-                                           uint32_t (&out)[4]) {
+__device__ __noinline__ uint4 poisoned_dims(const __nv_bfloat16* v, size_t step, int lo, int hi, int sinks) {
+  uint32_t out[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 1
   for (int j = 0; j < kBN; ++j) {
     if (!(window_bits(j, lo, hi, sinks) & 1u)) continue;
@@ -367,6 +380,7 @@ __device__ __noinline__ void poisoned_dims(const __nv_bfloat16* v, size_t step, 
       }
     }
   }
+  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // PAGED: variable-length rows over a paged cache. PCOPY (paged only): V is
@@ -384,6 +398,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
                         int* __restrict__ sched, const PagedArgs pa) {
   using C = PfCfg<D, NQ, NSK, NSV>;
   static_assert(!WIN || (PAGED && PCOPY), "windows: paged rows with the V copy");
+  constexpr bool PERSIST = !PAGED || WIN;  // a grid of one CTA per SM that walks the items
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -397,6 +412,11 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
   // in shared memory so that no warp holds registers for it.
   int* tail_info = reinterpret_cast<int*>(smem + C::MISC_OFF + 8);
   volatile int* item_slot = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 16);
+  // Windows: item it lies in slot it & 3 once its barrier's phase is over; the producer
+  // lets the claim of the next one go.
+  Work* const win_slot = reinterpret_cast<Work*>(smem + C::MISC_OFF + 32 + 40);
+  auto win_full = [&](int i) { return sbase + C::MISC_OFF + 32 + 8 * (i & 3); };
+  const uint32_t win_claim = sbase + C::MISC_OFF + 32 + 32;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -412,21 +432,15 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
   // each item in an item slot; the other roles read it there. Paged rows:
   // one item, the CTA's own (grid: head groups x the rows' query tiles, each
   // row's longest tile first).
-  const int G = PAGED ? 1 : int(gridDim.x);
+  const int G = PERSIST ? int(gridDim.x) : 1;
   const int n_items = PAGED ? 1 : n_hp * n_qblk;
   auto item_of_round = [&](int rr) {
     return rr * G + ((rr & 1) ? G - 1 - int(blockIdx.x) : int(blockIdx.x));
   };
   Work pw{};
-  if constexpr (PAGED) {
-    const int tile = int(blockIdx.y);
-    if (tile >= pa.tile_off[pa.B]) return;  // surplus CTA of the fixed grid
-    int lo = 0, hi = pa.B - 1;              // last row whose first tile <= tile
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pa.tile_off[mid] <= tile) lo = mid; else hi = mid - 1;
-    }
-    pw.hq0 = int(blockIdx.x) * NQ;
+  // The work of head group hp over query tile `tile`, which is row lo's.
+  auto paged_work = [&](int hp, int lo, int tile) {
+    pw.hq0 = hp * NQ;
     pw.kvh = pw.hq0 / (h / h_kv);
     pw.pb = lo;
     pw.qb = pa.tile_off[lo + 1] - 1 - tile;  // longest tile of the row first
@@ -434,7 +448,8 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     pw.q_len = pa.cu_q[lo + 1] - pw.q_tok0;
     int ctx = pa.seq_lens[lo];
     if (ctx < pw.q_len || ctx > pa.max_blocks * 16) {
-      if (threadIdx.x == 0) atomicOr(&g_prefill_err, ATTN_DEVERR_BAD_SEQ_LEN);
+      if (WIN ? (threadIdx.x & 31) == 0 : threadIdx.x == 0)
+        atomicOr(&g_prefill_err, ATTN_DEVERR_BAD_SEQ_LEN);
       ctx = ctx < pw.q_len ? pw.q_len : pa.max_blocks * 16;
     }
     pw.ctx = ctx;
@@ -450,7 +465,19 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       pw.sink_tiles = (min(pa.sinks, key_end) + kBN - 1) / kBN;
       pw.skip = max(pw.first / kBN - pw.sink_tiles, 0);
       pw.nkv -= pw.skip;
+      pw.all_hi = ctx - pw.q_len + pw.qb * kBM + 1;
+      pw.all_lo = key_end - pa.window;
     }
+  };
+  if constexpr (PAGED && !WIN) {
+    const int tile = int(blockIdx.y);
+    if (tile >= pa.tile_off[pa.B]) return;  // surplus CTA of the fixed grid
+    int lo = 0, hi = pa.B - 1;              // last row whose first tile <= tile
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pa.tile_off[mid] <= tile) lo = mid; else hi = mid - 1;
+    }
+    paged_work(int(blockIdx.x), lo, tile);
   }
   // The item's j-th key tile.
   auto tile_at = [&](const Work& w, int j) { return WIN && j >= w.sink_tiles ? j + w.skip : j; };
@@ -483,15 +510,15 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
   // The flags of key tiles j0 .. j0 + 31 (below n) as one bit each, for a
   // whole warp: one load per lane every 32 tiles instead of a load on every
   // tile's path to its MMAs and exponentials. Warp-collective.
-  auto wide_bits = [&](const int* tile_wide, int j0, int n) -> uint32_t {
+  auto wide_bits = [&](const int* tile_wide, int j0, int n, const Work& w) -> uint32_t {
     if (!tile_wide) return 0xffffffffu;
     const int jj = j0 + (threadIdx.x & 31);
-    return __ballot_sync(0xffffffffu, jj < n && __ldg(tile_wide + (WIN ? tile_at(pw, jj) : jj)) != 0);
+    return __ballot_sync(0xffffffffu, jj < n && __ldg(tile_wide + (WIN ? tile_at(w, jj) : jj)) != 0);
   };
   // Whether any of key tiles 0 .. n-1 is wide. Warp-collective.
-  auto item_has_wide = [&](const int* tile_wide, int n) -> bool {
+  auto item_has_wide = [&](const int* tile_wide, int n, const Work& w) -> bool {
     uint32_t any = 0;
-    for (int j0 = 0; j0 < n; j0 += 32) any |= wide_bits(tile_wide, j0, n);
+    for (int j0 = 0; j0 < n; j0 += 32) any |= wide_bits(tile_wide, j0, n, w);
     return any != 0;
   };
 
@@ -519,7 +546,14 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         tail_info[0] = pw.ctx % 16 != 0 ? pw.ctx / kBN : -1;
         tail_info[1] = (pw.ctx % kBN) | ((16 - pw.ctx % 16) << 8);
       }
-      if constexpr (WIN) tail_info[0] = 0;  // non-finite values taken out of a V tile
+      // Items (counted from 1, by parity) with non-finite values taken out of a V tile.
+      if constexpr (WIN) tail_info[0] = tail_info[1] = 0;
+    }
+  }
+  if constexpr (WIN) {
+    if (threadIdx.x >= 32 && threadIdx.x < 37) {
+      mbar_init(win_full(0) + 8 * (threadIdx.x - 32), 1u);  // the slots' four, then win_claim
+      fence_barrier_init();
     }
   }
   if (warp == C::MMA_WARP) tc::alloc(smem_u32(tmem_slot), C::TMEM_COLS);
@@ -539,6 +573,27 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       return __shfl_sync(0xffffffffu, item_slot[it & 1], 0);
     }
   };
+  // Whether there is an item it (item: as next_item's; false on an abort too), and its
+  // work: of windows by reference, in its slot (in registers it spilled 150 bytes), which
+  // is not written again before the roles are done with the item. Warp-uniform.
+  using WorkOf = typename std::conditional<WIN, const Work&, const Work>::type;
+  auto next_work = [&](int it, int& item) -> bool {
+    if constexpr (WIN) {
+      item = 0;
+      return __all_sync(0xffffffffu, wait_or_abort(win_full(it), (it >> 2) & 1, abort_flag)) &&
+             win_slot[it & 3].nkv > 0;
+    } else {
+      item = next_item(it);
+      return item >= 0;
+    }
+  };
+  auto work_of = [&](int it, int item) -> WorkOf {
+    if constexpr (WIN)
+      return win_slot[it & 3];
+    else
+      return work_at(item);
+  };
+  if constexpr (WIN) pdl_wait();  // the items are the V pass's output
 
   // Register shares move per warpgroup: every warp of a warpgroup executes
   // the same setmaxnreg, at the top of its role's code.
@@ -546,7 +601,98 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
   if constexpr (NQ == 2) regs_dec<C::REG_CONTROL>();
   if (warp == C::PRODUCER_WARP) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if constexpr (WIN) {
+      // The whole warp: table entries of four tiles at a time, one per lane, fetched four
+      // tiles ahead, and a lane per page box (one lane with 16 boxes and 8 entries a
+      // tile took longer than the tile's products).
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+      };
+      int k_issued = 0, v_issued = 0, q_issued = 0, g0 = 0, it = 0;
+      int stage_waited = 0, gl_even = 0, gl_odd = 0;  // as below
+      bool ok = true;
+      for (; ok; ++it) {
+        if (!wait(win_full(it), (it >> 2) & 1)) break;
+        const Work w = win_slot[it & 3];
+        if (w.nkv == 0) break;
+        const int32_t* table = pa.block_table + size_t(w.pb) * pa.max_blocks;
+        // Page `lane & 7` of tile j0 + lane / 8: -1 (reads as zeros) where the item's
+        // queries see none of it.
+        auto entries = [&](int j0) {
+          const int j = j0 + (lane >> 3), page = tile_at(w, j) * 8 + (lane & 7);
+          int phys = -1;
+          if (j < w.nkv && page < w.n_pages && (page * 16 + 16 > w.first || page * 16 < pa.sinks)) {
+            phys = table[page];
+            if (phys < 0 || phys >= pa.num_blocks) {
+              atomicOr(&g_prefill_err, ATTN_DEVERR_BAD_PAGE);
+              phys = -1;
+            }
+          }
+          return phys;
+        };
+        int ent = entries(0), next = -1;
+        for (int j = 0; ok && j < w.nkv; ++j) {
+          const int g = g0 + j, sk = g % NSK, sv = g % NSV;
+          if ((j & 3) == 0) {
+            if (j > 0) ent = next;
+            next = entries(j + 4);
+          }
+          if (g >= NSK && !wait(bars.k_empty(sk), ((g / NSK) - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          const int phys = __shfl_sync(0xffffffffu, ent, (j & 3) * 8 + (lane & 7));
+          if (lane == 0) mbar_arrive_expect_tx(bars.k_full(sk), C::KTILE);
+          __syncwarp();
+          if (lane < 8 * C::SUBS)
+            tma_load_4d(sbase + C::K_OFF + sk * C::KTILE + (lane >> 3) * C::SUB_BYTES + (lane & 7) * 16 * 128,
+                        &tmap_k, bars.k_full(sk), (lane >> 3) * 64, w.kvh, 0, phys);
+          __syncwarp();
+          k_issued = g + 1;
+          if (j == 0) {
+            // Q once the last S MMA of the item in front is done.
+            if (it > 0 && !wait(bars.q_empty(), (it - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bars.q_full(), NQ * C::QTILE);
+            __syncwarp();
+            if (lane < NQ * C::SUBS)
+              tma_load_3d(sbase + C::Q_OFF + lane * C::SUB_BYTES, &tmap_q, bars.q_full(),
+                          (lane % C::SUBS) * 64, w.hq0 + lane / C::SUBS, w.q_tok0 + w.qb * kBM);
+            __syncwarp();
+            q_issued = it + 1;
+          }
+          if (g >= NSV && !wait(bars.v_empty(sv), ((g / NSV) - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          while (ok && stage_waited < it && ((stage_waited & 1) ? gl_odd : gl_even) + 2 <= g) {
+            ok = wait(bars.stage_free(stage_waited & 1), (stage_waited >> 1) & 1);
+            ++stage_waited;
+          }
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bars.v_full(sv), C::KTILE);
+          __syncwarp();
+          if (lane < C::SUBS)  // (fp16, or the bf16 bits of a flagged tile)
+            tma_load_3d(sbase + C::V_OFF + sv * C::KTILE + lane * C::SUB_BYTES, &tmap_v16,
+                        bars.v_full(sv), lane * 64, w.kvh, (w.pb * pa.max_tiles + tile_at(w, j)) * kBN);
+          __syncwarp();
+          v_issued = g + 1;
+        }
+        if (!ok) break;
+        if (it & 1) gl_odd = g0 + w.nkv - 1; else gl_even = g0 + w.nkv - 1;
+        g0 += w.nkv;
+        if (lane == 0) mbar_arrive(win_claim);
+      }
+      if (*abort_flag) {  // drain, as below
+        if (q_issued > 0) (void)mbar_wait(bars.q_full(), (q_issued - 1) & 1, &g_prefill_err);
+        for (int g = max(0, k_issued - NSK); g < k_issued; ++g)
+          (void)mbar_wait(bars.k_full(g % NSK), (g / NSK) & 1, &g_prefill_err);
+        for (int g = max(0, v_issued - NSV); g < v_issued; ++g)
+          (void)mbar_wait(bars.v_full(g % NSV), (g / NSV) & 1, &g_prefill_err);
+      }
+    } else if (lane == 0) {
       // Loads issued so far (K and V tiles counted over all of this CTA's
       // items: tile g uses stage g % NS, phase (g / NS) & 1).
       int k_issued = 0, v_issued = 0, q_issued = 0;
@@ -598,8 +744,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
             for (int p = 0; p < 8; ++p) {
               const int page = j * 8 + p;
               int phys = -1;
-              // (windows: pages that the item's queries do not see read as zeros too)
-              if (page < w.n_pages && (!WIN || page * 16 + 16 > w.first || page * 16 < pa.sinks)) {
+              if (page < w.n_pages) {
                 phys = pa.block_table[size_t(w.pb) * pa.max_blocks + page];
                 if (phys < 0 || phys >= pa.num_blocks) {
                   atomicOr(&g_prefill_err, ATTN_DEVERR_BAD_PAGE);
@@ -628,15 +773,14 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         for (int j = 0; j < w.nkv; ++j) {
           const int g = g0 + j;
           const int sk = g % NSK, sv = g % NSV;
-          const int jt = tile_at(w, j);
-          fetch_pages(jt);
+          fetch_pages(j);
           if (g >= NSK && !wait_or_abort(bars.k_empty(sk), ((g / NSK) - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
           if (g != stall) {  // (the abort-path self-test requests nothing for one tile)
             mbar_arrive_expect_tx(bars.k_full(sk), C::KTILE);
-            load_tile(sbase + C::K_OFF + sk * C::KTILE, &tmap_k, bars.k_full(sk), jt);
+            load_tile(sbase + C::K_OFF + sk * C::KTILE, &tmap_k, bars.k_full(sk), j);
           }
           k_issued = g + 1;
           if (g >= NSV && !wait_or_abort(bars.v_empty(sv), ((g / NSV) - 1) & 1, abort_flag)) {
@@ -659,7 +803,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
             // 64-element column block instead of one box per page. It holds
             // fp16 bits, or bf16 bits for a flagged tile (a byte copy: the map's
             // fp16 type only sets the element size).
-            const int tok = w.pb * pa.max_tiles * kBN + jt * kBN;
+            const int tok = w.pb * pa.max_tiles * kBN + j * kBN;
             for (int s = 0; s < C::SUBS; ++s)
               tma_load_3d(sbase + C::V_OFF + sv * C::KTILE + s * C::SUB_BYTES, &tmap_v16,
                           bars.v_full(sv), s * 64, w.kvh, tok);
@@ -765,9 +909,10 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       bool ok = true;
       int g0 = 0;
       for (int it = 0; ok; ++it) {
-        const int item = next_item(it);
-        if (item < 0) break;
-        const Work w = work_at(item);
+        int item;
+        if (!next_work(it, item)) break;
+        WorkOf w = work_of(it, item);
+        const int nkv = w.nkv;
         const int* tile_wide = wide_flags(w);
         ok = wait(bars.q_full(), it & 1) && wait(bars.k_full(g0 % NSK), (g0 / NSK) & 1);
         if (!ok) break;
@@ -777,20 +922,20 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
           tc::commit_elect(bars.s_full(t));
         }
         tc::commit_elect(bars.k_empty(g0 % NSK));
-        if (w.nkv == 1) tc::commit_elect(bars.q_empty());
-        if (it == 0) pdl_wait();  // the tile flags below are the V pass's output
+        if (nkv == 1) tc::commit_elect(bars.q_empty());
+        if (!WIN && it == 0) pdl_wait();  // the tile flags below are the V pass's output
         // The loop is instantiated twice: for items without a wide tile (the
         // common case) it has no per-tile format branch at all.
         auto tiles = [&](auto any_wide) {
         constexpr bool MAYBE_WIDE = decltype(any_wide)::value;
         uint32_t wbits = 0;
-        for (int j = 0; ok && j < w.nkv; ++j) {
+        for (int j = 0; ok && j < nkv; ++j) {
           const int g = g0 + j;
           const int sv = g % NSV;
           const int sk1 = (g + 1) % NSK;
           bool wide = false;
           if constexpr (MAYBE_WIDE) {
-            if ((j & 31) == 0) wbits = wide_bits(tile_wide, j, w.nkv);
+            if ((j & 31) == 0) wbits = wide_bits(tile_wide, j, nkv, w);
             wide = (wbits >> (j & 31)) & 1u;
           }
           for (int t = 0; t < NQ && ok; ++t) {
@@ -798,27 +943,66 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
             if (t == 0 && !wait(bars.v_full(sv), (g / NSV) & 1)) { ok = false; break; }
             tc::fence_after();
             issue_pv(t, sv, j > 0, wide);
-            if (j == w.nkv - 1) tc::commit_elect(bars.o_final(t));
+            if (j == nkv - 1) tc::commit_elect(bars.o_final(t));
             if (t == NQ - 1) tc::commit_elect(bars.v_empty(sv));
-            if (j + 1 < w.nkv) {
+            if (j + 1 < nkv) {
               if (t == 0 && !wait(bars.k_full(sk1), ((g + 1) / NSK) & 1)) { ok = false; break; }
               tc::fence_after();
               issue_s(t, sk1);
               tc::commit_elect(bars.s_full(t));
               if (t == NQ - 1) {
                 tc::commit_elect(bars.k_empty(sk1));
-                if (j + 2 == w.nkv) tc::commit_elect(bars.q_empty());  // Q's last reader
+                if (j + 2 == nkv) tc::commit_elect(bars.q_empty());  // Q's last reader
               }
             }
           }
         }
         };
-        if (item_has_wide(tile_wide, w.nkv)) tiles(std::true_type{}); else tiles(std::false_type{});
-        g0 += w.nkv;
+        if (item_has_wide(tile_wide, nkv, w)) tiles(std::true_type{}); else tiles(std::false_type{});
+        g0 += nkv;
       }
       // Everything issued has completed once mma_done flips.
       tc::commit_elect(bars.mma_done());
       (void)__all_sync(0xffffffffu, mbar_wait(bars.mma_done(), 0, &g_prefill_err));
+    }
+  } else if (WIN && warp == C::MMA_WARP + 1) {
+    // ------------------------------------------------------------ items of windows
+    // Item i is head group i % n_hp of query tile i / n_hp. The CTA starts with item
+    // blockIdx.x and claims the others in order from *sched, each once the producer
+    // has issued the loads of the one in front. Slot it & 3 is free by then: the
+    // producer waited for the last S of item it - 2, which follows the softmax warps'
+    // weights of item it - 3.
+    const int n_all = n_hp * __ldcg(pa.tile_off + pa.B);
+    int cur = int(blockIdx.x);
+    for (int it = 0;; ++it) {
+      if (it > 0) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(win_claim, (it - 1) & 1, abort_flag))) break;
+        if (lane == 0) cur = G + atomicAdd(sched, 1);
+        cur = __shfl_sync(0xffffffffu, cur, 0);
+      }
+      pw.nkv = 0;
+      if (cur < n_all) {
+        // The last row whose first tile <= tile, 32 rows a step.
+        const int tile = cur / n_hp;
+        int lo = 0, n = pa.B;
+        while (n > 1) {
+          const int step = (n + 31) / 32, at = lane * step;
+          const int k = __popc(__ballot_sync(0xffffffffu, at < n && __ldcg(pa.tile_off + lo + at) <= tile)) - 1;
+          lo += k * step;
+          n = min(step, n - k * step);
+        }
+        paged_work(cur % n_hp, lo, tile);
+      }
+      if (lane == 0) {
+        win_slot[it & 3] = pw;
+        mbar_arrive(win_full(it));
+        if (pw.nkv > 0)  // its Q is loaded once the item in front's last S is done: from L2
+          for (int t = 0; t < NQ; ++t)
+            for (int s = 0; s < C::SUBS; ++s)
+              tma_prefetch_l2_3d(&tmap_q, s * 64, pw.hq0 + t, pw.q_tok0 + pw.qb * kBM);
+      }
+      __syncwarp();
+      if (pw.nkv == 0) break;
     }
   }
   } else {
@@ -831,11 +1015,15 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     const uint32_t tO = tS + 128;
     bool ok = true;
     int g0 = 0;
-    pdl_wait();  // the tile flags are the V pass's output
+    if constexpr (!WIN) pdl_wait();  // the tile flags are the V pass's output
     for (int it = 0; ok; ++it) {
-    const int item = next_item(it);
-    if (item < 0) break;
-    const Work w = work_at(item);
+    int item;
+    if (!next_work(it, item)) break;
+    WorkOf w = work_of(it, item);
+    const int nkv = w.nkv;
+    auto tile_of = [sink_tiles = WIN ? w.sink_tiles : 0, skip = WIN ? w.skip : 0](int j) {
+      return WIN && j >= sink_tiles ? j + skip : j;
+    };
     ATTN_DCHECK(w.hq0 + NQ <= h && w.kvh < h_kv && w.nkv >= 1 &&
                     w.nkv <= (PAGED ? pa.max_tiles : w.n_kv_all) &&
                     (PAGED || w.qb < n_qblk),
@@ -848,7 +1036,6 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     const bool row_valid = PAGED ? row < w.q_len : row < T;
     const int key_end =
         !PAGED ? 0 : (!row_valid ? 0 : (causal ? w.ctx - w.q_len + row + 1 : w.ctx));
-    const int key_lo = WIN ? max(key_end - pa.window, 0) : 0;  // first key of its window
     // m_ref: exp2-domain reference that l, O~ and this tile's P are relative
     // to (the row max of some tile seen so far, within 2^15 of the running
     // max).
@@ -859,12 +1046,12 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     auto tiles = [&](auto any_wide) {
     constexpr bool MAYBE_WIDE = decltype(any_wide)::value;
     uint32_t wbits = 0;
-    for (int j = 0; j < w.nkv; ++j) {
+    for (int j = 0; j < nkv; ++j) {
       const int g = g0 + j;
       // The format of P follows the format of this key tile's V.
       bool wide = false;
       if constexpr (MAYBE_WIDE) {
-        if ((j & 31) == 0) wbits = wide_bits(tile_wide, j, w.nkv);
+        if ((j & 31) == 0) wbits = wide_bits(tile_wide, j, nkv, w);
         wide = (wbits >> (j & 31)) & 1u;
       }
       // Warp-uniform outcome: the tensor-memory loads below are warp-collective.
@@ -902,23 +1089,27 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         if (wide && t == 0) {
           // Keys that some query of the item does not see have weight 0 in its
           // P V, but 0 * NaN is NaN. (Unflagged tiles hold finite values.)
-          const int k0 = tile_at(w, j) * kBN;
-          const int end = w.ctx - w.q_len + w.qb * kBM + 1;  // behind the first query's last key
-          const int lo = min(end + kBM - 1, w.ctx) - pa.window;  // the last query's first
-          if (k0 + kBN > end || (k0 < lo && k0 + kBN > pa.sinks)) {
+          const int k0 = tile_of(j) * kBN;
+          if (k0 + kBN > w.all_hi || (k0 < w.all_lo && k0 + kBN > pa.sinks)) {
             const int sv = g % NSV;
             if (wait_or_abort(bars.v_full(sv), (g / NSV) & 1, abort_flag) &&
                 clean_wide_v<D>(sbase + C::V_OFF + sv * C::KTILE, r))
-              *reinterpret_cast<volatile int*>(tail_info) = 1;
+              *reinterpret_cast<volatile int*>(tail_info + (it & 1)) = it + 1;
             fence_proxy_async_smem();  // the MMA reads V through the async proxy
           }
         }
       }
       tc::fence_after();
+      if constexpr (WIN) {
+        const int k0 = tile_of(j) * kBN;
+        if (k0 + kBN > w.all_hi || (k0 < w.all_lo && k0 + kBN > pa.sinks)) {
+          const int q = w.qb * kBM + r, end = q < w.q_len ? w.ctx - w.q_len + q + 1 : 0;
+          mask_window(tS, max(end - pa.window, 0) - k0, end - k0, pa.sinks - k0);
+        }
+      }
       int lim = kBN;
-      const int k0 = WIN ? tile_at(w, j) * kBN : 0;
       if constexpr (PAGED) {
-        lim = WIN ? key_end - k0 : min(kBN, key_end - j * kBN);
+        if constexpr (!WIN) lim = min(kBN, key_end - j * kBN);
       } else {
         if (j * kBN + kBN > T) lim = T - j * kBN;
         if (causal && j == w.qb) lim = min(lim, r + 1);
@@ -928,17 +1119,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
       tc::wait_ld();
-      if constexpr (WIN) {
-        if (lim < kBN || (k0 < key_lo && k0 + kBN > pa.sinks)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = window_bits(c * 32, key_lo - k0, lim, pa.sinks - k0);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((bits >> i) & 1u)) sr[c][i] = __float_as_uint(-INFINITY);
-          }
-        }
-      } else if (lim < kBN) {
+      if (lim < kBN) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -1011,7 +1192,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         unf2(add2(sumA, sumB), sa0, sa1);
         psum = sa0 + sa1;
       } else {
-        psum = softmax_p_two_term<WIN>(tS, lim, scale_log2, bias, key_lo - k0, pa.sinks - k0);
+        psum = softmax_p_two_term(tS, lim, scale_log2, bias);
       }
       if (rescale) {
         // sr is free once P is stored (tcgen05.st reads its registers at
@@ -1039,7 +1220,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       mbar_arrive(bars.p_full(t));
     }
     };
-    if (item_has_wide(tile_wide, w.nkv)) tiles(std::true_type{}); else tiles(std::false_type{});
+    if (item_has_wide(tile_wide, nkv, w)) tiles(std::true_type{}); else tiles(std::false_type{});
     if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bars.o_final(t), it & 1, abort_flag));
     if (!ok) break;
     {
@@ -1049,15 +1230,17 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       // and the LSE.
       const bool empty = l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
-      uint32_t bad[4] = {0u, 0u, 0u, 0u};  // windows: columns of non-finite values in sight
+      uint4 bad = make_uint4(0u, 0u, 0u, 0u);  // windows: columns of non-finite values in sight
       if constexpr (WIN) {
-        if (*reinterpret_cast<volatile int*>(tail_info) != 0)
-          for (int j = 0; j < w.nkv; ++j) {
-            const int jt = tile_at(w, j), k0 = jt * kBN;
+        if (*reinterpret_cast<volatile int*>(tail_info + (it & 1)) == it + 1)
+          for (int j = 0; j < nkv; ++j) {
+            const int jt = tile_of(j), k0 = jt * kBN;
             if (!is_wide(tile_wide, jt)) continue;
             const size_t tok = size_t(w.pb) * pa.max_tiles * kBN + k0;
-            poisoned_dims<D>(pa.v_copy + (tok * h_kv + w.kvh) * D, size_t(h_kv) * D, key_lo - k0,
-                             min(key_end - k0, kBN), pa.sinks - k0, bad);
+            const uint4 x = poisoned_dims<D>(pa.v_copy + (tok * h_kv + w.kvh) * D, size_t(h_kv) * D,
+                                             max(key_end - pa.window, 0) - k0, min(key_end - k0, kBN),
+                                             pa.sinks - k0);
+            bad = make_uint4(bad.x | x.x, bad.y | x.y, bad.z | x.z, bad.w | x.w);
           }
       }
       const size_t orow_idx = PAGED ? size_t(w.q_tok0 + row) * h + hq : size_t(hq) * T + row;
@@ -1080,18 +1263,18 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       constexpr int RB = D * 2;    // bytes per O row
       constexpr int CH = RB / 16;  // 16-byte chunks per row
       constexpr int RPI = 32 / CH; // rows per warp store instruction
-      const int gl = g0 + w.nkv - 1;
+      const int gl = g0 + nkv - 1;
       // With one key tile, head 0's stage (that of tile gl - 1) is the one
       // head 1 of the previous item staged in; it may still be reading it.
-      if (!PAGED && t == 0 && w.nkv == 1 && it > 0 &&
+      if (PERSIST && t == 0 && nkv == 1 && it > 0 &&
           !__all_sync(0xffffffffu,
                       wait_or_abort(bars.stage_free((it - 1) & 1), ((it - 1) >> 1) & 1, abort_flag)))
         break;
       uint8_t* stage =
-          PAGED ? smem + C::Q_OFF + t * C::QTILE + wq * (32 * RB)
+          !PERSIST ? smem + C::Q_OFF + t * C::QTILE + wq * (32 * RB)
                 : smem + C::V_OFF + ((t == 0 ? gl - 1 + NSV : gl) % NSV) * C::KTILE + wq * (32 * RB);
-      ATTN_DCHECK(stage >= smem + (PAGED ? C::Q_OFF : C::V_OFF) &&
-                      stage + 32 * RB <= smem + (PAGED ? C::K_OFF : C::BAR_OFF),
+      ATTN_DCHECK(stage >= smem + (!PERSIST ? C::Q_OFF : C::V_OFF) &&
+                      stage + 32 * RB <= smem + (!PERSIST ? C::K_OFF : C::BAR_OFF),
                   &g_prefill_err);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -1099,10 +1282,11 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         tc::ld32(tO + c * 32, ov);
         tc::wait_ld();
         if constexpr (WIN) {
-          if (bad[c] != 0u)
+          const uint32_t nan = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
+          if (nan != 0u)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if ((bad[c] >> i) & 1u) ov[i] = 0x7fc00000u;
+              if ((nan >> i) & 1u) ov[i] = 0x7fc00000u;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1140,7 +1324,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bars.stage_free(it & 1));
     }
-    g0 += w.nkv;
+    g0 += nkv;
     }
   }
 
@@ -1205,6 +1389,38 @@ __global__ void __launch_bounds__(256)
     vwide[size_t(kvh) * n_tiles + tile] = wide;
 }
 
+// Windows: row b's query tiles, tile_off[b+1] = tile_off[b] + ceil(q_len_b / 128), by
+// one warp, a row per lane. Rows with a query count below 0, above max_q_len or above
+// the table's capacity, or whose tokens lie outside [0, total_q), are flagged and get
+// none.
+__device__ __forceinline__ void window_tiles(const int32_t* __restrict__ cu_q, int B, int total_q,
+                                             int max_q_len, int max_blocks,
+                                             int32_t* __restrict__ tile_off) {
+  const int lane = threadIdx.x & 31;
+  int acc = 0;
+  if (lane == 0) tile_off[0] = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane;
+    int n = 0;
+    if (b < B) {
+      const int begin = cu_q[b], end = cu_q[b + 1];
+      if (begin < 0 || end > total_q || end < begin || end - begin > max_q_len ||
+          end - begin > max_blocks * 16)
+        atomicOr(&g_prefill_err, ATTN_DEVERR_BAD_SEQ_LEN);
+      else
+        n = end - begin;
+    }
+    int incl = (n + kBM - 1) / kBM;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (b < B) tile_off[b + 1] = acc + incl;
+    acc += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
 // Paged V -> a copy of the keys each row uses, token-contiguous per row:
 // [B, max_tiles * 128, h_kv, d_h] (row b's key t at token b * max_tiles * 128
 // + t), and flags [B, h_kv, max_tiles] with v_to_f16_kernel's meaning. A tile
@@ -1219,16 +1435,25 @@ __global__ void __launch_bounds__(256)
 // check and the store.
 //
 // WIN: with a window, tiles that no query of the row sees are left alone, and keys
-// that none sees are zeros in the others; their pages are not looked up.
+// that none sees are zeros in the others; their pages are not looked up. The first
+// CTA also plans the attention kernel's items.
 template <int CPR, bool WIN>
 __global__ void __launch_bounds__(256)
     paged_v_to_f16_kernel(const uint4* __restrict__ vc, const int32_t* __restrict__ block_table,
                           const int32_t* __restrict__ cu_q, const int32_t* __restrict__ seq_lens,
                           int max_blocks, int num_blocks, int h_kv, int max_tiles,
-                          int skip_single, int window, int sinks, uint4* __restrict__ v16,
-                          int* __restrict__ vwide) {
+                          int skip_single, int window, int sinks, int total_q, int max_q_len,
+                          int32_t* __restrict__ tile_off, int* __restrict__ sched,
+                          uint4* __restrict__ v16, int* __restrict__ vwide) {
   constexpr int PER = kBN * CPR / 256;  // chunks per thread
   const int jt = blockIdx.x, b = blockIdx.y, kvh = blockIdx.z;
+  if constexpr (WIN) {
+    pdl_trigger();  // the attention kernel sets up meanwhile; it waits for this grid
+    if (jt == 0 && b == 0 && kvh == 0 && threadIdx.x < 32) {
+      if (threadIdx.x == 0) *sched = 0;
+      window_tiles(cu_q, gridDim.y, total_q, max_q_len, max_blocks, tile_off);
+    }
+  }
   const int cap = max_blocks * 16;
   const int q_len = cu_q[b + 1] - cu_q[b];
   if (q_len < 0 || q_len > cap || (skip_single && q_len == 1)) return;
@@ -1360,35 +1585,6 @@ __global__ void paged_tiles_kernel(const int32_t* __restrict__ cu_q, int B, int 
   }
 }
 
-// The same for windows, by a warp, a row per lane. Rows whose tokens lie outside
-// [0, total_q) get no tiles either.
-__global__ void window_tiles_kernel(const int32_t* __restrict__ cu_q, int B, int total_q, int max_q_len,
-                                    int max_blocks, int32_t* __restrict__ tile_off) {
-  const int lane = threadIdx.x;
-  int acc = 0;
-  if (lane == 0) tile_off[0] = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    int n = 0;
-    if (b < B) {
-      const int begin = cu_q[b], end = cu_q[b + 1];
-      n = end - begin;
-      if (begin < 0 || end > total_q || end < begin || n > max_q_len || n > max_blocks * 16) {
-        atomicOr(&g_prefill_err, ATTN_DEVERR_BAD_SEQ_LEN);
-        n = 0;
-      }
-    }
-    int incl = (n + kBM - 1) / kBM;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (b < B) tile_off[b + 1] = acc + incl;
-    acc += __shfl_sync(0xffffffffu, incl, 31);
-  }
-}
-
 template <int D, int NQ, int NSK, int NSV>
 cudaError_t launch_paged(const PagedPrefill& a, cudaStream_t stream) {
   using C = PfCfg<D, NQ, NSK, NSV>;
@@ -1429,35 +1625,47 @@ cudaError_t launch_paged(const PagedPrefill& a, cudaStream_t stream) {
     auto pass = a.window > 0 ? paged_v_to_f16_kernel<D / 8, true> : paged_v_to_f16_kernel<D / 8, false>;
     pass<<<dim3(max_tiles, a.B, a.h_kv), 256, 0, stream>>>(
         static_cast<const uint4*>(a.v_cache), a.block_table, a.cu_q, a.seq_lens, a.max_blocks,
-        a.num_blocks, a.h_kv, max_tiles, a.decode_rows_apart, a.window, a.sinks,
-        static_cast<uint4*>(a.v16), a.vwide);
+        a.num_blocks, a.h_kv, max_tiles, a.decode_rows_apart, a.window, a.sinks, a.total_q,
+        a.max_q_len, a.tile_off, a.sched, static_cast<uint4*>(a.v16), a.vwide);
     const cudaError_t e0 = cudaGetLastError();
     if (e0 != cudaSuccess) return e0;
   }
-  if (a.window > 0)
-    window_tiles_kernel<<<1, 32, 0, stream>>>(a.cu_q, a.B, a.total_q, a.max_q_len, a.max_blocks,
-                                              a.tile_off);
-  else
-    paged_tiles_kernel<<<1, 32, 0, stream>>>(a.cu_q, a.B, a.max_q_len, a.max_blocks,
-                                             a.decode_rows_apart, a.tile_off);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  auto kern = a.window > 0 ? prefill_bf16_kernel<D, NQ, NSK, NSV, true, true, true>
-              : a.v16      ? prefill_bf16_kernel<D, NQ, NSK, NSV, true, true>
-                           : prefill_bf16_kernel<D, NQ, NSK, NSV, true, false>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
+  PagedArgs pa{a.block_table, a.cu_q,       a.seq_lens,   a.tile_off,
+               a.B,           a.max_blocks, a.num_blocks, max_tiles,
+               static_cast<const __nv_bfloat16*>(a.v16), a.window, a.sinks};
   // At most one partial tile per row beyond ceil(total_q / 128), and no row
   // has more than ceil(max_q_len / 128) tiles.
   const long long by_total = (static_cast<long long>(a.total_q) + kBM - 1) / kBM + a.B;
   const long long by_row = static_cast<long long>(a.B) * ((a.max_q_len + kBM - 1) / kBM);
   const long long tiles = by_total < by_row ? by_total : by_row;
+  if (a.window > 0) {
+    // The slots of the items, behind the other instances' shared memory.
+    constexpr int kSmem = C::SMEM + 40 + 4 * int(sizeof(Work));
+    static_assert(kSmem <= 232448, "shared memory budget");
+    auto kern = prefill_bf16_kernel<D, NQ, NSK, NSV, true, true, true>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long items = tiles * (a.h / NQ);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(C::THREADS),
+                      size_t(kSmem), stream, tq, tk, tv, tv16, static_cast<const int*>(a.vwide),
+                      static_cast<__nv_bfloat16*>(a.o), a.lse, 0, a.h, a.h_kv, 1, a.scale * kLog2e, 0,
+                      a.sched, pa);
+  }
+  paged_tiles_kernel<<<1, 32, 0, stream>>>(a.cu_q, a.B, a.max_q_len, a.max_blocks,
+                                           a.decode_rows_apart, a.tile_off);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  auto kern = a.v16 ? prefill_bf16_kernel<D, NQ, NSK, NSV, true, true>
+                    : prefill_bf16_kernel<D, NQ, NSK, NSV, true, false>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
   if (tiles <= 0) return cudaSuccess;
   if (tiles > 65535) return cudaErrorNotSupported;  // query tiles index grid y
   const dim3 grid(a.h / NQ, static_cast<unsigned>(tiles));
-  PagedArgs pa{a.block_table, a.cu_q,       a.seq_lens,   a.tile_off,
-               a.B,           a.max_blocks, a.num_blocks, max_tiles,
-               static_cast<const __nv_bfloat16*>(a.v16), a.window, a.sinks};
   kern<<<grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, tv16, a.v16 ? a.vwide : nullptr,
                                                static_cast<__nv_bfloat16*>(a.o), a.lse, 0, a.h,
                                                a.h_kv, a.causal, a.scale * kLog2e, 0, nullptr,

@@ -23,7 +23,7 @@ def call(lib, **kw):
 
 def test_refuses(lib):
     need = attn.attn_prefill_window_workspace_bytes(2, 20, 8, 128)
-    assert need == attn.attn_prefill_paged_workspace_bytes(2, 20, 8, 128, v16=True) > 0
+    assert need == attn.attn_prefill_paged_workspace_bytes(2, 20, 8, 128, v16=True) + 256 > 256
     for kw in (dict(B=-1), dict(B=65536), dict(total=-1), dict(h=0), dict(h=30), dict(h=65544), dict(h_kv=0), dict(nb=0),
                dict(mb=0), dict(mb=1 << 27), dict(scale=0.0), dict(scale=float("inf")), dict(wsb=need - 1),
                dict(ws=4096 + 16), dict(lse=4098), dict(max_q=0), dict(window=0), dict(window=-5), dict(sinks=-1)):
@@ -31,7 +31,7 @@ def test_refuses(lib):
     for name in ("q", "kc", "vc", "table", "cu", "lens", "ws", "o"):
         assert call(lib, **{name: None}) == BAD, name
         assert call(lib, **{name: ARGS[name] + 2}) == BAD, name
-    for kw in (dict(d=96), dict(page=32), dict(B=40000, mb=1 << 20)):
+    for kw in (dict(d=96), dict(page=32), dict(B=40000, mb=1 << 20), dict(total=2 ** 31 - 1, h=8192)):
         assert call(lib, **kw) == UNSUP, kw
     assert call(lib, B=0, q=None, ws=None, o=None) == 0
     assert call(lib, total=0, q=None, ws=None, o=None) == 0
