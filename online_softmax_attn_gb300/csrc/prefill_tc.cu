@@ -230,10 +230,15 @@ struct Work {
   int nkv;       // key tiles the block visits
   int n_kv_all;  // key tiles of the KV head (contiguous) or row (paged)
   int pb, q_tok0, q_len, ctx, n_pages;  // paged rows only
-  // Windows: tiles before the gap, tiles in it, first key behind it; keys that all of
-  // the item's queries see: from all_lo (and below sinks) to all_hi - 1.
-  int sink_tiles, skip, first, all_lo, all_hi;
+  // Windows: tiles before the gap, tiles in it, first key behind it. Tiles that some of
+  // the item's queries may not see all of: j < edge_lo or j >= edge_hi.
+  int sink_tiles, skip, first, edge_lo, edge_hi;
+  int wide;    // windows: whether any of its V tiles is flagged; -1: not looked at
+  int narrow;  // windows: the first tile holds keys below kSinkKeys alone that are seen
 };
+// A tile of sinks alone has its S product and its weights for this many keys.
+constexpr int kSinkKeys = 32;
+
 
 // Windows: which of the keys kb .. kb + 31 a query sees that sees keys lo .. hi - 1 and
 // those below sinks, one bit each.
@@ -316,8 +321,8 @@ __device__ __noinline__ float softmax_p_two_term(uint32_t tS, int lim, float sca
 
 // Windows: masks an S tile in tensor memory: -inf for the keys that the row does not
 // see (as window_bits, from the tile's first key on). Out of line, so that the softmax
-// loop holds neither its code nor its registers (with the bits tested in the loop it
-// spilled, which cost every tile: 8 x 1024 queries, window 4096, 457 us). Warp-collective.
+// loop holds neither its code nor its registers (with the selection in the loop every
+// tile took 3% longer). Warp-collective.
 __device__ __noinline__ void mask_window(uint32_t tS, int lo, int hi, int sinks) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -331,6 +336,40 @@ __device__ __noinline__ void mask_window(uint32_t tS, int lo, int hi, int sinks)
     tc::st32(tS + c * 32, s);
   }
   tc::wait_st();
+}
+
+// Windows: an item's first tile where it holds sinks alone, below kSinkKeys: the scores of
+// 32 keys, of which the row sees those of `bits`, to fp16 weights in the S tile's first 16
+// columns, and their reference and sum. (The whole tile took 2.3 us of an item's 21 with
+// a window of 1024.) Out of line, so that the softmax loop holds
+// neither its code nor its registers. Warp-collective.
+__device__ __noinline__ float2 sink_weights(uint32_t tS, uint32_t bits, float scale_log2) {
+  uint32_t s[32];
+  tc::ld32(tS, s);
+  tc::wait_ld();
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (!((bits >> i) & 1u)) s[i] = __float_as_uint(-INFINITY);
+    mx = fmaxf(mx, __uint_as_float(s[i]));
+  }
+  // As the first tile of the loop: the reference goes kRefHeadroom above the maximum.
+  const float m = mx == -INFINITY ? -INFINITY : mx * scale_log2 + kRefHeadroom;
+  const float bias = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), scale_log2, -bias));
+    const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), scale_log2, -bias));
+    sum += p0 + p1;
+    s[i] = pack_f16x2(p0, p1);
+  }
+  uint32_t p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p[i] = s[i];
+  tc::st16(tS, p);
+  tc::wait_st();
+  return make_float2(m, sum);
 }
 
 // Windows: a flagged V tile (bf16) at `base` that some query of the item sees only in
@@ -465,8 +504,11 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       pw.sink_tiles = (min(pa.sinks, key_end) + kBN - 1) / kBN;
       pw.skip = max(pw.first / kBN - pw.sink_tiles, 0);
       pw.nkv -= pw.skip;
-      pw.all_hi = ctx - pw.q_len + pw.qb * kBM + 1;
-      pw.all_lo = key_end - pa.window;
+      // All see the keys from the last query's first one up to the first query's last.
+      const int all_lo = max(key_end - pa.window, 0), all_hi = ctx - pw.q_len + pw.qb * kBM + 1;
+      pw.edge_lo = all_lo == 0 ? 0 : (all_lo + kBN - 1) / kBN - pw.skip;
+      pw.edge_hi = all_hi / kBN - pw.skip;
+      pw.narrow = pa.sinks > 0 && pa.sinks <= kSinkKeys && pw.first >= kBN;
     }
   };
   if constexpr (PAGED && !WIN) {
@@ -864,14 +906,14 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       const uint64_t dq0 = tc::sw128_desc(sbase + C::Q_OFF, 16, 1024);
       const uint64_t dk0 = tc::sw128_desc(sbase + C::K_OFF, 16, 1024);
       const uint64_t dv0 = tc::sw128_desc(sbase + C::V_OFF, C::SUB_BYTES, 1024);
-      auto issue_s = [&](int t, int st) {
+      auto issue_s = [&](int t, int st, uint32_t id) {
         const uint64_t da = dq0 + uint64_t((t * C::QTILE) >> 4);
         const uint64_t db = dk0 + uint64_t((st * C::KTILE) >> 4);
         const uint32_t dS = tmem + t * 256;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off16 = ((kk >> 2) * C::SUB_BYTES + (kk & 3) * 32) >> 4;
-          tc::mma_ss_elect(dS, da + off16, db + off16, idS, kk > 0 ? 1u : 0u);
+          tc::mma_ss_elect(dS, da + off16, db + off16, id, kk > 0 ? 1u : 0u);
         }
       };
       constexpr uint32_t idO16 = tc::idesc_f16_f32(kBM, D, false, true);
@@ -913,12 +955,16 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         if (!next_work(it, item)) break;
         WorkOf w = work_of(it, item);
         const int nkv = w.nkv;
+        const bool narrow = WIN && w.narrow;
         const int* tile_wide = wide_flags(w);
         ok = wait(bars.q_full(), it & 1) && wait(bars.k_full(g0 % NSK), (g0 / NSK) & 1);
         if (!ok) break;
         tc::fence_after();
         for (int t = 0; t < NQ; ++t) {
-          issue_s(t, g0 % NSK);
+          if (WIN && w.narrow)
+            issue_s(t, g0 % NSK, tc::idesc_bf16_f32(kBM, kSinkKeys, false, false));
+          else
+            issue_s(t, g0 % NSK, idS);
           tc::commit_elect(bars.s_full(t));
         }
         tc::commit_elect(bars.k_empty(g0 % NSK));
@@ -942,13 +988,22 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
             if (!wait(bars.p_full(t), g & 1)) { ok = false; break; }
             if (t == 0 && !wait(bars.v_full(sv), (g / NSV) & 1)) { ok = false; break; }
             tc::fence_after();
-            issue_pv(t, sv, j > 0, wide);
+            if (WIN && j == 0 && narrow && !wide) {
+              // Two steps of 16 keys: the other weights are not there.
+              const uint64_t dvb = dv0 + uint64_t((sv * C::KTILE) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kSinkKeys / 16; ++kk)
+                tc::mma_ts_elect(tmem + t * 256 + 128, tmem + t * 256 + kk * 8,
+                                 dvb + uint64_t((kk * 16 * 128) >> 4), idO16, kk > 0 ? 1u : 0u);
+            } else {
+              issue_pv(t, sv, j > 0, wide);
+            }
             if (j == nkv - 1) tc::commit_elect(bars.o_final(t));
             if (t == NQ - 1) tc::commit_elect(bars.v_empty(sv));
             if (j + 1 < nkv) {
               if (t == 0 && !wait(bars.k_full(sk1), ((g + 1) / NSK) & 1)) { ok = false; break; }
               tc::fence_after();
-              issue_s(t, sk1);
+              issue_s(t, sk1, idS);
               tc::commit_elect(bars.s_full(t));
               if (t == NQ - 1) {
                 tc::commit_elect(bars.k_empty(sk1));
@@ -958,7 +1013,8 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
           }
         }
         };
-        if (item_has_wide(tile_wide, nkv, w)) tiles(std::true_type{}); else tiles(std::false_type{});
+        if (WIN && w.wide >= 0 ? w.wide != 0 : item_has_wide(tile_wide, nkv, w)) tiles(std::true_type{});
+        else tiles(std::false_type{});
         g0 += nkv;
       }
       // Everything issued has completed once mma_done flips.
@@ -992,6 +1048,8 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
           n = min(step, n - k * step);
         }
         paged_work(cur % n_hp, lo, tile);
+        // (The first item is not held up for its flags: its roles look for themselves.)
+        pw.wide = it == 0 ? -1 : item_has_wide(wide_flags(pw), pw.nkv, pw);
       }
       if (lane == 0) {
         win_slot[it & 3] = pw;
@@ -1021,37 +1079,48 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     if (!next_work(it, item)) break;
     WorkOf w = work_of(it, item);
     const int nkv = w.nkv;
-    auto tile_of = [sink_tiles = WIN ? w.sink_tiles : 0, skip = WIN ? w.skip : 0](int j) {
-      return WIN && j >= sink_tiles ? j + skip : j;
-    };
+    const int edge_lo = WIN ? w.edge_lo : 0, edge_hi = WIN ? w.edge_hi : 0;
     ATTN_DCHECK(w.hq0 + NQ <= h && w.kvh < h_kv && w.nkv >= 1 &&
                     w.nkv <= (PAGED ? pa.max_tiles : w.n_kv_all) &&
                     (PAGED || w.qb < n_qblk),
                 &g_prefill_err);
     const int* tile_wide = wide_flags(w);
-    const int row = w.qb * kBM + r;  // query index within the row (paged) or the sequence
-    const int hq = w.hq0 + t;
+    // (Windows: worked out again behind the loop, which has no registers for them.)
+    const int row = WIN ? 0 : w.qb * kBM + r;  // query index within the row (paged) or the sequence
     // Paged rows: keys [0, key_end) are visible to this query (none for the
     // padding rows of a row's last tile).
-    const bool row_valid = PAGED ? row < w.q_len : row < T;
+    const bool row_valid = WIN ? false : PAGED ? row < w.q_len : row < T;
     const int key_end =
-        !PAGED ? 0 : (!row_valid ? 0 : (causal ? w.ctx - w.q_len + row + 1 : w.ctx));
+        !PAGED || WIN ? 0 : (!row_valid ? 0 : (causal ? w.ctx - w.q_len + row + 1 : w.ctx));
     // m_ref: exp2-domain reference that l, O~ and this tile's P are relative
     // to (the row max of some tile seen so far, within 2^15 of the running
     // max).
     float m_ref = -INFINITY;
     float l = 0.f;
+    int j0 = 0;  // first tile of the loop below
+    if constexpr (WIN) {
+      if (w.narrow && !(w.wide && is_wide(tile_wide, 0))) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(bars.s_full(t), g0 & 1, abort_flag))) break;
+        tc::fence_after();
+        const float2 x = sink_weights(tS, w.qb * kBM + r < w.q_len ? (2u << (pa.sinks - 1)) - 1u : 0u, scale_log2);
+        m_ref = x.x;
+        l = x.y;
+        tc::fence_before();
+        mbar_arrive(bars.p_full(t));
+        j0 = 1;
+      }
+    }
     // Instantiated twice, as the MMA warp's loop: without a wide tile in the
     // item, no tile takes the format branch.
     auto tiles = [&](auto any_wide) {
     constexpr bool MAYBE_WIDE = decltype(any_wide)::value;
     uint32_t wbits = 0;
-    for (int j = 0; j < nkv; ++j) {
+    for (int j = j0; j < nkv; ++j) {
       const int g = g0 + j;
       // The format of P follows the format of this key tile's V.
       bool wide = false;
       if constexpr (MAYBE_WIDE) {
-        if ((j & 31) == 0) wbits = wide_bits(tile_wide, j, nkv, w);
+        if ((j & 31) == 0 || (WIN && j == j0)) wbits = wide_bits(tile_wide, j & ~31, nkv, w);
         wide = (wbits >> (j & 31)) & 1u;
       }
       // Warp-uniform outcome: the tensor-memory loads below are warp-collective.
@@ -1089,8 +1158,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         if (wide && t == 0) {
           // Keys that some query of the item does not see have weight 0 in its
           // P V, but 0 * NaN is NaN. (Unflagged tiles hold finite values.)
-          const int k0 = tile_of(j) * kBN;
-          if (k0 + kBN > w.all_hi || (k0 < w.all_lo && k0 + kBN > pa.sinks)) {
+          if (j < edge_lo || j >= edge_hi) {
             const int sv = g % NSV;
             if (wait_or_abort(bars.v_full(sv), (g / NSV) & 1, abort_flag) &&
                 clean_wide_v<D>(sbase + C::V_OFF + sv * C::KTILE, r))
@@ -1101,8 +1169,8 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       }
       tc::fence_after();
       if constexpr (WIN) {
-        const int k0 = tile_of(j) * kBN;
-        if (k0 + kBN > w.all_hi || (k0 < w.all_lo && k0 + kBN > pa.sinks)) {
+        if (j < edge_lo || j >= edge_hi) {
+          const int k0 = tile_at(w, j) * kBN;
           const int q = w.qb * kBM + r, end = q < w.q_len ? w.ctx - w.q_len + q + 1 : 0;
           mask_window(tS, max(end - pa.window, 0) - k0, end - k0, pa.sinks - k0);
         }
@@ -1220,7 +1288,8 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       mbar_arrive(bars.p_full(t));
     }
     };
-    if (item_has_wide(tile_wide, nkv, w)) tiles(std::true_type{}); else tiles(std::false_type{});
+    if (WIN && w.wide >= 0 ? w.wide != 0 : item_has_wide(tile_wide, nkv, w)) tiles(std::true_type{});
+    else tiles(std::false_type{});
     if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bars.o_final(t), it & 1, abort_flag));
     if (!ok) break;
     {
@@ -1230,20 +1299,25 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       // and the LSE.
       const bool empty = l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
+      const int hq = w.hq0 + t;
+      const int out_row = WIN ? w.qb * kBM + r : row;
+      const bool out_valid = WIN ? out_row < w.q_len : row_valid;
       uint4 bad = make_uint4(0u, 0u, 0u, 0u);  // windows: columns of non-finite values in sight
       if constexpr (WIN) {
         if (*reinterpret_cast<volatile int*>(tail_info + (it & 1)) == it + 1)
           for (int j = 0; j < nkv; ++j) {
-            const int jt = tile_of(j), k0 = jt * kBN;
+            const int jt = tile_at(w, j), k0 = jt * kBN;
+            const int end = out_valid ? w.ctx - w.q_len + out_row + 1 : 0;
             if (!is_wide(tile_wide, jt)) continue;
             const size_t tok = size_t(w.pb) * pa.max_tiles * kBN + k0;
             const uint4 x = poisoned_dims<D>(pa.v_copy + (tok * h_kv + w.kvh) * D, size_t(h_kv) * D,
-                                             max(key_end - pa.window, 0) - k0, min(key_end - k0, kBN),
+                                             max(end - pa.window, 0) - k0, min(end - k0, kBN),
                                              pa.sinks - k0);
             bad = make_uint4(bad.x | x.x, bad.y | x.y, bad.z | x.z, bad.w | x.w);
           }
       }
-      const size_t orow_idx = PAGED ? size_t(w.q_tok0 + row) * h + hq : size_t(hq) * T + row;
+      const size_t orow_idx =
+          PAGED ? size_t(w.q_tok0 + out_row) * h + hq : size_t(hq) * T + out_row;
       // Output rows (debug checks): h * T, or h per packed query token.
       auto out_rows = [&]() -> size_t {
         return PAGED ? size_t(pa.cu_q[pa.B]) * h : size_t(h) * T;
@@ -1315,7 +1389,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
           }
         }
       }
-      if (row_valid && lse != nullptr && ATTN_GUARD(orow_idx < out_rows(), &g_prefill_err))
+      if (out_valid && lse != nullptr && ATTN_GUARD(orow_idx < out_rows(), &g_prefill_err))
         lse[orow_idx] = empty ? -INFINITY : (m_ref + log2f(l)) * kLn2;
       // The warp's rows have left the stage (each lane's loads completed
       // before its stores issued); the fence orders these generic accesses
