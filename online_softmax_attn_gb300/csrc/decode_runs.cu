@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256, 1)
 // Joins the partial states of each (row, head) that a run border cut, and
 // writes empty rows. One CTA per (row, head), warps take its partials in turn
 // (a row alone on the GPU has 38 per head: one round trip).
-template <int D>
+template <int D, int kUnit>
 __global__ void __launch_bounds__(128)
     decode_runs_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m_part,
                          const float* __restrict__ l_part, const long long* __restrict__ plan,
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(256, 1) __cluster_dims__(kClusterCtas)
     return;
   }
   const int per = max(kMinRun, (wu + kClusterCtas * 8 - 1) / (kClusterCtas * 8)) * 8;
-  const int c0 = kUnit / per, n = (wu - 1) / per - c0 + 1;
+  const int c0 = R::kUnit / per, n = (wu - 1) / per - c0 + 1;
   if (n == 1) return;  // finished by its CTA
   float m[kClusterCtas], l[kClusterCtas], x[kClusterCtas][VEC];
   float M = kNone;
@@ -281,11 +281,11 @@ cudaError_t sm_count(int* sms) {
 
 namespace {
 // `most`: pages that a row can have, known on the host.
-template <bool E8, int NST128, int NST64, class R>
+template <bool E8, int NST128, int NST64, class One, class R>
 cudaError_t launch_runs(const DecodeRunsArgs& a, int most, cudaStream_t stream) {
   const long long units = static_cast<long long>(a.B) * a.h_kv * ((a.h / a.h_kv + 7) / 8);
   if (units <= kUnitMost && most <= kUnitBlocks)
-    return a.d_h == 128 ? launch_unit<E8, 128, NST128, R>(a, stream) : launch_unit<E8, 64, NST64, R>(a, stream);
+    return a.d_h == 128 ? launch_unit<E8, 128, NST128, One>(a, stream) : launch_unit<E8, 64, NST64, One>(a, stream);
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
@@ -293,7 +293,7 @@ cudaError_t launch_runs(const DecodeRunsArgs& a, int most, cudaStream_t stream) 
                    : launch_cfg<E8, 64, NST64, R>(a, sms, stream);
   if (e != cudaSuccess) return e;
   const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
-  auto merge = a.d_h == 128 ? decode_runs_merge_kernel<128> : decode_runs_merge_kernel<64>;
+  auto merge = a.d_h == 128 ? decode_runs_merge_kernel<128, R::kUnit> : decode_runs_merge_kernel<64, R::kUnit>;
   return launch_pdl(merge, dim3(unsigned(a.B) * a.h), dim3(128), 0, stream,
                     static_cast<const float*>(a.o_part), static_cast<const float*>(a.m_part),
                     static_cast<const float*>(a.l_part), static_cast<const long long*>(a.plan), a.h,
@@ -302,15 +302,21 @@ cudaError_t launch_runs(const DecodeRunsArgs& a, int most, cudaStream_t stream) 
 }  // namespace
 
 cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream) {
-  return launch_runs<true, 4, 6, Rows>(a, a.max_blocks, stream);
+  return launch_runs<true, 4, 6, Rows, Rows>(a, a.max_blocks, stream);
 }
 
+// Units of windows are short, so what one weighs beside its pages matters: 200 rows of
+// the 8-bit cache, window 2001, take 157.8 us with 1, 147.7 with 3, 142.2 with 5, 142.8
+// with 8 (66 rows of the bf16 cache, window 4096: 158.2, 159.0, 158.9, 159.4).
+constexpr int kWindowUnit = 5;
 cudaError_t launch_decode_window(const DecodeRunsArgs& a, cudaStream_t stream) {
   // The window's pages (one more where it starts inside a page) and the sinks'.
   const long long seen = (a.window + 14ll) / kPage + 1 + (a.sinks + 15ll) / kPage;
   const int most = seen < a.max_blocks ? static_cast<int>(seen) : a.max_blocks;
-  return a.k_exp != nullptr ? launch_runs<true, 4, 6, WindowRows>(a, most, stream)
-                            : launch_runs<false, 3, 6, WindowRows>(a, most, stream);
+  using One = WindowRows<kRunsUnit>;  // a unit on its own is cut as a whole row's
+  using Many = WindowRows<kWindowUnit>;
+  return a.k_exp != nullptr ? launch_runs<true, 4, 6, One, Many>(a, most, stream)
+                            : launch_runs<false, 3, 6, One, Many>(a, most, stream);
 }
 
 unsigned int decode_runs_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {

@@ -182,7 +182,6 @@ struct RunOut {
   float* lse;
 };
 
-constexpr int kUnit = kRunsUnit;  // a unit's query, state and epilogue, in pages
 constexpr int kMinRun = 1;      // least weight of a warp's run
 constexpr int kLenCache = 128;  // row lengths kept in shared memory
 
@@ -201,6 +200,7 @@ struct Rows {
   const int32_t* seq_lens;
   int B, max_len, upr, n_gb;  // units per row, and per (row, KV head)
   static constexpr bool kWindow = false;
+  static constexpr int kUnit = kRunsUnit;  // a unit's query, state and epilogue, in pages
   __device__ __forceinline__ int pages(int len) const { return (len + kPage - 1) / kPage; }
   __device__ __forceinline__ int page_at(int, int i) const { return i; }
 };
@@ -208,9 +208,11 @@ struct Rows {
 // walks are the pages that hold such keys, laid end to end: sink_pages of them,
 // then the window's from page first on. Every one of them holds a visible key, so
 // no page's scores are all masked, and pages in between are never looked up.
+template <int UNIT>
 struct WindowRows : Rows {
   int window, sinks;
   static constexpr bool kWindow = true;
+  static constexpr int kUnit = UNIT;
   __device__ __forceinline__ int first_key(int len) const { return max(len - window, 0); }
   __device__ __forceinline__ int sink_pages(int len) const {
     return (min(sinks, len) + kPage - 1) / kPage;
@@ -248,7 +250,7 @@ __device__ __forceinline__ int row_len(const Rows& rw, const int* cached, int b)
 }
 template <class R>
 __device__ __forceinline__ int row_weight(const R& rw, int len) {  // of one unit of the row
-  return len > 0 ? rw.pages(len) + kUnit : 0;
+  return len > 0 ? rw.pages(len) + R::kUnit : 0;
 }
 // a / b for a >= 0, b > 0: in 32 bits where both fit (64-bit division costs
 // several hundred cycles).
@@ -257,6 +259,7 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return a / b;
 }
 // Opens unit w.u of row w.b at weight `off` within it.
+template <int kUnit>
 __device__ __forceinline__ void walk_open(Walk& w, long long off) {
   const long long take = min(w.np + kUnit - off, w.rem);
   w.lo = static_cast<int>(max(off - kUnit, 0ll));
@@ -276,7 +279,7 @@ __device__ __forceinline__ bool walk_next(Walk& w, const R& rw, const int* cache
     } while (w.len == 0);
     w.np = rw.pages(w.len);
   }
-  walk_open(w, 0);
+  walk_open<R::kUnit>(w, 0);
   return true;
 }
 
@@ -457,9 +460,9 @@ __device__ __forceinline__ void runs_body(
   cw.np = rw.pages(cw.len);
   cw.rem = plan.rem;
   {
-    const int wu = cw.np + kUnit;
+    const int wu = cw.np + R::kUnit;
     cw.u = static_cast<int>(div_ll(off, wu));
-    walk_open(cw, off - static_cast<long long>(cw.u) * wu);
+    walk_open<R::kUnit>(cw, off - static_cast<long long>(cw.u) * wu);
   }
 
   // ---- producer state: the same walk, NST pages ahead ----
