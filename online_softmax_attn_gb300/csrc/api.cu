@@ -550,7 +550,7 @@ attn_status_t decode_runs(const void* q, const void* k_cache, const void* v_cach
       !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
     return ATTN_ERR_INVALID_ARG;
   const RunsLayout L = runs_layout(B, d_h);
-  if (workspace_bytes < L.total) return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < L.total + (window > 0 ? kRunsCutBytes : 0)) return ATTN_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeRunsArgs a;
   a.q = q;
@@ -575,6 +575,7 @@ attn_status_t decode_runs(const void* q, const void* k_cache, const void* v_cach
   a.lse = lse;
   a.window = window;
   a.sinks = sinks;
+  a.cut = ws + L.total;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return from_cuda(window > 0 ? launch_decode_window(a, s) : launch_decode8(a, s));
 }
@@ -592,7 +593,8 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
 }
 
 size_t attn_decode_window_workspace_bytes(int B, int h, int h_kv, int d_h) {
-  return attn_decode_e4m3_workspace_bytes(B, h, h_kv, d_h);
+  const size_t n = attn_decode_e4m3_workspace_bytes(B, h, h_kv, d_h);
+  return n == 0 ? 0 : n + kRunsCutBytes;
 }
 
 attn_status_t attn_decode_paged_window(const void* q, const void* k_cache, const void* v_cache,

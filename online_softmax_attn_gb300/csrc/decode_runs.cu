@@ -27,40 +27,25 @@ __global__ void __launch_bounds__(256, 1)
                                              ~uintptr_t(1023));
   pdl_wait();     // lengths, table, q and the cache are earlier kernels' output
   pdl_trigger();
+  if constexpr (R::kWindow) {
+    if (threadIdx.x == 0) out.cut[blockIdx.x].parts = 0;
+  }
   runs_body<E8, D, 8, NST>(kc, vc, ks, vs, q, block_table, rw, h, h_kv, g, max_blocks,
                            num_blocks, qscale, out, smem, sh, blockIdx.x, gridDim.x,
                            &g_decode_runs_err, [] { __syncthreads(); });
 }
 
-// Joins the partial states of each (row, head) that a run border cut, and
-// writes empty rows. One CTA per (row, head), warps take its partials in turn
-// (a row alone on the GPU has 38 per head: one round trip).
-template <int D, int kUnit>
-__global__ void __launch_bounds__(128)
-    decode_runs_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m_part,
-                         const float* __restrict__ l_part, const long long* __restrict__ plan,
-                         int h, int g, int n_gb, int upr, __nv_bfloat16* __restrict__ o,
-                         float* __restrict__ lse) {
+// Joins the n partial states of (row, head) `row`, head hh of its block, that the CTAs
+// from c0 on hold, and divides once. A CTA of 128 threads: warps take the states in
+// turn (a row alone on the GPU has 38 per head: one round trip).
+template <int D>
+__device__ __forceinline__ void merge_parts(const float* __restrict__ o_part, const float* __restrict__ m_part,
+                                            const float* __restrict__ l_part, long long c0, int n, int hh,
+                                            size_t row, __nv_bfloat16* __restrict__ o,
+                                            float* __restrict__ lse) {
   constexpr int VEC = D / 32, U = 10, NW = 4;  // 40 states in flight
   __shared__ float sm[NW], sl[NW], so[NW][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x / h, hq = blockIdx.x % h;
-  pdl_wait();
-  pdl_trigger();
-  const long long per = __ldcg(plan), at = __ldcg(plan + 1 + b);
-  const long long wu = __ldcg(plan + 2 + b) - at;  // weight of one unit: its pages + kUnit
-  const size_t row = static_cast<size_t>(b) * h + hq;
-  if (!ATTN_GUARD(row < gridDim.x && per > 0 && wu >= 0, &g_decode_runs_err)) return;
-  if (wu == 0) {
-    for (int i = threadIdx.x; i < D / 2; i += 128) reinterpret_cast<uint32_t*>(o + row * D)[i] = 0u;
-    if (lse != nullptr && threadIdx.x == 0) lse[row] = -INFINITY;
-    return;
-  }
-  const int u = (hq / g) * n_gb + (hq % g) / 8;
-  const long long s = at * upr + u * wu;
-  const long long c0 = (s + kUnit) / per;  // CTAs of the unit's first and last page
-  const int n = static_cast<int>((s + wu - 1) / per - c0) + 1;
-  if (n == 1) return;  // finished by its CTA
   float M = kNone, L = 0.f, acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
@@ -74,7 +59,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x[i][e] = 0.f;
       if (j < n) {
-        const size_t slot = (2 * (c0 + j) + (j == 0 ? 1 : 0)) * 8 + (hq % g) % 8;
+        const size_t slot = (2 * (c0 + j) + (j == 0 ? 1 : 0)) * 8 + hh;
         ATTN_DCHECK(slot < 2 * kRunsMaxCtas * 8, &g_decode_runs_err);
         m[i] = __ldcg(m_part + slot);
         l[i] = __ldcg(l_part + slot);
@@ -125,6 +110,64 @@ __global__ void __launch_bounds__(128)
     o[row * D + e] = __float2bfloat16(empty ? 0.f : v * inv);
   }
   if (lse != nullptr && threadIdx.x == 0) lse[row] = empty ? -INFINITY : Mt * kLn2 + logf(Lt);
+}
+
+// Merge of the rows that the runs' borders cut, and of empty rows. One CTA per (row,
+// head).
+template <int D>
+__global__ void __launch_bounds__(128)
+    decode_runs_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m_part,
+                         const float* __restrict__ l_part, const long long* __restrict__ plan,
+                         int h, int g, int n_gb, int upr, __nv_bfloat16* __restrict__ o,
+                         float* __restrict__ lse) {
+  const int b = blockIdx.x / h, hq = blockIdx.x % h;
+  pdl_wait();
+  pdl_trigger();
+  const long long per = __ldcg(plan), at = __ldcg(plan + 1 + b);
+  const long long wu = __ldcg(plan + 2 + b) - at;  // weight of one unit: its pages + kRunsUnit
+  const size_t row = static_cast<size_t>(b) * h + hq;
+  if (!ATTN_GUARD(row < gridDim.x && per > 0 && wu >= 0, &g_decode_runs_err)) return;
+  if (wu == 0) {
+    for (int i = threadIdx.x; i < D / 2; i += 128) reinterpret_cast<uint32_t*>(o + row * D)[i] = 0u;
+    if (lse != nullptr && threadIdx.x == 0) lse[row] = -INFINITY;
+    return;
+  }
+  const int u = (hq / g) * n_gb + (hq % g) / 8;
+  const long long s = at * upr + u * wu;
+  const long long c0 = (s + kRunsUnit) / per;  // CTAs of the unit's first and last page
+  const int n = static_cast<int>((s + wu - 1) / per - c0) + 1;
+  if (n == 1) return;  // finished by its CTA
+  merge_parts<D>(o_part, m_part, l_part, c0, n, (hq % g) % 8, row, o, lse);
+}
+
+// The same for windows, whose units are many and short: head blockIdx.y of the unit
+// that begins in CTA blockIdx.x of the runs and goes on behind it, and empty rows. (A
+// CTA per (row, head) took 6 us for 66 rows of 32 heads and 10 for 200, most of them
+// finished already.)
+template <int D>
+__global__ void __launch_bounds__(128)
+    decode_window_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m_part,
+                               const float* __restrict__ l_part, const RunCut* __restrict__ cut,
+                               const Rows rw, int h, __nv_bfloat16* __restrict__ o,
+                               float* __restrict__ lse) {
+  const int hh = blockIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  const int parts = __ldcg(&cut[blockIdx.x].parts);
+  if (parts > 0) {
+    const int row0 = __ldcg(&cut[blockIdx.x].row0), nh = __ldcg(&cut[blockIdx.x].nh);
+    const size_t row = static_cast<size_t>(row0) + hh;
+    if (hh < nh && ATTN_GUARD(row < static_cast<size_t>(rw.B) * h, &g_decode_runs_err))
+      merge_parts<D>(o_part, m_part, l_part, blockIdx.x, parts, hh, row, o, lse);
+  }
+  for (int b = blockIdx.x + gridDim.x * hh; b < rw.B; b += gridDim.x * gridDim.y) {
+    if (row_len(rw, b) > 0) continue;
+    const size_t row = static_cast<size_t>(b) * h;
+    for (int i = threadIdx.x; i < h * (D / 8); i += 128)
+      reinterpret_cast<uint4*>(o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (lse != nullptr)
+      for (int i = threadIdx.x; i < h; i += 128) lse[row + i] = -INFINITY;
+  }
 }
 
 // Few rows of few keys: one kernel. A cluster of 8 CTAs has one unit (row, KV
@@ -263,7 +306,8 @@ cudaError_t launch_cfg(const DecodeRunsArgs& a, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int grid = sms < kRunsMaxCtas ? sms : kRunsMaxCtas;
   const RunOut out{a.plan,  a.o_part, a.m_part, a.l_part, nullptr,
-                   nullptr, nullptr,  static_cast<__nv_bfloat16*>(a.o), a.lse};
+                   nullptr, nullptr,  static_cast<__nv_bfloat16*>(a.o), a.lse,
+                   static_cast<RunCut*>(a.cut)};
   return launch_pdl(kern, dim3(grid), dim3(256), size_t(kSmem), stream,
                     static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache), a.k_exp, a.v_exp,
                     static_cast<const __nv_bfloat16*>(a.q), a.block_table, rows_of<R>(a), a.h, a.h_kv,
@@ -293,7 +337,16 @@ cudaError_t launch_runs(const DecodeRunsArgs& a, int most, cudaStream_t stream) 
                    : launch_cfg<E8, 64, NST64, R>(a, sms, stream);
   if (e != cudaSuccess) return e;
   const int g = a.h / a.h_kv, n_gb = (g + 7) / 8;
-  auto merge = a.d_h == 128 ? decode_runs_merge_kernel<128, R::kUnit> : decode_runs_merge_kernel<64, R::kUnit>;
+  if constexpr (R::kWindow) {
+    const int ctas = sms < kRunsMaxCtas ? sms : kRunsMaxCtas;
+    auto merge = a.d_h == 128 ? decode_window_merge_kernel<128> : decode_window_merge_kernel<64>;
+    const Rows rw = rows_of<Rows>(a);
+    return launch_pdl(merge, dim3(unsigned(ctas), unsigned(g < 8 ? g : 8)), dim3(128), 0, stream,
+                      static_cast<const float*>(a.o_part), static_cast<const float*>(a.m_part),
+                      static_cast<const float*>(a.l_part), static_cast<const RunCut*>(a.cut), rw, a.h,
+                      static_cast<__nv_bfloat16*>(a.o), a.lse);
+  }
+  auto merge = a.d_h == 128 ? decode_runs_merge_kernel<128> : decode_runs_merge_kernel<64>;
   return launch_pdl(merge, dim3(unsigned(a.B) * a.h), dim3(128), 0, stream,
                     static_cast<const float*>(a.o_part), static_cast<const float*>(a.m_part),
                     static_cast<const float*>(a.l_part), static_cast<const long long*>(a.plan), a.h,

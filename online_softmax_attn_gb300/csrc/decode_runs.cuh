@@ -171,6 +171,12 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t page, int r, int c) {
     return page + (c >> 3) * (kPage * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// What a merge reads of the unit that begins in a CTA and goes on behind it: parts
+// (0: there is none), first (row, head), heads.
+struct RunCut {
+  int parts, row0, nh, unused;
+};
+
 // Where states and results go. Units cut by a run border: part (two slots of 8
 // heads per CTA). Other units: o and lse themselves (8-bit decode), or a state
 // per (row, head) in row_* (shared-prefix decode, whose merge adds the prefix).
@@ -180,6 +186,7 @@ struct RunOut {
   float *o_row, *m_row, *l_row;
   __nv_bfloat16* o;
   float* lse;
+  RunCut* cut = nullptr;  // [CTAs] (windows)
 };
 
 constexpr int kMinRun = 1;      // least weight of a warp's run
@@ -192,7 +199,7 @@ struct RunShared {
   int b[NW];          // its first row
   int kind[NW];       // its stored part: 0 none, 1 the unit goes on, 2 it ends
   int own[NW];        // the unit behind it: 0 none, 1 began in its run, 2 before the CTA
-  int own_row[NW], own_nh[NW];
+  int own_row[NW], own_nh[NW], own_left[NW];  // left: its pages behind the warp's run
   int len[kLenCache];
 };
 
@@ -288,6 +295,7 @@ __device__ __forceinline__ bool walk_next(Walk& w, const R& rw, const int* cache
 struct RunPlan {
   long long rem, off;
   int b, len;
+  long long per;  // weight of every run
 };
 
 // Plans the runs, one per warp; CTA 0 leaves the plan for the merge (none: nullptr,
@@ -329,7 +337,7 @@ __device__ __forceinline__ RunPlan plan_runs(const R rw, long long* plan, RunSha
       if (lane < rw.B) plan[1 + lane] = incl - w;
       if (lane == rw.B - 1) plan[1 + rw.B] = incl;
     }
-    if (per * NW * cta >= all) return RunPlan{-1, 0, 0, 0};
+    if (per * NW * cta >= all) return RunPlan{-1, 0, 0, 0, 0};
     p0 = per * (static_cast<long long>(NW) * cta + warp);
     have = p0 < all;
     const long long at = static_cast<long long>(incl - w) * rw.upr;
@@ -376,7 +384,7 @@ __device__ __forceinline__ RunPlan plan_runs(const R rw, long long* plan, RunSha
         if (b == rw.B - 1) plan[1 + rw.B] = at;
       }
     }
-    if (cta0 >= all) return RunPlan{-1, 0, 0, 0};
+    if (cta0 >= all) return RunPlan{-1, 0, 0, 0, 0};
     long long at = before * rw.upr;
     const long long end = (before + sum) * rw.upr;
     if (cta0 + per * NW > at && cta0 < end) {
@@ -401,6 +409,7 @@ __device__ __forceinline__ RunPlan plan_runs(const R rw, long long* plan, RunSha
     r.len = row_len(rw, sh.len, r.b);
   }
   r.rem = have ? min(per, all - p0) : 0;
+  r.per = per;
   return r;
 }
 
@@ -881,6 +890,7 @@ __device__ __forceinline__ void runs_body(
           s_own[warp] = begins ? 1 : 2;
           s_own_row[warp] = static_cast<int>(row0);
           s_own_nh[warp] = nh;
+          if constexpr (WIN) sh.own_left[warp] = cw.np - cw.hi;
         } else {
           s_kind[warp] = ends ? 2 : 1;
         }
@@ -893,7 +903,7 @@ __device__ __forceinline__ void runs_body(
   sync();
   if (warp < KS) {
     const int k = warp;
-    int open = 0, row0 = 0, nh = 0;  // the chain: 0 none, else its s_own
+    int open = 0, row0 = 0, nh = 0, opened = 0;  // the chain: 0 none, else its s_own; its warp
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     float M0 = 0.f, M1 = 0.f, L0 = 0.f, L1 = 0.f;
 #pragma unroll 1
@@ -920,6 +930,7 @@ __device__ __forceinline__ void runs_body(
       if (own != 0) {
         const float* t = tail_of(w);
         open = own;
+        opened = w;
         row0 = s_own_row[w];
         nh = s_own_nh[w];
         M0 = t[C::NREG * 32 + 2 * tq];
@@ -932,6 +943,14 @@ __device__ __forceinline__ void runs_body(
     }
     if (open != 0)
       emit(2ll * cta + (open == 1 ? 1 : 0), row0, nh, k, x, M0, M1, L0, L1);
+    if constexpr (WIN) {
+      // The unit that began in this CTA and goes on behind it: the weight that is left
+      // of it is spread over the CTAs behind.
+      if (out.cut != nullptr && tid == 0 && open == 1) {
+        const long long left = sh.own_left[opened] - plan.per * (NW - 1 - opened);
+        out.cut[cta] = RunCut{static_cast<int>(1 + div_ll(left + plan.per * NW - 1, plan.per * NW)), row0, nh, 0};
+      }
+    }
   }
 }
 

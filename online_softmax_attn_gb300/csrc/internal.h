@@ -112,6 +112,7 @@ inline RunsLayout runs_layout(int B, int d_h) {
   L.total = L.l_off + size_t(2 * kRunsMaxCtas) * 8 * sizeof(float);
   return L;
 }
+constexpr size_t kRunsCutBytes = kRunsMaxCtas * 16;  // windows: behind runs_layout
 struct DecodeRunsArgs {
   const void* q;
   const void* k_cache;
@@ -132,6 +133,7 @@ struct DecodeRunsArgs {
   void* o = nullptr;       // 8-bit cache and windows
   float* lse = nullptr;
   int window = 0, sinks = 0;  // windows only
+  void* cut = nullptr;        // windows only: 16 bytes per CTA
 };
 cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream);  // and its merge
 // The same over each row's last `window` keys and first `sinks`, of the 8-bit cache
