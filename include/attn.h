@@ -849,7 +849,7 @@ attn_status_t attn_selftest_wait_timeout(unsigned int limit_us, void* stream);
 /*
  * attn_selftest_prefill_stall -- exercise the bf16 prefill's abort path
  * without a fault; builds compiled with -DATTN_DEBUG only. From the next
- * contiguous tensor-core prefill on, every CTA skips loading K for the
+ * contiguous or windowed tensor-core prefill on, every CTA skips loading K for the
  * key_tile-th key tile it visits (counted over its work items; nothing is
  * requested for that tile), so the MMA warp's bounded wait for it gives up
  * after 2 s and raises ATTN_DEVERR_WAIT_TIMEOUT; every role of the CTA then
@@ -868,6 +868,13 @@ attn_status_t attn_selftest_prefill_stall(int key_tile);
  * INVALID_ARG for any other `what`.
  */
 attn_status_t attn_selftest_shared_stall(int key_tile, int what);
+
+/*
+ * attn_selftest_tree_stall -- the same for attn_decode_paged_tree: every CTA leaves
+ * out one load of the key_tile-th key tile that it visits, K (what 0) or V (1).
+ * INVALID_ARG for any other `what`.
+ */
+attn_status_t attn_selftest_tree_stall(int key_tile, int what);
 
 /*
  * attn_selftest_delayed_copy -- test aid for the decode kernels' reads before

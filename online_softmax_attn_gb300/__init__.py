@@ -43,6 +43,7 @@ __all__ = [
     "attn_get_last_device_error",
     "attn_selftest_prefill_stall",
     "attn_selftest_shared_stall",
+    "attn_selftest_tree_stall",
     "attn_status_string",
     "library",
     "ATTN_MAX_SPLITS",
@@ -154,6 +155,8 @@ def library() -> ctypes.CDLL:
     lib.attn_selftest_prefill_stall.restype = I
     lib.attn_selftest_shared_stall.argtypes = [I, I]
     lib.attn_selftest_shared_stall.restype = I
+    lib.attn_selftest_tree_stall.argtypes = [I, I]
+    lib.attn_selftest_tree_stall.restype = I
     lib.attn_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_uint)]
     lib.attn_get_device_error.restype = I
     lib.attn_get_last_device_error.argtypes = [P]
@@ -811,6 +814,13 @@ def attn_selftest_shared_stall(key_tile: int, what: int = 0) -> None:
     out K (what 0), V (1) or V's second load (2) of the key_tile-th key tile of
     the prefix that they visit. Raises AttnError (UNSUPPORTED) on a release build."""
     _check("attn_selftest_shared_stall", library().attn_selftest_shared_stall(int(key_tile), int(what)))
+
+
+def attn_selftest_tree_stall(key_tile: int, what: int = 0) -> None:
+    """Debug builds only: make every CTA of the next attn_decode_paged_tree calls
+    leave out the K (what 0) or V (1) load of its key_tile-th key tile (key_tile <
+    0: off). Raises AttnError (UNSUPPORTED) on a release build."""
+    _check("attn_selftest_tree_stall", library().attn_selftest_tree_stall(int(key_tile), int(what)))
 
 
 def attn_get_device_error(stream=None) -> int:

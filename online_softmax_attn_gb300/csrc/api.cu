@@ -825,6 +825,13 @@ attn_status_t attn_selftest_shared_stall(int key_tile, int what) {
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+attn_status_t attn_selftest_tree_stall(int key_tile, int what) {
+  if (what < 0 || what > 1) return ATTN_ERR_INVALID_ARG;
+  const cudaError_t e = attn::tree_set_stall(key_tile < 0 ? -1 : key_tile, what);
+  if (e == cudaErrorNotSupported) return ATTN_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 attn_status_t attn_selftest_delayed_copy(int32_t* dst, const int32_t* src, int n,
                                          unsigned int delay_us, void* stream) {
   if (n < 0 || delay_us > 1000 || (n > 0 && (!dst || !src)) || !aligned(dst, 4) ||

@@ -45,6 +45,11 @@
 namespace attn {
 
 static __device__ unsigned int g_tree_err;
+#ifdef ATTN_DEBUG
+// The key tile, in each CTA's own order, and which of its loads is not requested
+// (attn_selftest_tree_stall): 0 K, 1 V.
+static __device__ int g_tree_stall[2] = {-1, 0};
+#endif
 
 namespace {
 
@@ -453,6 +458,11 @@ __global__ void __launch_bounds__(384, 1)
       const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
       int g = 0;
       bool ok = true;
+#ifdef ATTN_DEBUG
+      const int stall = g_tree_stall[1] == (is_k ? 0 : 1) ? g_tree_stall[0] : -1;
+#else
+      constexpr int stall = -1;
+#endif
       for (int it = 0; ok && open(it); ++it) {
         const TreeSeg s = segs[it & 1];
         close(it);
@@ -471,14 +481,15 @@ __global__ void __launch_bounds__(384, 1)
             ok = false;
             break;
           }
-          load_tile(ring + st * C::TILE, map, bar(full + st), s.kvh, ent, (j & 3) * 8, page0, n_pages);
+          if (g != stall)
+            load_tile(ring + st * C::TILE, map, bar(full + st), s.kvh, ent, (j & 3) * 8, page0, n_pages);
         }
       }
       if (*abort_flag) {
         // Drain: the newest load of each stage is the only one that can still be in
         // flight. Bounded waits, error already recorded.
         for (int i = max(0, g - ns); i < g; ++i)
-          (void)mbar_wait(bar(full + i % ns), (i / ns) & 1, &g_tree_err);
+          if (i != stall) (void)mbar_wait(bar(full + i % ns), (i / ns) & 1, &g_tree_err);
       }
     } else if (warp == C::Q_WARP) {
       // The run's segments, and query tile q (counted over them) in slot q & 1.
@@ -961,6 +972,17 @@ cudaError_t launch_d(const TreeDecode& t, cudaStream_t stream) {
 
 cudaError_t launch_decode_tree(const TreeDecode& t, cudaStream_t stream) {
   return t.d_h == 128 ? launch_d<128>(t, stream) : launch_d<64>(t, stream);
+}
+
+cudaError_t tree_set_stall(int key_tile, int what) {
+#ifdef ATTN_DEBUG
+  const int v[2] = {key_tile, what};
+  return cudaMemcpyToSymbol(g_tree_stall, v, sizeof(v));
+#else
+  (void)key_tile;
+  (void)what;
+  return cudaErrorNotSupported;
+#endif
 }
 
 unsigned int tree_read_and_clear_error(cudaStream_t stream, cudaError_t* st) {

@@ -230,6 +230,9 @@ struct TreeDecode {
   float* lse;
 };
 cudaError_t launch_decode_tree(const TreeDecode& t, cudaStream_t stream);  // and its merge
+// Debug builds: the load (0 K, 1 V) of the key tile that each CTA does not request (-1:
+// none); cudaErrorNotSupported in release builds.
+cudaError_t tree_set_stall(int key_tile, int what);
 unsigned int tree_read_and_clear_error(cudaStream_t stream, cudaError_t* st);
 
 // prefill_simt.cu ----------------------------------------------------------

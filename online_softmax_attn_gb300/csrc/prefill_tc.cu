@@ -653,6 +653,11 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       int k_issued = 0, v_issued = 0, q_issued = 0, g0 = 0, it = 0;
       int stage_waited = 0, gl_even = 0, gl_odd = 0;  // as below
       bool ok = true;
+#ifdef ATTN_DEBUG
+      const int stall = g_prefill_stall_tile;
+#else
+      constexpr int stall = -1;
+#endif
       for (; ok; ++it) {
         if (!wait(win_full(it), (it >> 2) & 1)) break;
         const Work w = win_slot[it & 3];
@@ -684,9 +689,9 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
             break;
           }
           const int phys = __shfl_sync(0xffffffffu, ent, (j & 3) * 8 + (lane & 7));
-          if (lane == 0) mbar_arrive_expect_tx(bars.k_full(sk), C::KTILE);
+          if (lane == 0 && g != stall) mbar_arrive_expect_tx(bars.k_full(sk), C::KTILE);
           __syncwarp();
-          if (lane < 8 * C::SUBS)
+          if (lane < 8 * C::SUBS && g != stall)
             tma_load_4d(sbase + C::K_OFF + sk * C::KTILE + (lane >> 3) * C::SUB_BYTES + (lane & 7) * 16 * 128,
                         &tmap_k, bars.k_full(sk), (lane >> 3) * 64, w.kvh, 0, phys);
           __syncwarp();
@@ -730,7 +735,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       if (*abort_flag) {  // drain, as below
         if (q_issued > 0) (void)mbar_wait(bars.q_full(), (q_issued - 1) & 1, &g_prefill_err);
         for (int g = max(0, k_issued - NSK); g < k_issued; ++g)
-          (void)mbar_wait(bars.k_full(g % NSK), (g / NSK) & 1, &g_prefill_err);
+          if (g != stall) (void)mbar_wait(bars.k_full(g % NSK), (g / NSK) & 1, &g_prefill_err);
         for (int g = max(0, v_issued - NSV); g < v_issued; ++g)
           (void)mbar_wait(bars.v_full(g % NSV), (g / NSV) & 1, &g_prefill_err);
       }
