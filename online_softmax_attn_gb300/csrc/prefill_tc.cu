@@ -399,27 +399,34 @@ __device__ __noinline__ bool clean_wide_v(uint32_t base, int row) {
   }
   return found;
 }
-// Dims that are non-finite in the values of a flagged tile (bf16 at v, `step` bf16
-// numbers from key to key) that a query sees: bits of window_bits. Rare.
+// Windows: the non-finite values that clean_wide_v took out of an item's V tiles, in the
+// output row of query q (of its row), staged in shared memory at `staged` with its
+// 16-byte chunks at chunk ^ (lane mod 8): NaN in each column where a flagged tile (bf16
+// in the copy) holds one at a key that the query sees. Rare.
 template <int D>
-__device__ __noinline__ uint4 poisoned_dims(const __nv_bfloat16* v, size_t step, int lo, int hi, int sinks) {
-  uint32_t out[4] = {0u, 0u, 0u, 0u};
+__device__ __noinline__ void poison_row(const Work& w, const int* tile_wide, const __nv_bfloat16* v_copy,
+                                        int h_kv, int max_tiles, int window, int sinks, int q,
+                                        uint8_t* staged) {
+  const int end = q < w.q_len ? w.ctx - w.q_len + q + 1 : 0, lo = max(end - window, 0);
 #pragma unroll 1
-  for (int j = 0; j < kBN; ++j) {
-    if (!(window_bits(j, lo, hi, sinks) & 1u)) continue;
-    const uint4* x = reinterpret_cast<const uint4*>(v + j * step);
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 y = __ldcg(x + c);
-      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if ((w[k] & 0x7f80u) == 0x7f80u) out[c >> 2] |= 1u << ((c & 3) * 8 + 2 * k);
-        if ((w[k] & 0x7f800000u) == 0x7f800000u) out[c >> 2] |= 2u << ((c & 3) * 8 + 2 * k);
+  for (int j = 0; j < w.nkv; ++j) {
+    const int jt = j >= w.sink_tiles ? j + w.skip : j, k0 = jt * kBN;
+    if (tile_wide != nullptr && __ldcg(tile_wide + jt) == 0) continue;
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(
+        v_copy + ((size_t(w.pb) * max_tiles * kBN + k0) * h_kv + w.kvh) * D);
+#pragma unroll 1
+    for (int i = 0; i < kBN; ++i, v += size_t(h_kv) * D / 2) {
+      const int key = k0 + i;
+      if (key >= end || (key < lo && key >= sinks)) continue;
+#pragma unroll 1
+      for (int c = 0; c < D / 2; ++c) {
+        const uint32_t x = __ldcg(v + c);
+        uint16_t* at = reinterpret_cast<uint16_t*>(staged + (((c >> 2) ^ (threadIdx.x & 7)) << 4)) + 2 * (c & 3);
+        if ((x & 0x7f80u) == 0x7f80u) at[0] = 0x7fc0u;
+        if ((x & 0x7f800000u) == 0x7f800000u) at[1] = 0x7fc0u;
       }
     }
   }
-  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // PAGED: variable-length rows over a paged cache. PCOPY (paged only): V is
@@ -546,8 +553,11 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
                   : vwide + (PAGED ? (size_t(w.pb) * h_kv + w.kvh) * pa.max_tiles
                                    : size_t(w.kvh) * w.n_kv_all);
   };
+  // Windows: this kernel may be resident while the V pass writes the flags, so not by
+  // the non-coherent path.
+  auto flag = [](const int* p) { return WIN ? __ldcg(p) : __ldg(p); };
   auto is_wide = [&](const int* tile_wide, int j) {
-    return tile_wide ? (__ldg(tile_wide + j) != 0) : true;
+    return tile_wide ? (flag(tile_wide + j) != 0) : true;
   };
   // The flags of key tiles j0 .. j0 + 31 (below n) as one bit each, for a
   // whole warp: one load per lane every 32 tiles instead of a load on every
@@ -555,7 +565,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
   auto wide_bits = [&](const int* tile_wide, int j0, int n, const Work& w) -> uint32_t {
     if (!tile_wide) return 0xffffffffu;
     const int jj = j0 + (threadIdx.x & 31);
-    return __ballot_sync(0xffffffffu, jj < n && __ldg(tile_wide + (WIN ? tile_at(w, jj) : jj)) != 0);
+    return __ballot_sync(0xffffffffu, jj < n && flag(tile_wide + (WIN ? tile_at(w, jj) : jj)) != 0);
   };
   // Whether any of key tiles 0 .. n-1 is wide. Warp-collective.
   auto item_has_wide = [&](const int* tile_wide, int n, const Work& w) -> bool {
@@ -1307,20 +1317,6 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       const int hq = w.hq0 + t;
       const int out_row = WIN ? w.qb * kBM + r : row;
       const bool out_valid = WIN ? out_row < w.q_len : row_valid;
-      uint4 bad = make_uint4(0u, 0u, 0u, 0u);  // windows: columns of non-finite values in sight
-      if constexpr (WIN) {
-        if (*reinterpret_cast<volatile int*>(tail_info + (it & 1)) == it + 1)
-          for (int j = 0; j < nkv; ++j) {
-            const int jt = tile_at(w, j), k0 = jt * kBN;
-            const int end = out_valid ? w.ctx - w.q_len + out_row + 1 : 0;
-            if (!is_wide(tile_wide, jt)) continue;
-            const size_t tok = size_t(w.pb) * pa.max_tiles * kBN + k0;
-            const uint4 x = poisoned_dims<D>(pa.v_copy + (tok * h_kv + w.kvh) * D, size_t(h_kv) * D,
-                                             max(end - pa.window, 0) - k0, min(end - k0, kBN),
-                                             pa.sinks - k0);
-            bad = make_uint4(bad.x | x.x, bad.y | x.y, bad.z | x.z, bad.w | x.w);
-          }
-      }
       const size_t orow_idx =
           PAGED ? size_t(w.q_tok0 + out_row) * h + hq : size_t(hq) * T + out_row;
       // Output rows (debug checks): h * T, or h per packed query token.
@@ -1360,13 +1356,6 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         uint32_t ov[32];
         tc::ld32(tO + c * 32, ov);
         tc::wait_ld();
-        if constexpr (WIN) {
-          const uint32_t nan = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
-          if (nan != 0u)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((nan >> i) & 1u) ov[i] = 0x7fc00000u;
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint4 pk;
@@ -1377,6 +1366,11 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
           const int ch = c * 4 + i;
           *reinterpret_cast<uint4*>(stage + lane * RB + ((ch ^ (lane & 7)) << 4)) = pk;
         }
+      }
+      if constexpr (WIN) {
+        if (*reinterpret_cast<volatile int*>(tail_info + (it & 1)) == it + 1)
+          poison_row<D>(w, tile_wide, pa.v_copy, h_kv, pa.max_tiles, pa.window, pa.sinks, out_row,
+                        stage + lane * RB);
       }
       __syncwarp();
       {
