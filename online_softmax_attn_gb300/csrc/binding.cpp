@@ -1,6 +1,7 @@
 // binding.cpp -- the Python binding of the calls whose host time matters: the
-// 8-bit cache's write and read, its decode, and the decodes with a window, a shared
-// prefix or a tree of drafts, and the prefill with a window, run in a few microseconds on small inputs, as long as ctypes and checks written in
+// 8-bit cache's write and read, its decode, the decodes with a window, a shared prefix
+// or a tree of drafts, and the prefill with a window run in a few microseconds on
+// small inputs, as long as ctypes and checks written in
 // Python take (of 10.2 us a call for the write of one token, 6.3 were checks and
 // argument conversion). Each function checks its tensors, as the other
 // entry points of the package do in Python, and calls the C entry point of the

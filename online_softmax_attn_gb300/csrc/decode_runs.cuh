@@ -52,6 +52,12 @@
 // on behind it), which the merge kernel joins in run order. (Splitting a unit over all warps of a CTA and joining at every unit's
 // end instead took 57 us for 64 rows of up to 1000 keys, 131 MB: rows of a few
 // pages cost a CTA as much as rows of hundreds.)
+//
+// Windows are bound by the visible pages' bytes in the same way: 66 rows of up to
+// 16384 keys, window 4096 and 4 sinks, 32 query heads over 8 of 128, take 153 us of the
+// bf16 cache, 0.94 of the copy rate; 200 rows of the 8-bit cache, window 2001 and 18
+// sinks, 136 us, 0.85 (a unit is 128 pages, and has its query and its output). Masking
+// only the pages at a part's ends: 158 -> 154 us.
 #pragma once
 
 #include "common.cuh"

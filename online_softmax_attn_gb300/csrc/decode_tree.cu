@@ -38,6 +38,14 @@
 // is not 0, non-finite numbers among the drafts' values are taken out of the V tile
 // and put back as NaN, at the end, in the rows that see them. Only tiles that hold
 // drafts are looked at for that, and for slots past the row's end.
+//
+// Measured (GB300): 64 rows of up to 16384 keys and 24 drafts, 32 query heads over 8
+// of 128: 341 us, the keys' bytes at 0.95 of the copy rate. One row of 32768 keys and
+// 26 drafts: 38.2 us, 20 of them the bytes; the others are the launch, the CTA's
+// set-up, the first keys' way and the merge. 24 rows of up to 8192 keys, 61 drafts, 8
+// heads over one of 64 (two row tiles, 4 blocks of rows): 32 us, where the two
+// streams' chain S, weights, P V takes 1.2 us a key tile. One row of 500 keys and 8
+// drafts: 11.8 us, latency.
 #include "decode_runs.cuh"
 #include "pdl.cuh"
 #include "tc.cuh"
@@ -54,7 +62,10 @@ static __device__ int g_tree_stall[2] = {-1, 0};
 namespace {
 
 constexpr int kBM = 128, kBN = 128;
-constexpr int kTreeUnit = 3;  // a unit's weight beside its key tiles: query, states, output
+// A unit's weight beside its key tiles: query, states, output. (64 rows of up to 16384
+// keys: 341 us with 2 to 4, 343 with 6; 24 rows, two row tiles: 32 with 2 and 3, 34 with
+// 4 and 6.)
+constexpr int kTreeUnit = 3;
 // A row's reference moves, to the largest score so far, when one passes it by more
 // than this (log2 units).
 constexpr float kRise = 8.0f;
@@ -859,7 +870,9 @@ __global__ void __launch_bounds__(384, 1)
 
 // Joins the partial states of the unit that begins in attention CTA blockIdx.x and
 // goes on behind it, in run order. A CTA takes 8 of its query rows, a thread 4 dims
-// of one over all parts, kMergeUnroll of them in flight.
+// of one over all parts, kMergeUnroll of them in flight. (One row of 32768 keys, all
+// in all: 38.2 us; with 4 rows a CTA 39.6, with 16 39.9, with 20 parts in flight 40.5,
+// with the parts over four groups of threads 42.7.)
 constexpr int kMergeRows = 8, kMergeUnroll = 8;
 template <int D>
 __global__ void __launch_bounds__(kMergeRows* D / 4)
