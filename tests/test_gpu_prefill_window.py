@@ -267,6 +267,24 @@ def test_captured_and_replayed_with_new_rows():
     assert attn.attn_get_device_error() == 0
 
 
+def test_inputs_rewritten_just_before():
+    """The kernel in front lets the call start at once and rewrites one of q, the
+    caches, table, offsets and lengths 50 us later."""
+    c = Case([300, 0, 33], [40, 200, 3], 2, 4, 128, seed=22, window=150, sinks=4)
+    O, L = c.reference()
+    dev = c.args()
+    words = lambda t: t.reshape(-1).view(torch.int32)
+    for i in range(6):
+        old = torch.zeros_like(dev[i])
+        now = dev[:i] + [old] + dev[i + 1:]
+        attn.attn_prefill_paged_window(*now, 150, 4, c.max_q)  # warm: lines of the old contents
+        attn.attn_selftest_delayed_copy(words(old), words(dev[i]), delay_us=50)
+        o, lse = attn.attn_prefill_paged_window(*now, 150, 4, c.max_q)
+        check_out(o, O, torch.bfloat16)
+        check_lse(lse, L)
+    attn.attn_get_device_error()  # (the warm calls' rows may be shorter than their queries)
+
+
 def test_two_streams_at_once():
     a, b = Case([3000], [500], 2, 4, 128, 16, 1000, 4), Case([30] * 20, [40] * 20, 2, 4, 128, 17, 33, 1)
     want = [a.run(), b.run()]
