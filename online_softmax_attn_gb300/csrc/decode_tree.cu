@@ -45,7 +45,7 @@
 // set-up, the first keys' way and the merge. 24 rows of up to 8192 keys, 61 drafts, 8
 // heads over one of 64 (two row tiles, 4 blocks of rows): 32 us, where the two
 // streams' chain S, weights, P V takes 1.2 us a key tile. One row of 500 keys and 8
-// drafts: 11.8 us, latency.
+// drafts: 11.1 us, latency.
 #include "decode_runs.cuh"
 #include "pdl.cuh"
 #include "tc.cuh"
@@ -74,10 +74,10 @@ constexpr float kRise = 8.0f;
 struct TreeRow {
   int n, len, tok0, nt, n_rb;
 };
-// Where the CTA's run starts, and the warps' sums of the rows' weights.
+// Where the CTA's run starts, a run's weight, and the warps' sums of the rows' weights.
 struct TreePlan {
   long long sum[12];
-  long long off;
+  long long off, per;
   int b;
   TreeRow row;
 };
@@ -210,8 +210,13 @@ struct TreeWalk {
   int b, u;            // row, unit within it
   TreeRow r;
   TreeRaw ahead;       // row b + 1
+  TreeRaw held;        // few rows (B <= 32): that of row `lane`
   __device__ __forceinline__ void look_ahead(const TreeRows& a) {
-    ahead = b + 1 < a.B ? tree_raw(a, b + 1) : TreeRaw{0, 0, 0};
+    if (a.B <= 32)
+      ahead = TreeRaw{__shfl_sync(0xffffffffu, held.begin, b + 1), __shfl_sync(0xffffffffu, held.end, b + 1),
+                      __shfl_sync(0xffffffffu, held.len, b + 1)};
+    else
+      ahead = b + 1 < a.B ? tree_raw(a, b + 1) : TreeRaw{0, 0, 0};
   }
   __device__ __forceinline__ bool next(const TreeRows& a, TreeSeg& s) {
     while (rem > 0) {
@@ -343,6 +348,16 @@ __device__ __noinline__ uint4 poisoned_dims(const __nv_bfloat16* vc, const TreeR
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// Inclusive sums over the warp.
+__device__ __forceinline__ long long warp_sums(long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 template <int D>
 __global__ void __launch_bounds__(384, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -383,49 +398,49 @@ __global__ void __launch_bounds__(384, 1)
   }
   if (warp == C::MMA_WARP) tc::alloc(smem_u32(tmem_slot), 512);
   tc::fence_before();
-  pdl_wait();  // q, lengths, tables, masks and pages are earlier kernels' output
-
-  // ---- the runs: prefix sums of the rows' weights ----
-  const int per_t = (a.B + C::THREADS - 1) / C::THREADS;
-  const int b0 = min(tid * per_t, a.B), b1 = min(b0 + per_t, a.B);
-  long long sum = 0;
-  TreeRow mine{0, 0, 0, 0, 0};
-  for (int b = b0; b < b1; ++b) {
-    mine = tree_row(a, tree_raw(a, b), cta == 0);
-    sum += tree_weight(a, mine);
-  }
-  long long incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) plan.sum[warp] = incl;
-  __syncthreads();
-  long long at = incl - sum, all = 0;
-#pragma unroll
-  for (int w = 0; w < 12; ++w) {
-    if (w < warp) at += plan.sum[w];
-    all += plan.sum[w];
-  }
-  const long long per = max(1ll, div_ll(all + gridDim.x - 1, gridDim.x));
-  const long long p0 = per * cta;
-  if (p0 >= at && p0 < at + sum) {
-    for (int b = b0; b < b1; ++b) {
-      if (per_t > 1) mine = tree_row(a, tree_raw(a, b), false);
-      const long long w = tree_weight(a, mine);
-      if (p0 >= at && p0 < at + w) {
-        plan.b = b;
-        plan.off = p0 - at;
-        plan.row = mine;
-      }
-      at += w;
-    }
-  }
-  if (tid == 0) out.cut[cta].parts = 0;
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // q, lengths, tables, masks and pages are earlier kernels' output
+
+  // ---- the runs: prefix sums of the rows' weights. Of at most 32 rows the Q warp, which
+  // alone walks them, has one a lane and plans for itself (one row of 500 keys 11.8 -> 11.1
+  // us, 24 rows 34.1 -> 32.8) ----
+  long long per = 0, all = 0;  // the weight of a run and of all
+  if (a.B > 32) {
+    const int per_t = (a.B + C::THREADS - 1) / C::THREADS;
+    const int b0 = min(tid * per_t, a.B), b1 = min(b0 + per_t, a.B);
+    long long sum = 0;
+    TreeRow mine{0, 0, 0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+      mine = tree_row(a, tree_raw(a, b), cta == 0);
+      sum += tree_weight(a, mine);
+    }
+    const long long incl = warp_sums(sum, lane);
+    if (lane == 31) plan.sum[warp] = incl;
+    __syncthreads();
+    long long at = incl - sum;
+#pragma unroll
+    for (int w = 0; w < 12; ++w) {
+      if (w < warp) at += plan.sum[w];
+      all += plan.sum[w];
+    }
+    per = max(1ll, div_ll(all + gridDim.x - 1, gridDim.x));
+    const long long p0 = per * cta;
+    if (p0 >= at && p0 < at + sum) {
+      for (int b = b0; b < b1; ++b) {
+        if (per_t > 1) mine = tree_row(a, tree_raw(a, b), false);
+        const long long w = tree_weight(a, mine);
+        if (p0 >= at && p0 < at + w) {
+          plan.b = b;
+          plan.off = p0 - at;
+          plan.row = mine;
+        }
+        at += w;
+      }
+    }
+    __syncthreads();
+  }
   // Steps e = 0, 1, ... of a segment alternate between the streams (stream e & 1), which
   // share its key tiles, or have them in turn.
   auto n_of = [](int nt, bool two, int t) { return two ? nt : (nt + 1 - t) >> 1; };
@@ -505,18 +520,39 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == C::Q_WARP) {
       // The run's segments, and query tile q (counted over them) in slot q & 1.
       TreeWalk walk;
-      walk.rem = p0 < all ? min(per, all - p0) : 0;
       walk.off = 0;
       walk.b = walk.u = 0;
       walk.r = TreeRow{0, 0, 0, 0, 0};
-      walk.ahead = TreeRaw{0, 0, 0};
-      if (walk.rem > 0) {
+      walk.ahead = walk.held = TreeRaw{0, 0, 0};
+      if (lane == 0) out.cut[cta].parts = 0;
+      long long off = 0;  // the run's start within its first row
+      if (a.B <= 32) {
+        if (lane < a.B) walk.held = tree_raw(a, lane);
+        TreeRow mine{0, 0, 0, 0, 0};
+        if (lane < a.B) mine = tree_row(a, walk.held, cta == 0);
+        const long long w = tree_weight(a, mine), incl = warp_sums(w, lane);
+        all = __shfl_sync(0xffffffffu, incl, 31);
+        per = max(1ll, div_ll(all + gridDim.x - 1, gridDim.x));
+        const long long p0 = per * cta;
+        if (p0 >= incl - w && p0 < incl) {
+          plan.b = lane;
+          plan.off = p0 - (incl - w);
+          plan.row = mine;
+        }
+        __syncwarp();
+      }
+      if (per * cta < all) {
         walk.b = plan.b;
         walk.r = plan.row;
+        off = plan.off;
+      }
+      if (lane == 0) plan.per = per;
+      walk.rem = per * cta < all ? min(per, all - per * cta) : 0;
+      if (walk.rem > 0) {
         walk.look_ahead(a);
         const long long wu = walk.r.nt + kTreeUnit;
-        walk.u = static_cast<int>(div_ll(plan.off, wu));
-        walk.off = plan.off - walk.u * wu;
+        walk.u = static_cast<int>(div_ll(off, wu));
+        walk.off = off - walk.u * wu;
       }
       int q = 0;
       bool ok = true;
@@ -852,7 +888,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (tid == 0 && s.begins && s.left > 0)
-        out.cut[cta] = TreeCut{static_cast<int>(1 + div_ll(s.left + per - 1, per)), s.tok0 + s.first,
+        out.cut[cta] = TreeCut{static_cast<int>(1 + div_ll(s.left + plan.per - 1, plan.per)), s.tok0 + s.first,
                                min(2 * a.tpt, s.n - s.first), s.kvh};
       close(it);
       // O is read out before the next segment's first P V, which waits for this

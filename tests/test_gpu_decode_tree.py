@@ -133,6 +133,16 @@ def test_batches_cut_over_the_gpu(B, old, draft, h_kv, d):
     assert torch.equal(o, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("B", [31, 32, 33])
+def test_rows_around_a_warps_lanes(B):
+    """At most 32 rows are planned by one warp, a row a lane."""
+    g = torch.Generator().manual_seed(B)
+    olds = torch.randint(0, 900, (B,), generator=g).tolist()
+    news = torch.randint(0, 12, (B,), generator=g).tolist()
+    news[-1], olds[-1] = 9, 700
+    Case(olds, news, 2, 4, 128, seed=B).check()
+
+
 def test_many_rows():
     """More rows than a CTA has threads; most without a draft."""
     B = 1000
