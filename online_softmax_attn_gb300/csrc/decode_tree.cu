@@ -41,11 +41,11 @@
 //
 // Measured (GB300): 64 rows of up to 16384 keys and 24 drafts, 32 query heads over 8
 // of 128: 341 us, the keys' bytes at 0.95 of the copy rate. One row of 32768 keys and
-// 26 drafts: 38.2 us, 20 of them the bytes; the others are the launch, the CTA's
+// 26 drafts: 35.9 us, 20 of them the bytes; the others are the launch, the CTA's
 // set-up, the first keys' way and the merge. 24 rows of up to 8192 keys, 61 drafts, 8
-// heads over one of 64 (two row tiles, 4 blocks of rows): 32 us, where the two
-// streams' chain S, weights, P V takes 1.2 us a key tile. One row of 500 keys and 8
-// drafts: 11.1 us, latency.
+// heads over one of 64 (two row tiles each): 31 us, where the two streams' chain S,
+// weights, P V takes 2.1 us a key tile. One row of 500 keys and 8 drafts: 11.0 us,
+// latency.
 #include "decode_runs.cuh"
 #include "pdl.cuh"
 #include "tc.cuh"
@@ -904,73 +904,115 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == C::MMA_WARP) tc::dealloc(tmem, 512);
 }
 
-// Joins the partial states of the unit that begins in attention CTA blockIdx.x and
-// goes on behind it, in run order. A CTA takes 8 of its query rows, a thread 4 dims
-// of one over all parts, kMergeUnroll of them in flight. (One row of 32768 keys, all
-// in all: 38.2 us; with 4 rows a CTA 39.6, with 16 39.9, with 20 parts in flight 40.5,
-// with the parts over four groups of threads 42.7.)
-constexpr int kMergeRows = 8, kMergeUnroll = 8;
+// Joins the partial states of each unit that begins in an attention CTA and goes on
+// behind it, in run order. An item is kMergeThreads / (D / 4) query rows of a cut unit,
+// a thread 4 dims of one over all parts, kMergeUnroll of them in flight. One CTA per
+// attention CTA: it looks at all cuts, and its groups take their share of the items. One
+// row of 32768 keys takes 35.9 us all in all, 24 rows with two row tiles 32.2; with a CTA
+// per cut and 8 rows, most of them without work, 38.0 and 34.0; with 8 parts in flight
+// 36.5 and 31.9, with 20 38.1 and 32.1; with two CTAs 2 us more (what the looks at the
+// cuts cost: all read the same lines; a look per warp 5 us more).
+constexpr int kMergeThreads = 128, kMergeGroups = 4, kMergeUnroll = 10;
 template <int D>
-__global__ void __launch_bounds__(kMergeRows* D / 4)
+__global__ void __launch_bounds__(kMergeThreads* kMergeGroups)
     tree_merge_kernel(const TreeOut out, int h, int g, int tpt, int total_q) {
-  constexpr int U = kMergeUnroll;
+  constexpr int U = kMergeUnroll, R = kMergeThreads / (D / 4);
+  constexpr int PER = kRunsMaxCtas / 32;  // cuts a lane: lane + 32 k
+  static_assert(kRunsMaxCtas % 32 == 0, "a warp looks at the cuts");
+  __shared__ TreeCut cuts[kRunsMaxCtas];  // [lane][k], and the items up to each one's end
+  __shared__ int ends[kRunsMaxCtas];
   pdl_wait();
   pdl_trigger();
-  const TreeCut* cut = out.cut + blockIdx.x;
-  const int parts = __ldcg(&cut->parts);
-  if (parts == 0) return;
-  const int tok = __ldcg(&cut->tok), n_tok = __ldcg(&cut->n_tok), kvh = __ldcg(&cut->kvh);
-  const int c = threadIdx.x / kMergeRows, r = blockIdx.y * kMergeRows + threadIdx.x % kMergeRows;
-  if (r >= n_tok * g) return;
-  const int tile = r / (tpt * g), in_tile = r % (tpt * g);
-  const size_t row = static_cast<size_t>(tok + r / g) * h + kvh * g + r % g;
-  if (!ATTN_GUARD(row < static_cast<size_t>(total_q) * h, &g_tree_err)) return;
-  float M = kNone, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = 0; base < parts; base += U) {
-    float m[U], l[U];
-    float4 x[U];
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    TreeCut mine[PER];
+    int sum = 0;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int j = base + i;
-      m[i] = kNone;
-      l[i] = 0.f;
-      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j < parts) {
-        const int slot = 2 * (static_cast<int>(blockIdx.x) + j) + (j == 0 ? 1 : 0);
-        ATTN_DCHECK(slot < 2 * kRunsMaxCtas, &g_tree_err);
-        const size_t pt = static_cast<size_t>(slot) * 2 + tile;
-        m[i] = __ldcg(out.m_part + pt * kBM + in_tile);
-        l[i] = __ldcg(out.l_part + pt * kBM + in_tile);
-        x[i] = __ldcg(reinterpret_cast<const float4*>(out.o_part + pt * (kBM * D)) + c * kBM + in_tile);
+    for (int k = 0; k < PER; ++k) {
+      const int i = lane + 32 * k;
+      int4 x = make_int4(0, 0, 0, 0);
+      if (i < static_cast<int>(gridDim.x)) x = __ldcg(reinterpret_cast<const int4*>(out.cut) + i);
+      mine[k] = TreeCut{x.x, x.y, x.z, x.w};
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      sum += mine[k].parts > 0 ? (mine[k].n_tok * g + R - 1) / R : 0;
+      cuts[lane * PER + k] = mine[k];
+      ends[lane * PER + k] = sum;
+    }
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    before -= sum;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) ends[lane * PER + k] += before;
+  }
+  __syncthreads();
+  const int total = ends[kRunsMaxCtas - 1], lane = threadIdx.x & 31;
+  const int tid = threadIdx.x % kMergeThreads, group = threadIdx.x / kMergeThreads;
+  for (int item = blockIdx.x + gridDim.x * group; item < total; item += gridDim.x * kMergeGroups) {
+    int at = 0;  // the cut that the item is of
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      at += __popc(__ballot_sync(0xffffffffu, ends[lane * PER + k] <= item));
+    const int cta = at / PER + 32 * (at % PER), first = at > 0 ? ends[at - 1] : 0;
+    const TreeCut cut = cuts[at];
+    const int parts = cut.parts, tok = cut.tok, n_tok = cut.n_tok, kvh = cut.kvh;
+    const int c = tid / R, r = (item - first) * R + tid % R;
+    if (r >= n_tok * g) continue;
+    const int tile = r / (tpt * g), in_tile = r % (tpt * g);
+    const size_t row = static_cast<size_t>(tok + r / g) * h + kvh * g + r % g;
+    if (!ATTN_GUARD(row < static_cast<size_t>(total_q) * h, &g_tree_err)) continue;
+    float M = kNone, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = 0; base < parts; base += U) {
+      float m[U], l[U];
+      float4 x[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int j = base + i;
+        m[i] = kNone;
+        l[i] = 0.f;
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < parts) {
+          const int slot = 2 * (cta + j) + (j == 0 ? 1 : 0);
+          ATTN_DCHECK(slot < 2 * kRunsMaxCtas, &g_tree_err);
+          const size_t pt = static_cast<size_t>(slot) * 2 + tile;
+          m[i] = __ldcg(out.m_part + pt * kBM + in_tile);
+          l[i] = __ldcg(out.l_part + pt * kBM + in_tile);
+          x[i] = __ldcg(reinterpret_cast<const float4*>(out.o_part + pt * (kBM * D)) + c * kBM + in_tile);
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int i = 0; i < U; ++i) Mn = fmaxf(Mn, m[i]);
+      const float sc = ex2_approx(M - Mn);
+      M = Mn;
+      L *= sc;
+      acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const float w = ex2_approx(m[i] - Mn);
+        L = fmaf(w, l[i], L);
+        acc.x = fmaf(w, x[i].x, acc.x);
+        acc.y = fmaf(w, x[i].y, acc.y);
+        acc.z = fmaf(w, x[i].z, acc.z);
+        acc.w = fmaf(w, x[i].w, acc.w);
       }
     }
-    float Mn = M;
-#pragma unroll
-    for (int i = 0; i < U; ++i) Mn = fmaxf(Mn, m[i]);
-    const float sc = ex2_approx(M - Mn);
-    M = Mn;
-    L *= sc;
-    acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const float w = ex2_approx(m[i] - Mn);
-      L = fmaf(w, l[i], L);
-      acc.x = fmaf(w, x[i].x, acc.x);
-      acc.y = fmaf(w, x[i].y, acc.y);
-      acc.z = fmaf(w, x[i].z, acc.z);
-      acc.w = fmaf(w, x[i].w, acc.w);
+    const bool empty = L == 0.f;
+    const float inv = empty ? 0.f : 1.f / L;
+    uint2 y = make_uint2(0u, 0u);
+    if (!empty) {
+      y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+      y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
     }
+    *reinterpret_cast<uint2*>(out.o + row * D + c * 4) = y;
+    if (out.lse != nullptr && c == 0) out.lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
   }
-  const bool empty = L == 0.f;
-  const float inv = empty ? 0.f : 1.f / L;
-  uint2 y = make_uint2(0u, 0u);
-  if (!empty) {
-    y.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-    y.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-  }
-  *reinterpret_cast<uint2*>(out.o + row * D + c * 4) = y;
-  if (out.lse != nullptr && c == 0) out.lse[row] = empty ? -INFINITY : M * kLn2 + logf(L);
 }
 
 template <int D>
@@ -1012,9 +1054,8 @@ cudaError_t launch_d(const TreeDecode& t, cudaStream_t stream) {
   e = launch_pdl(kern, dim3(unsigned(grid)), dim3(C::THREADS), size_t(C::SMEM), stream, tq, tk, tv,
                  static_cast<const __nv_bfloat16*>(t.v_cache), a, out, t.scale * kLog2e);
   if (e != cudaSuccess) return e;
-  const int rows = (t.max_q_len < 2 * tpt ? t.max_q_len : 2 * tpt) * g;  // of a unit, at most
-  return launch_pdl(tree_merge_kernel<D>, dim3(unsigned(grid), unsigned((rows + kMergeRows - 1) / kMergeRows)),
-                    dim3(unsigned(kMergeRows * D / 4)), 0, stream, out, t.h, g, tpt, t.total_q);
+  return launch_pdl(tree_merge_kernel<D>, dim3(unsigned(grid)), dim3(kMergeThreads * kMergeGroups), 0, stream, out,
+                    t.h, g, tpt, t.total_q);
 }
 
 }  // namespace
