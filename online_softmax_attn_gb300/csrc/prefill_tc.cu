@@ -324,6 +324,50 @@ __device__ __noinline__ float softmax_p_two_term(uint32_t tS, int lim, float sca
   return sa0 + sa1;
 }
 
+// Windows: below this magnitude of the reference the roundings of a product and of the
+// reference cannot take a weight past fp16's range.
+constexpr float kFar = 0x1p20f;
+
+// Windows: the weights of a tile that is no common case, to the S tile in tensor memory
+// that they are of: P_hi (upper 16 bits, columns 0-63) and P_lo = bf16(p - P_hi) (columns
+// 64-127) where V stays bf16 (`two`), else fp16 as in the common case. The scores enter as
+// rounded products minus the reference, which is exact near it at any magnitude of the
+// logits: with one fma the product's residual, half a step of the logit, moves the largest
+// weight, out of fp16's range from logits of 2^27 on. Returns the weights' sum. Out of
+// line, as softmax_p_two_term. Warp-collective.
+__device__ __noinline__ float rare_weights(uint32_t tS, float scale_log2, float bias, bool two) {
+  uint32_t sr[4][32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
+  tc::wait_ld();
+  float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t hi[32], lo[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int key = 64 * half + 2 * i;
+      const float x0 = __uint_as_float(sr[key >> 5][key & 31]);
+      const float x1 = __uint_as_float(sr[key >> 5][(key & 31) + 1]);
+      const float p0 = ex2_approx(__fsub_rn(__fmul_rn(x0, scale_log2), bias));
+      const float p1 = ex2_approx(__fsub_rn(__fmul_rn(x1, scale_log2), bias));
+      sum0 += p0;
+      sum1 += p1;
+      const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+      if (two) {
+        asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(hi[i]) : "r"(u0), "r"(u1));
+        lo[i] = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u), p1 - __uint_as_float(u1 & 0xffff0000u));
+      } else {
+        hi[i] = pack_f16x2(p0, p1);
+        lo[i] = 0u;
+      }
+    }
+    tc::st32(tS + 32 * half, hi);
+    if (two) tc::st32(tS + 64 + 32 * half, lo);
+  }
+  return sum0 + sum1;
+}
+
 // Windows: masks an S tile in tensor memory: -inf for the keys that the row does not
 // see (as window_bits, from the tile's first key on). Out of line, so that the softmax
 // loop holds neither its code nor its registers (with the selection in the loop every
@@ -366,8 +410,8 @@ __device__ __noinline__ float2 sink_weights(uint32_t tS, uint32_t bits, float sc
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), scale_log2, -bias));
-    const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), scale_log2, -bias));
+    const float p0 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(s[2 * i]), scale_log2), bias));
+    const float p1 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(s[2 * i + 1]), scale_log2), bias));
     sum += p0 + p1;
     s[i] = pack_f16x2(p0, p1);
   }
@@ -1121,6 +1165,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     float m_ref = -INFINITY;
     float l = 0.f;
     int j0 = 0;  // first tile of the loop below
+    bool far = false;  // windows: whether a reference of the warp is kFar or more
     if constexpr (WIN) {
       if (w.narrow && !(w.wide && is_wide(tile_wide, 0))) {
         if (!__all_sync(0xffffffffu, wait_or_abort(bars.s_full(t), g0 & 1, abort_flag))) break;
@@ -1128,6 +1173,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         const float2 x = sink_weights(tS, w.qb * kBM + r < w.q_len ? (2u << (pa.sinks - 1)) - 1u : 0u, scale_log2);
         m_ref = x.x;
         l = x.y;
+        far = __any_sync(0xffffffffu, m_ref != -INFINITY && fabsf(m_ref) >= kFar);
         tc::fence_before();
         mbar_arrive(bars.p_full(t));
         j0 = 1;
@@ -1236,7 +1282,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       const float mx = fmaxf(max3f(cm[0], cm[1], cm[2]), cm[3]);
       const float m_cand = mx * scale_log2;
       float alpha = 1.f;
-      if (m_cand > m_ref + kRescaleBits) {
+      if (m_cand - m_ref > kRescaleBits) {  // (the difference is exact, m_ref + 15 is not)
         const float m_new = m_cand + kRefHeadroom;
         alpha = ex2_approx(m_ref - m_new);  // 0 on the first tile
         l *= alpha;
@@ -1246,11 +1292,12 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       // after them) and is scaled by alpha before this tile's P V adds to it.
       // That happens after P is stored, in the registers S occupied, so that
       // the exponent loop carries no extra live state for it.
-      const bool rescale = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+      const bool moved = __any_sync(0xffffffffu, alpha != 1.f), rescale = j > 0 && moved;
       const float bias = (m_ref == -INFINITY) ? 0.f : m_ref;
       const uint64_t nb2 = f2(-bias, -bias);
       float psum;  // row sum of this tile's weights
-      if (!wide) {
+      if (WIN && moved) far = __any_sync(0xffffffffu, fabsf(bias) >= kFar);
+      if (!wide && !far) {
         uint64_t sumA = f2(0.f, 0.f), sumB = f2(0.f, 0.f);
         // P in fp16 (11 significant bits). Key pair (2i, 2i+1) of chunk c
         // goes to P column 16c + i, i.e. the first 64 columns of the S tile
@@ -1283,7 +1330,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         unf2(add2(sumA, sumB), sa0, sa1);
         psum = sa0 + sa1;
       } else {
-        psum = softmax_p_two_term(tS, lim, scale_log2, bias);
+        psum = WIN ? rare_weights(tS, scale_log2, bias, wide) : softmax_p_two_term(tS, lim, scale_log2, bias);
       }
       if (rescale) {
         // sr is free once P is stored (tcgen05.st reads its registers at
