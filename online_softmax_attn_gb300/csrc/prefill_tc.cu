@@ -236,10 +236,15 @@ struct Work {
   int n_kv_all;  // key tiles of the KV head (contiguous) or row (paged)
   int pb, q_tok0, q_len, ctx, n_pages;  // paged rows only
   // Windows: tiles before the gap, tiles in it, first key behind it. Tiles that some of
-  // the item's queries may not see all of: j < edge_lo or j >= edge_hi.
+  // the item's queries may not see all of: full() <= j < edge_lo or j >= edge_hi.
   int sink_tiles, skip, first, edge_lo, edge_hi;
   int wide;    // windows: whether any of its V tiles is flagged; -1: not looked at
   int narrow;  // windows: the first tile holds keys below kSinkKeys alone that are seen
+  // Tiles of sinks that all see: keys below the first query's end.
+  __device__ __forceinline__ int full(int sinks) const { return min(sinks, ctx - q_len + qb * kBM + 1) / kBN; }
+  __device__ __forceinline__ bool edge(int j, int sinks) const {
+    return (j >= full(sinks) && j < edge_lo) || j >= edge_hi;
+  }
 };
 // A tile of sinks alone has its S product and its weights for this many keys.
 constexpr int kSinkKeys = 32;
@@ -453,28 +458,45 @@ __device__ __noinline__ bool clean_wide_v(uint32_t base, int row) {
 // Windows: the non-finite values that clean_wide_v took out of an item's V tiles, in the
 // output row of query q (of its row), staged in shared memory at `staged` with its
 // 16-byte chunks at chunk ^ (lane mod 8): NaN in each column where a flagged tile (bf16
-// in the copy) holds one at a key that the query sees. Rare.
+// in the copy) that clean_wide_v looked at holds one at a key that the query sees. An
+// item has at most five such tiles, so this ends well within the other roles' waits
+// whatever the row's length: a key is 16 loads in turn, a tile 1 to 2 ms. Rare. (Loads in
+// eights, and `full` kept in the item: 139.7 us for 8192 tokens without any such value
+// instead of 136.7, code and data that push others out.)
 template <int D>
 __device__ __noinline__ void poison_row(const Work& w, const int* tile_wide, const __nv_bfloat16* v_copy,
                                         int h_kv, int max_tiles, int window, int sinks, int q,
                                         uint8_t* staged) {
   const int end = q < w.q_len ? w.ctx - w.q_len + q + 1 : 0, lo = max(end - window, 0);
 #pragma unroll 1
-  for (int j = 0; j < w.nkv; ++j) {
+  for (int j = w.full(sinks); j < w.nkv; ++j) {
+    if (!w.edge(j, sinks)) {  // (the first tile behind those that all see)
+      j = w.edge_hi - 1;
+      continue;
+    }
     const int jt = j >= w.sink_tiles ? j + w.skip : j, k0 = jt * kBN;
     if (tile_wide != nullptr && __ldcg(tile_wide + jt) == 0) continue;
-    const uint32_t* v = reinterpret_cast<const uint32_t*>(
+    const uint4* v = reinterpret_cast<const uint4*>(
         v_copy + ((size_t(w.pb) * max_tiles * kBN + k0) * h_kv + w.kvh) * D);
 #pragma unroll 1
-    for (int i = 0; i < kBN; ++i, v += size_t(h_kv) * D / 2) {
+    for (int i = 0; i < kBN; ++i, v += size_t(h_kv) * D / 8) {
       const int key = k0 + i;
       if (key >= end || (key < lo && key >= sinks)) continue;
 #pragma unroll 1
-      for (int c = 0; c < D / 2; ++c) {
-        const uint32_t x = __ldcg(v + c);
-        uint16_t* at = reinterpret_cast<uint16_t*>(staged + (((c >> 2) ^ (threadIdx.x & 7)) << 4)) + 2 * (c & 3);
-        if ((x & 0x7f80u) == 0x7f80u) at[0] = 0x7fc0u;
-        if ((x & 0x7f800000u) == 0x7f800000u) at[1] = 0x7fc0u;
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = __ldcg(v + c);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        uint32_t most;  // largest exponent fields, of either half
+        asm("max.u16x2 %0, %1, %2;" : "=r"(most) : "r"(u[0] & 0x7f807f80u), "r"(u[1] & 0x7f807f80u));
+        asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(u[2] & 0x7f807f80u));
+        asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(u[3] & 0x7f807f80u));
+        if ((most & 0xffffu) != 0x7f80u && (most >> 16) != 0x7f80u) continue;
+        uint16_t* at = reinterpret_cast<uint16_t*>(staged + ((c ^ (threadIdx.x & 7)) << 4));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((u[k] & 0x7f80u) == 0x7f80u) at[2 * k] = 0x7fc0u;
+          if ((u[k] & 0x7f800000u) == 0x7f800000u) at[2 * k + 1] = 0x7fc0u;
+        }
       }
     }
   }
@@ -563,7 +585,8 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       pw.sink_tiles = (min(pa.sinks, key_end) + kBN - 1) / kBN;
       pw.skip = max(pw.first / kBN - pw.sink_tiles, 0);
       pw.nkv -= pw.skip;
-      // All see the keys from the last query's first one up to the first query's last.
+      // All see the keys from the last query's first one, and the sinks, up to the first
+      // query's last.
       const int all_lo = max(key_end - pa.window, 0), all_hi = ctx - pw.q_len + pw.qb * kBM + 1;
       pw.edge_lo = all_lo == 0 ? 0 : (all_lo + kBN - 1) / kBN - pw.skip;
       pw.edge_hi = all_hi / kBN - pw.skip;
@@ -1227,7 +1250,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
         if (wide && t == 0) {
           // Keys that some query of the item does not see have weight 0 in its
           // P V, but 0 * NaN is NaN. (Unflagged tiles hold finite values.)
-          if (j < edge_lo || j >= edge_hi) {
+          if (w.edge(j, pa.sinks)) {
             const int sv = g % NSV;
             if (wait_or_abort(bars.v_full(sv), (g / NSV) & 1, abort_flag) &&
                 clean_wide_v<D>(sbase + C::V_OFF + sv * C::KTILE, r))
@@ -1238,6 +1261,8 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       }
       tc::fence_after();
       if constexpr (WIN) {
+        // (Tiles of sinks that all see are masked too, to no effect: with edge() here
+        // every tile pays for it, 140.4 instead of 137.9 us for 8192 tokens.)
         if (j < edge_lo || j >= edge_hi) {
           const int k0 = tile_at(w, j) * kBN;
           const int q = w.qb * kBM + r, end = q < w.q_len ? w.ctx - w.q_len + q + 1 : 0;

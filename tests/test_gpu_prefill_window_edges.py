@@ -88,3 +88,44 @@ def test_logits_that_rise_by_steps(exp):
         assert torch.isfinite(o).all() and o.abs().max() <= c.v.double().abs().max() * (1 + 2.0 ** -8), (exp, step)
         want = 2.0 ** exp * np.log(2.0)
         assert ((lse.double().cpu() - want).abs() <= want * 2.0 ** -20 + 130).all(), (exp, step)
+
+
+@pytest.mark.parametrize("window,sinks", [(700, 3), (2000, 0), (300, 400)])
+def test_infinities_that_every_query_of_a_tile_sees(window, sinks):
+    """An infinity in a tile that all of a block's queries see reaches them as an
+    infinity, also where another tile's NaN is put into their rows at the end."""
+    c = Case([1000], [128], 2, 4, 128, 23, window, sinks)
+    inside, edge = 640, 1050  # (tile 5 of each query's keys; the tile that ends them)
+    put(c, c.v, 0, inside, float("inf"), kv=1, e=7)
+    put(c, c.v, 0, edge, float("nan"), kv=1, e=9)
+    some = edge - 1000
+    put(c, c.v, 0, 1000, 3e5, kv=1, e=11)
+    o, lse = c.run()
+    o = o.float().cpu()[:, 4:]  # KV head 1
+    # (A weight whose second bf16 term is 0, one in 2^8, gives 0 * inf; no other NaN.)
+    assert (o[..., 7] == float("inf")).float().mean() > 0.9 and not torch.isfinite(o[..., 7]).any()
+    assert torch.isnan(o[some:, :, 9]).all() and torch.isfinite(o[:some, :, 9]).all()
+    keep = [e for e in range(128) if e not in (7, 9)]
+    assert torch.isfinite(o[..., keep]).all()
+    assert attn.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(60000, 0), (500, 40000)])
+def test_one_nan_among_many_flagged_tiles(window, sinks):
+    """Each V tile holds a value that fp16 does not, and one tile that some queries see in
+    part a NaN: looked for there alone, in far less than the waits' 2 s."""
+    c = Case([60000], [70], 1, 2, 128, 24, window, sinks)
+    c.v[:, ::5, :, 3] = 1e5
+    put(c, c.v, 0, 60030, float("nan"), e=5)
+    o, lse = c.run()
+    assert attn.attn_get_device_error() == 0
+    o = o.float().cpu()
+    assert torch.isnan(o[30:, :, 5]).all() and torch.isfinite(o[:30]).all()
+    assert torch.isfinite(o[30:][..., [e for e in range(128) if e != 5]]).all()
+    e0, e1 = torch.cuda.Event(True), torch.cuda.Event(True)
+    args = c.args()
+    e0.record()
+    attn.attn_prefill_paged_window(*args, c.window, c.sinks, c.max_q)
+    e1.record()
+    torch.cuda.synchronize()
+    assert e0.elapsed_time(e1) < 100
