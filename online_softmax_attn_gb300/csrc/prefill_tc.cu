@@ -83,6 +83,17 @@ constexpr float kRescaleBits = 15.0f;
 // most 2^-17 of the sum per key.
 constexpr float kRefHeadroom = 8.0f;
 
+// Windows: the fp16 copy holds V times kVScale, which is exact from 2^(-17 - 8) (8 bits
+// above fp16's smallest step, 2^-24) to below 2^(16 - 8), and at 0; a tile with a number
+// outside is flagged and keeps bf16, its two-term weights taking the factor instead. So
+// values enter exactly whatever their size. (N(0, 1) values: a tile in 2500 is flagged.
+// Without the factor one in 10 would be.) Flags are kVWide, and kVHuge for a tile with a
+// magnitude of 2^64 or more: an item with one keeps its weights at 2^-8 at most, so that
+// weight, factor and value stay within fp32.
+constexpr float kVScale = 256.0f;
+constexpr uint32_t kVLeast = (127 - 25) << 7, kVMost = (127 + 8) << 7, kV64 = (127 + 64) << 7;  // bf16 bits
+constexpr int kVWide = 1, kVHuge = 2;
+
 template <int D, int NQ, int NSK, int NSV>
 struct PfCfg {
   static constexpr int SUBS = D / 64;                // 64-element swizzle atoms along d_h
@@ -338,8 +349,9 @@ constexpr float kFar = 0x1p20f;
 // 64-127) where V stays bf16 (`two`), else fp16 as in the common case. The scores enter as
 // rounded products minus the reference, which is exact near it at any magnitude of the
 // logits: with one fma the product's residual, half a step of the logit, moves the largest
-// weight, out of fp16's range from logits of 2^27 on. Returns the weights' sum. Out of
-// line, as softmax_p_two_term. Warp-collective.
+// weight, out of fp16's range from logits of 2^27 on. Bf16 tiles have their weights times
+// kVScale; the sum that is returned has not. Out of line, as softmax_p_two_term.
+// Warp-collective.
 __device__ __noinline__ float rare_weights(uint32_t tS, float scale_log2, float bias, bool two) {
   uint32_t sr[4][32];
 #pragma unroll
@@ -358,10 +370,11 @@ __device__ __noinline__ float rare_weights(uint32_t tS, float scale_log2, float 
       const float p1 = ex2_approx(__fsub_rn(__fmul_rn(x1, scale_log2), bias));
       sum0 += p0;
       sum1 += p1;
-      const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
       if (two) {
+        const float y0 = p0 * kVScale, y1 = p1 * kVScale;
+        const uint32_t u0 = __float_as_uint(y0), u1 = __float_as_uint(y1);
         asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(hi[i]) : "r"(u0), "r"(u1));
-        lo[i] = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u), p1 - __uint_as_float(u1 & 0xffff0000u));
+        lo[i] = pack_bf16x2(y0 - __uint_as_float(u0 & 0xffff0000u), y1 - __uint_as_float(u1 & 0xffff0000u));
       } else {
         hi[i] = pack_f16x2(p0, p1);
         lo[i] = 0u;
@@ -426,6 +439,16 @@ __device__ __noinline__ float2 sink_weights(uint32_t tS, uint32_t bits, float sc
   tc::st16(tS, p);
   tc::wait_st();
   return make_float2(m, sum);
+}
+
+// Windows: whether an item with a flagged V tile has one with huge values. (Out of line:
+// with every role's look at the flags giving both answers 8192 tokens took 140.9 us
+// instead of 139.0.) Warp-collective.
+__device__ __noinline__ bool item_has_huge(const Work& w, const int* tile_wide) {
+  uint32_t any = 0;
+  for (int j = threadIdx.x & 31; j < w.nkv; j += 32)
+    any |= __ldcg(tile_wide + (j >= w.sink_tiles ? j + w.skip : j));
+  return __any_sync(0xffffffffu, any & kVHuge);
 }
 
 // Windows: a flagged V tile (bf16) at `base` that some query of the item sees only in
@@ -1207,6 +1230,10 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     auto tiles = [&](auto any_wide) {
     constexpr bool MAYBE_WIDE = decltype(any_wide)::value;
     uint32_t wbits = 0;
+    // How far above the reference a maximum may come: with huge values not above the
+    // largest so far, kRefHeadroom below the reference.
+    float rise = kRescaleBits;
+    if constexpr (WIN && MAYBE_WIDE) rise = item_has_huge(w, tile_wide) ? -kRefHeadroom : kRescaleBits;
     for (int j = j0; j < nkv; ++j) {
       const int g = g0 + j;
       // The format of P follows the format of this key tile's V.
@@ -1307,7 +1334,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       const float mx = fmaxf(max3f(cm[0], cm[1], cm[2]), cm[3]);
       const float m_cand = mx * scale_log2;
       float alpha = 1.f;
-      if (m_cand - m_ref > kRescaleBits) {  // (the difference is exact, m_ref + 15 is not)
+      if (m_cand - m_ref > rise) {  // (the difference is exact, m_ref + 15 is not)
         const float m_new = m_cand + kRefHeadroom;
         alpha = ex2_approx(m_ref - m_new);  // 0 on the first tile
         l *= alpha;
@@ -1393,7 +1420,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       // -inf). A NaN l (a NaN logit, or 0 * inf) is not empty: it reaches O
       // and the LSE.
       const bool empty = l == 0.f;
-      const float inv = empty ? 0.f : 1.f / l;
+      const float inv = empty ? 0.f : (WIN ? 1.f / kVScale : 1.f) / l;
       const int hq = w.hq0 + t;
       const int out_row = WIN ? w.qb * kBM + r : row;
       const bool out_valid = WIN ? out_row < w.q_len : row_valid;
@@ -1577,9 +1604,9 @@ __device__ __forceinline__ void window_tiles(const int32_t* __restrict__ cu_q, i
 // Paged V -> a copy of the keys each row uses, token-contiguous per row:
 // [B, max_tiles * 128, h_kv, d_h] (row b's key t at token b * max_tiles * 128
 // + t), and flags [B, h_kv, max_tiles] with v_to_f16_kernel's meaning. A tile
-// is written as fp16 when every value converts exactly, else (flagged) as
-// the bf16 values themselves, so the attention kernel reads every V tile of
-// the row from this copy. Keys from the row's last key to the end of its last
+// is written as fp16 when it holds no magnitude of 2^16 or more (values below
+// 2^-14 within 2^-25), else (flagged) as the bf16 values themselves, so the
+// attention kernel reads every V tile of the row from this copy. Keys from the row's last key to the end of its last
 // 128-key tile, and pages whose block-table entry lies outside the cache, are
 // written as zeros, whatever the cache holds there. Rows the attention kernel
 // skips (query count above the row's capacity) are left alone. The key count
@@ -1588,8 +1615,9 @@ __device__ __forceinline__ void window_tiles(const int32_t* __restrict__ cu_q, i
 // check and the store.
 //
 // WIN: with a window, tiles that no query of the row sees are left alone, and keys
-// that none sees are zeros in the others; their pages are not looked up. The first
-// CTA also plans the attention kernel's items.
+// that none sees are zeros in the others; their pages are not looked up. The copy holds
+// V times kVScale, and tiles that this does not convert exactly are flagged. The first CTA
+// also plans the attention kernel's items.
 template <int CPR, bool WIN>
 __global__ void __launch_bounds__(256)
     paged_v_to_f16_kernel(const uint4* __restrict__ vc, const int32_t* __restrict__ block_table,
@@ -1621,7 +1649,7 @@ __global__ void __launch_bounds__(256)
   const int first = WIN ? max(ctx - q_len + 1 - window, 0) : 0;  // the first query's first key
   if (WIN && (q_len == 0 || (jt * kBN + kBN <= first && jt * kBN >= sinks))) return;
   uint4 x[PER];
-  uint32_t mx = 0;
+  uint32_t mx = 0, mn = 0x7fff7fffu;  // largest magnitudes; WIN: smallest but 0, as below
 #pragma unroll
   for (int u = 0; u < PER; ++u) {
     const int i = threadIdx.x + 256 * u;
@@ -1640,19 +1668,29 @@ __global__ void __launch_bounds__(256)
     asm("max.u16x2 %0, %0, %1;" : "+r"(m2) : "r"(x[u].z & 0x7fff7fffu));
     asm("max.u16x2 %0, %0, %1;" : "+r"(m2) : "r"(x[u].w & 0x7fff7fffu));
     asm("max.u16x2 %0, %0, %1;" : "+r"(mx) : "r"(m2));
+    if constexpr (WIN) {
+      // Magnitude less 1 behind a sign bit, in order as signed halves, 0 the largest.
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) asm("min.s16x2 %0, %0, %1;" : "+r"(mn) : "r"((w[k] | 0x80008000u) - 0x00010001u));
+    }
   }
   // bf16 bits 0x4780 = 2^16: the first magnitude fp16 cannot hold.
-  const int wide = __syncthreads_or((mx & 0xffffu) >= 0x4780u || (mx >> 16) >= 0x4780u);
+  const uint32_t most = max(mx & 0xffffu, mx >> 16);
+  const int least = min(static_cast<int16_t>(mn & 0xffffu), static_cast<int16_t>(mn >> 16)) + 0x8000;  // less 1
+  int wide = __syncthreads_or(WIN ? most >= kVMost || least < int(kVLeast) - 1 : most >= 0x4780u);
+  if (WIN && wide) wide = __syncthreads_or(most >= kV64) ? kVWide | kVHuge : kVWide;
 #pragma unroll
   for (int u = 0; u < PER; ++u) {
     const int i = threadIdx.x + 256 * u;
     const int tok = i / CPR, c = i % CPR;
     uint4 y = x[u];
     if (!wide) {
-      y.x = pack_f16x2(bf16lo(x[u].x), bf16hi(x[u].x));
-      y.y = pack_f16x2(bf16lo(x[u].y), bf16hi(x[u].y));
-      y.z = pack_f16x2(bf16lo(x[u].z), bf16hi(x[u].z));
-      y.w = pack_f16x2(bf16lo(x[u].w), bf16hi(x[u].w));
+      constexpr float k = WIN ? kVScale : 1.f;
+      y.x = pack_f16x2(bf16lo(x[u].x) * k, bf16hi(x[u].x) * k);
+      y.y = pack_f16x2(bf16lo(x[u].y) * k, bf16hi(x[u].y) * k);
+      y.z = pack_f16x2(bf16lo(x[u].z) * k, bf16hi(x[u].z) * k);
+      y.w = pack_f16x2(bf16lo(x[u].w) * k, bf16hi(x[u].w) * k);
     }
     const size_t vi = ((size_t(b) * max_tiles * kBN + size_t(jt) * kBN + tok) * h_kv + kvh) * CPR + c;
     if (ATTN_GUARD(tok < kBN && vi < size_t(gridDim.y) * max_tiles * kBN * h_kv * CPR,

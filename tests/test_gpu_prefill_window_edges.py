@@ -129,3 +129,85 @@ def test_one_nan_among_many_flagged_tiles(window, sinks):
     e1.record()
     torch.cuda.synchronize()
     assert e0.elapsed_time(e1) < 100
+
+
+@pytest.mark.parametrize("exp", [-120, -60, -30, -22, -20, -16, 7, 9, 60, 64, 66, 100, 118])
+@pytest.mark.parametrize("window,sinks", [(100, 3), (400, 0)])
+def test_values_of_any_size(exp, window, sinks):
+    """Values enter exactly: the same bound at every magnitude."""
+    c = Case([300, 0], [150, 140], 1, 4, 128, 25, window, sinks)
+    c.v = (c.v.double() * 2.0 ** exp).to(torch.bfloat16)
+    O, L = c.reference()
+    o, lse = c.run()
+    check_out(o.double().cpu() * 2.0 ** -exp, O * 2.0 ** -exp, torch.bfloat16)
+    check_lse(lse, L)
+    assert attn.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("low,high", [(-30, 0), (-60, 3), (-24, 12), (-100, 100), (0, 118), (-25, 8)])
+def test_columns_of_different_size(low, high):
+    """Every other column 2^low, the others 2^high: each within its own bound."""
+    c = Case([500, 30], [200, 140], 2, 2, 64, 26, 300, 4)
+    size = torch.full((64,), 2.0 ** high, dtype=torch.float64)
+    size[::2] = 2.0 ** low
+    c.v = (c.v.double() * size).to(torch.bfloat16)
+    O, L = c.reference()
+    o, lse = c.run()
+    check_out(o.double().cpu() / size, O / size.numpy(), torch.bfloat16)
+    check_lse(lse, L)
+
+
+@pytest.mark.parametrize("lead", [2, 640])
+@pytest.mark.parametrize("exp", [-118, -40, -24, -20, 0, 30, 120])
+@pytest.mark.parametrize("gap", [10, 13])
+def test_the_leading_key_alone_has_a_small_or_large_value(lead, exp, gap):
+    """A row is its leading key's value, whatever the others' sizes."""
+    c = leading(gap, ((0, lead), (1, 3)), 1, 300, 4, 128)
+    c.v = (c.v.float() * torch.where(torch.arange(16) % 3 == 0, 1e4, 1e-3)[:, None, None]).to(torch.bfloat16)
+    for b, j in ((0, lead), (1, 3)):
+        put(c, c.v, b, j, (torch.linspace(-1.9, 1.9, 128) * 2.0 ** exp).to(torch.bfloat16))
+    O, L = c.reference()
+    o, lse = c.run()
+    # The weight's rounding (2^-12) cancels in part against the sum's; bf16's is 2^-9. The
+    # other keys' logits are 2^gap / sqrt(128) or more below, so their weights are zeros in
+    # fp16: at most 720 values of 4.5e4 at e^-that are lost (2^10: e^-90.5, 2e-32 in all).
+    lost = 720 * 4.5e4 * np.exp(-2.0 ** gap / 128 ** 0.5)
+    assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -8 * np.abs(O) + lost).all()
+
+
+@pytest.mark.parametrize("exp", [17, 63, 64, 120])
+def test_one_large_value_leaves_the_other_columns_alone(exp):
+    c = Case([200], [200], 2, 2, 64, 27, 130, 4)
+    O, L = c.reference()
+    for j in (1, 150, 330, 399):
+        put(c, c.v, 0, j, 2.0 ** exp, kv=1, e=7)
+    o, lse = c.run()
+    others = [e for e in range(64) if e != 7]
+    check_out(o[..., others], O[..., others], torch.bfloat16)
+    check_out(o[:, :2], O[:, :2], torch.bfloat16)
+    check_lse(lse, L)
+    P, _ = c.reference()
+    o = o[..., 7].double().cpu().numpy()
+    assert (np.abs(o - P[..., 7])[:, 2:] <= 2.0 ** -7 * np.abs(P[..., 7])[:, 2:] + 4e-3).all()
+
+
+def test_every_bf16_number_as_a_value():
+    """All 65280 finite numbers, each the only key that its query weighs."""
+    c = Case([0], [4], 1, 1, 64, 28, 1, 0)
+    n = 1020
+    bits = torch.arange(65536, dtype=torch.int32)
+    bits = bits[(bits & 0x7f80) != 0x7f80].to(torch.int16).view(torch.bfloat16)
+    v = bits.view(n, 64)
+    pages = (n + 15) // 16
+    vc = torch.zeros((pages * 16, 1, 64), dtype=torch.bfloat16)
+    vc[:n, 0] = v
+    kc = torch.zeros((pages, 16, 1, 64), dtype=torch.bfloat16).cuda()
+    q = torch.zeros((n, 1, 64), dtype=torch.bfloat16).cuda()
+    table = torch.arange(pages, dtype=torch.int32)[None].cuda()
+    o, lse = attn.attn_prefill_paged_window(q, kc, vc.view(pages, 16, 1, 64).cuda(), table, i32([0, n]).cuda(),
+                                            i32([n]).cuda(), 1, 0, n)
+    o, want = o[:, 0].double().cpu(), v.double()
+    normal = want.abs() >= 2.0 ** -126  # (bf16 subnormals may come out as zeros)
+    assert torch.equal(o[normal], want[normal])
+    assert (o[~normal].abs() <= 2.0 ** -126).all()
+    assert torch.equal(lse.cpu(), torch.zeros_like(lse.cpu()))
