@@ -712,14 +712,15 @@ attn_status_t attn_prefill_paged_window(const void* q, const void* k_cache, cons
   if (static_cast<long long>(max_blocks_per_seq) * page_size > (1ll << 30)) return ATTN_ERR_INVALID_ARG;
   if (B == 0 || total_q == 0) return ATTN_OK;
   if (max_q_len < 1) return ATTN_ERR_INVALID_ARG;
+  // (Before the workspace: a caller who asked for its size holds none.)
+  const PagedV16Layout L = paged_v16_layout(B, max_blocks_per_seq, h_kv, d_h);
+  if (L.total == 0) return ATTN_ERR_UNSUPPORTED;
   if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens_q || !seq_lens || !workspace || !o)
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
       !aligned(block_table, 4) || !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) ||
       !aligned(lse, 4) || !aligned(workspace, 256))
     return ATTN_ERR_INVALID_ARG;
-  const PagedV16Layout L = paged_v16_layout(B, max_blocks_per_seq, h_kv, d_h);
-  if (L.total == 0) return ATTN_ERR_UNSUPPORTED;
   if (workspace_bytes < align256(L.total) + 256) return ATTN_ERR_INVALID_ARG;
   // Query tiles times heads are counted in 32 bits.
   if ((static_cast<long long>(total_q) / 128 + B + 1) * h > 0x3fffffffll) return ATTN_ERR_UNSUPPORTED;

@@ -49,3 +49,13 @@ def test_binding_refuses_cpu_tensors():
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError):
         attn.attn_prefill_paged_window(q, c, c, i.view(1, 1), torch.zeros(2, dtype=torch.int32), i, 5, 0, 1)
+
+
+def test_sizes_without_a_workspace_are_unsupported(lib):
+    """Where the size function gives 0 a caller holds no workspace: the call says why."""
+    big = dict(B=40000, mb=1 << 20)
+    assert attn.attn_prefill_window_workspace_bytes(40000, 1 << 20, 8, 128) == 0
+    assert call(lib, **big, ws=None, wsb=0) == UNSUP
+    assert call(lib, **big, wsb=0) == UNSUP
+    assert call(lib, ws=None, wsb=0) == BAD
+    assert call(lib, **big, window=0, ws=None) == BAD
