@@ -178,7 +178,10 @@ __global__ void __launch_bounds__(128)
 // else with two kernels: one row of 16, 1000, 4000, 8000 keys, 8 KV heads of 128
 // 6.7, 7.5, 9.4, 12.0, else 8.1, 9.0, 10.1, 11.8; of 64 1000, 4000 keys 6.7, 8.0,
 // else 7.7, 8.5; 14 units of 1000 keys 7.6, else 9.3; 16 units 12.7, else 9.4 (not
-// all clusters fit at a time).
+// all clusters fit at a time). Windows of the bf16 cache, whose pages are twice as long,
+// have the same borders: one row, 8 KV heads of 128, windows of 1000, 2000, 4000 keys 7.8,
+// 8.0, 9.8, else 8.5, 9.1, 10.0; 14 units 8.2, 8.7, 10.7, else 9.1, 10.3, 12.0; 16 units
+// 13.7, 14.4, 18.0, else 9.2, 10.4, 12.8 (one head alone crosses at 3500: 8.8, else 8.6).
 constexpr int kClusterCtas = 8;
 constexpr int kUnitMost = 14, kUnitBlocks = 256;
 static_assert(kUnitMost * kClusterCtas <= kRunsMaxCtas, "workspace of the partial states");
@@ -301,11 +304,12 @@ cudaError_t launch_cfg(const DecodeRunsArgs& a, int sms, cudaStream_t stream) {
   using C = Cfg<E8, D, 8, NST>;
   constexpr int kSmem = C::SMEM + 1024;
   static_assert(kSmem + sizeof(RunShared<8>) <= 227 * 1024, "shared memory of an SM");
+  static_assert(sizeof(RunCut) * kRunsMaxCtas <= kRunsCutBytes, "workspace");
   auto kern = decode_runs_kernel<E8, D, NST, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int grid = sms < kRunsMaxCtas ? sms : kRunsMaxCtas;
-  const RunOut out{a.plan,  a.o_part, a.m_part, a.l_part, nullptr,
+  const RunOut out{R::kWindow ? nullptr : a.plan, a.o_part, a.m_part, a.l_part, nullptr,
                    nullptr, nullptr,  static_cast<__nv_bfloat16*>(a.o), a.lse,
                    static_cast<RunCut*>(a.cut)};
   return launch_pdl(kern, dim3(grid), dim3(256), size_t(kSmem), stream,

@@ -179,8 +179,8 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t page, int r, int c) {
 
 // What a merge reads of the unit that begins in a CTA and goes on behind it: parts
 // (0: there is none), first (row, head), heads.
-struct RunCut {
-  int parts, row0, nh, unused;
+struct alignas(16) RunCut {
+  int parts, row0, nh;
 };
 
 // Where states and results go. Units cut by a run border: part (two slots of 8
@@ -304,8 +304,8 @@ struct RunPlan {
   long long per;  // weight of every run
 };
 
-// Plans the runs, one per warp; CTA 0 leaves the plan for the merge (none: nullptr,
-// up to 32 rows).
+// Plans the runs, one per warp; CTA 0 leaves the plan for a merge that reads it (else
+// nullptr).
 template <int NW, class R, class Sync>
 __device__ __forceinline__ RunPlan plan_runs(const R rw, long long* plan, RunShared<NW>& sh, int cta,
                                           int n_cta, unsigned int* err, Sync sync) {
@@ -381,7 +381,7 @@ __device__ __forceinline__ RunPlan plan_runs(const R rw, long long* plan, RunSha
     all = total * rw.upr;
     per = per_of(all);
     const long long cta0 = per * NW * cta;
-    if (cta == 0) {  // for the merge
+    if (cta == 0 && plan != nullptr) {  // for the merge
       if (tid == 0) plan[0] = per * NW;
       long long at = before;
       for (int b = b0; b < b1; ++b) {
@@ -954,7 +954,7 @@ __device__ __forceinline__ void runs_body(
       // of it is spread over the CTAs behind.
       if (out.cut != nullptr && tid == 0 && open == 1) {
         const long long left = sh.own_left[opened] - plan.per * (NW - 1 - opened);
-        out.cut[cta] = RunCut{static_cast<int>(1 + div_ll(left + plan.per * NW - 1, plan.per * NW)), row0, nh, 0};
+        out.cut[cta] = RunCut{static_cast<int>(1 + div_ll(left + plan.per * NW - 1, plan.per * NW)), row0, nh};
       }
     }
   }
