@@ -211,3 +211,13 @@ def test_every_bf16_number_as_a_value():
     assert torch.equal(o[normal], want[normal])
     assert (o[~normal].abs() <= 2.0 ** -126).all()
     assert torch.equal(lse.cpu(), torch.zeros_like(lse.cpu()))
+
+
+def test_table_much_wider_than_the_rows():
+    """Rows of 1 to 2000 keys in a table of 8192 pages: the results of a tight table."""
+    c = Case([700, 0, 1500, 33], [300, 1, 500, 7], 1, 4, 128, 29, 1024, 4)
+    want, lse_w = c.check()
+    c.table = torch.cat([c.table, c.table.new_full((4, 8192 - c.table.shape[1]), 2 ** 31 - 1)], 1)
+    o, lse = c.run()
+    assert torch.equal(o, want) and torch.equal(lse, lse_w)
+    assert attn.attn_get_device_error() == 0
