@@ -423,7 +423,7 @@ __device__ __noinline__ float2 sink_weights(uint32_t tS, uint32_t bits, float sc
     mx = fmaxf(mx, __uint_as_float(s[i]));
   }
   // As the first tile of the loop: the reference goes kRefHeadroom above the maximum.
-  const float m = mx == -INFINITY ? -INFINITY : mx * scale_log2 + kRefHeadroom;
+  const float m = mx == -INFINITY ? -INFINITY : __fadd_rn(__fmul_rn(mx, scale_log2), kRefHeadroom);
   const float bias = m == -INFINITY ? 0.f : m;
   float sum = 0.f;
 #pragma unroll
@@ -1332,7 +1332,9 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
                       fmaxf(a[9], a[10]));
       }
       const float mx = fmaxf(max3f(cm[0], cm[1], cm[2]), cm[3]);
-      const float m_cand = mx * scale_log2;
+      // (Rounded, as rare_weights has it: joined with the difference or the sum below it
+      // would leave its residual in them.)
+      const float m_cand = __fmul_rn(mx, scale_log2);
       float alpha = 1.f;
       if (m_cand - m_ref > rise) {  // (the difference is exact, m_ref + 15 is not)
         const float m_new = m_cand + kRefHeadroom;

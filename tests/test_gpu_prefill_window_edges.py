@@ -46,7 +46,8 @@ def test_large_logits(exp, mult, window, sinks, flagged):
         put(c, c.v, 1, 1, 3e5)
     O, L = c.reference()
     o, lse = c.run()
-    # The weight's rounding (2^-12) cancels in part against the sum's; bf16's is 2^-9.
+    # (Half a bf16 step is up to 2^-8 of a number; a weight's rounding, 2^-12, moves the one
+    # that the row is by less.)
     assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -8 * np.abs(O) + 2.0 ** -24).all()
     # Factor, product, ln 2 and the product with it: 5 roundings of 2^-24.
     assert (np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -21 * np.abs(L)).all()
@@ -66,8 +67,23 @@ def test_large_logits_that_are_equal(exp, window, sinks, leads, flagged):
     O, L = c.reference()
     o, lse = c.run()
     # Half a bf16 step of the result, and 2^-11 of the values that are averaged.
-    assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -9 * np.abs(O) + 2.0 ** -11 * 6).all()
+    assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -8 * np.abs(O) + 2.0 ** -11 * 6).all()
     assert (np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -21 * np.abs(L) + 1e-6).all()
+
+
+@pytest.mark.parametrize("exp", range(24, 34))
+@pytest.mark.parametrize("window,sinks,flagged", [(300, 4, False), (300, 40, False), (1000, 0, True)])
+def test_large_logits_of_every_mantissa(exp, window, sinks, flagged):
+    """160 queries' factors, so that products lie anywhere between two fp32 numbers."""
+    c = leading(exp, ((0, 650), (1, 3)), 1, window, sinks, 64)
+    c.q[:, :, 0] = ((1 + torch.arange(c.q.shape[0] * 8) % 128 / 128.0) * 2.0 ** exp).view(-1, 8).to(torch.bfloat16)
+    if flagged:
+        put(c, c.v, 0, 500, 3e5)
+        put(c, c.v, 1, 1, 3e5)
+    O, L = c.reference()
+    o, lse = c.run()
+    assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -8 * np.abs(O) + 2.0 ** -24).all()  # as above
+    assert (np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -21 * np.abs(L)).all()
 
 
 @pytest.mark.parametrize("exp", range(20, 30))
@@ -168,9 +184,9 @@ def test_the_leading_key_alone_has_a_small_or_large_value(lead, exp, gap):
         put(c, c.v, b, j, (torch.linspace(-1.9, 1.9, 128) * 2.0 ** exp).to(torch.bfloat16))
     O, L = c.reference()
     o, lse = c.run()
-    # The weight's rounding (2^-12) cancels in part against the sum's; bf16's is 2^-9. The
-    # other keys' logits are 2^gap / sqrt(128) or more below, so their weights are zeros in
-    # fp16: at most 720 values of 4.5e4 at e^-that are lost (2^10: e^-90.5, 2e-32 in all).
+    # (As for large logits.) The other keys' logits are 2^gap / sqrt(128) or more below, so
+    # their weights are zeros in fp16: at most 720 values of 4.5e4 at e^-that are lost (2^10:
+    # e^-90.5, 2e-32 in all).
     lost = 720 * 4.5e4 * np.exp(-2.0 ** gap / 128 ** 0.5)
     assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -8 * np.abs(O) + lost).all()
 
