@@ -82,6 +82,15 @@ constexpr float kRescaleBits = 15.0f;
 // error at most 2^-25 against a row sum of at least 2^-kRefHeadroom, i.e. at
 // most 2^-17 of the sum per key.
 constexpr float kRefHeadroom = 8.0f;
+// Windows: the reference goes 4 below instead, so that a key loses at most 2^-29 of the
+// row's largest weight so far: one key may outweigh thousands that matter together (12
+// nats below a sink each of 8192 equal keys came out as 0, and with them the 4.7 % that
+// they hold). A narrow tile of sinks sets it to their maximum (2^-25 a key): the keys of
+// the window often pass it. 8192 tokens 139.7 -> 140.5 us, 142.6 with 4 below for the sinks
+// too (the whole-row prefill, its logits' deviation 9, would take 369.0 instead of 355.7).
+// A window that no row of the table reaches keeps 8, and with it attn_prefill_paged's
+// results to the bit.
+constexpr float kWindowHeadroom = -4.0f;
 
 // Windows: the fp16 copy holds V times kVScale, which is exact from 2^(-17 - 8) (8 bits
 // above fp16's smallest step, 2^-24) to below 2^(16 - 8), and at 0; a tile with a number
@@ -236,6 +245,7 @@ struct PagedArgs {
   int max_tiles;  // 128-key tiles per row in the fp16 V copy: ceil(max_blocks / 8)
   const __nv_bfloat16* v_copy;  // WIN kernels: the V copy (flagged tiles: bf16)
   int window, sinks;  // WIN kernels: the query at position p sees keys > p - window, and < sinks
+  float headroom;     // WIN kernels: how far above a row's maximum the reference goes
 };
 
 // One work item: a 128-query block of NQ query heads that share a KV head.
@@ -422,8 +432,7 @@ __device__ __noinline__ float2 sink_weights(uint32_t tS, uint32_t bits, float sc
     if (!((bits >> i) & 1u)) s[i] = __float_as_uint(-INFINITY);
     mx = fmaxf(mx, __uint_as_float(s[i]));
   }
-  // As the first tile of the loop: the reference goes kRefHeadroom above the maximum.
-  const float m = mx == -INFINITY ? -INFINITY : __fadd_rn(__fmul_rn(mx, scale_log2), kRefHeadroom);
+  const float m = __fmul_rn(mx, scale_log2);
   const float bias = m == -INFINITY ? 0.f : m;
   float sum = 0.f;
 #pragma unroll
@@ -1233,7 +1242,9 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
     // How far above the reference a maximum may come: with huge values not above the
     // largest so far, kRefHeadroom below the reference.
     float rise = kRescaleBits;
-    if constexpr (WIN && MAYBE_WIDE) rise = item_has_huge(w, tile_wide) ? -kRefHeadroom : kRescaleBits;
+    if constexpr (WIN && MAYBE_WIDE) {
+      if (item_has_huge(w, tile_wide)) rise = -kRefHeadroom;
+    }
     for (int j = j0; j < nkv; ++j) {
       const int g = g0 + j;
       // The format of P follows the format of this key tile's V.
@@ -1317,7 +1328,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       }
       // Row max: per 32-column chunk a tree of 3-input maxima (11 -> 4 -> 1),
       // then the four chunk maxima. Then the lazy reference rule: the
-      // reference moves (to kRefHeadroom above the row max) only when the row
+      // reference moves (to the headroom above the row max) only when the row
       // max exceeds it by more than kRescaleBits, so every weight stays at
       // most 2^15 and fits fp16; otherwise l and O~ keep their scale.
       float cm[4];
@@ -1337,7 +1348,7 @@ __global__ void __launch_bounds__(PfCfg<D, NQ, NSK, NSV>::THREADS, 1)
       const float m_cand = __fmul_rn(mx, scale_log2);
       float alpha = 1.f;
       if (m_cand - m_ref > rise) {  // (the difference is exact, m_ref + 15 is not)
-        const float m_new = m_cand + kRefHeadroom;
+        const float m_new = m_cand + (!WIN || (MAYBE_WIDE && rise < 0.f) ? kRefHeadroom : pa.headroom);
         alpha = ex2_approx(m_ref - m_new);  // 0 on the first tile
         l *= alpha;
         m_ref = m_new;
@@ -1840,7 +1851,8 @@ cudaError_t launch_paged(const PagedPrefill& a, cudaStream_t stream) {
   }
   PagedArgs pa{a.block_table, a.cu_q,       a.seq_lens,   a.tile_off,
                a.B,           a.max_blocks, a.num_blocks, max_tiles,
-               static_cast<const __nv_bfloat16*>(a.v16), a.window, a.sinks};
+               static_cast<const __nv_bfloat16*>(a.v16), a.window, a.sinks,
+               a.window >= static_cast<long long>(a.max_blocks) * 16 ? kRefHeadroom : kWindowHeadroom};
   // At most one partial tile per row beyond ceil(total_q / 128), and no row
   // has more than ceil(max_q_len / 128) tiles.
   const long long by_total = (static_cast<long long>(a.total_q) + kBM - 1) / kBM + a.B;

@@ -106,6 +106,41 @@ def test_logits_that_rise_by_steps(exp):
         assert ((lse.double().cpu() - want).abs() <= want * 2.0 ** -20 + 130).all(), (exp, step)
 
 
+def outweighed(window, sinks, lead, gap, steps=0):
+    """8300 keys and 40 queries; every key's logit is 0 but the lead's, `gap`, and with
+    `steps` one key's in 128, gap - steps. The leads have the value 0, the others 1 in
+    column 0."""
+    c = Case([8300], [40], 1, 2, 128, 30, window, sinks)
+    c.q.zero_()
+    c.q[..., 0] = 8.0
+    c.k.zero_()
+    c.v[..., 0] = 1.0
+    for j in range(64, 8300, 128) if steps else ():
+        put(c, c.k, 0, j, (gap - steps) * 128 ** 0.5 / 8.0, e=0)
+        put(c, c.v, 0, j, 0.0, e=0)
+    put(c, c.k, 0, lead, gap * 128 ** 0.5 / 8.0, e=0)
+    put(c, c.v, 0, lead, 0.0, e=0)
+    return c
+
+
+@pytest.mark.parametrize("gap", [6, 10, 12, 13, 14, 17])
+@pytest.mark.parametrize("window,sinks,lead,steps", [(8192, 4, 1, 0), (8000, 4, 1, 0), (8000, 100, 99, 0), (8192, 0, 300, 0),
+                                                     (8000, 0, 8200, 0), (8000, 4, 1, 3), (8192, 0, 300, 3)])
+def test_one_key_outweighs_thousands(window, sinks, lead, steps, gap):
+    """What thousands of keys hold together is not lost beside one that outweighs each of
+    them by e^gap, a sink or any other."""
+    c = outweighed(window, sinks, lead, gap, steps)
+    O, L = c.reference()
+    o, lse = c.run()
+    check_out(o, O, torch.bfloat16)
+    check_lse(lse, L)
+    # Half a bf16 step is up to 2^-8 of a number; a weight's rounding to fp16 2^-12 of itself,
+    # and at most 2^-29 of the row's largest (2^-25 of a sink's).
+    lost = 8192 * 2.0 ** (-25 if lead < sinks else -29)
+    o, O = o[..., 0].double().cpu().numpy(), O[..., 0]
+    assert (np.abs(o - O) <= (2.0 ** -8 + 2.0 ** -12) * O + lost).all()
+
+
 @pytest.mark.parametrize("window,sinks", [(700, 3), (2000, 0), (300, 400)])
 def test_infinities_that_every_query_of_a_tile_sees(window, sinks):
     """An infinity in a tile that all of a block's queries see reaches them as an
