@@ -128,7 +128,13 @@ size_t attn_prefill_workspace_bytes(int T, int h_kv, int d_h, attn_dtype_t dtype
  *           (workspace_bytes ignored): the bf16 path then forms every P V
  *           product as P_hi V + P_lo V in bf16, exact but slower. With a
  *           workspace, V is first copied to fp16 (one extra kernel) and
- *           P V is a single fp16 product wherever V fits fp16.
+ *           P V is a single fp16 product in every 128-key tile without a
+ *           magnitude of 2^16 or more (or inf, NaN).
+ * Limits of the bf16 path: logits (scale q.k) have to stay below 2^26 in
+ * magnitude. In the single fp16 product a weight enters within 2^-11 of itself
+ * or 2^-17 of the row's largest so far, whichever is more (a key 12 nats below
+ * another takes no part beside it), and a value of V below 2^-14 within 2^-25.
+ * In the two-term form weights enter within 2^-15 of themselves, V as it is.
  * Errors: INVALID_ARG for NULL q/k/v/o (T > 0), T < 0, h < 1, h > 65535,
  * h_kv < 1, h % h_kv != 0, misaligned pointers, scale not finite and > 0, a
  * non-NULL workspace that is misaligned or smaller than required;
@@ -219,9 +225,9 @@ attn_status_t attn_prefill_host(const void* q, const void* k, const void* v, voi
  * bf16 and takes the exact two-term bf16 P; with the larger one
  * (attn_prefill_paged_v16_workspace_bytes) a pre-pass copies the pages each
  * row uses into an fp16 buffer in the workspace, row by row, and a 128-key
- * tile that converts exactly takes an fp16 P against it (one MMA instead of
- * two); a tile holding |v| >= 2^16, inf or NaN keeps the bf16 path (read
- * from the copy too, where it is stored as bf16).
+ * tile takes an fp16 P against it (one MMA instead of two), with the limits
+ * stated at attn_prefill; a tile holding |v| >= 2^16, inf or NaN keeps the
+ * bf16 path (read from the copy too, where it is stored as bf16).
  * Rows of one query (decode rows of a mixed batch): with decode_splits > 0
  * they get no query tile; after the prefill kernel the call runs the
  * split-KV decode of attn_decode_paged_adaptive over those rows alone
@@ -747,7 +753,14 @@ attn_status_t attn_decode_paged_window_e4m3(const void* q, const void* k_cache, 
  * Rows of one query run as 1-row query tiles; attn_decode_paged_window is made for
  * them. Keys that a query does not see never reach it, whatever they and their values
  * hold; a non-finite value that it does see makes its column NaN or that infinity.
- * Errors, device errors and limits: as attn_prefill_paged, where offsets outside
+ * q, K and V enter as they are, whatever their magnitudes and the logits'. A weight is
+ * one fp16 number, within 2^-11 of itself or 2^-25 of the row's largest so far, whichever
+ * is more; against a 128-key tile of V with a magnitude of 2^8 or more or one below 2^-25
+ * that is not 0, two bf16 terms, within 2^-15 of itself. (2^-17 of the largest for a block
+ * of queries with a value of 2^64 or more among its tiles, and where window >=
+ * max_blocks_per_seq * 16: the weights are then those of attn_prefill_paged.)
+ * A row's sum of |v| in a column has to stay below 2^127.
+ * Errors and device errors: as attn_prefill_paged, where offsets outside
  * [0, total_q] also set ATTN_DEVERR_BAD_SEQ_LEN (the row is skipped); plus INVALID_ARG
  * for B > 65535, window < 1, sinks < 0 and a workspace below its size, UNSUPPORTED
  * where that size is 0 or (total_q / 128 + B + 1) * h is 2^30 or more (there is no
@@ -775,9 +788,9 @@ attn_status_t attn_prefill_paged_window(const void* q, const void* k_cache, cons
  * are ignored. The query rows of a KV head (drafts times heads of the group) share
  * its keys, which are read once per 256 / (h / h_kv) drafts. The work is divided over
  * the GPU on the device (any mix of lengths and of drafts); two kernels, whose
- * launches depend on h, h_kv and max_q_len only (capturable, replayable with new
- * offsets, lengths, masks and tables); no atomics, the result does not depend on
- * timing.
+ * launches depend on none of them (capturable, replayable with new offsets,
+ * lengths, masks and tables); no atomics, the result does not depend on
+ * timing. (A captured graph keeps total_q, max_q_len and mask_words.)
  *   q            [total_q, h, d_h] bf16                               (read)
  *   k_cache,
  *   v_cache      [num_blocks, page_size, h_kv, d_h] bf16              (read)

@@ -363,8 +363,9 @@ cudaError_t launch_decode8(const DecodeRunsArgs& a, cudaStream_t stream) {
 }
 
 // Units of windows are short, so what one weighs beside its pages matters: 200 rows of
-// the 8-bit cache, window 2001, take 157.8 us with 1, 147.7 with 3, 142.2 with 5, 142.8
-// with 8 (66 rows of the bf16 cache, window 4096: 158.2, 159.0, 158.9, 159.4).
+// the 8-bit cache, window 2001, took 157.8 us with 1, 147.7 with 3, 142.2 with 5, 142.8
+// with 8 (66 rows of the bf16 cache, window 4096: 158.2, 159.0, 158.9, 159.4), before the
+// merge went by the runs' borders (now 134.5 and 155.5).
 constexpr int kWindowUnit = 5;
 cudaError_t launch_decode_window(const DecodeRunsArgs& a, cudaStream_t stream) {
   // The window's pages (one more where it starts inside a page) and the sinks'.

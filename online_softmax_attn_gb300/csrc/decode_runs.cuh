@@ -54,10 +54,10 @@
 // pages cost a CTA as much as rows of hundreds.)
 //
 // Windows are bound by the visible pages' bytes in the same way: 66 rows of up to
-// 16384 keys, window 4096 and 4 sinks, 32 query heads over 8 of 128, take 153 us of the
-// bf16 cache, 0.94 of the copy rate; 200 rows of the 8-bit cache, window 2001 and 18
-// sinks, 136 us, 0.85 (a unit is 128 pages, and has its query and its output). Masking
-// only the pages at a part's ends: 158 -> 154 us.
+// 16384 keys, window 4096 and 4 sinks, 32 query heads over 8 of 128, take 153 to 157 us of
+// the bf16 cache, 0.94 to 0.91 of the copy rate; 200 rows of the 8-bit cache, window 2001
+// and 18 sinks, 134.5 us, 0.86 (a unit is 128 pages, and has its query and its output).
+// Masking only the pages at a part's ends took the first from 158 to 154 us.
 #pragma once
 
 #include "common.cuh"

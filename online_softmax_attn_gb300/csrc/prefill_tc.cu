@@ -12,8 +12,8 @@
 // weights P share one exp2-domain reference m_ref, which need not be the row
 // max. Every tile takes its row max; the reference moves only when that max
 // passes it by more than 15 (weights then still fit fp16), and it moves to 8
-// above the max, so O~ is rescaled rarely; the rescale runs after P is
-// stored, in the registers S held. O = O~ / l and LSE are independent of the
+// above the max (windows: 4 below), so O~ is rescaled rarely; the rescale runs
+// after P is stored, in the registers S held. O = O~ / l and LSE are independent of the
 // reference.
 //
 // GB300 design (work item: a 128-query block of a pair of query heads that
@@ -22,16 +22,18 @@
 //   * softmax warpgroups (warps 0-3, 4-7), one per query head; thread = row
 //     (tensor-memory lane), so row sums and maxima need no shuffles. P is
 //     written over the first columns of its own S tile: fp16 for a V tile
-//     that converts to fp16 exactly, else bf16 P_hi and P_lo.
+//     read as fp16, else bf16 P_hi and P_lo.
 //   * control warpgroup: warp 8 is the TMA producer (Q of both heads per item,
 //     then K and V of the shared KV head through rings of their own, 128-byte
 //     swizzle, 64-element boxes); warp 9 allocates tensor memory and issues
 //     the MMAs as a whole warp (elect.sync picks the issuing lane):
 //     S_t = Q_t K^T (SS, M=N=128, K=d_h) and O_t += P_t V (TS: P from tensor
-//     memory, V from shared memory, MN-major as stored); warps 10-11 idle.
+//     memory, V from shared memory, MN-major as stored); the warp behind it
+//     claims the items of windows, the other one idles.
 //   * before it, v_to_f16_kernel converts V once per KV head into an fp16
-//     copy (exact for |v| < 2^16) and flags each 128-key tile holding a value
-//     fp16 cannot carry; flagged tiles are read as bf16 and take P_hi + P_lo.
+//     copy (exact from 2^-14 to below 2^16, within 2^-25 below) and flags each
+//     128-key tile with a magnitude of 2^16 or more; flagged tiles are read as
+//     bf16 and take P_hi + P_lo. (Windows: exact everywhere, see kVScale.)
 //   The two heads ping-pong: while one warpgroup exponentiates its S tile,
 //   the tensor core runs the other head's P V and next Q K^T.
 //   Causal items visit only key tiles up to the diagonal (the masked half of
@@ -43,12 +45,13 @@
 //   With a window (attn_prefill_paged_window) an item visits the key tiles that hold
 //   the first tokens (sinks), then those of its queries' windows; both parts' edges
 //   are masked per query. Its items are short, so these paged rows run a persistent
-//   grid too: warp 10 claims the items, finds their rows and publishes them.
+//   grid too: the warp behind the MMA's claims the items, finds their rows and publishes
+//   them.
 //   8192 tokens, window 1024 and 4 sinks, 32 heads over 8 of 128 (66 us of products for
-//   the visible pairs at the tensor cores' rate): 137 us, the V pass among them. An item
-//   takes 18.7 us: nine tiles of 1.62, the sinks' 1.1, the edges' masks twice 0.7, and
+//   the visible pairs at the tensor cores' rate): 140 us, the V pass among them. An item
+//   takes about 19 us: nine tiles of 1.62, the sinks' 1.1, the edges' masks twice 0.7, and
 //   about 2 from its last product to the next one's first weights. 8 rows of 1024 tokens
-//   over 8192 keys, window 4096: 415 us for 281.
+//   over 8192 keys, window 4096: 420 to 437 us, box to box, for 281.
 //   Every mbarrier wait is bounded; on a timeout the CTA raises the error
 //   word, drains its copies and MMAs (bounded), frees tensor memory and exits.
 #include <climits>
@@ -122,8 +125,8 @@ struct PfCfg {
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM = MISC_OFF + 32 + 1024;  // + alignment slack
   static constexpr int TMEM_COLS = NQ == 1 ? 256 : 512;
-  // NQ softmax warpgroups + one control warpgroup (TMA warp, MMA warp, two
-  // idle warps: setmaxnreg moves registers per whole warpgroup).
+  // NQ softmax warpgroups + one control warpgroup (TMA warp, MMA warp, the item
+  // warp of windows, an idle one: setmaxnreg moves registers per whole warpgroup).
   static constexpr int THREADS = NQ * 128 + 128;
   static constexpr int PRODUCER_WARP = NQ * 4;
   static constexpr int MMA_WARP = NQ * 4 + 1;
@@ -420,7 +423,7 @@ __device__ __noinline__ void mask_window(uint32_t tS, int lo, int hi, int sinks)
 // columns, and their reference and sum. (The whole tile took 2.3 us of an item's 21 with
 // a window of 1024. With the scores in the O tile's columns and the weights behind the
 // second tile's, so that the sinks have no turn of their own, 8192 tokens took 145 us
-// instead of 137.) Out of line, so that the softmax loop holds neither its code nor its
+// where an earlier state of this form took 137.) Out of line, so that the softmax loop holds neither its code nor its
 // registers. Warp-collective.
 __device__ __noinline__ float2 sink_weights(uint32_t tS, uint32_t bits, float scale_log2) {
   uint32_t s[32];
