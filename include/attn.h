@@ -622,7 +622,8 @@ attn_status_t attn_cache_read_e4m3(const void* k_cache, const void* v_cache,
  * head's largest magnitude, within 2^-39 of it below that. A key's weight (times
  * its value's scale) is one fp16 number, within 2^-11 of itself down to 2^-27 of
  * the row's largest and within 2^-38 of the largest below that. A row's sum of
- * exp(s - max) |v| has to stay below 2^126.
+ * exp(s - max) |v|, max being the largest score so far, has to stay below 2^126 (a sum
+ * of |v| below it will do).
  * Errors: INVALID_ARG for NULL or misaligned pointers, B outside [0, 65535],
  * bad sizes, num_blocks * h_kv or B * h beyond int32, scale not finite and
  * > 0, a small workspace; UNSUPPORTED for d_h other than 64 / 128 or page_size
@@ -668,7 +669,8 @@ attn_status_t attn_decode_paged_e4m3(const void* q, const void* k_cache, const v
  * a row; non-finite keys and values that are attended do, as in
  * attn_decode_paged.
  * Keys and values enter as they are, whatever their magnitudes, as long as a
- * row's sum of exp(s - max) |v| stays below 2^126. A weight exp(s - max) of a
+ * row's sum of exp(s - max) |v|, max being the largest score so far, stays below
+ * 2^126 (a sum of |v| below it will do). A weight exp(s - max) of a
  * prefix key is one fp16 number, within 2^-11 of itself down to 2^-27 of the
  * row's largest and within 2^-38 of the largest below that; where values of its
  * 128 keys reach 128, or are not zero and below 2^-25, and for the rows' own
@@ -713,7 +715,8 @@ attn_status_t attn_decode_paged_shared(const void* q, const void* k_cache, const
  * (ATTN_DEVERR_BAD_SEQ_LEN); a visible page outside the cache reads as zeros
  * (ATTN_DEVERR_BAD_PAGE). Slots out of sight never reach a row, whatever they hold.
  * q, K and V enter as they are; a weight is two bf16 terms, within 2^-15 of itself.
- * A row's sum of exp(s - max) |v| has to stay below 2^126.
+ * A row's sum of exp(s - max) |v|, max being the largest score so far, has to stay below
+ * 2^126 (a sum of |v| below it will do).
  * Errors: as attn_decode_paged_e4m3, plus INVALID_ARG for window < 1 or sinks < 0.
  *
  * attn_decode_paged_window_e4m3 -- the same over the 8-bit cache (arguments, number
@@ -814,7 +817,8 @@ attn_status_t attn_prefill_paged_window(const void* q, const void* k_cache, cons
  * outside [n_b, max_blocks_per_seq * 16] set it and are clamped; pages outside the
  * cache read as zeros (ATTN_DEVERR_BAD_PAGE).
  * q, K and V enter as they are; a weight is two bf16 terms, within 2^-15 of itself.
- * A row's sum of exp(s - max) |v| has to stay below 2^118.
+ * A row's sum of exp(s - max) |v|, max being the largest score so far, has to stay below
+ * 2^118 (a sum of |v| below it will do).
  * Errors: INVALID_ARG for NULL or misaligned pointers, negative or zero sizes, h %
  * h_kv != 0, B > 65535, total_q * h beyond int32, max_q_len < 1 or mask_words * 32 <
  * max_q_len, scale not finite and > 0, a small workspace; UNSUPPORTED for d_h other
