@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int k = 0; k < 8; ++k) m8[k] = max3(x(4 * k), x(4 * k + 1), fmaxf(x(4 * k + 2), x(4 * k + 3)));
             cm[c] = fmaxf(max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), m8[6]), m8[7]);
           }
-          const float cand = fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]) * scale_log2;
+          const float cand = __fmul_rn(fmaxf(max3(cm[0], cm[1], cm[2]), cm[3]), scale_log2);
           float alpha = 1.f;
           if (cand - ref > kRise) {
             alpha = ex2_approx(ref - cand);
@@ -721,9 +721,15 @@ __global__ void __launch_bounds__(384, 1)
           }
           const bool rescale = i > 0 && __any_sync(0xffffffffu, alpha != 1.f);
           // Scores enter as rounded products minus the reference, which is exact near it
-          // at any magnitude of the logits. P_hi is p's upper 16 bits, P_lo =
-          // bf16(p - P_hi); keys 2k, 2k + 1 of half h in columns 32 h + k, 64 + 32 h + k.
-          const uint64_t c2 = f2(scale_log2, scale_log2), n2 = f2(-ref, -ref);
+          // at any magnitude of the logits: with the product's residual left in, up to half
+          // a step of the logit, the largest weight passed fp32 from logits of 2^30 on. (So
+          // the products are not packed: a packed product and sum are joined to one fma
+          // whatever their rounding modifiers; 24 rows of two row tiles took 30.0 us so, and
+          // 31.4 now, the other cases 1 % more at most. The exact form out of line, for
+          // large references alone: 64 rows 370 us instead of 346.) P_hi is p's upper 16
+          // bits, P_lo = bf16(p - P_hi); keys 2k, 2k + 1 of half h in columns 32 h + k,
+          // 64 + 32 h + k.
+          const uint64_t n2 = f2(-ref, -ref);
           uint64_t sumA = f2(0.f, 0.f), sumB = f2(0.f, 0.f);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -732,9 +738,8 @@ __global__ void __launch_bounds__(384, 1)
             for (int k = 0; k < 32; ++k) {
               const int key = 64 * half + 2 * k;
               float y0, y1;
-              unf2(add2(mul2(f2(__uint_as_float(sr[key >> 5][key & 31]),
-                                __uint_as_float(sr[key >> 5][(key & 31) + 1])),
-                             c2),
+              unf2(add2(f2(__fmul_rn(__uint_as_float(sr[key >> 5][key & 31]), scale_log2),
+                           __fmul_rn(__uint_as_float(sr[key >> 5][(key & 31) + 1]), scale_log2)),
                         n2),
                    y0, y1);
               const float q0 = ex2_approx(y0), q1 = ex2_approx(y1);
