@@ -726,10 +726,11 @@ __device__ __forceinline__ void runs_body(
         fa = lds_u8(ep + 16 + gid);
         fb = lds_u8(ep + 24 + gid);
         // hc ka may be infinite where the score is not, its two parts' products cannot.
-        s[0] = s[0] * (lo0 * ka) * up0;
-        s[1] = s[1] * (lo1 * ka) * up1;
-        s[2] = s[2] * (lo0 * kb) * up0;
-        s[3] = s[3] * (lo1 * kb) * up1;
+        // (Rounded here, and not joined with the differences from the reference below.)
+        s[0] = __fmul_rn(s[0] * (lo0 * ka), up0);
+        s[1] = __fmul_rn(s[1] * (lo1 * ka), up1);
+        s[2] = __fmul_rn(s[2] * (lo0 * kb), up0);
+        s[3] = __fmul_rn(s[3] * (lo1 * kb), up1);
       } else {
         float s2[4] = {0.f, 0.f, 0.f, 0.f};  // two chains: half the latency
 #pragma unroll
@@ -741,7 +742,7 @@ __device__ __forceinline__ void runs_body(
           mma_bf16(s2, x.z, y.z, x.w, y.w, qb[2 * c + 1][0], qb[2 * c + 1][1]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = (s[i] + s2[i]) * (i & 1 ? hc1 : hc0);
+        for (int i = 0; i < 4; ++i) s[i] = __fmul_rn(s[i] + s2[i], i & 1 ? hc1 : hc0);  // (as above)
       }
 
       // ---- weights: p relative to m, w (8-bit) relative to r ----

@@ -80,3 +80,35 @@ def test_values_of_any_size(exp, lens):
     o, lse = run(args, window, sinks)
     check_out(o.double().cpu() * 2.0 ** -exp, O * 2.0 ** -exp, torch.bfloat16)
     check_lse(lse, L)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("exp", [24, 28, 30, 31, 32, 35, 60, 100])
+@pytest.mark.parametrize("rows", [1, 16])
+def test_large_logits_of_every_mantissa(exp, rows, eight):
+    """Queries' factors with every mantissa, so that products lie anywhere between two fp32
+    numbers. One visible key leads: a row is that key's value."""
+    window, sinks, n = 600, 4, 1000
+    for at in range(0, 128, 8 * rows):
+        args = case([n] * rows, 2, 4, 64, 15, 10 ** 6, 0, eight)
+        q, k = args[0], args[1]
+        q.zero_()
+        q[:, :, 0] = ((1 + (at + torch.arange(rows * 8)).view(rows, 8) / 128.0) * 2.0 ** exp).to(torch.bfloat16)
+        lead = args[-2][:, 950 // 16].long()
+        if eight:  # codes 0 to 7 and 8, exponent 0
+            codes = torch.zeros(k.shape)
+            codes[..., 0] = torch.randint(-8, 8, k.shape[:-1], generator=torch.Generator().manual_seed(1)).float()
+            codes[lead, :, 950 % 16, 0] = 8
+            args[1] = codes.to(torch.float8_e4m3fn)
+            args[3].fill_(127)
+        else:
+            k.zero_()
+            k[..., 0] = torch.randint(-8, 8, k.shape[:-1], generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+            k[lead, 950 % 16, :, 0] = 8
+        O, L = reference(args, window, sinks)
+        o, lse = run(args, window, sinks)
+        # (Half a bf16 step is up to 2^-8 of a number; a weight's rounding moves the one that
+        # the row is by less.)
+        assert (np.abs(o.double().cpu().numpy() - O) <= 2.0 ** -8 * np.abs(O) + 2.0 ** -24).all()
+        # Factor, product, ln 2 and the product with it, the keys' exponent: 6 roundings of 2^-24.
+        assert (np.abs(lse.double().cpu().numpy() - L) <= 2.0 ** -21 * np.abs(L)).all()
