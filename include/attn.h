@@ -379,6 +379,8 @@ size_t attn_decode_workspace_bytes(int B, int h, int num_splits, int d_h);
  * table entry outside [0, num_blocks) is treated as a page of zeros and sets
  * ATTN_DEVERR_BAD_PAGE. A seq_len below 0 or above max_blocks_per_seq *
  * page_size is clamped into that range and sets ATTN_DEVERR_BAD_SEQ_LEN.
+ * Logits (scale q.k) have to stay below 2^28 in magnitude (in the other forms of this
+ * call too; the windowed, shared-prefix, 8-bit and tree decodes take any).
  * Errors: INVALID_ARG for NULL pointers (B > 0), bad sizes, misalignment or
  * workspace_bytes too small; UNSUPPORTED for other d_h / g / page_size.
  */

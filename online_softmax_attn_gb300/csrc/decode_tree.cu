@@ -41,11 +41,11 @@
 //
 // Measured (GB300): 64 rows of up to 16384 keys and 24 drafts, 32 query heads over 8
 // of 128: 341 to 370 us, box to box, the keys' bytes at 0.95 to 0.87 of the copy rate. One
-// row of 32768 keys and 26 drafts: 35.7 us, 20 of them the bytes; the others are the
+// row of 32768 keys and 26 drafts: 36 us, 20 of them the bytes; the others are the
 // launch, the CTA's set-up, the first keys' way and the merge. 24 rows of up to 8192 keys,
-// 61 drafts, 8 heads over one of 64 (two row tiles each): 26.7 us (31 on another box),
-// where the two streams' chain S, weights, P V takes 2.1 us a key tile. One row of 500
-// keys and 8 drafts: 10.7 us, latency. (Figures beside a choice below compare two forms on
+// 61 drafts, 8 heads over one of 64 (two row tiles each): 27 to 33 us, box to box, where
+// the two streams' chain S, weights, P V takes 2.1 us a key tile. One row of 500 keys and
+// 8 drafts: 11 us, latency. (Figures beside a choice below compare two forms on
 // one box, at the state of the kernel when it was made.)
 #include "decode_runs.cuh"
 #include "pdl.cuh"
