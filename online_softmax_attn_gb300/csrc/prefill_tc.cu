@@ -92,7 +92,7 @@ constexpr float kRefHeadroom = 8.0f;
 // the window often pass it. 8192 tokens 139.7 -> 140.5 us, 142.6 with 4 below for the sinks
 // too (the whole-row prefill, its logits' deviation 9, would take 369.0 instead of 355.7).
 // A window that no row of the table reaches keeps 8, and with it attn_prefill_paged's
-// results to the bit.
+// weights to the bit.
 constexpr float kWindowHeadroom = -4.0f;
 
 // Windows: the fp16 copy holds V times kVScale, which is exact from 2^(-17 - 8) (8 bits
@@ -423,8 +423,8 @@ __device__ __noinline__ void mask_window(uint32_t tS, int lo, int hi, int sinks)
 // columns, and their reference and sum. (The whole tile took 2.3 us of an item's 21 with
 // a window of 1024. With the scores in the O tile's columns and the weights behind the
 // second tile's, so that the sinks have no turn of their own, 8192 tokens took 145 us
-// where an earlier state of this form took 137.) Out of line, so that the softmax loop holds neither its code nor its
-// registers. Warp-collective.
+// where an earlier state of this form took 137.) Out of line, so that the softmax loop
+// holds neither its code nor its registers. Warp-collective.
 __device__ __noinline__ float2 sink_weights(uint32_t tS, uint32_t bits, float scale_log2) {
   uint32_t s[32];
   tc::ld32(tS, s);
@@ -1622,13 +1622,13 @@ __device__ __forceinline__ void window_tiles(const int32_t* __restrict__ cu_q, i
 // + t), and flags [B, h_kv, max_tiles] with v_to_f16_kernel's meaning. A tile
 // is written as fp16 when it holds no magnitude of 2^16 or more (values below
 // 2^-14 within 2^-25), else (flagged) as the bf16 values themselves, so the
-// attention kernel reads every V tile of the row from this copy. Keys from the row's last key to the end of its last
-// 128-key tile, and pages whose block-table entry lies outside the cache, are
-// written as zeros, whatever the cache holds there. Rows the attention kernel
-// skips (query count above the row's capacity) are left alone. The key count
-// is clamped as the attention kernel clamps it. One CTA per (tile, row, KV
-// head); each thread holds its CPR / 2 chunks of 16 bytes between the range
-// check and the store.
+// attention kernel reads every V tile of the row from this copy. Keys from
+// the row's last key to the end of its last 128-key tile, and pages whose
+// block-table entry lies outside the cache, are written as zeros, whatever the
+// cache holds there. Rows the attention kernel skips (query count above the
+// row's capacity) are left alone. The key count is clamped as the attention
+// kernel clamps it. One CTA per (tile, row, KV head); each thread holds its
+// CPR / 2 chunks of 16 bytes between the range check and the store.
 //
 // WIN: with a window, tiles that no query of the row sees are left alone, and keys
 // that none sees are zeros in the others; their pages are not looked up. The copy holds
