@@ -40,13 +40,13 @@
 // drafts are looked at for that, and for slots past the row's end.
 //
 // Measured (GB300): 64 rows of up to 16384 keys and 24 drafts, 32 query heads over 8
-// of 128: 341 to 370 us, box to box, the keys' bytes at 0.95 to 0.87 of the copy rate. One
+// of 128: 341 to 370 us, GPU to GPU, the keys' bytes at 0.95 to 0.87 of the copy rate. One
 // row of 32768 keys and 26 drafts: 36 us, 20 of them the bytes; the others are the
 // launch, the CTA's set-up, the first keys' way and the merge. 24 rows of up to 8192 keys,
-// 61 drafts, 8 heads over one of 64 (two row tiles each): 27 to 33 us, box to box, where
+// 61 drafts, 8 heads over one of 64 (two row tiles each): 27 to 33 us, GPU to GPU, where
 // the two streams' chain S, weights, P V takes 2.1 us a key tile. One row of 500 keys and
 // 8 drafts: 11 us, latency. (Figures beside a choice below compare two forms on
-// one box, at the state of the kernel when it was made.)
+// one GPU, at the state of the kernel when it was made.)
 #include "decode_runs.cuh"
 #include "pdl.cuh"
 #include "tc.cuh"
@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(384, 1)
 // behind it, in run order. An item is kMergeThreads / (D / 4) query rows of a cut unit,
 // a thread 4 dims of one over all parts, kMergeUnroll of them in flight. One CTA per
 // attention CTA: it looks at all cuts, and its groups take their share of the items. (On
-// one box one row of 32768 keys took 35.9 us all in all, 24 rows with two row tiles 32.2;
+// one GPU one row of 32768 keys took 35.9 us all in all, 24 rows with two row tiles 32.2;
 // with a CTA per cut and 8 rows, most of them without work, 38.0 and 34.0; with 8 parts in
 // flight 36.5 and 31.9, with 20 38.1 and 32.1; with two CTAs 2 us more (what the looks at the
 // cuts cost: all read the same lines; a look per warp 5 us more).)

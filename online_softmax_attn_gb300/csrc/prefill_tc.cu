@@ -51,7 +51,7 @@
 //   the visible pairs at the tensor cores' rate): 140 us, the V pass among them. An item
 //   takes about 19 us: nine tiles of 1.62, the sinks' 1.1, the edges' masks twice 0.7, and
 //   about 2 from its last product to the next one's first weights. 8 rows of 1024 tokens
-//   over 8192 keys, window 4096: 420 to 437 us, box to box, for 281.
+//   over 8192 keys, window 4096: 420 to 437 us, GPU to GPU, for 281.
 //   Every mbarrier wait is bounded; on a timeout the CTA raises the error
 //   word, drains its copies and MMAs (bounded), frees tensor memory and exits.
 #include <climits>
